@@ -394,6 +394,95 @@ FOS_API fos_status fos_quantize_grouped(const void* x, fos_dtype dt, int64_t row
                                 float* group_amax, uint8_t* codes, uint8_t* scales,
                                 fos_stream_t stream);
 
+/*
+ * ------------------------------------------------------------------------
+ * The feed-forward block around the quantized products: the norm before
+ * them, products with an epilogue, and the backward pass of both.
+ *
+ * 8-bit block format: a tensor [rows, cols], cols % 32 == 0, is held as E4M3
+ * codes [rows, cols] (one byte an element) and one UE8M0 scale byte per 32
+ * consecutive elements of a row: value = e4m3(code) * 2^(scale - 127).  The
+ * scale of a block with largest magnitude a (NaN dropped) is the smallest
+ * power of two 2^e, e >= -127, with a <= 448 * 2^e; a code is
+ * E4M3_rn_satfinite(v * 2^-e); a NaN element keeps a NaN code.  Scales are
+ * plain [rows, cols/32] (FOS_SCALES_PLAIN) or in the tiled layout of
+ * fos_swizzle_scales applied to that matrix (FOS_SCALES_TILED, padding
+ * zeroed by the call, what the products read): fos_scales8_bytes gives their
+ * size, -1 for negative sizes, cols % 32 != 0 or a bad layout.
+ *
+ * Sums, the norm's statistics and every step before the one rounding to the
+ * output's type are fp32.  Sums have a fixed order: equal calls give equal
+ * bits.  Outputs must not overlap inputs or one another.  rows and cols below
+ * 2^30.  Tensors 32-byte, codes 16-byte (codes_t 32-byte), tiled scales
+ * 4-byte, workspaces 256-byte aligned.  Errors: FOS_ERR_INVALID_ARG (bad
+ * enum, negative size, missing pointer, codes without scales, pointers on
+ * different devices, a workspace too small), FOS_ERR_UNSUPPORTED (cols % 32,
+ * sizes above the limits), FOS_ERR_MISALIGNED.
+ */
+FOS_API int64_t fos_scales8_bytes(int64_t rows, int64_t cols, int scale_layout);
+
+/*
+ * fos_rms_norm -- h = x + residual (residual may be NULL: h = x), rstd =
+ * 1 / sqrt(mean(h^2) + eps) per row, y = h * rstd * weight.  Writes whichever
+ * of these is given: h and y rounded to dt, the 8-bit codes and scales of
+ * the unrounded y, rstd [rows] fp32 (what the backward pass reads).  weight
+ * [cols] is fp32 or of type dt.  eps finite and >= 0.  A row with an infinity
+ * has rstd 0; a NaN spreads over its row.  cols == 0 is refused.
+ */
+FOS_API fos_status fos_rms_norm(const void* x, const void* residual, const void* weight,
+                                fos_dtype dt, fos_dtype weight_dt, int64_t rows, int64_t cols,
+                                float eps, int scale_layout, void* h, void* y, uint8_t* codes,
+                                uint8_t* scales, float* rstd, fos_stream_t stream);
+
+/*
+ * fos_rms_norm_backward -- with g = dy * weight:
+ *   dx = rstd * g - h * rstd^3 * mean(g * h) + dh
+ *   dweight[c] = sum over rows of dy * h * rstd            (fp32)
+ * dy, h, dx are of type dt; dh (the gradient that reaches h past the norm)
+ * may be NULL; dx is the gradient of x and, the same, of the residual.
+ * dweight may be NULL.  With dweight, workspace holds
+ * fos_rms_norm_backward_workspace_bytes(rows, cols) bytes of device memory.
+ */
+FOS_API size_t fos_rms_norm_backward_workspace_bytes(int64_t rows, int64_t cols);
+FOS_API fos_status fos_rms_norm_backward(const void* dy, const void* h, const void* dh,
+                                         const float* rstd, const void* weight, fos_dtype dt,
+                                         fos_dtype weight_dt, int64_t rows, int64_t cols, void* dx,
+                                         float* dweight, void* workspace, size_t workspace_bytes,
+                                         fos_stream_t stream);
+
+/*
+ * fos_quantize8 -- x [rows, cols] in the 8-bit block format along its rows
+ * (codes, scales) and / or along its columns: codes_t [cols, R], scales_t of
+ * a [cols, R] tensor, R = rows rounded up to a multiple of 32, are the format
+ * of x^T with zeros past the last row (the operand of a weight-gradient
+ * product, or a weight for the input gradient), from the same read.  Either
+ * pair may be NULL.
+ */
+FOS_API fos_status fos_quantize8(const void* x, fos_dtype dt, int64_t rows, int64_t cols,
+                                 int scale_layout, uint8_t* codes, uint8_t* scales,
+                                 uint8_t* codes_t, uint8_t* scales_t, fos_stream_t stream);
+
+/* Activations of the product's epilogue: v; max(v, 0); v (1 + erf(v / sqrt 2)) / 2;
+ * v (1 + tanh(sqrt(2/pi) (v + 0.044715 v^3))) / 2; v / (1 + exp(-v)). */
+enum { FOS_ACT_NONE = 0, FOS_ACT_RELU = 1, FOS_ACT_GELU = 2, FOS_ACT_GELU_TANH = 3,
+       FOS_ACT_SILU = 4 };
+
+/*
+ * fos_act_backward -- d = dout * act'(pre), the gradient at the epilogue's
+ * pre-activation (pre as fos_linear8 / fos_linear4 store it; with
+ * FOS_ACT_NONE it is not read), in any of: d rounded to dt, its 8-bit rows
+ * (for the input gradient's product), its 8-bit columns (for the weight
+ * gradient's), and dbias [cols] fp32, the sum of its columns.  dbias over
+ * more than 128 rows needs fos_act_backward_workspace_bytes(rows, cols)
+ * bytes of workspace.  relu'(0) = 0.
+ */
+FOS_API size_t fos_act_backward_workspace_bytes(int64_t rows, int64_t cols);
+FOS_API fos_status fos_act_backward(const void* dout, const void* pre, fos_dtype dt, int64_t rows,
+                                    int64_t cols, int act, int scale_layout, void* d,
+                                    uint8_t* codes, uint8_t* scales, uint8_t* codes_t,
+                                    uint8_t* scales_t, float* dbias, void* workspace,
+                                    size_t workspace_bytes, fos_stream_t stream);
+
 /* Static, human-readable name of a status code. */
 FOS_API const char* fos_status_string(fos_status s);
 

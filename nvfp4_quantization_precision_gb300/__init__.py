@@ -19,6 +19,10 @@ Entry points (names follow the C ABI):
   quantize_colwise(x, ...)                  -> (codes_t, scales_t, amax[, codes, scales])
   swizzle_scales(scales, rows, cols)        -> scales in the tiled GEMM layout
   mm(a_codes, a_tiled, a_amax, b_codes, b_tiled, b_amax) -> fp32 a . b^T
+  rms_norm(x, weight, residual, ...)        -> (codes, scales, y, h, rstd), 8-bit blocks
+  rms_norm_backward(dy, h, rstd, weight, dh) -> (dx, dweight)
+  quantize8(x, ...)                         -> (codes, scales, codes_t, scales_t)
+  act_backward(dout, pre, act, ...)         -> (codes, scales, codes_t, scales_t, d, dbias)
 """
 import ctypes
 import os
@@ -106,6 +110,19 @@ def lib():
                   "fos_dequantize", "fos_qdq", "fos_qdq_fused", "fos_workspace_error",
                   "fos_quantize_grouped", "fos_diag_convert"):
             getattr(L, n).restype = ctypes.c_int
+        L.fos_scales8_bytes.argtypes = [I64, I64, I]
+        L.fos_scales8_bytes.restype = ctypes.c_int64
+        L.fos_rms_norm.argtypes = [P, P, P, I, I, I64, I64, ctypes.c_float, I, P, P, P, P, P, P]
+        L.fos_rms_norm_backward.argtypes = [P, P, P, P, P, I, I, I64, I64, P, P, P,
+                                            ctypes.c_size_t, P]
+        L.fos_quantize8.argtypes = [P, I, I64, I64, I, P, P, P, P, P]
+        L.fos_act_backward.argtypes = [P, P, I, I64, I64, I, I, P, P, P, P, P, P, P,
+                                       ctypes.c_size_t, P]
+        for n in ("fos_rms_norm", "fos_rms_norm_backward", "fos_quantize8", "fos_act_backward"):
+            getattr(L, n).restype = ctypes.c_int
+        for n in ("fos_rms_norm_backward_workspace_bytes", "fos_act_backward_workspace_bytes"):
+            getattr(L, n).argtypes = [I64, I64]
+            getattr(L, n).restype = ctypes.c_size_t
         L.fos_status_string.argtypes = [I]
         L.fos_status_string.restype = ctypes.c_char_p
         L.fos_version.restype = ctypes.c_int
@@ -448,6 +465,208 @@ def quantize_grouped(x, offs, cfg=Config(), group_amax=None, codes=None, scales=
                                       _p(group_amax), _p(codes), _p(scales), _stream(x)),
            "fos_quantize_grouped")
     return codes, scales, group_amax
+
+
+# ------------------------------------------------------------------ feed-forward operators
+ACT_NONE, ACT_RELU, ACT_GELU, ACT_GELU_TANH, ACT_SILU = range(5)
+_ACTS = {"none": ACT_NONE, "relu": ACT_RELU, "gelu": ACT_GELU, "gelu_tanh": ACT_GELU_TANH,
+         "silu": ACT_SILU}
+
+
+def _act(act):
+    if act not in _ACTS:
+        raise ValueError("act must be one of %s" % ", ".join(_ACTS))
+    return _ACTS[act]
+
+
+def _a(t):
+    """Address of an optional tensor (None: null)."""
+    return t.data_ptr() if t is not None else None
+
+
+def _like(t, name, shape, dtype, dev):
+    """Checks an operand or a caller's output buffer: a contiguous CUDA tensor
+    of this shape, type and device."""
+    if t.dtype != dtype or t.shape != shape or t.device != dev or not t.is_contiguous():
+        raise ValueError("%s must be a contiguous %s tensor of shape %s on %s"
+                         % (name, dtype, tuple(shape), dev))
+    return t
+
+
+def _data(t, name):
+    """Checks a rank-2 floating-point input; returns (rows, cols, type, device)."""
+    _cuda(t, name)
+    if t.dim() != 2 or t.dtype not in _DT:
+        raise ValueError("%s must be a rank-2 bf16, fp16 or fp32 tensor" % name)
+    return t.shape[0], t.shape[1], _DT[t.dtype], t.device
+
+
+def _weight(w, cols, dtype, dev):
+    if not isinstance(w, torch.Tensor) or w.dtype not in (torch.float32, dtype):
+        raise ValueError("weight must be float32 or of the input's type")
+    return _DT[_like(w, "weight", (cols,), w.dtype, dev).dtype]
+
+
+def _pair8(rows, cols, tiled, codes, scales, dev, names=("codes", "scales")):
+    """Code and scale buffers of a [rows, cols] tensor in the 8-bit block
+    format: the caller's, checked, or new ones."""
+    if cols % 32:
+        raise FosError(FOS_ERR_UNSUPPORTED, names[0])
+    if codes is None:
+        codes = torch.empty((rows, cols), dtype=torch.uint8, device=dev)
+    else:
+        _like(codes, names[0], (rows, cols), torch.uint8, dev)
+    shape = ((rows + 127) // 128 * ((cols + 127) // 128) * 512,) if tiled else (rows, cols // 32)
+    if scales is None:
+        scales = torch.empty(shape, dtype=torch.uint8, device=dev)
+    else:
+        _like(scales, names[1], shape, torch.uint8, dev)
+    return codes, scales
+
+
+def scales8_shape(rows, cols, tiled=True):
+    """Shape of the scale bytes of a [rows, cols] tensor in the 8-bit block format."""
+    n = lib().fos_scales8_bytes(int(rows), int(cols), int(bool(tiled)))
+    if n < 0:
+        raise ValueError("bad shape for 8-bit block scales")
+    return (n,) if tiled else (rows, cols // 32)
+
+
+def rms_norm(x, weight, residual=None, eps=1e-6, scale_tiled=True, quantized=True,
+             normalized=False, codes=None, scales=None, y=None, h=None, rstd=None):
+    """fos_rms_norm: h = x + residual, y = h / sqrt(mean(h^2) + eps) * weight
+    over the rows of x [rows, cols].  Returns (codes, scales, y, h, rstd):
+    y's 8-bit codes and scales (None without quantized), y itself with
+    normalized (else None), h (x itself without a residual) and rstd [rows]."""
+    R, C, dt, dev = _data(x, "x")
+    wdt = _weight(weight, C, x.dtype, dev)
+    if residual is not None:
+        _like(residual, "residual", x.shape, x.dtype, dev)
+        h = torch.empty_like(x) if h is None else _like(h, "h", x.shape, x.dtype, dev)
+    elif h is not None:
+        raise ValueError("h is an output of a norm with a residual")
+    if quantized:
+        codes, scales = _pair8(R, C, scale_tiled, codes, scales, dev)
+    else:
+        codes = scales = None
+    if normalized:
+        y = torch.empty_like(x) if y is None else _like(y, "y", x.shape, x.dtype, dev)
+    else:
+        y = None
+    if rstd is None:
+        rstd = torch.empty(R, dtype=torch.float32, device=dev)
+    else:
+        _like(rstd, "rstd", (R,), torch.float32, dev)
+    _check(lib().fos_rms_norm(x.data_ptr(), _a(residual), weight.data_ptr(), dt, wdt, R, C, eps,
+                              int(bool(scale_tiled)), _a(h), _a(y), _a(codes), _a(scales),
+                              rstd.data_ptr(), _stream(x)), "fos_rms_norm")
+    return codes, scales, y, x if h is None else h, rstd
+
+
+def _workspace(workspace, need, dev):
+    if need == 0:
+        return None, 0
+    if workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    else:
+        _cuda(workspace, "workspace")
+        if workspace.dtype != torch.uint8 or workspace.device != dev:
+            raise ValueError("workspace must be a uint8 tensor on %s" % dev)
+    return workspace, workspace.numel()
+
+
+def rms_norm_backward(dy, h, rstd, weight, dh=None, weight_grad=True, dx=None, dweight=None,
+                      workspace=None):
+    """fos_rms_norm_backward: (dx, dweight) from the gradient dy of the norm's
+    output, the h and rstd the forward call returned, and optionally the
+    gradient dh that reaches h from elsewhere.  dx is the gradient of x and of
+    the residual; dweight is fp32 (None without weight_grad).  workspace: at
+    least fos_rms_norm_backward_workspace_bytes of uint8, allocated when None."""
+    R, C, dt, dev = _data(dy, "dy")
+    _like(h, "h", dy.shape, dy.dtype, dev)
+    _like(rstd, "rstd", (R,), torch.float32, dev)
+    wdt = _weight(weight, C, dy.dtype, dev)
+    if dh is not None:
+        _like(dh, "dh", dy.shape, dy.dtype, dev)
+    dx = torch.empty_like(dy) if dx is None else _like(dx, "dx", dy.shape, dy.dtype, dev)
+    nws = 0
+    if weight_grad:
+        if dweight is None:
+            dweight = torch.empty(C, dtype=torch.float32, device=dev)
+        else:
+            _like(dweight, "dweight", (C,), torch.float32, dev)
+        workspace, nws = _workspace(workspace, lib().fos_rms_norm_backward_workspace_bytes(R, C),
+                                    dev)
+    else:
+        dweight = workspace = None
+    _check(lib().fos_rms_norm_backward(dy.data_ptr(), h.data_ptr(), _a(dh), rstd.data_ptr(),
+                                       weight.data_ptr(), dt, wdt, R, C, dx.data_ptr(),
+                                       _a(dweight), _a(workspace), nws, _stream(dy)),
+           "fos_rms_norm_backward")
+    return dx, dweight
+
+
+def quantize8(x, scale_tiled=True, rowwise=True, colwise=False, codes=None, scales=None,
+              codes_t=None, scales_t=None):
+    """fos_quantize8: x [rows, cols] in the 8-bit block format.  Returns
+    (codes, scales, codes_t, scales_t); the first two are the rows of x (None
+    without rowwise), the last two the rows of x.T padded with zeros to a
+    multiple of 32 (None without colwise)."""
+    R, C, dt, dev = _data(x, "x")
+    if rowwise:
+        codes, scales = _pair8(R, C, scale_tiled, codes, scales, dev)
+    else:
+        codes = scales = None
+    if colwise:
+        codes_t, scales_t = _pair8(C, (R + 31) // 32 * 32, scale_tiled, codes_t, scales_t, dev,
+                                   ("codes_t", "scales_t"))
+    else:
+        codes_t = scales_t = None
+    _check(lib().fos_quantize8(x.data_ptr(), dt, R, C, int(bool(scale_tiled)), _a(codes),
+                               _a(scales), _a(codes_t), _a(scales_t), _stream(x)),
+           "fos_quantize8")
+    return codes, scales, codes_t, scales_t
+
+
+def act_backward(dout, pre, act, scale_tiled=True, rowwise=True, colwise=True, value=False,
+                 bias_grad=True, codes=None, scales=None, codes_t=None, scales_t=None, d=None,
+                 dbias=None, workspace=None):
+    """fos_act_backward: d = dout * act'(pre), as (codes, scales, codes_t,
+    scales_t, d, dbias): its 8-bit rows (rowwise), its 8-bit columns
+    (colwise), d itself (value) and the fp32 sum of its columns (bias_grad);
+    what is not asked for is None.  act: "none", "relu", "gelu", "gelu_tanh",
+    "silu"; pre may be None with "none"."""
+    R, C, dt, dev = _data(dout, "dout")
+    a = _act(act)
+    if pre is not None:
+        _like(pre, "pre", dout.shape, dout.dtype, dev)
+    if rowwise:
+        codes, scales = _pair8(R, C, scale_tiled, codes, scales, dev)
+    else:
+        codes = scales = None
+    if colwise:
+        codes_t, scales_t = _pair8(C, (R + 31) // 32 * 32, scale_tiled, codes_t, scales_t, dev,
+                                   ("codes_t", "scales_t"))
+    else:
+        codes_t = scales_t = None
+    if value:
+        d = torch.empty_like(dout) if d is None else _like(d, "d", dout.shape, dout.dtype, dev)
+    else:
+        d = None
+    nws = 0
+    if bias_grad:
+        if dbias is None:
+            dbias = torch.empty(C, dtype=torch.float32, device=dev)
+        else:
+            _like(dbias, "dbias", (C,), torch.float32, dev)
+        workspace, nws = _workspace(workspace, lib().fos_act_backward_workspace_bytes(R, C), dev)
+    else:
+        dbias = workspace = None
+    _check(lib().fos_act_backward(dout.data_ptr(), _a(pre), dt, R, C, a, int(bool(scale_tiled)),
+                                  _a(d), _a(codes), _a(scales), _a(codes_t), _a(scales_t),
+                                  _a(dbias), _a(workspace), nws, _stream(dout)),
+           "fos_act_backward")
+    return codes, scales, codes_t, scales_t, d, dbias
 
 
 DIAG_E2M1_ENCODE, DIAG_E2M1_DECODE, DIAG_E4M3_ENCODE, DIAG_E4M3_DECODE = 0, 1, 2, 3

@@ -15,6 +15,7 @@
 
 #include "../../include/fos.h"
 #include "../../include/fos_diag.h"
+#include "fos_host.cuh"
 #include "fos_launch.cuh"
 
 using namespace fos;
@@ -22,8 +23,6 @@ using namespace fos;
 namespace {
 
 constexpr int kVersion = 10000;  // 1.0.0
-
-bool valid_dtype(int dt) { return dt == FOS_BF16 || dt == FOS_FP16 || dt == FOS_FP32; }
 
 fos_status check_config(const fos_config* cfg) {
     if (!cfg) return FOS_ERR_INVALID_ARG;
@@ -93,65 +92,6 @@ fos_status check_shape(int64_t rows, int64_t cols, bool b16) {
     if (cols > 0 && rows > (int64_t)(INT64_C(1) << 40) / cols) return FOS_ERR_UNSUPPORTED;
     return FOS_OK;
 }
-
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
-
-// Device that owns a pointer, or -1 when the pointer is not device memory.
-int device_of(const void* p) {
-    cudaPointerAttributes at;
-    if (cudaPointerGetAttributes(&at, p) != cudaSuccess) {
-        cudaGetLastError();
-        return -1;
-    }
-    if (at.type != cudaMemoryTypeDevice && at.type != cudaMemoryTypeManaged) return -1;
-    return at.device;
-}
-
-// Switches to the device owning the data for the lifetime of the object.
-struct DeviceScope {
-    int prev = -1;
-    int dev = -1;
-    bool switched = false;
-    fos_status st = FOS_OK;
-    explicit DeviceScope(int d) : dev(d) {
-        if (cudaGetDevice(&prev) != cudaSuccess) {
-            cudaGetLastError();
-            st = FOS_ERR_CUDA;
-            return;
-        }
-        if (prev != dev) {
-            if (cudaSetDevice(dev) != cudaSuccess) {
-                cudaGetLastError();
-                st = FOS_ERR_CUDA;
-                return;
-            }
-            switched = true;
-        }
-    }
-    ~DeviceScope() {
-        if (switched) cudaSetDevice(prev);
-    }
-};
-
-// All listed device pointers must live on one device; returns it or -1.
-int common_device(std::initializer_list<const void*> ptrs) {
-    int dev = -1;
-    for (const void* p : ptrs) {
-        const int d = device_of(p);
-        if (d < 0) return -1;
-        if (dev >= 0 && d != dev) return -1;
-        dev = d;
-    }
-    return dev;
-}
-
-fos_status cuda_status(cudaError_t e) {
-    if (e == cudaSuccess) return FOS_OK;
-    cudaGetLastError();
-    return FOS_ERR_CUDA;
-}
-
-In in_of(fos_dtype dt) { return dt == FOS_BF16 ? In::BF16 : (dt == FOS_FP16 ? In::F16 : In::F32); }
 
 cudaError_t run_amax(const void* x, fos_dtype dt, int64_t rows, int64_t cols, Src scope,
                      float* amax, const int32_t* offs, int G, cudaStream_t s,

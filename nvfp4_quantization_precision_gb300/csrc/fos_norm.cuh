@@ -1,0 +1,506 @@
+// fos_norm.cuh -- root-mean-square norm with the residual's addition and an
+// 8-bit block-scaled output, and its backward pass.
+//
+//   forward   h = x + residual; rstd = 1 / sqrt(mean(h^2) + eps);
+//             y = h * rstd * w; codes and scales of y's rows (fos_block8.cuh)
+//   backward  g = dy * w; dx = rstd * g - h * (rstd^3 * mean(g * h)) + dh;
+//             dw[c] = sum over rows of dy * h * rstd
+//
+// Both are bound by HBM: forward 2 * e bytes read (x, residual), e + 1 + 1/32
+// written per element of e bytes (e with the residual), backward 2e or 3e read
+// and e written.  So a row is read once and lives in registers: a group of
+// kT threads owns a row, thread t the 16-element segments t, t + kT, ..., the
+// row's sum crosses the group by shuffles and one barrier, and the next row's
+// loads are issued before the current row is finished.  Two neighbouring lanes
+// hold one 32-element block.  kT is the smallest group that leaves at most two
+// segments (one in the backward pass, whose weight gradient takes 16 more
+// registers a segment) to a thread; rows of up to 1024 elements go one to a
+// warp, without a barrier.
+#pragma once
+
+#include "fos_block8.cuh"
+#include "fos_kernels.cuh"
+
+namespace fos {
+
+struct NormArgs {
+    const void* x;
+    const void* res;    // optional
+    const void* w;
+    void* h;            // optional: x + res rounded to the data's type
+    void* y;            // optional: the norm's output rounded to the data's type
+    uint8_t* codes;     // optional, with scales
+    uint8_t* scales;
+    float* rstd;        // optional, [rows]
+    int64_t rows;
+    int64_t cols;
+    int64_t pc4;        // tiled scales: 4-block tiles per tile-row
+    float inv_cols;     // 1 / cols
+    float eps;
+    int w32;            // weight is fp32 (else the data's type)
+    int tiled;
+};
+
+// a + b with its rounding error (D. Knuth, TAOCP vol. 2, 4.2.2, theorem B).
+__device__ __forceinline__ void two_sum(float a, float b, float& s, float& e) {
+    s = fadd(a, b);
+    const float t = __fsub_rn(s, a);
+    e = fadd(__fsub_rn(a, __fsub_rn(s, t)), __fsub_rn(b, t));
+}
+
+// Sum over a warp, every lane gets the same value: the lanes' errors are
+// carried along, so the sum is as exact as its fp32 terms.  The codes that
+// follow jump by 1/16 where y crosses a rounding boundary, and every bit that
+// rstd is off moves the boundary for a whole row.
+__device__ __forceinline__ float2 warp_sum2(float hi, float lo) {
+#pragma unroll
+    for (int m = 16; m >= 1; m >>= 1) {
+        const float oh = __shfl_xor_sync(0xFFFFFFFFu, hi, m);
+        const float ol = __shfl_xor_sync(0xFFFFFFFFu, lo, m);
+        float s, e;
+        // both partners add the same two numbers in the same order
+        if ((threadIdx.x & m) == 0) two_sum(hi, oh, s, e);
+        else two_sum(oh, hi, s, e);
+        hi = s;
+        lo = fadd(fadd(lo, ol), e);
+    }
+    return make_float2(hi, lo);
+}
+
+// 1 / sqrt(m) as a pair: an approximation r (a few ulp) and the correction of
+// one Newton step from the exact residual 1 - m r^2, m = mh + ml.
+__device__ __forceinline__ float2 rsqrt2(float mh, float ml) {
+    const float r = rsqrtf(mh);
+    const float t = fmul(mh, r), tl = __fmaf_rn(mh, r, -t);       // mh * r = t + tl
+    float e = __fmaf_rn(-t, r, 1.0f);                             // 1 - mh r^2
+    e = __fmaf_rn(-tl, r, e);
+    e = __fmaf_rn(-fmul(ml, r), r, e);
+    const float lo = fmul(fmul(0.5f, r), e);
+    // a zero or infinite mean has no finite correction
+    return make_float2(r, isfinite(lo) ? lo : 0.0f);
+}
+
+// Sum of the squares of 16 values, added to two packed accumulators.
+__device__ __forceinline__ void add_squares(const uint64_t (&v)[8], uint64_t& a0, uint64_t& a1) {
+#pragma unroll
+    for (int j = 0; j < 8; j += 2) {
+        a0 = fma2(v[j], v[j], a0);
+        a1 = fma2(v[j + 1], v[j + 1], a1);
+    }
+}
+
+// y = h * (rstd * w) with the products' rounding errors folded into one final
+// rounding: rstd = r.x + r.y.
+__device__ __forceinline__ void normed(const uint64_t (&h)[8], const uint64_t (&w)[8], float2 r,
+                                       uint64_t (&y)[8]) {
+    const uint64_t rh = pk(r.x, r.x), rl = pk(r.y, r.y), neg = pk(-1.0f, -1.0f);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const uint64_t p = mul2(w[j], rh);
+        const uint64_t q = fma2(w[j], rl, fma2(w[j], rh, mul2(p, neg)));
+        y[j] = fma2(h[j], p, mul2(h[j], q));
+    }
+}
+
+// Outputs of one segment of a finished row; every lane of a pair takes part.
+template <In IT>
+__device__ __forceinline__ void emit_norm(const NormArgs& a, int64_t row, int64_t seg, bool in,
+                                          const uint64_t (&h)[8], const uint64_t (&w)[8],
+                                          float2 r) {
+    constexpr int64_t kElt = (IT == In::F32) ? 4 : 2;
+    uint64_t y[8];
+    normed(h, w, r, y);
+    float m = seg_amax(y);
+    m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+    if (!in) return;
+    const int64_t at = row * a.cols + seg * 16;
+    if (a.h) store_seg<IT>(static_cast<char*>(a.h) + at * kElt, h);
+    if (a.y) store_seg<IT>(static_cast<char*>(a.y) + at * kElt, y);
+    if (a.codes) {
+        const uint32_t sc = scale8_code(m);
+        uint32_t c[4];
+        encode8(y, scale8_inv(sc), c);
+        st128(a.codes + at, c);
+        if ((seg & 1) == 0)
+            st8(a.scales + scale8_at(a.tiled, row, seg >> 1, a.cols / 32, a.pc4), sc);
+    }
+}
+
+template <In IT, bool RES>
+__device__ __forceinline__ void load_row_seg(const NormArgs& a, int64_t row, int64_t seg, bool in,
+                                             Raw<IT>& x, Raw<IT>& r) {
+    constexpr int64_t kElt = (IT == In::F32) ? 4 : 2;
+    const int64_t at = (row * a.cols + seg * 16) * kElt;
+    if (in) {
+        load_seg<IT, L2::FIRST>(x, static_cast<const char*>(a.x) + at);
+        if constexpr (RES) load_seg<IT, L2::FIRST>(r, static_cast<const char*>(a.res) + at);
+    } else {
+        zero_seg(x);
+        if constexpr (RES) zero_seg(r);
+    }
+}
+
+template <In IT, bool RES>
+__device__ __forceinline__ void row_values(const Raw<IT>& x, const Raw<IT>& r, uint64_t (&h)[8]) {
+    widen<IT>(x, h);
+    if constexpr (RES) {
+        uint64_t b[8];
+        widen<IT>(r, b);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) h[j] = add2(h[j], b[j]);
+    }
+}
+
+// A row per warp (kT = 32) or per CTA (kT = 64 .. 512 threads).
+template <In IT, bool RES, int kT, int kSeg>
+__global__ void __launch_bounds__(kT < 256 ? 256 : kT) k_rms_norm(const NormArgs a) {
+    chain_wait();
+    chain_release();
+    constexpr int kCta = kT < 256 ? 256 : kT;      // threads of a CTA
+    constexpr int kGroups = kCta / kT;             // rows of a CTA at a time
+    constexpr int kW = kT / 32;                    // warps of a row
+    __shared__ float2 s_part[2][kCta / 32];
+    const int t = threadIdx.x % kT, g = threadIdx.x / kT;
+    const int64_t nseg = a.cols / 16;
+    const int64_t step = (int64_t)gridDim.x * kGroups;
+    uint64_t w[kSeg][8];
+    bool in[kSeg];
+    Raw<IT> x[kSeg], r[kSeg];
+    int64_t row = (int64_t)blockIdx.x * kGroups + g;
+#pragma unroll
+    for (int k = 0; k < kSeg; ++k) {
+        in[k] = t + k * kT < nseg;
+        load_row_seg<IT, RES>(a, row, t + k * kT, in[k] && row < a.rows, x[k], r[k]);
+    }
+#pragma unroll
+    for (int k = 0; k < kSeg; ++k) {
+        if (in[k]) load_weight<IT>(a.w, (t + k * kT) * 16, a.w32, w[k]);
+        else
+#pragma unroll
+            for (int j = 0; j < 8; ++j) w[k][j] = 0;
+    }
+    if (a.tiled && a.codes)
+        clear_tiled_pad(a.scales, a.rows, a.cols / 32, a.pc4, blockIdx.x * kCta + threadIdx.x,
+                        gridDim.x * kCta);
+    // all groups of a CTA make the same number of turns (they share barriers)
+    const int64_t first = (int64_t)blockIdx.x * kGroups;
+    int parity = 0;
+    for (int64_t base = first; base < a.rows; base += step, row += step, parity ^= 1) {
+        uint64_t h[kSeg][8], a0 = 0, a1 = 0;
+#pragma unroll
+        for (int k = 0; k < kSeg; ++k) {
+            row_values<IT, RES>(x[k], r[k], h[k]);
+            add_squares(h[k], a0, a1);
+            load_row_seg<IT, RES>(a, row + step, t + k * kT, in[k] && row + step < a.rows, x[k],
+                                  r[k]);
+        }
+        float p0, p1, p2, p3;
+        upk(a0, p0, p1);
+        upk(a1, p2, p3);
+        float2 s = warp_sum2(fadd(fadd(p0, p1), fadd(p2, p3)), 0.0f);
+        if constexpr (kW > 1) {
+            const int wid = threadIdx.x >> 5;
+            if ((threadIdx.x & 31) == 0) s_part[parity][wid] = s;
+            __syncthreads();
+            float hi = 0.0f, lo = 0.0f;
+#pragma unroll
+            for (int i = 0; i < kW; ++i) {
+                const float2 o = s_part[parity][g * kW + i];
+                float e;
+                two_sum(hi, o.x, hi, e);
+                lo = fadd(lo, fadd(o.y, e));
+            }
+            s = make_float2(hi, lo);
+        }
+        // mean + eps as a pair
+        const float mh = fmul(s.x, a.inv_cols);
+        float mlo = __fmaf_rn(s.x, a.inv_cols, -mh);
+        mlo = __fmaf_rn(s.y, a.inv_cols, mlo);
+        float m, e;
+        two_sum(mh, a.eps, m, e);
+        const float2 rs = rsqrt2(m, fadd(e, mlo));
+        if (t == 0 && a.rstd && row < a.rows) a.rstd[row] = fadd(rs.x, rs.y);
+#pragma unroll
+        for (int k = 0; k < kSeg; ++k)
+            emit_norm<IT>(a, row, t + k * kT, in[k] && row < a.rows, h[k], w[k], rs);
+    }
+}
+
+// Rows of more than 16384 elements: a CTA per row reads it twice, the second
+// time from L2 (a row of x and residual is at most a few MB).
+template <In IT, bool RES>
+__global__ void __launch_bounds__(512) k_rms_norm_wide(const NormArgs a) {
+    chain_wait();
+    chain_release();
+    constexpr int kT = 512;
+    __shared__ float2 s_part[2][kT / 32];
+    const int t = threadIdx.x;
+    const int64_t nseg = a.cols / 16;
+    if (a.tiled && a.codes)
+        clear_tiled_pad(a.scales, a.rows, a.cols / 32, a.pc4, blockIdx.x * kT + t,
+                        gridDim.x * kT);
+    int parity = 0;
+    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, parity ^= 1) {
+        float hi = 0.0f, lo = 0.0f;
+        for (int64_t sg = t; sg < nseg; sg += kT) {
+            Raw<IT> x, r;
+            uint64_t h[8], a0 = 0, a1 = 0;
+            load_row_seg<IT, RES>(a, row, sg, true, x, r);
+            row_values<IT, RES>(x, r, h);
+            add_squares(h, a0, a1);
+            float p0, p1, p2, p3, e;
+            upk(a0, p0, p1);
+            upk(a1, p2, p3);
+            two_sum(hi, fadd(fadd(p0, p1), fadd(p2, p3)), hi, e);
+            lo = fadd(lo, e);
+        }
+        float2 s = warp_sum2(hi, lo);
+        if ((t & 31) == 0) s_part[parity][t >> 5] = s;
+        __syncthreads();
+        hi = lo = 0.0f;
+#pragma unroll
+        for (int i = 0; i < kT / 32; ++i) {
+            const float2 o = s_part[parity][i];
+            float e;
+            two_sum(hi, o.x, hi, e);
+            lo = fadd(lo, fadd(o.y, e));
+        }
+        const float mh = fmul(hi, a.inv_cols);
+        float mlo = __fmaf_rn(hi, a.inv_cols, -mh);
+        mlo = __fmaf_rn(lo, a.inv_cols, mlo);
+        float m, e;
+        two_sum(mh, a.eps, m, e);
+        const float2 rs = rsqrt2(m, fadd(e, mlo));
+        if (t == 0 && a.rstd) a.rstd[row] = fadd(rs.x, rs.y);
+        for (int64_t base = 0; base < nseg; base += kT) {  // whole warps for the block shuffles
+            const int64_t sg = base + t;
+            const bool in = sg < nseg;
+            Raw<IT> x, r;
+            uint64_t h[8], w[8];
+            load_row_seg<IT, RES>(a, row, sg, in, x, r);
+            row_values<IT, RES>(x, r, h);
+            if (in) load_weight<IT>(a.w, sg * 16, a.w32, w);
+            else
+#pragma unroll
+                for (int j = 0; j < 8; ++j) w[j] = 0;
+            emit_norm<IT>(a, row, sg, in, h, w, rs);
+        }
+    }
+}
+
+// ------------------------------------------------------------------ backward
+struct NormBwdArgs {
+    const void* dy;
+    const void* h;
+    const void* dh;       // optional
+    const float* rstd;
+    const void* w;
+    void* dx;
+    float* part;          // [gridDim.x, cols] partial weight gradients, or null
+    int64_t rows, cols;
+    float inv_cols;
+    int w32;
+};
+
+template <In IT>
+__device__ __forceinline__ void load_bwd_seg(const NormBwdArgs& a, int64_t at, bool in, Raw<IT>& dy,
+                                             Raw<IT>& h, Raw<IT>& dh) {
+    constexpr int64_t kElt = (IT == In::F32) ? 4 : 2;
+    if (in) {
+        load_seg<IT, L2::FIRST>(dy, static_cast<const char*>(a.dy) + at * kElt);
+        load_seg<IT, L2::FIRST>(h, static_cast<const char*>(a.h) + at * kElt);
+        if (a.dh) load_seg<IT, L2::FIRST>(dh, static_cast<const char*>(a.dh) + at * kElt);
+        else zero_seg(dh);
+    } else {
+        zero_seg(dy);
+        zero_seg(h);
+        zero_seg(dh);
+    }
+}
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+    for (int m = 16; m >= 1; m >>= 1) v = fadd(v, __shfl_xor_sync(0xFFFFFFFFu, v, m));
+    return v;
+}
+
+// dx of one segment from g = dy * w: fma(g, rstd, dh) - h * c.
+__device__ __forceinline__ void bwd_dx(const uint64_t (&g)[8], const uint64_t (&h)[8],
+                                       const uint64_t (&dh)[8], float rstd, float c,
+                                       uint64_t (&dx)[8]) {
+    const uint64_t r2 = pk(rstd, rstd), c2 = pk(-c, -c);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) dx[j] = fma2(h[j], c2, fma2(g[j], r2, dh[j]));
+}
+
+// A row per group of kT threads, one 16-element segment a thread; the weight
+// gradient of the thread's columns is kept in registers over all of its rows
+// and leaves as one partial row per CTA (the groups of a CTA are added in
+// order through shared memory), so the sum has one fixed order.
+template <In IT, int kT>
+__global__ void __launch_bounds__(kT < 256 ? 256 : kT) k_rms_bwd(const NormBwdArgs a) {
+    chain_wait();
+    chain_release();
+    constexpr int kCta = kT < 256 ? 256 : kT;
+    constexpr int kGroups = kCta / kT, kW = kT / 32;
+    constexpr bool kAhead = kCta <= 512 && IT != In::F32;  // next row in registers (64 or 128 of them)
+    __shared__ float s_part[2][kCta / 32];
+    __shared__ float s_dw[kGroups > 1 ? kCta * 16 : 1];
+    const int t = threadIdx.x % kT, g = threadIdx.x / kT;
+    const bool col_in = (int64_t)t * 16 < a.cols;
+    const int64_t step = (int64_t)gridDim.x * kGroups;
+    uint64_t w[8], dw[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) w[j] = dw[j] = 0;
+    int64_t row = (int64_t)blockIdx.x * kGroups + g;
+    Raw<IT> dy, h, dh;
+    if constexpr (kAhead)
+        load_bwd_seg<IT>(a, row * a.cols + t * 16, col_in && row < a.rows, dy, h, dh);
+    if (col_in) load_weight<IT>(a.w, (int64_t)t * 16, a.w32, w);
+    int parity = 0;
+    for (int64_t base = (int64_t)blockIdx.x * kGroups; base < a.rows;
+         base += step, row += step, parity ^= 1) {
+        const bool in = col_in && row < a.rows;
+        if constexpr (!kAhead) load_bwd_seg<IT>(a, row * a.cols + t * 16, in, dy, h, dh);
+        const float rstd = row < a.rows ? __ldg(a.rstd + row) : 0.0f;
+        uint64_t v[8], hv[8], acc = 0;
+        widen<IT>(dy, v);
+        widen<IT>(h, hv);
+        const uint64_t r2 = pk(rstd, rstd);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            dw[j] = fma2(v[j], mul2(hv[j], r2), dw[j]);
+            v[j] = mul2(v[j], w[j]);
+            acc = fma2(v[j], hv[j], acc);
+        }
+        uint64_t dhv[8];
+        widen<IT>(dh, dhv);
+        if constexpr (kAhead)
+            load_bwd_seg<IT>(a, (row + step) * a.cols + t * 16, col_in && row + step < a.rows, dy, h,
+                             dh);
+        float p0, p1;
+        upk(acc, p0, p1);
+        float s = warp_sum(fadd(p0, p1));
+        if constexpr (kW > 1) {
+            if ((threadIdx.x & 31) == 0) s_part[parity][threadIdx.x >> 5] = s;
+            __syncthreads();
+            s = 0.0f;
+#pragma unroll
+            for (int i = 0; i < kW; ++i) s = fadd(s, s_part[parity][g * kW + i]);
+        }
+        if (in) {
+            constexpr int64_t kElt = (IT == In::F32) ? 4 : 2;
+            const float c = fmul(fmul(fmul(s, rstd), fmul(a.inv_cols, rstd)), rstd);
+            uint64_t dx[8];
+            bwd_dx(v, hv, dhv, rstd, c, dx);
+            store_seg<IT>(static_cast<char*>(a.dx) + (row * a.cols + t * 16) * kElt, dx);
+        }
+    }
+    if (!a.part) return;
+    float* out = a.part + (int64_t)blockIdx.x * a.cols + (int64_t)t * 16;
+    if constexpr (kGroups > 1) {
+        float* mine = s_dw + threadIdx.x * 16;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) upk(dw[j], mine[2 * j], mine[2 * j + 1]);
+        __syncthreads();
+        // column i of the CTA's partial: the groups in order
+        for (int64_t i = threadIdx.x; i < a.cols; i += kCta) {
+            float s = s_dw[i];
+#pragma unroll
+            for (int k = 1; k < kGroups; ++k) s = fadd(s, s_dw[k * kT * 16 + i]);
+            a.part[(int64_t)blockIdx.x * a.cols + i] = s;
+        }
+    } else if (col_in) {
+        store_seg<In::F32>(out, dw);
+    }
+}
+
+// Rows too wide for a segment per thread: a CTA per row, two sweeps of it for
+// dx (the second from L2), no weight gradient.
+template <In IT>
+__global__ void __launch_bounds__(512) k_rms_bwd_wide(const NormBwdArgs a) {
+    chain_wait();
+    chain_release();
+    constexpr int kT = 512;
+    constexpr int64_t kElt = (IT == In::F32) ? 4 : 2;
+    __shared__ float s_part[2][kT / 32];
+    const int t = threadIdx.x;
+    const int64_t nseg = a.cols / 16;
+    int parity = 0;
+    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, parity ^= 1) {
+        const float rstd = __ldg(a.rstd + row);
+        uint64_t acc = 0;
+        for (int64_t sg = t; sg < nseg; sg += kT) {
+            Raw<IT> dy, h;
+            uint64_t v[8], hv[8], w[8];
+            const int64_t at = (row * a.cols + sg * 16) * kElt;
+            load_seg<IT>(dy, static_cast<const char*>(a.dy) + at);
+            load_seg<IT>(h, static_cast<const char*>(a.h) + at);
+            load_weight<IT>(a.w, sg * 16, a.w32, w);
+            widen<IT>(dy, v);
+            widen<IT>(h, hv);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) acc = fma2(mul2(v[j], w[j]), hv[j], acc);
+        }
+        float p0, p1;
+        upk(acc, p0, p1);
+        float s = warp_sum(fadd(p0, p1));
+        if ((t & 31) == 0) s_part[parity][t >> 5] = s;
+        __syncthreads();
+        s = 0.0f;
+#pragma unroll
+        for (int i = 0; i < kT / 32; ++i) s = fadd(s, s_part[parity][i]);
+        const float c = fmul(fmul(fmul(s, rstd), fmul(a.inv_cols, rstd)), rstd);
+        for (int64_t sg = t; sg < nseg; sg += kT) {
+            Raw<IT> dy, h, dh;
+            uint64_t v[8], hv[8], dhv[8], w[8], dx[8];
+            load_bwd_seg<IT>(a, row * a.cols + sg * 16, true, dy, h, dh);
+            load_weight<IT>(a.w, sg * 16, a.w32, w);
+            widen<IT>(dy, v);
+            widen<IT>(h, hv);
+            widen<IT>(dh, dhv);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = mul2(v[j], w[j]);
+            bwd_dx(v, hv, dhv, rstd, c, dx);
+            store_seg<IT>(static_cast<char*>(a.dx) + (row * a.cols + sg * 16) * kElt, dx);
+        }
+    }
+}
+
+// Weight gradient of wide rows: CTA (strip, y) sums rows y, y + gridDim.y, ...
+// of a strip of 4096 columns into partial row y.
+template <In IT>
+__global__ void __launch_bounds__(256) k_rms_dw_wide(const NormBwdArgs a) {
+    chain_wait();
+    chain_release();
+    constexpr int64_t kElt = (IT == In::F32) ? 4 : 2;
+    const int64_t c0 = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 16;
+    if (c0 >= a.cols) return;
+    uint64_t dw[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) dw[j] = 0;
+    for (int64_t row = blockIdx.y; row < a.rows; row += gridDim.y) {
+        const float rstd = __ldg(a.rstd + row);
+        const uint64_t r2 = pk(rstd, rstd);
+        Raw<IT> dy, h;
+        uint64_t v[8], hv[8];
+        const int64_t at = (row * a.cols + c0) * kElt;
+        load_seg<IT>(dy, static_cast<const char*>(a.dy) + at);
+        load_seg<IT>(h, static_cast<const char*>(a.h) + at);
+        widen<IT>(dy, v);
+        widen<IT>(h, hv);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) dw[j] = fma2(v[j], mul2(hv[j], r2), dw[j]);
+    }
+    store_seg<In::F32>(a.part + (int64_t)blockIdx.y * a.cols + c0, dw);
+}
+
+// ------------------------------------------------------------------ column sums
+// out[c] = sum over the `parts` partial rows, in a fixed order: a CTA takes 32
+// columns, its 32 warps every 32nd row each, and the warps' sums are added in
+// order.
+constexpr int kSumWarps = 32;
+__global__ void __launch_bounds__(32 * kSumWarps) k_column_sums(const float* part, int64_t parts,
+                                                                int64_t cols, float* out);
+
+}  // namespace fos

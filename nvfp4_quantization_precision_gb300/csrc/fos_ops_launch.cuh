@@ -1,0 +1,67 @@
+// fos_ops_launch.cuh -- host-side launch helpers and launcher declarations of
+// the feed-forward operators (norm, 8-bit quantization, linear).
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include "fos_launch.cuh"
+
+namespace fos {
+
+struct NormArgs;
+struct NormBwdArgs;
+struct Quant8Args;
+enum class Act : int;
+
+// Resident CTAs per SM of a kernel with `threads` threads (cached per kernel,
+// size and device: the query costs host time on every launch otherwise).
+template <class Kernel>
+inline int resident_ctas_of(Kernel kernel, int threads, size_t smem) {
+    static std::mutex mu;
+    static std::unordered_map<const void*, int> cache[16];
+    int dev = 0;
+    cudaGetDevice(&dev);
+    const void* key = reinterpret_cast<const void*>(kernel);
+    std::lock_guard<std::mutex> g(mu);
+    auto& c = cache[dev & 15];
+    auto it = c.find(key);
+    if (it != c.end()) return it->second;
+    int occ = 1;
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, kernel, threads, smem) != cudaSuccess ||
+        occ < 1) {
+        cudaGetLastError();
+        occ = 1;
+    }
+    c[key] = occ;
+    return occ;
+}
+
+// A launch that may be placed while the previous kernel of the stream drains
+// (every kernel waits for it before its first global access).
+template <class Kernel, class... Args>
+inline cudaError_t launch_chained(Kernel kernel, dim3 grid, int threads, size_t smem,
+                                  cudaStream_t s, Args... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+// Partial rows a column sum may take (rows of its workspace).
+constexpr int64_t kMaxParts = 1024;
+
+cudaError_t launch_column_sums(const float* part, int64_t parts, int64_t cols, float* out,
+                               cudaStream_t);
+cudaError_t launch_rms_norm(In, const NormArgs&, cudaStream_t);
+cudaError_t launch_rms_bwd(In, NormBwdArgs, float* dw, float* part, int64_t max_parts,
+                           cudaStream_t);
+cudaError_t launch_quant8(In, Act, const Quant8Args&, cudaStream_t);
+
+}  // namespace fos
