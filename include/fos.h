@@ -483,6 +483,40 @@ FOS_API fos_status fos_act_backward(const void* dout, const void* pre, fos_dtype
                                     uint8_t* scales_t, float* dbias, void* workspace,
                                     size_t workspace_bytes, fos_stream_t stream);
 
+/* What a product's epilogue does, in this order, in fp32 with one rounding per
+ * stored tensor: v = product + bias; pre = v; out = act(v) + residual. */
+typedef struct {
+    int act;              /* FOS_ACT_*                                          */
+    int out_dt;           /* fos_dtype of out, residual and pre                 */
+    int bias_dt;          /* fos_dtype of bias: FOS_FP32 or out_dt              */
+    const void* bias;     /* [N] or NULL                                        */
+    const void* residual; /* [M, N] or NULL                                     */
+    void* pre;            /* [M, N] or NULL: kept for fos_act_backward          */
+} fos_epilogue;
+
+/*
+ * fos_linear8 -- out [M, N] = act(a . b^T + bias) + residual from operands in
+ * the 8-bit block format: a [M, K] (tokens) and b [N, K] (weights), codes
+ * [M, K] and [N, K], scales tiled.  N % 16 == 0, K % 32 == 0, K > 0; M any
+ * number from 0, one token included.
+ * fos_linear4 -- the same from NVFP4 operands as fos_mm takes them (1x16
+ * codes [M, K/2] and [N, K/2], tiled scales, amaxes; cfg->granularity
+ * FOS_SCALE_ROW: a_amax [M]); the product is (D * g_a(m)) * g_b as in fos_mm.
+ * Products run on the tensor cores with fp32 accumulation; the order of the
+ * sum over K is fixed by the sizes.  out, residual, pre, bias, codes and
+ * scales 16-byte aligned.  Waits are bounded as in fos_mm: a CTA whose wait
+ * gave up writes NaN into the first element of its first tile.
+ */
+FOS_API fos_status fos_linear8(const uint8_t* a_codes, const uint8_t* a_scales_tiled,
+                               const uint8_t* b_codes, const uint8_t* b_scales_tiled, int64_t M,
+                               int64_t N, int64_t K, const fos_epilogue* epilogue, void* out,
+                               fos_stream_t stream);
+FOS_API fos_status fos_linear4(const uint8_t* a_codes, const uint8_t* a_scales_tiled,
+                               const float* a_amax, const uint8_t* b_codes,
+                               const uint8_t* b_scales_tiled, const float* b_amax, int64_t M,
+                               int64_t N, int64_t K, const fos_config* cfg,
+                               const fos_epilogue* epilogue, void* out, fos_stream_t stream);
+
 /* Static, human-readable name of a status code. */
 FOS_API const char* fos_status_string(fos_status s);
 

@@ -22,6 +22,8 @@ Entry points (names follow the C ABI):
   rms_norm(x, weight, residual, ...)        -> (codes, scales, y, h, rstd), 8-bit blocks
   rms_norm_backward(dy, h, rstd, weight, dh) -> (dx, dweight)
   quantize8(x, ...)                         -> (codes, scales, codes_t, scales_t)
+  linear8(a_codes, a_scales, b_codes, b_scales, ...) -> act(a . b^T + bias) + residual
+  linear4(a_codes, a_scales, a_amax, b_codes, b_scales, b_amax, ...) -> the same, NVFP4
   act_backward(dout, pre, act, ...)         -> (codes, scales, codes_t, scales_t, d, dbias)
 """
 import ctypes
@@ -56,6 +58,11 @@ class FosConfig(ctypes.Structure):
                 ("err_precision", ctypes.c_int), ("e4m3_bound", ctypes.c_int),
                 ("granularity", ctypes.c_int), ("amax_is_input", ctypes.c_int),
                 ("err_order", ctypes.c_int), ("scale_layout", ctypes.c_int)]
+
+
+class FosEpilogue(ctypes.Structure):
+    _fields_ = [("act", ctypes.c_int), ("out_dt", ctypes.c_int), ("bias_dt", ctypes.c_int),
+                ("bias", ctypes.c_void_p), ("residual", ctypes.c_void_p), ("pre", ctypes.c_void_p)]
 
 
 @dataclass(frozen=True)
@@ -118,7 +125,11 @@ def lib():
         L.fos_quantize8.argtypes = [P, I, I64, I64, I, P, P, P, P, P]
         L.fos_act_backward.argtypes = [P, P, I, I64, I64, I, I, P, P, P, P, P, P, P,
                                        ctypes.c_size_t, P]
-        for n in ("fos_rms_norm", "fos_rms_norm_backward", "fos_quantize8", "fos_act_backward"):
+        EP = ctypes.POINTER(FosEpilogue)
+        L.fos_linear8.argtypes = [P, P, P, P, I64, I64, I64, EP, P, P]
+        L.fos_linear4.argtypes = [P, P, P, P, P, P, I64, I64, I64, CFG, EP, P, P]
+        for n in ("fos_rms_norm", "fos_rms_norm_backward", "fos_quantize8", "fos_act_backward",
+                  "fos_linear8", "fos_linear4"):
             getattr(L, n).restype = ctypes.c_int
         for n in ("fos_rms_norm_backward_workspace_bytes", "fos_act_backward_workspace_bytes"):
             getattr(L, n).argtypes = [I64, I64]
@@ -667,6 +678,83 @@ def act_backward(dout, pre, act, scale_tiled=True, rowwise=True, colwise=True, v
                                   _a(dbias), _a(workspace), nws, _stream(dout)),
            "fos_act_backward")
     return codes, scales, codes_t, scales_t, d, dbias
+
+
+def _operand(codes, scales, name, blk, dev=None):
+    """Checks a product operand's codes [rows, bytes] and flat tiled scales
+    (blk elements per scale, 32 / blk elements per byte)."""
+    _cuda(codes, name + "_codes")
+    dev = dev or codes.device
+    if codes.dim() != 2 or codes.dtype != torch.uint8 or codes.device != dev:
+        raise ValueError("%s_codes must be a rank-2 uint8 tensor on %s" % (name, dev))
+    R, n = codes.shape
+    K = n * (32 // blk)
+    if not isinstance(scales, torch.Tensor) or scales.dtype != torch.uint8 or \
+            scales.device != dev or not scales.is_contiguous() or \
+            scales.numel() != (R + 127) // 128 * ((K + 4 * blk - 1) // (4 * blk)) * 512:
+        raise ValueError("%s_scales must be the tiled uint8 scales of %s_codes" % (name, name))
+    return R, K, dev
+
+
+def _epilogue(M, N, act, bias, residual, out_dtype, save_pre, out, pre, dev):
+    if out_dtype not in _DT:
+        raise ValueError("out_dtype must be bf16, fp16 or fp32")
+    if bias is not None:
+        if bias.dtype not in (torch.float32, out_dtype):
+            raise ValueError("bias must be float32 or of the output's type")
+        _like(bias, "bias", (N,), bias.dtype, dev)
+    if residual is not None:
+        _like(residual, "residual", (M, N), out_dtype, dev)
+    if out is None:
+        out = torch.empty((M, N), dtype=out_dtype, device=dev)
+    else:
+        _like(out, "out", (M, N), out_dtype, dev)
+    if not save_pre:
+        pre = None
+    elif pre is None:
+        pre = torch.empty((M, N), dtype=out_dtype, device=dev)
+    else:
+        _like(pre, "pre", (M, N), out_dtype, dev)
+    return FosEpilogue(_act(act), _DT[out_dtype], _DT[bias.dtype] if bias is not None else FOS_FP32,
+                       _a(bias), _a(residual), _a(pre)), out, pre
+
+
+def linear8(a_codes, a_scales, b_codes, b_scales, act="none", bias=None, residual=None,
+            out_dtype=torch.bfloat16, save_pre=False, out=None, pre=None):
+    """fos_linear8: act(a . b^T + bias) + residual from 8-bit block operands a
+    [M, K] and b [N, K] (codes, tiled scales).  bias [N] is fp32 or of the
+    output's type, residual [M, N] of the output's type.  Returns out, or (out,
+    pre) with save_pre: pre is the value before the activation, which
+    act_backward reads."""
+    M, K, dev = _operand(a_codes, a_scales, "a", 32)
+    N, Kb, _ = _operand(b_codes, b_scales, "b", 32, dev)
+    if K != Kb:
+        raise ValueError("a and b must have the same K")
+    ep, out, pre = _epilogue(M, N, act, bias, residual, out_dtype, save_pre, out, pre, dev)
+    _check(lib().fos_linear8(a_codes.data_ptr(), a_scales.data_ptr(), b_codes.data_ptr(),
+                             b_scales.data_ptr(), M, N, K, ctypes.byref(ep), out.data_ptr(),
+                             _stream(a_codes)), "fos_linear8")
+    return (out, pre) if save_pre else out
+
+
+def linear4(a_codes, a_scales, a_amax, b_codes, b_scales, b_amax, act="none", bias=None,
+            residual=None, out_dtype=torch.bfloat16, save_pre=False, cfg=Config(), out=None,
+            pre=None):
+    """fos_linear4: linear8 for NVFP4 operands (1x16 codes, tiled scales, and
+    the amaxes they were quantized with; cfg.row_scaled when a has one per row)."""
+    M, K, dev = _operand(a_codes, a_scales, "a", 16)
+    N, Kb, _ = _operand(b_codes, b_scales, "b", 16, dev)
+    if K != Kb:
+        raise ValueError("a and b must have the same K")
+    _like(a_amax, "a_amax", (M if cfg.row_scaled else 1,), torch.float32, dev)
+    _like(b_amax, "b_amax", (1,), torch.float32, dev)
+    ep, out, pre = _epilogue(M, N, act, bias, residual, out_dtype, save_pre, out, pre, dev)
+    cc = cfg.c(True)
+    _check(lib().fos_linear4(a_codes.data_ptr(), a_scales.data_ptr(), a_amax.data_ptr(),
+                             b_codes.data_ptr(), b_scales.data_ptr(), b_amax.data_ptr(), M, N, K,
+                             ctypes.byref(cc), ctypes.byref(ep), out.data_ptr(),
+                             _stream(a_codes)), "fos_linear4")
+    return (out, pre) if save_pre else out
 
 
 DIAG_E2M1_ENCODE, DIAG_E2M1_DECODE, DIAG_E4M3_ENCODE, DIAG_E4M3_DECODE = 0, 1, 2, 3

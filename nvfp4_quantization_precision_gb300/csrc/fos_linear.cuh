@@ -1,0 +1,476 @@
+// fos_linear.cuh -- products of quantized operands with an epilogue, on the
+// 5th-generation tensor cores of sm_103a (tcgen05):
+//
+//   v[m][n]   = (a . b^T)[m][n] * g_a(m) * g_b + bias[n]
+//   pre[m][n] = v                         (optional)
+//   out[m][n] = act(v) + residual[m][n]
+//
+// a [M, K] are tokens, b [N, K] weights.  Formats (struct F8, F4): E4M3 codes
+// with a UE8M0 scale per 32 elements (kind::mxf8f6f4, scale_vec::1X; the g are
+// 1), or E2M1 codes with an E4M3 scale per 16 (kind::mxf4nvf4, scale_vec::4X;
+// g the global decode scales).  Both keep 128 code bytes of a row per K stage
+// (the 128-byte swizzle) and take four MMAs of 32 bytes each; their scales
+// come as the 512-byte tiles of the tiled layout, one tile per 128 rows and 4
+// scale blocks, copied from shared to tensor memory by tcgen05.cp in the very
+// form the MMA reads them: scale j of row 32 i + l in byte j of column i of
+// lane l, for every quadrant of lanes.  F4 takes one tile per MMA (its four
+// 16-element blocks), F8 one tile per stage, the MMA choosing byte j.
+#pragma once
+
+#include <cuda.h>
+
+#include "fos_act.cuh"
+#include "fos_kernels.cuh"
+#include "fos_mma.cuh"
+
+namespace fos {
+namespace lin {
+
+using mma::bar_arrive;
+using mma::bar_init;
+using mma::bulk_load;
+using mma::desc_sw128;
+using mma::tc_commit;
+using mma::tc_fence_after;
+using mma::tc_fence_before;
+
+}  // namespace lin
+
+// Everything the epilogue needs.
+struct Epilogue {
+    const void* bias;      // [N], fp32 or the output's type, or null
+    const void* residual;  // [M, N], the output's type, or null
+    void* pre;             // [M, N], the output's type, or null
+    void* out;
+    const float* a_amax;   // F4: [1] or [M]
+    const float* b_amax;   // F4: [1]
+    int a_row;             // F4: a_amax per row
+    int act;
+    int bias32;
+    float six_bound;
+};
+
+// One product, as the host passes it to the launchers.
+struct LinearCall {
+    const uint8_t *a, *as, *b, *bs;  // codes and tiled scales
+    int64_t M, N, K;
+    Epilogue ep;
+    In out;                          // type of out, residual and pre
+    bool fmt4;
+};
+
+namespace lin {
+
+struct F8 {
+    static constexpr int kStageK = 128;   // K elements of a stage
+    static constexpr int kSfTiles = 1;    // scale tiles of a stage, per 128 rows
+    static constexpr bool kGlobal = false;
+};
+struct F4 {
+    static constexpr int kStageK = 256;
+    static constexpr int kSfTiles = 4;
+    static constexpr bool kGlobal = true;
+};
+constexpr int kRowBytes = 128;      // code bytes of a row per stage
+constexpr int kSfTileBytes = 512;
+
+// Shared-memory descriptor of a scale tile (no swizzle: 8-row x 16-byte core
+// matrices 128 bytes apart).
+__device__ __forceinline__ uint64_t desc_sf(uint32_t saddr) {
+    return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)(128 >> 4) << 16) |
+           ((uint64_t)(128 >> 4) << 32) | ((uint64_t)1 << 46);
+}
+
+// Instruction descriptor: element formats (E4M3 0, E2M1 1 or in the F8 kind
+// E4M3 0) in bits 7-9 and 10-12, N >> 3 in 17-22, scale type in 23 (UE8M0 1),
+// M >> 4 in 24-28, scale bytes of b and a in 4-5 and 29-30.
+template <class F>
+__device__ __forceinline__ uint32_t idesc(int m, int n, int sf_id) {
+    const uint32_t fmt = F::kGlobal ? (1u << 7) | (1u << 10) : (1u << 23);
+    return fmt | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24) |
+           ((uint32_t)sf_id << 4) | ((uint32_t)sf_id << 29);
+}
+
+template <class F, int kPair>
+__device__ __forceinline__ void mma_issue(uint32_t acc, uint64_t ad, uint64_t bd, uint32_t id,
+                                          uint32_t sfa, uint32_t sfb, bool accumulate) {
+    const uint32_t p = accumulate ? 1u : 0u;
+    if constexpr (F::kGlobal && kPair == 1)
+        asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+                     "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X "
+                     "[%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(acc), "l"(ad), "l"(bd), "r"(id),
+                     "r"(sfa), "r"(sfb), "r"(p) : "memory");
+    else if constexpr (F::kGlobal)
+        asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+                     "tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.scale_vec::4X "
+                     "[%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(acc), "l"(ad), "l"(bd), "r"(id),
+                     "r"(sfa), "r"(sfb), "r"(p) : "memory");
+    else if constexpr (kPair == 1)
+        asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+                     "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X "
+                     "[%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(acc), "l"(ad), "l"(bd), "r"(id),
+                     "r"(sfa), "r"(sfb), "r"(p) : "memory");
+    else
+        asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+                     "tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X "
+                     "[%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(acc), "l"(ad), "l"(bd), "r"(id),
+                     "r"(sfa), "r"(sfb), "r"(p) : "memory");
+}
+
+template <int kPair>
+__device__ __forceinline__ void sf_copy(uint32_t taddr, uint32_t saddr) {
+    if constexpr (kPair == 1)
+        asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr),
+                     "l"(desc_sf(saddr)) : "memory");
+    else
+        asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr),
+                     "l"(desc_sf(saddr)) : "memory");
+}
+
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&v)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+        "%14,%15}, [%16];"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]),
+          "=r"(v[7]), "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]),
+          "=r"(v[14]), "=r"(v[15])
+        : "r"(taddr));
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+
+template <Out OT>
+__device__ __forceinline__ float load_out(const void* p, int64_t i) {
+    if constexpr (OT == Out::BF16)
+        return __uint_as_float((uint32_t)__ldg(static_cast<const unsigned short*>(p) + i) << 16);
+    else if constexpr (OT == Out::F16) {
+        float f;
+        asm("cvt.f32.f16 %0, %1;" : "=f"(f) : "h"(__ldg(static_cast<const unsigned short*>(p) + i)));
+        return f;
+    } else
+        return __ldg(static_cast<const float*>(p) + i);
+}
+template <Out OT>
+__device__ __forceinline__ void store_out(void* p, int64_t i, float v) {
+    if constexpr (OT == Out::F32) static_cast<float*>(p)[i] = v;
+    else st16(static_cast<unsigned short*>(p) + i, out_pair<OT>(pk(v, 0.0f)));
+}
+
+template <int kN>
+__device__ __forceinline__ void act_apply(int act, float (&v)[kN]) {
+    switch (static_cast<Act>(act)) {
+        case Act::RELU:
+#pragma unroll
+            for (int i = 0; i < kN; ++i) v[i] = act_value<Act::RELU>(v[i]);
+            break;
+        case Act::GELU:
+#pragma unroll
+            for (int i = 0; i < kN; ++i) v[i] = act_value<Act::GELU>(v[i]);
+            break;
+        case Act::GELU_TANH:
+#pragma unroll
+            for (int i = 0; i < kN; ++i) v[i] = act_value<Act::GELU_TANH>(v[i]);
+            break;
+        case Act::SILU:
+#pragma unroll
+            for (int i = 0; i < kN; ++i) v[i] = act_value<Act::SILU>(v[i]);
+            break;
+        default: break;
+    }
+}
+
+// ------------------------------------------------------------------ few tokens
+// k_linear_rows: the weights are the MMA's 128 rows and the tokens its
+// columns, so one token costs 16 columns of tensor work instead of 128 rows,
+// and the time is that of streaming the weights.  A CTA takes 128 weight rows
+// x nt <= 256 tokens; with few such tiles the K axis is split over the S CTAs
+// of a cluster, whose fp32 partial tiles meet in shared memory: CTA r adds
+// tokens r, r + S, ... of all S partials, read through the cluster's
+// distributed shared memory in rank order (one fixed order of the sum).
+//   warp 0    TMA producer (one thread): b tile, a tile, scale tiles of a stage
+//   warp 1    tensor memory; one thread copies scales and issues the MMAs
+//   warps 2-5 epilogue: lane quadrant warp % 4 of the accumulator
+// The scales of stage g go to ring buffer g % 4 of the tensor memory, after
+// the MMAs of stage g - 4 have completed (the ring of stages is at least as
+// long, so that stage's barrier is still in the phase waited for).  Every wait is bounded; a CTA whose
+// wait gave up writes NaN into the first element of its output.
+struct RowsArgs {
+    CUtensorMap tp;      // b codes, box 128 bytes x 128 rows
+    CUtensorMap tq;      // a codes, box 128 bytes x nt rows
+    const uint8_t* sfp;  // b scales, tiled
+    const uint8_t* sfq;  // a scales, tiled
+    Epilogue ep;
+    int64_t M, N;
+    int64_t tiles;       // tiles_p * tiles_q
+    int kb;              // scale tiles along K (4 blocks each)
+    int nkb;             // stages along K
+    int tiles_p;
+    int nt;              // tokens per tile (multiple of 16)
+    int splits;          // cluster size
+    int stages;
+};
+
+constexpr int kRowsThreads = 192;
+constexpr int kMaxStages = 12;
+constexpr int kSfRing = 4;
+constexpr uint32_t kAllColumns = 512;
+
+struct __align__(8) RowsShared {
+    uint64_t full[kMaxStages], empty[kMaxStages], acc_full, acc_empty, done;
+    uint32_t tmem;
+    int fail;
+};
+
+template <class F>
+__host__ __device__ constexpr int rows_q_atoms(int nt) { return (nt + 127) / 128; }
+// Bytes of one stage: codes of both operands, scale tiles of both.
+template <class F>
+__host__ __device__ constexpr int rows_stage_bytes(int nt) {
+    return (128 + nt) * kRowBytes + (1 + rows_q_atoms<F>(nt)) * F::kSfTiles * kSfTileBytes;
+}
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;"
+                 ::: "memory");
+}
+__device__ __forceinline__ float ld_cluster(uint32_t saddr, uint32_t rank) {
+    float v;
+    asm volatile("{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %1, %2;\n\t"
+                 "ld.shared::cluster.f32 %0, [a];\n\t}"
+                 : "=f"(v) : "r"(saddr), "r"(rank) : "memory");
+    return v;
+}
+
+// The epilogue of kN tokens m, m + dm, ... (the first cnt of them) at weight
+// row n.
+template <class F, Out OT, int kN>
+__device__ __forceinline__ void finish_rows(const Epilogue& e, float (&v)[kN], int64_t m, int dm,
+                                            int cnt, int64_t N, int64_t n, float ga0, float gb,
+                                            float bias) {
+#pragma unroll
+    for (int i = 0; i < kN; ++i) {
+        if constexpr (F::kGlobal) {
+            float ga = ga0;
+            if (e.a_row && i < cnt)
+                ga = fdiv(1.0f, global_scale(__ldg(e.a_amax + m + i * dm), e.six_bound));
+            v[i] = fmul(fmul(v[i], ga), gb);
+        }
+        v[i] = fadd(v[i], bias);
+    }
+    const int64_t at = m * N + n, dat = (int64_t)dm * N;
+    if (e.pre) {
+#pragma unroll
+        for (int i = 0; i < kN; ++i)
+            if (i < cnt) store_out<OT>(e.pre, at + i * dat, v[i]);
+    }
+    act_apply(e.act, v);
+    if (e.residual) {
+        float r[kN];
+#pragma unroll
+        for (int i = 0; i < kN; ++i) r[i] = i < cnt ? load_out<OT>(e.residual, at + i * dat) : 0.0f;
+#pragma unroll
+        for (int i = 0; i < kN; ++i) v[i] = fadd(v[i], r[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < kN; ++i)
+        if (i < cnt) store_out<OT>(e.out, at + i * dat, v[i]);
+}
+
+template <class F, Out OT>
+__global__ void __launch_bounds__(kRowsThreads, 1) k_linear_rows(const __grid_constant__ RowsArgs a) {
+    extern __shared__ __align__(1024) unsigned char s_raw[];
+    __shared__ RowsShared sh;
+    unsigned char* base = s_raw + ((1024u - (smem_u32(s_raw) & 1023u)) & 1023u);
+    const int nt = a.nt, S = a.splits, qa = rows_q_atoms<F>(nt), ns = a.stages;
+    const int qbytes = nt * kRowBytes;
+    constexpr int kPBytes = 128 * kRowBytes, kSfP = F::kSfTiles * kSfTileBytes;
+    unsigned char* sP = base;
+    unsigned char* sQ = sP + ns * kPBytes;
+    unsigned char* sFP = sQ + ns * qbytes;
+    unsigned char* sFQ = sFP + ns * kSfP;
+    float* red = reinterpret_cast<float*>(base);  // [nt][128] partial tile, over the ring
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = S > 1 ? (int)cluster_rank() : 0;
+    const int64_t first = blockIdx.x / S, step = gridDim.x / S;
+    // this CTA's stages of every tile
+    const int k_lo = (int)((int64_t)a.nkb * rank / S), k_hi = (int)((int64_t)a.nkb * (rank + 1) / S);
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < ns; ++s) {
+            bar_init(&sh.full[s], 1);
+            bar_init(&sh.empty[s], 1);
+        }
+        bar_init(&sh.acc_full, 1);
+        bar_init(&sh.acc_empty, 4);
+        bar_init(&sh.done, 1);
+        sh.fail = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    chain_wait();
+    chain_release();
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                         smem_u32(&sh.tmem)), "r"(kAllColumns) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = sh.tmem;
+    uint32_t g = 0;   // stages issued (warp 0) or consumed (warp 1) so far
+    bool bad = false;
+    int j = 0;        // tiles of this CTA so far
+    for (int64_t t = first; t < a.tiles; t += step, ++j) {
+        const int64_t n0 = (t % a.tiles_p) * 128, m0 = (t / a.tiles_p) * nt;
+        if (warp == 0) {
+            if (lane == 0 && !bad) {
+                for (int i = k_lo; i < k_hi; ++i, ++g) {
+                    const int s = (int)(g % ns);
+                    if (g >= (uint32_t)ns && !mbar_wait(&sh.empty[s], ((g / ns) - 1) & 1)) {
+                        bad = true;
+                        break;
+                    }
+                    const int nk = min(F::kSfTiles, a.kb - F::kSfTiles * i);
+                    mbar_expect_tx(&sh.full[s], (uint32_t)(kPBytes + qbytes +
+                                                           (1 + qa) * nk * kSfTileBytes));
+                    tma_load_2d(sP + s * kPBytes, &a.tp, i * kRowBytes, (int32_t)n0, &sh.full[s]);
+                    tma_load_2d(sQ + s * qbytes, &a.tq, i * kRowBytes, (int32_t)m0, &sh.full[s]);
+                    bulk_load(sFP + s * kSfP,
+                              a.sfp + ((n0 / 128) * a.kb + F::kSfTiles * i) * kSfTileBytes,
+                              (uint32_t)(nk * kSfTileBytes), &sh.full[s]);
+                    for (int q = 0; q < qa; ++q) {
+                        // token tiles past the end of a have no scale tile: any
+                        // finite scales do (their codes are zeros)
+                        const int64_t qt = min(m0 / 128 + q, (a.M + 127) / 128 - 1);
+                        bulk_load(sFQ + (s * qa + q) * kSfP,
+                                  a.sfq + (qt * a.kb + F::kSfTiles * i) * kSfTileBytes,
+                                  (uint32_t)(nk * kSfTileBytes), &sh.full[s]);
+                    }
+                }
+            }
+            __syncwarp();
+        } else if (warp == 1) {
+            if (lane == 0 && !bad) {
+                if (j >= 1 && S == 1 && !mbar_wait(&sh.acc_empty, (uint32_t)(j - 1) & 1)) bad = true;
+                tc_fence_after();
+                const uint32_t ring = tmem + 256;
+                for (int i = k_lo; i < k_hi && !bad; ++i, ++g) {
+                    const int s = (int)(g % ns);
+                    if (!mbar_wait(&sh.full[s], (g / ns) & 1) ||
+                        (g >= (uint32_t)kSfRing &&
+                         !mbar_wait(&sh.empty[(g - kSfRing) % ns], ((g - kSfRing) / ns) & 1))) {
+                        bad = true;
+                        break;
+                    }
+                    tc_fence_after();
+                    const int nk = min(F::kSfTiles, a.kb - F::kSfTiles * i);
+                    const uint32_t sfp = ring + (g % kSfRing) * 48, sfq = sfp + 4 * F::kSfTiles;
+                    for (int kk = 0; kk < nk; ++kk) {
+                        sf_copy<1>(sfp + 4 * kk, smem_u32(sFP + s * kSfP) + kk * kSfTileBytes);
+                        for (int q = 0; q < qa; ++q)
+                            sf_copy<1>(sfq + 4 * (kk * qa + q),
+                                       smem_u32(sFQ + (s * qa + q) * kSfP) + kk * kSfTileBytes);
+                    }
+                    const uint32_t p0 = smem_u32(sP + s * kPBytes), q0 = smem_u32(sQ + s * qbytes);
+                    const int steps = F::kGlobal ? nk : 4;
+                    for (int kk = 0; kk < steps; ++kk)
+                        mma_issue<F, 1>(tmem, desc_sw128(p0 + kk * 32), desc_sw128(q0 + kk * 32),
+                                        idesc<F>(128, nt, F::kGlobal ? 0 : kk),
+                                        F::kGlobal ? sfp + 4 * kk : sfp,
+                                        F::kGlobal ? sfq + 4 * kk * qa : sfq, i > k_lo || kk > 0);
+                    tc_commit(&sh.empty[s]);
+                }
+                if (!bad) tc_commit(&sh.acc_full);
+            }
+            __syncwarp();
+        } else {
+            const int q = warp & 3;
+            const int nl = 32 * q + lane;            // weight row of the tile
+            const int64_t n = n0 + nl;
+            const int mt = (int)min((int64_t)nt, a.M - m0);
+            if (!bad && !mbar_wait(&sh.acc_full, (uint32_t)j & 1)) bad = true;
+            __syncwarp();
+            tc_fence_after();
+            const uint32_t lane_base = tmem + ((uint32_t)(32 * q) << 16);
+            const bool nin = n < a.N;
+            float gb = 1.0f, ga0 = 1.0f, bias = 0.0f;
+            if constexpr (F::kGlobal) {
+                gb = fdiv(1.0f, global_scale(a.ep.b_amax[0], a.ep.six_bound));
+                if (!a.ep.a_row) ga0 = fdiv(1.0f, global_scale(a.ep.a_amax[0], a.ep.six_bound));
+            }
+            if (a.ep.bias && nin)
+                bias = a.ep.bias32 ? __ldg(static_cast<const float*>(a.ep.bias) + n)
+                                   : load_out<OT>(a.ep.bias, n);
+            for (int c0 = 0; c0 < mt; c0 += 16) {
+                uint32_t v[16];
+                tmem_ld16(lane_base + (uint32_t)c0, v);
+                if (S > 1) {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        if (c0 + i < mt) red[(c0 + i) * 128 + nl] = __uint_as_float(v[i]);
+                } else if (nin) {
+                    float f[16];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) f[i] = __uint_as_float(v[i]);
+                    finish_rows<F, OT>(a.ep, f, m0 + c0, 1, mt - c0, a.N, n, ga0, gb, bias);
+                }
+                __syncwarp();
+            }
+            if (S == 1) {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) bar_arrive(&sh.acc_empty);
+            } else {
+                tc_fence_before();
+                cluster_sync();  // every partial of the tile is written
+                if (nin) {
+                    for (int c = rank; c < mt; c += 4 * S) {
+                        // four tokens at a time: 4 S loads in flight
+                        const int cnt = (mt - c + S - 1) / S;
+                        float f[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const uint32_t at = smem_u32(red + (i < cnt ? c + i * S : c) * 128 + nl);
+                            f[i] = ld_cluster(at, 0u);
+                            for (int k = 1; k < S; ++k) f[i] = fadd(f[i], ld_cluster(at, (uint32_t)k));
+                        }
+                        finish_rows<F, OT>(a.ep, f, m0 + c, S, cnt, a.N, n, ga0, gb, bias);
+                    }
+                }
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                __syncwarp();
+                cluster_sync();  // every partial has been read: the ring is free again
+            }
+        }
+        if (S > 1 && warp < 2) {
+            cluster_sync();
+            cluster_sync();
+            tc_fence_after();
+        }
+    }
+    // drain: every copy and MMA issued has completed before the CTA leaves
+    if (warp == 0 && lane == 0) {
+        for (uint32_t s = 0; s < (uint32_t)ns; ++s)
+            if (g > s && !mbar_wait(&sh.full[s], ((g - 1 - s) / ns) & 1)) bad = true;
+    } else if (warp == 1 && lane == 0) {
+        tc_commit(&sh.done);
+        if (!mbar_wait(&sh.done, 0)) bad = true;
+    }
+    if (bad) sh.fail = 1;
+    tc_fence_before();
+    __syncthreads();
+    if (sh.fail && threadIdx.x == 0 && first < a.tiles)
+        store_out<OT>(a.ep.out, (first / a.tiles_p) * nt * a.N + (first % a.tiles_p) * 128,
+                      __int_as_float(0x7FC00000));
+    if (warp == 1) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
+                     "r"(kAllColumns) : "memory");
+    }
+}
+
+}  // namespace lin
+}  // namespace fos

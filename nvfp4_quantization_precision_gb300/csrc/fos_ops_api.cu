@@ -8,6 +8,7 @@
 #include "../../include/fos.h"
 #include "fos_act.cuh"
 #include "fos_host.cuh"
+#include "fos_linear.cuh"
 #include "fos_norm.cuh"
 #include "fos_ops_launch.cuh"
 #include "fos_quant8.cuh"
@@ -107,6 +108,37 @@ fos_status run_quant8(const void* x, const void* pre, fos_dtype dt, int64_t rows
     cudaError_t e = launch_quant8(in_of(dt), static_cast<Act>(act), a, s);
     if (e == cudaSuccess && sums) e = launch_column_sums(a.part, tiles_r, cols, dbias, s);
     return cuda_status(e);
+}
+
+fos_status run_linear(LinearCall c, const fos_epilogue* e, void* out, cudaStream_t s) {
+    if (!e || !valid_dtype(e->out_dt) || !valid_act(e->act) ||
+        (e->bias && e->bias_dt != FOS_FP32 && e->bias_dt != e->out_dt))
+        return FOS_ERR_INVALID_ARG;
+    if (c.M < 0 || c.N < 0 || c.K < 0) return FOS_ERR_INVALID_ARG;
+    if (c.N % 16 || c.K % 32 || c.K == 0) return FOS_ERR_UNSUPPORTED;
+    if (c.M >= (INT64_C(1) << 30) || c.N >= (INT64_C(1) << 30) || c.K >= (INT64_C(1) << 30) ||
+        (c.N > 0 && c.M > (INT64_C(1) << 40) / c.N))
+        return FOS_ERR_UNSUPPORTED;
+    if (c.M == 0 || c.N == 0) return FOS_OK;
+    if (!c.a || !c.as || !c.b || !c.bs || !out || (c.fmt4 && (!c.ep.a_amax || !c.ep.b_amax)))
+        return FOS_ERR_INVALID_ARG;
+    if (!aligned(c.a, 16) || !aligned(c.as, 16) || !aligned(c.b, 16) || !aligned(c.bs, 16) ||
+        !aligned(out, 16) || !aligned(e->residual, 16) || !aligned(e->pre, 16) ||
+        !aligned(e->bias, 16))
+        return FOS_ERR_MISALIGNED;
+    const int dev = device_of_given({c.a, c.as, c.b, c.bs, c.ep.a_amax, c.ep.b_amax, e->bias,
+                                     e->residual, e->pre, out});
+    if (dev < 0) return FOS_ERR_INVALID_ARG;
+    DeviceScope scope(dev);
+    if (scope.st) return scope.st;
+    c.ep.bias = e->bias;
+    c.ep.bias32 = e->bias_dt == FOS_FP32;
+    c.ep.residual = e->residual;
+    c.ep.pre = e->pre;
+    c.ep.out = out;
+    c.ep.act = e->act;
+    c.out = in_of(static_cast<fos_dtype>(e->out_dt));
+    return cuda_status(launch_linear(c, s));
 }
 
 }  // namespace
@@ -223,6 +255,44 @@ fos_status fos_act_backward(const void* dout, const void* pre, fos_dtype dt, int
                             void* workspace, size_t workspace_bytes, fos_stream_t stream) {
     return run_quant8(dout, pre, dt, rows, cols, act, scale_layout, d, codes, scales, codes_t,
                       scales_t, dbias, workspace, workspace_bytes, stream_of(stream));
+}
+
+fos_status fos_linear8(const uint8_t* a_codes, const uint8_t* a_scales_tiled,
+                       const uint8_t* b_codes, const uint8_t* b_scales_tiled, int64_t M, int64_t N,
+                       int64_t K, const fos_epilogue* epilogue, void* out, fos_stream_t stream) {
+    LinearCall c{};
+    c.a = a_codes;
+    c.as = a_scales_tiled;
+    c.b = b_codes;
+    c.bs = b_scales_tiled;
+    c.M = M;
+    c.N = N;
+    c.K = K;
+    return run_linear(c, epilogue, out, stream_of(stream));
+}
+
+fos_status fos_linear4(const uint8_t* a_codes, const uint8_t* a_scales_tiled, const float* a_amax,
+                       const uint8_t* b_codes, const uint8_t* b_scales_tiled, const float* b_amax,
+                       int64_t M, int64_t N, int64_t K, const fos_config* cfg,
+                       const fos_epilogue* epilogue, void* out, fos_stream_t stream) {
+    if (!cfg || (cfg->granularity != FOS_SCALE_TENSOR && cfg->granularity != FOS_SCALE_ROW))
+        return FOS_ERR_INVALID_ARG;
+    if (cfg->block != FOS_BLOCK_1X16 || (cfg->e4m3_bound != 448 && cfg->e4m3_bound != 256))
+        return FOS_ERR_UNSUPPORTED;
+    LinearCall c{};
+    c.a = a_codes;
+    c.as = a_scales_tiled;
+    c.b = b_codes;
+    c.bs = b_scales_tiled;
+    c.M = M;
+    c.N = N;
+    c.K = K;
+    c.fmt4 = true;
+    c.ep.a_amax = a_amax;
+    c.ep.b_amax = b_amax;
+    c.ep.a_row = cfg->granularity == FOS_SCALE_ROW;
+    c.ep.six_bound = 6.0f * (float)cfg->e4m3_bound;
+    return run_linear(c, epilogue, out, stream_of(stream));
 }
 
 }  // extern "C"

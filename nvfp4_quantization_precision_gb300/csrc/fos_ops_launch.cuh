@@ -11,6 +11,7 @@ namespace fos {
 struct NormArgs;
 struct NormBwdArgs;
 struct Quant8Args;
+struct LinearCall;
 enum class Act : int;
 
 // Resident CTAs per SM of a kernel with `threads` threads (cached per kernel,
@@ -62,6 +63,7 @@ cudaError_t launch_column_sums(const float* part, int64_t parts, int64_t cols, f
 cudaError_t launch_rms_norm(In, const NormArgs&, cudaStream_t);
 cudaError_t launch_rms_bwd(In, NormBwdArgs, float* dw, float* part, int64_t max_parts,
                            cudaStream_t);
+cudaError_t launch_linear(const LinearCall&, cudaStream_t);
 cudaError_t launch_quant8(In, Act, const Quant8Args&, cudaStream_t);
 
 }  // namespace fos

@@ -1,13 +1,12 @@
 // mm.cu -- A . B^T from quantized operands on the tensor cores: the launch of
 // the persistent block-scaled NVFP4 kernel (fos_mma.cuh) with its three TMA
 // descriptors (a codes, b codes, out).
-#include <cudaTypedefs.h>
-
 #include <cstring>
 #include <mutex>
 
 #include "fos_launch.cuh"
 #include "fos_mma.cuh"
+#include "fos_tma_host.cuh"
 
 namespace fos {
 
@@ -16,24 +15,6 @@ namespace {
 // Epilogue shape of the launch: warps and staging chunks per warp.
 constexpr int kMmEpi = 4;
 constexpr int kMmBufs = 2;
-
-// cuTensorMapEncodeTiled is a driver function; its address comes from the
-// runtime once (no link against the driver library).
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
-    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-    static std::once_flag once;
-    std::call_once(once, [] {
-        void* p = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000,
-                                             cudaEnableDefault, &q) == cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-        else
-            cudaGetLastError();
-    });
-    return fn;
-}
 
 // Codes [rows, K/2] bytes as a 2D tensor, box 128 bytes x box_rows rows with
 // the 128-byte swizzle the MMA descriptors expect; rows past the end read 0.
