@@ -29,7 +29,6 @@ namespace lin {
 using mma::bar_arrive;
 using mma::bar_init;
 using mma::bulk_load;
-using mma::desc_sw128;
 using mma::tc_commit;
 using mma::tc_fence_after;
 using mma::tc_fence_before;
@@ -74,13 +73,6 @@ struct F4 {
 constexpr int kRowBytes = 128;      // code bytes of a row per stage
 constexpr int kSfTileBytes = 512;
 
-// Shared-memory descriptor of a scale tile (no swizzle: 8-row x 16-byte core
-// matrices 128 bytes apart).
-__device__ __forceinline__ uint64_t desc_sf(uint32_t saddr) {
-    return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)(128 >> 4) << 16) |
-           ((uint64_t)(128 >> 4) << 32) | ((uint64_t)1 << 46);
-}
-
 // Instruction descriptor: element formats (E4M3 0, E2M1 1 or in the F8 kind
 // E4M3 0) in bits 7-9 and 10-12, N >> 3 in 17-22, scale type in 23 (UE8M0 1),
 // M >> 4 in 24-28, scale bytes of b and a in 4-5 and 29-30.
@@ -91,40 +83,63 @@ __device__ __forceinline__ uint32_t idesc(int m, int n, int sf_id) {
            ((uint32_t)sf_id << 4) | ((uint32_t)sf_id << 29);
 }
 
-template <class F, int kPair>
-__device__ __forceinline__ void mma_issue(uint32_t acc, uint64_t ad, uint64_t bd, uint32_t id,
-                                          uint32_t sfa, uint32_t sfb, bool accumulate) {
-    const uint32_t p = accumulate ? 1u : 0u;
-    if constexpr (F::kGlobal && kPair == 1)
-        asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
-                     "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X "
-                     "[%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(acc), "l"(ad), "l"(bd), "r"(id),
-                     "r"(sfa), "r"(sfb), "r"(p) : "memory");
-    else if constexpr (F::kGlobal)
-        asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
-                     "tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.scale_vec::4X "
-                     "[%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(acc), "l"(ad), "l"(bd), "r"(id),
-                     "r"(sfa), "r"(sfb), "r"(p) : "memory");
-    else if constexpr (kPair == 1)
-        asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
-                     "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X "
-                     "[%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(acc), "l"(ad), "l"(bd), "r"(id),
-                     "r"(sfa), "r"(sfb), "r"(p) : "memory");
-    else
-        asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
-                     "tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X "
-                     "[%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(acc), "l"(ad), "l"(bd), "r"(id),
-                     "r"(sfa), "r"(sfb), "r"(p) : "memory");
+// One lane of the warp, the same one each time: the warp's loops run converged
+// (their values stay in uniform registers, where the tensor instructions take
+// their operands from) and only the issue itself is one lane's.
+__device__ __forceinline__ bool elect_lane() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(p));
+    return p != 0;
 }
 
-template <int kPair>
-__device__ __forceinline__ void sf_copy(uint32_t taddr, uint32_t saddr) {
-    if constexpr (kPair == 1)
-        asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr),
-                     "l"(desc_sf(saddr)) : "memory");
+// Descriptors are a constant high word and a low word that holds the address;
+// moving by b bytes adds b / 16 to the low word.
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);  // of desc_sw128
+constexpr uint32_t kSfDescHi = (128u >> 4) | (1u << 14);               // of a scale tile
+__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr) {
+    return ((saddr & 0x3FFFFu) >> 4) | (1u << 16);
+}
+__device__ __forceinline__ uint32_t sf_desc_lo(uint32_t saddr) {
+    return ((saddr & 0x3FFFFu) >> 4) | ((128u >> 4) << 16);
+}
+
+#define FOS_MMA_TEXT(group, kind)                                                              \
+    "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tsetp.ne.b32 p, %6, 0;\n\t"                      \
+    "mov.b64 a, {%1, %7};\n\tmov.b64 b, {%2, %7};\n\t"                                        \
+    "tcgen05.mma.cta_group::" group ".kind::" kind " [%0], a, b, %3, [%4], [%5], p;\n\t}"
+
+// One MMA: accumulator, low descriptor words of both operands, instruction
+// descriptor, scale columns.
+template <class F, int kPair>
+__device__ __forceinline__ void mma_issue(uint32_t acc, uint32_t alo, uint32_t blo, uint32_t id,
+                                          uint32_t sfa, uint32_t sfb, uint32_t accumulate) {
+    if constexpr (F::kGlobal && kPair == 1)
+        asm volatile(FOS_MMA_TEXT("1", "mxf4nvf4.block_scale.scale_vec::4X") ::"r"(acc), "r"(alo),
+                     "r"(blo), "r"(id), "r"(sfa), "r"(sfb), "r"(accumulate), "r"(kDescHi) : "memory");
+    else if constexpr (F::kGlobal)
+        asm volatile(FOS_MMA_TEXT("2", "mxf4nvf4.block_scale.scale_vec::4X") ::"r"(acc), "r"(alo),
+                     "r"(blo), "r"(id), "r"(sfa), "r"(sfb), "r"(accumulate), "r"(kDescHi) : "memory");
+    else if constexpr (kPair == 1)
+        asm volatile(FOS_MMA_TEXT("1", "mxf8f6f4.block_scale.scale_vec::1X") ::"r"(acc), "r"(alo),
+                     "r"(blo), "r"(id), "r"(sfa), "r"(sfb), "r"(accumulate), "r"(kDescHi) : "memory");
     else
-        asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr),
-                     "l"(desc_sf(saddr)) : "memory");
+        asm volatile(FOS_MMA_TEXT("2", "mxf8f6f4.block_scale.scale_vec::1X") ::"r"(acc), "r"(alo),
+                     "r"(blo), "r"(id), "r"(sfa), "r"(sfb), "r"(accumulate), "r"(kDescHi) : "memory");
+}
+#undef FOS_MMA_TEXT
+
+// One scale tile from shared (low descriptor word) to tensor memory.
+template <int kPair>
+__device__ __forceinline__ void sf_copy(uint32_t taddr, uint32_t lo) {
+    if constexpr (kPair == 1)
+        asm volatile("{\n\t.reg .b64 d;\n\tmov.b64 d, {%1, %2};\n\t"
+                     "tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], d;\n\t}" ::"r"(taddr), "r"(lo),
+                     "r"(kSfDescHi) : "memory");
+    else
+        asm volatile("{\n\t.reg .b64 d;\n\tmov.b64 d, {%1, %2};\n\t"
+                     "tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], d;\n\t}" ::"r"(taddr), "r"(lo),
+                     "r"(kSfDescHi) : "memory");
 }
 
 __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&v)[16]) {
@@ -245,6 +260,44 @@ __device__ __forceinline__ float ld_cluster(uint32_t saddr, uint32_t rank) {
     return v;
 }
 
+// Position in a ring of n slots: slot and the parity of its current use.
+struct Ring {
+    int slot = 0;
+    uint32_t parity = 0;
+    __device__ __forceinline__ void next(int n) {
+        if (++slot == n) {
+            slot = 0;
+            parity ^= 1u;
+        }
+    }
+};
+
+// The scale copies and MMAs of one stage (one lane): kQ scale tiles of tokens
+// per weight scale tile, nk scale tiles along K.
+template <class F, int kQ>
+__device__ __forceinline__ void rows_stage(uint32_t acc, uint32_t p0, uint32_t q0, uint32_t id,
+                                           uint32_t sfp, uint32_t sfq, uint32_t lp, uint32_t lq,
+                                           int nk, uint32_t more) {
+    constexpr uint32_t kT = kSfTileBytes >> 4;
+#pragma unroll
+    for (int kk = 0; kk < F::kSfTiles; ++kk) {
+        if (kk < nk) {
+            sf_copy<1>(sfp + 4 * kk, lp + kk * kT);
+#pragma unroll
+            for (int q = 0; q < kQ; ++q)
+                sf_copy<1>(sfq + 4 * (kk * kQ + q), lq + (q * F::kSfTiles + kk) * kT);
+        }
+    }
+#pragma unroll
+    for (int kk = 0; kk < 4; ++kk) {
+        if (F::kGlobal && kk >= nk) break;
+        mma_issue<F, 1>(acc, p0 + 2 * kk, q0 + 2 * kk,
+                        F::kGlobal ? id : id | ((uint32_t)kk << 4) | ((uint32_t)kk << 29),
+                        F::kGlobal ? sfp + 4 * kk : sfp, F::kGlobal ? sfq + 4 * kk * kQ : sfq,
+                        kk == 0 ? more : 1u);
+    }
+}
+
 // The epilogue of kN tokens m, m + dm, ... (the first cnt of them) at weight
 // row n.
 template <class F, Out OT, int kN>
@@ -321,15 +374,17 @@ __global__ void __launch_bounds__(kRowsThreads, 1) k_linear_rows(const __grid_co
     tc_fence_after();
     const uint32_t tmem = sh.tmem;
     uint32_t g = 0;   // stages issued (warp 0) or consumed (warp 1) so far
+    Ring r, w;        // the stage in work; warp 1: the one whose scales are overwritten
+    const bool elected = elect_lane();
     bool bad = false;
     int j = 0;        // tiles of this CTA so far
     for (int64_t t = first; t < a.tiles; t += step, ++j) {
         const int64_t n0 = (t % a.tiles_p) * 128, m0 = (t / a.tiles_p) * nt;
         if (warp == 0) {
             if (lane == 0 && !bad) {
-                for (int i = k_lo; i < k_hi; ++i, ++g) {
-                    const int s = (int)(g % ns);
-                    if (g >= (uint32_t)ns && !mbar_wait(&sh.empty[s], ((g / ns) - 1) & 1)) {
+                for (int i = k_lo; i < k_hi; ++i, ++g, r.next(ns)) {
+                    const int s = r.slot;
+                    if (g >= (uint32_t)ns && !mbar_wait(&sh.empty[s], r.parity ^ 1u)) {
                         bad = true;
                         break;
                     }
@@ -353,38 +408,35 @@ __global__ void __launch_bounds__(kRowsThreads, 1) k_linear_rows(const __grid_co
             }
             __syncwarp();
         } else if (warp == 1) {
-            if (lane == 0 && !bad) {
-                if (j >= 1 && S == 1 && !mbar_wait(&sh.acc_empty, (uint32_t)(j - 1) & 1)) bad = true;
+            if (!bad && j >= 1 && S == 1 && !mbar_wait(&sh.acc_empty, (uint32_t)(j - 1) & 1)) bad = true;
+            tc_fence_after();
+            for (int i = k_lo; i < k_hi && !bad; ++i) {
+                const int s = r.slot;
+                if (!mbar_wait(&sh.full[s], r.parity) ||
+                    (g >= (uint32_t)kSfRing && !mbar_wait(&sh.empty[w.slot], w.parity))) {
+                    bad = true;
+                    break;
+                }
+                if (g >= (uint32_t)kSfRing) w.next(ns);
                 tc_fence_after();
-                const uint32_t ring = tmem + 256;
-                for (int i = k_lo; i < k_hi && !bad; ++i, ++g) {
-                    const int s = (int)(g % ns);
-                    if (!mbar_wait(&sh.full[s], (g / ns) & 1) ||
-                        (g >= (uint32_t)kSfRing &&
-                         !mbar_wait(&sh.empty[(g - kSfRing) % ns], ((g - kSfRing) / ns) & 1))) {
-                        bad = true;
-                        break;
-                    }
-                    tc_fence_after();
-                    const int nk = min(F::kSfTiles, a.kb - F::kSfTiles * i);
-                    const uint32_t sfp = ring + (g % kSfRing) * 48, sfq = sfp + 4 * F::kSfTiles;
-                    for (int kk = 0; kk < nk; ++kk) {
-                        sf_copy<1>(sfp + 4 * kk, smem_u32(sFP + s * kSfP) + kk * kSfTileBytes);
-                        for (int q = 0; q < qa; ++q)
-                            sf_copy<1>(sfq + 4 * (kk * qa + q),
-                                       smem_u32(sFQ + (s * qa + q) * kSfP) + kk * kSfTileBytes);
-                    }
-                    const uint32_t p0 = smem_u32(sP + s * kPBytes), q0 = smem_u32(sQ + s * qbytes);
-                    const int steps = F::kGlobal ? nk : 4;
-                    for (int kk = 0; kk < steps; ++kk)
-                        mma_issue<F, 1>(tmem, desc_sw128(p0 + kk * 32), desc_sw128(q0 + kk * 32),
-                                        idesc<F>(128, nt, F::kGlobal ? 0 : kk),
-                                        F::kGlobal ? sfp + 4 * kk : sfp,
-                                        F::kGlobal ? sfq + 4 * kk * qa : sfq, i > k_lo || kk > 0);
+                const int nk = min(F::kSfTiles, a.kb - F::kSfTiles * i);
+                const uint32_t sfp = tmem + 256 + (g % kSfRing) * 48, sfq = sfp + 4 * F::kSfTiles;
+                const uint32_t lp = sf_desc_lo(smem_u32(sFP) + s * kSfP);
+                const uint32_t lq = sf_desc_lo(smem_u32(sFQ) + s * qa * kSfP);
+                const uint32_t p0 = desc_lo(smem_u32(sP) + s * kPBytes);
+                const uint32_t q0 = desc_lo(smem_u32(sQ) + s * qbytes);
+                const uint32_t id = idesc<F>(128, nt, 0);
+                const uint32_t more = i > k_lo;
+                if (elected) {
+                    if (qa == 1) rows_stage<F, 1>(tmem, p0, q0, id, sfp, sfq, lp, lq, nk, more);
+                    else rows_stage<F, 2>(tmem, p0, q0, id, sfp, sfq, lp, lq, nk, more);
                     tc_commit(&sh.empty[s]);
                 }
-                if (!bad) tc_commit(&sh.acc_full);
+                __syncwarp();
+                ++g;
+                r.next(ns);
             }
+            if (!bad && elected) tc_commit(&sh.acc_full);
             __syncwarp();
         } else {
             const int q = warp & 3;
@@ -455,8 +507,8 @@ __global__ void __launch_bounds__(kRowsThreads, 1) k_linear_rows(const __grid_co
     if (warp == 0 && lane == 0) {
         for (uint32_t s = 0; s < (uint32_t)ns; ++s)
             if (g > s && !mbar_wait(&sh.full[s], ((g - 1 - s) / ns) & 1)) bad = true;
-    } else if (warp == 1 && lane == 0) {
-        tc_commit(&sh.done);
+    } else if (warp == 1) {
+        if (elected) tc_commit(&sh.done);
         if (!mbar_wait(&sh.done, 0)) bad = true;
     }
     if (bad) sh.fail = 1;

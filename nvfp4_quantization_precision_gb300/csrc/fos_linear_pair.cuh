@@ -1,0 +1,473 @@
+// fos_linear_pair.cuh -- the product with an epilogue for many tokens: a pair
+// of SMs per output tile (tcgen05 cta_group::2, M = 256).
+//
+// A persistent kernel of clusters of two CTAs walks 256 x 192 tiles of out.
+// CTA r of a pair holds tokens 128 r .. 128 r + 127 of the tile and, of the
+// weights, rows 96 r .. 96 r + 95: the pair's MMA reads each half of b from
+// the SM that holds it, so an SM stages 16 KB of a and 12 KB of b for 128 x
+// 192 outputs where a single SM would stage 16 + 24.  Roles of a CTA's warps:
+//   warp 0     TMA producer (one thread): its halves of a and b and the scale
+//              tiles (its own of a, both of b) into a ring of stages; the
+//              bytes of both CTAs are counted by the full barrier of CTA 0
+//   warp 1     tensor memory; in CTA 0 one thread copies the scales of both
+//              CTAs (tcgen05.cp) and issues the pair's MMAs, whose completion
+//              frees the stage in both CTAs
+//   warps 2-5  epilogue of the CTA's 128 tokens, lane quadrant warp % 4
+// Tensor memory: two accumulators of 192 columns (the epilogue of a tile runs
+// under the MMAs of the next) and a ring of scale buffers in the other 128.
+// The epilogue goes by chunks of 32 tokens x 128 bytes of out.  A chunk's
+// residual is fetched by TMA into the very buffer its result will leave from:
+// a lane reads its 16-byte pieces, adds, and writes them back in place, so
+// three buffers a warp hold the fetch of the chunk after next, the chunk in
+// work and the store of the last.
+#pragma once
+
+#include "fos_linear.cuh"
+
+namespace fos {
+namespace lin {
+
+constexpr int kPairM = 256, kPairN = 192;
+constexpr int kPairABytes = 128 * kRowBytes, kPairBBytes = 96 * kRowBytes;
+constexpr int kPairThreads = 192;
+constexpr int kPairMaxStages = 8;
+constexpr int kChunkBytes = 32 * 128;
+constexpr int kPairGroupM = 8;     // tile rows per band of the tile order
+constexpr int kPairSfCol = 2 * kPairN;
+
+template <class F> constexpr int pair_sf_bytes() { return 3 * F::kSfTiles * kSfTileBytes; }
+template <class F> constexpr int pair_stage_bytes() {
+    return kPairABytes + kPairBBytes + pair_sf_bytes<F>();
+}
+// The ring of scale buffers in the 128 columns the accumulators leave: a
+// buffer holds the scales of a unit, a stage (F8) or half of one (F4); a
+// unit's copies may go once the MMAs that read its buffer are done, that is
+// those of the stage kLag before, waited for at the stage's last unit (for the
+// first unit of two, the wait of the stage before has covered it).
+template <class F> struct SfRing;
+template <> struct SfRing<F8> {
+    static constexpr int kUnits = 1, kCols = 16, kBufs = 4, kLag = 4;
+};
+template <> struct SfRing<F4> {
+    static constexpr int kUnits = 2, kCols = 24, kBufs = 5, kLag = 2;
+};
+
+struct PairArgs {
+    CUtensorMap ta;    // a codes, box 128 bytes x 128 rows
+    CUtensorMap tb;    // b codes, box 128 bytes x 96 rows
+    CUtensorMap tsa;   // a scales as [tiles, 512 bytes], box kSfTiles tiles
+    CUtensorMap tsb;   // b scales likewise
+    CUtensorMap tout;  // out, residual, pre: box 128 bytes x 32 rows
+    CUtensorMap tres;
+    CUtensorMap tpre;
+    Epilogue ep;
+    int64_t M, N;
+    int tiles_m, tiles_n;
+    int kb, nkb;
+    int stages;
+    int bufs;          // chunk buffers of an epilogue warp
+};
+
+struct __align__(8) PairShared {
+    uint64_t full[kPairMaxStages], empty[kPairMaxStages], acc_full[2], acc_empty[2], done;
+    uint64_t res_full[4][4];
+    uint32_t tmem;
+    int fail;
+};
+
+__device__ __forceinline__ uint32_t map_rank(uint32_t saddr, uint32_t rank) {
+    uint32_t r;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(saddr), "r"(rank));
+    return r;
+}
+// Load into this CTA's shared memory, bytes counted at `bar` (a cluster address).
+__device__ __forceinline__ void pair_load_2d(void* dst, const CUtensorMap* map, int32_t x, int32_t y,
+                                             uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%2, %3}], [%4];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar) : "memory");
+}
+__device__ __forceinline__ void pair_commit(uint64_t* bar) {
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
+        "[%0], %1;" ::"r"(smem_u32(bar)), "h"((unsigned short)3) : "memory");
+}
+__device__ __forceinline__ void cluster_arrive(uint32_t bar) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&v)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
+        "%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]),
+          "=r"(v[7]), "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]),
+          "=r"(v[14]), "=r"(v[15]), "=r"(v[16]), "=r"(v[17]), "=r"(v[18]), "=r"(v[19]),
+          "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]), "=r"(v[24]), "=r"(v[25]),
+          "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
+        : "r"(taddr));
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+
+// Tile order: bands of kPairGroupM tile rows, down the rows first, so that the
+// tiles in work at one time share a and b tiles in L2.
+__device__ __forceinline__ void pair_tile(const PairArgs& a, int t, int32_t& m0, int32_t& n0) {
+    const int per_band = kPairGroupM * a.tiles_n;
+    const int band = t / per_band, r = t - band * per_band;
+    const int rows = min(kPairGroupM, a.tiles_m - band * kPairGroupM);
+    const int col = r / rows;
+    m0 = (band * kPairGroupM + r - col * rows) * kPairM;
+    n0 = col * kPairN;
+}
+
+// 32 biases from column n (the same for every lane; columns past N are not read).
+template <Out OT>
+__device__ __forceinline__ void add_bias(const Epilogue& e, int64_t n, int64_t N, float (&v)[32]) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        if (n + 16 * h >= N) break;
+        if (OT == Out::F32 || e.bias32) {
+            const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(e.bias) + n + 16 * h);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float4 b = __ldg(p + i);
+                v[16 * h + 4 * i] = fadd(v[16 * h + 4 * i], b.x);
+                v[16 * h + 4 * i + 1] = fadd(v[16 * h + 4 * i + 1], b.y);
+                v[16 * h + 4 * i + 2] = fadd(v[16 * h + 4 * i + 2], b.z);
+                v[16 * h + 4 * i + 3] = fadd(v[16 * h + 4 * i + 3], b.w);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                v[16 * h + i] = fadd(v[16 * h + i], load_out<OT>(e.bias, n + 16 * h + i));
+        }
+    }
+}
+
+// 32 values as 128-bit pieces of a chunk's row: pieces p0, p0 + 1, ... of the
+// 128-byte swizzle.
+template <Out OT>
+__device__ __forceinline__ void put_pieces(uint32_t row_addr, int lane, int p0, const float (&v)[32]) {
+    constexpr int kPer = OT == Out::F32 ? 4 : 8;
+#pragma unroll
+    for (int k = 0; k < 32 / kPer; ++k) {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (OT == Out::F32) w[i] = __float_as_uint(v[4 * k + i]);
+            else w[i] = out_pair<OT>(pk(v[8 * k + 2 * i], v[8 * k + 2 * i + 1]));
+        }
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
+                         row_addr + (((p0 + k) ^ (lane & 7)) << 4)),
+                     "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]) : "memory");
+    }
+}
+template <Out OT>
+__device__ __forceinline__ void add_pieces(uint32_t row_addr, int lane, int p0, float (&v)[32]) {
+    constexpr int kPer = OT == Out::F32 ? 4 : 8;
+#pragma unroll
+    for (int k = 0; k < 32 / kPer; ++k) {
+        uint32_t w[4];
+        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                     : "r"(row_addr + (((p0 + k) ^ (lane & 7)) << 4)));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (OT == Out::F32) {
+                v[4 * k + i] = fadd(v[4 * k + i], __uint_as_float(w[i]));
+            } else if constexpr (OT == Out::BF16) {
+                v[8 * k + 2 * i] = fadd(v[8 * k + 2 * i], __uint_as_float(w[i] << 16));
+                v[8 * k + 2 * i + 1] = fadd(v[8 * k + 2 * i + 1], __uint_as_float(w[i] & 0xFFFF0000u));
+            } else {
+                float lo, hi;
+                upk(f16x2_f32x2(w[i]), lo, hi);
+                v[8 * k + 2 * i] = fadd(v[8 * k + 2 * i], lo);
+                v[8 * k + 2 * i + 1] = fadd(v[8 * k + 2 * i + 1], hi);
+            }
+        }
+    }
+}
+
+__device__ __forceinline__ void store_chunk(const CUtensorMap* map, int32_t x, int32_t y, uint32_t buf) {
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
+                     map), "r"(x), "r"(y), "r"(buf) : "memory");
+}
+
+// Scale copies and MMAs of unit u of a stage (one lane): the scales of the
+// pair's 256 rows of a (each CTA its 128) and of both scale tiles of b go to
+// columns col ..., the MMAs read b's from `off` on.
+template <class F>
+__device__ __forceinline__ void pair_unit(uint32_t acc, uint32_t a0, uint32_t b0, uint32_t col,
+                                          uint32_t la, uint32_t lb, uint32_t off, int u, int nk,
+                                          uint32_t more) {
+    constexpr uint32_t kT = kSfTileBytes >> 4;
+    constexpr int kTiles = F::kSfTiles / SfRing<F>::kUnits;  // scale tiles of a unit
+    const uint32_t sfa = col, sfb = col + 4 * kTiles;
+#pragma unroll
+    for (int i = 0; i < kTiles; ++i) {
+        const int kk = u * kTiles + i;
+        if (kk < nk) {
+            sf_copy<2>(sfa + 4 * i, la + kk * kT);
+            sf_copy<2>(sfb + 8 * i, lb + kk * kT);
+            sf_copy<2>(sfb + 8 * i + 4, lb + (F::kSfTiles + kk) * kT);
+        }
+    }
+    constexpr int kSteps = 4 / SfRing<F>::kUnits;
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i) {
+        const int kk = u * kSteps + i;
+        if (F::kGlobal && kk >= nk) break;
+        mma_issue<F, 2>(acc, a0 + 2 * kk, b0 + 2 * kk, idesc<F>(kPairM, kPairN, F::kGlobal ? 0 : kk),
+                        F::kGlobal ? sfa + 4 * i : sfa, (F::kGlobal ? sfb + 8 * i : sfb) + off,
+                        kk == 0 ? more : 1u);
+    }
+}
+
+template <class F, Out OT>
+__global__ void __launch_bounds__(kPairThreads, 1) k_linear_pair(const __grid_constant__ PairArgs a) {
+    extern __shared__ __align__(1024) unsigned char s_raw[];
+    __shared__ PairShared sh;
+    unsigned char* base = s_raw + ((1024u - (smem_u32(s_raw) & 1023u)) & 1023u);
+    const int ns = a.stages;
+    constexpr int kSf = F::kSfTiles * kSfTileBytes;  // scale bytes of 128 rows, one stage
+    unsigned char* sA = base;
+    unsigned char* sB = sA + ns * kPairABytes;
+    unsigned char* sC = sB + ns * kPairBBytes;       // epilogue chunks
+    unsigned char* sSA = sC + 4 * a.bufs * kChunkBytes;
+    unsigned char* sSB = sSA + ns * kSf;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = (int)cluster_rank();
+    const int tiles = a.tiles_m * a.tiles_n;
+    const int first = (int)(blockIdx.x >> 1), step = (int)(gridDim.x >> 1);
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < ns; ++s) {
+            bar_init(&sh.full[s], 1);
+            bar_init(&sh.empty[s], 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            bar_init(&sh.acc_full[b], 1);
+            bar_init(&sh.acc_empty[b], 8);
+        }
+        for (int w = 0; w < 4; ++w)
+            for (int b = 0; b < 4; ++b) bar_init(&sh.res_full[w][b], 1);
+        bar_init(&sh.done, 1);
+        sh.fail = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    chain_wait();
+    chain_release();
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                         smem_u32(&sh.tmem)), "r"(kAllColumns) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();  // both CTAs' barriers are set up
+    tc_fence_after();
+    const uint32_t tmem = sh.tmem;
+    bool bad = false;
+    if (warp == 0) {
+        if (lane == 0) {
+            Ring r;
+            uint32_t g = 0;
+            for (int t = first; t < tiles && !bad; t += step) {
+                int32_t m0, n0;
+                pair_tile(a, t, m0, n0);
+                const int32_t sa_row = (m0 / 128 + rank) * a.kb, sb_row = (n0 / 128) * a.kb;
+                for (int i = 0; i < a.nkb; ++i, ++g, r.next(ns)) {
+                    const int s = r.slot;
+                    if (g >= (uint32_t)ns && !mbar_wait(&sh.empty[s], r.parity ^ 1u)) {
+                        bad = true;
+                        break;
+                    }
+                    const uint32_t bar = map_rank(smem_u32(&sh.full[s]), 0);
+                    if (rank == 0)
+                        mbar_expect_tx(&sh.full[s], (uint32_t)(2 * pair_stage_bytes<F>()));
+                    pair_load_2d(sA + s * kPairABytes, &a.ta, i * kRowBytes, m0 + 128 * rank, bar);
+                    pair_load_2d(sB + s * kPairBBytes, &a.tb, i * kRowBytes, n0 + 96 * rank, bar);
+                    pair_load_2d(sSA + s * kSf, &a.tsa, 0, sa_row + F::kSfTiles * i, bar);
+                    pair_load_2d(sSB + s * 2 * kSf, &a.tsb, 0, sb_row + F::kSfTiles * i, bar);
+                    pair_load_2d(sSB + s * 2 * kSf + kSf, &a.tsb, 0, sb_row + a.kb + F::kSfTiles * i, bar);
+                }
+            }
+            // every copy issued has landed (and been read) before the CTA leaves:
+            // the stages' last uses, by the barriers this CTA has
+            for (int k = 0; k < ns && (uint32_t)k < g; ++k) {
+                // slot r.slot - 1 - k, its latest use
+                int s = r.slot - 1 - k;
+                uint32_t p = r.parity;
+                if (s < 0) {
+                    s += ns;
+                    p ^= 1u;
+                }
+                if (!mbar_wait(&sh.empty[s], p)) bad = true;
+            }
+        }
+    } else if (warp == 1) {
+        if (rank == 0) {
+            const bool elected = elect_lane();
+            Ring r, w;      // the stage in work; the one whose scales are overwritten
+            uint32_t g = 0, buf = 0;
+            int j = 0;
+            for (int t = first; t < tiles && !bad; t += step, ++j) {
+                int32_t m0, n0;
+                pair_tile(a, t, m0, n0);
+                const int ab = j & 1;
+                if (j >= 2 && !mbar_wait(&sh.acc_empty[ab], (uint32_t)((j >> 1) - 1) & 1)) {
+                    bad = true;
+                    break;
+                }
+                const uint32_t acc = tmem + (uint32_t)(ab * kPairN);
+                const uint32_t off = (n0 & 127) ? 2u : 0u;  // b starts half-way into a scale tile
+                for (int i = 0; i < a.nkb; ++i) {
+                    const int s = r.slot;
+                    if (!mbar_wait(&sh.full[s], r.parity)) {
+                        bad = true;
+                        break;
+                    }
+                    const int nk = min(F::kSfTiles, a.kb - F::kSfTiles * i);
+                    const uint32_t la = sf_desc_lo(smem_u32(sSA) + s * kSf);
+                    const uint32_t lb = sf_desc_lo(smem_u32(sSB) + s * 2 * kSf);
+                    const uint32_t a0 = desc_lo(smem_u32(sA) + s * kPairABytes);
+                    const uint32_t b0 = desc_lo(smem_u32(sB) + s * kPairBBytes);
+                    const uint32_t more = i > 0;
+                    bool ok = true;
+#pragma unroll
+                    for (int u = 0; u < SfRing<F>::kUnits; ++u) {
+                        if (u == SfRing<F>::kUnits - 1 && g >= (uint32_t)SfRing<F>::kLag) {
+                            ok = mbar_wait(&sh.empty[w.slot], w.parity);
+                            w.next(ns);
+                        }
+                        tc_fence_after();
+                        if (elected && ok)
+                            pair_unit<F>(acc, a0, b0, tmem + kPairSfCol + buf * SfRing<F>::kCols, la, lb,
+                                         off, u, nk, more);
+                        buf = buf + 1 == SfRing<F>::kBufs ? 0 : buf + 1;
+                    }
+                    if (!ok) {
+                        bad = true;
+                        break;
+                    }
+                    if (elected) pair_commit(&sh.empty[s]);
+                    __syncwarp();
+                    ++g;
+                    r.next(ns);
+                }
+                if (!bad && elected) pair_commit(&sh.acc_full[ab]);
+                __syncwarp();
+            }
+            if (elected) pair_commit(&sh.done);
+            __syncwarp();
+        }
+    } else {
+        const int q = warp & 3, e = warp - 2;
+        constexpr int kElt = OT == Out::F32 ? 4 : 2;
+        constexpr int kCols = 128 / kElt;               // columns of a chunk
+        constexpr int kChunks = kPairN / kCols;         // chunks of a tile
+        const bool pre = a.ep.pre != nullptr, res = a.ep.residual != nullptr;
+        const int nb = a.bufs, use = pre ? 2 : 1;       // buffers a chunk uses
+        const int ahead = nb / use - 1;                 // chunks a residual is fetched ahead
+        unsigned char* bufs = sC + e * nb * kChunkBytes;
+        const int mine = first < tiles ? (tiles - first + step - 1) / step : 0;
+        const int total = mine * kChunks;
+        // chunk c: buffer, and the coordinates of its piece of out
+        auto buf_of = [&](int c) { return (c * use) % nb; };
+        auto fetch = [&](int c) {                       // one lane
+            int32_t m0, n0;
+            pair_tile(a, first + (c / kChunks) * step, m0, n0);
+            uint64_t* bar = &sh.res_full[e][buf_of(c)];
+            mbar_expect_tx(bar, kChunkBytes);
+            tma_load_2d(bufs + buf_of(c) * kChunkBytes, &a.tres, n0 + (c % kChunks) * kCols,
+                        m0 + 128 * rank + 32 * q, bar);
+        };
+        int fetched = 0;
+        if (res && lane == 0)
+            for (; fetched < ahead && fetched < total; ++fetched) fetch(fetched);
+        float gb = 1.0f, ga0 = 1.0f;
+        if constexpr (F::kGlobal) {
+            gb = fdiv(1.0f, global_scale(a.ep.b_amax[0], a.ep.six_bound));
+            if (!a.ep.a_row) ga0 = fdiv(1.0f, global_scale(a.ep.a_amax[0], a.ep.six_bound));
+        }
+        int c = 0, j = 0;
+        for (int t = first; t < tiles; t += step, ++j) {
+            int32_t m0, n0;
+            pair_tile(a, t, m0, n0);
+            const int32_t mw = m0 + 128 * rank + 32 * q;  // first token of this warp
+            float ga = ga0;
+            if constexpr (F::kGlobal)
+                if (a.ep.a_row && mw + lane < a.M)
+                    ga = fdiv(1.0f, global_scale(__ldg(a.ep.a_amax + mw + lane), a.ep.six_bound));
+            const int ab = j & 1;
+            if (!bad && !mbar_wait(&sh.acc_full[ab], (uint32_t)(j >> 1) & 1)) bad = true;
+            __syncwarp();
+            tc_fence_after();
+            for (int k = 0; k < kChunks; ++k, ++c) {
+                const int b = buf_of(c);
+                const uint32_t buf = smem_u32(bufs + b * kChunkBytes);
+                const uint32_t pbuf = smem_u32(bufs + ((b + 1) % nb) * kChunkBytes);
+                if (res) {
+                    const uint32_t use_no = (uint32_t)(c * use / nb);
+                    if (!bad && !mbar_wait(&sh.res_full[e][b], use_no & 1)) bad = true;
+                }
+                __syncwarp();
+#pragma unroll
+                for (int h = 0; h < kCols / 32; ++h) {
+                    const int32_t col = k * kCols + 32 * h;
+                    uint32_t u[32];
+                    tmem_ld32(tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(ab * kPairN + col), u);
+                    if (col + 32 == kPairN) {  // this warp has read the accumulator
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) cluster_arrive(map_rank(smem_u32(&sh.acc_empty[ab]), 0));
+                    }
+                    float v[32];
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) {
+                        v[i] = __uint_as_float(u[i]);
+                        if constexpr (F::kGlobal) v[i] = fmul(fmul(v[i], ga), gb);
+                    }
+                    if (a.ep.bias) add_bias<OT>(a.ep, n0 + col, a.N, v);
+                    constexpr int kPieces = 32 * kElt / 16;
+                    if (pre) put_pieces<OT>(pbuf + lane * 128, lane, kPieces * h, v);
+                    act_apply(a.ep.act, v);
+                    if (res) add_pieces<OT>(buf + lane * 128, lane, kPieces * h, v);
+                    put_pieces<OT>(buf + lane * 128, lane, kPieces * h, v);
+                }
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                __syncwarp();
+                if (lane == 0) {
+                    store_chunk(&a.tout, n0 + k * kCols, mw, buf);
+                    if (pre) store_chunk(&a.tpre, n0 + k * kCols, mw, pbuf);
+                    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+                    // the store before this one has read its buffers: they are
+                    // the next ones to be written or fetched into
+                    asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+                    if (res && fetched < total) fetch(fetched++);
+                }
+            }
+        }
+        if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+        __syncwarp();
+    }
+    // every MMA issued has completed before the tensor memory is freed
+    if (warp == 1 && !mbar_wait(&sh.done, 0)) bad = true;
+    if (bad) sh.fail = 1;
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();  // neither CTA leaves while the other may touch its memory
+    if (sh.fail && threadIdx.x == 0 && first < tiles) {
+        int32_t m0, n0;
+        pair_tile(a, first, m0, n0);
+        if (m0 + 128 * rank < a.M)
+            store_out<OT>(a.ep.out, (int64_t)(m0 + 128 * rank) * a.N + n0, __int_as_float(0x7FC00000));
+    }
+    if (warp == 1) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem),
+                     "r"(kAllColumns) : "memory");
+    }
+}
+
+}  // namespace lin
+}  // namespace fos

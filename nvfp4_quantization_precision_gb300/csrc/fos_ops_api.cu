@@ -117,7 +117,8 @@ fos_status run_linear(LinearCall c, const fos_epilogue* e, void* out, cudaStream
     if (c.M < 0 || c.N < 0 || c.K < 0) return FOS_ERR_INVALID_ARG;
     if (c.N % 16 || c.K % 32 || c.K == 0) return FOS_ERR_UNSUPPORTED;
     if (c.M >= (INT64_C(1) << 30) || c.N >= (INT64_C(1) << 30) || c.K >= (INT64_C(1) << 30) ||
-        (c.N > 0 && c.M > (INT64_C(1) << 40) / c.N))
+        (c.N > 0 && c.M > (INT64_C(1) << 40) / c.N) || c.M > (INT64_C(1) << 40) / c.K ||
+        c.N > (INT64_C(1) << 40) / c.K)
         return FOS_ERR_UNSUPPORTED;
     if (c.M == 0 || c.N == 0) return FOS_OK;
     if (!c.a || !c.as || !c.b || !c.bs || !out || (c.fmt4 && (!c.ep.a_amax || !c.ep.b_amax)))

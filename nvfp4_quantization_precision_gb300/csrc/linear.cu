@@ -2,6 +2,7 @@
 #include <cstring>
 
 #include "fos_linear.cuh"
+#include "fos_linear_pair.cuh"
 #include "fos_ops_launch.cuh"
 #include "fos_tma_host.cuh"
 
@@ -111,12 +112,69 @@ cudaError_t rows_go(const LinearCall& c, cudaStream_t s) {
     return launch_clusters(k, clusters, best, kRowsThreads, smem, a, s);
 }
 
+// Scale tiles [tiles, 512 bytes], a box of `n` consecutive ones.
+bool scale_map(CUtensorMap* m, const uint8_t* scales, int64_t rows, int kb, int n) {
+    return matrix_map(m, CU_TENSOR_MAP_DATA_TYPE_UINT32, 4, scales, (rows + 127) / 128 * kb,
+                      kSfTileBytes, kSfTileBytes / 4, n, CU_TENSOR_MAP_SWIZZLE_NONE,
+                      CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
+}
+
+// [M, N] of the output's type, box 32 rows x 128 bytes with the 128-byte swizzle.
+template <Out OT>
+bool chunk_map(CUtensorMap* m, const void* p, int64_t M, int64_t N) {
+    constexpr int elt = OT == Out::F32 ? 4 : 2;
+    const CUtensorMapDataType dt = OT == Out::F32   ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                   : OT == Out::F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                                    : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    return matrix_map(m, dt, elt, p, M, N * elt, 128 / elt, 32, CU_TENSOR_MAP_SWIZZLE_128B,
+                      CU_TENSOR_MAP_L2_PROMOTION_NONE);
+}
+
+template <class F, Out OT>
+cudaError_t pair_go(const LinearCall& c, cudaStream_t s) {
+    PairArgs a;
+    std::memset(&a, 0, sizeof(a));
+    const int64_t row_bytes = F::kGlobal ? c.K / 2 : c.K;
+    const int blk4 = F::kGlobal ? 64 : 128;
+    a.kb = (int)((c.K + blk4 - 1) / blk4);
+    a.nkb = (a.kb + F::kSfTiles - 1) / F::kSfTiles;
+    if (!code_map(&a.ta, c.a, c.M, row_bytes, 128) || !code_map(&a.tb, c.b, c.N, row_bytes, 96) ||
+        !scale_map(&a.tsa, c.as, c.M, a.kb, F::kSfTiles) ||
+        !scale_map(&a.tsb, c.bs, c.N, a.kb, F::kSfTiles) ||
+        !chunk_map<OT>(&a.tout, c.ep.out, c.M, c.N) ||
+        (c.ep.residual && !chunk_map<OT>(&a.tres, c.ep.residual, c.M, c.N)) ||
+        (c.ep.pre && !chunk_map<OT>(&a.tpre, c.ep.pre, c.M, c.N)))
+        return cudaErrorInvalidValue;
+    a.ep = c.ep;
+    a.M = c.M;
+    a.N = c.N;
+    a.tiles_m = (int)((c.M + kPairM - 1) / kPairM);
+    a.tiles_n = (int)((c.N + kPairN - 1) / kPairN);
+    a.bufs = c.ep.pre ? 4 : 3;
+    const int epi = 4 * a.bufs * kChunkBytes;
+    a.stages = (kSmemLimit - 2048 - epi) / pair_stage_bytes<F>();
+    if (a.stages > kPairMaxStages) a.stages = kPairMaxStages;
+    const int smem = a.stages * pair_stage_bytes<F>() + epi + 1024;
+    auto k = k_linear_pair<F, OT>;
+    cudaError_t e = allow_smem(reinterpret_cast<const void*>(k), (size_t)kSmemLimit - 1024);
+    if (e != cudaSuccess) return e;
+    const int tiles = a.tiles_m * a.tiles_n;
+    int clusters = resident_clusters(k, kPairThreads, smem, 2);
+    if (clusters > tiles) clusters = tiles;
+    return launch_clusters(k, clusters, 2, kPairThreads, smem, a, s);
+}
+
+template <class F, Out OT>
+cudaError_t go(const LinearCall& c, cudaStream_t s) {
+    return c.M > 256 ? pair_go<F, OT>(c, s) : rows_go<F, OT>(c, s);
+}
+
 template <class F>
 cudaError_t by_out(const LinearCall& c, cudaStream_t s) {
     switch (c.out) {
-        case In::BF16: return rows_go<F, Out::BF16>(c, s);
-        case In::F16: return rows_go<F, Out::F16>(c, s);
-        case In::F32: return rows_go<F, Out::F32>(c, s);
+        case In::BF16: return go<F, Out::BF16>(c, s);
+        case In::F16: return go<F, Out::F16>(c, s);
+        case In::F32: return go<F, Out::F32>(c, s);
     }
     return cudaErrorInvalidValue;
 }
