@@ -55,8 +55,8 @@ template <> struct SfRing<F4> {
 struct PairArgs {
     CUtensorMap ta;    // a codes, box 128 bytes x 128 rows
     CUtensorMap tb;    // b codes, box 128 bytes x 96 rows
-    CUtensorMap tsa;   // a scales as [tiles, 512 bytes], box kSfTiles tiles
-    CUtensorMap tsb;   // b scales likewise
+    CUtensorMap tsa;   // a scales as [row tiles, kb, 512 bytes], box 1 x kSfTiles x 512
+    CUtensorMap tsb;   // b scales likewise, box 2 x kSfTiles x 512
     CUtensorMap tout;  // out, residual, pre: box 128 bytes x 32 rows
     CUtensorMap tres;
     CUtensorMap tpre;
@@ -87,6 +87,14 @@ __device__ __forceinline__ void pair_load_2d(void* dst, const CUtensorMap* map, 
         "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes "
         "[%0], [%1, {%2, %3}], [%4];" ::"r"(smem_u32(dst)),
         "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar) : "memory");
+}
+// Scale tiles (x: the whole tile, k along K, r along the rows).
+__device__ __forceinline__ void pair_load_3d(void* dst, const CUtensorMap* map, int32_t k, int32_t r,
+                                             uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(k), "r"(r), "r"(bar) : "memory");
 }
 __device__ __forceinline__ void pair_commit(uint64_t* bar) {
     asm volatile(
@@ -268,41 +276,45 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_linear_pair(const __grid_co
     const uint32_t tmem = sh.tmem;
     bool bad = false;
     if (warp == 0) {
-        if (lane == 0) {
-            Ring r;
-            uint32_t g = 0;
-            for (int t = first; t < tiles && !bad; t += step) {
-                int32_t m0, n0;
-                pair_tile(a, t, m0, n0);
-                const int32_t sa_row = (m0 / 128 + rank) * a.kb, sb_row = (n0 / 128) * a.kb;
-                for (int i = 0; i < a.nkb; ++i, ++g, r.next(ns)) {
-                    const int s = r.slot;
-                    if (g >= (uint32_t)ns && !mbar_wait(&sh.empty[s], r.parity ^ 1u)) {
-                        bad = true;
-                        break;
-                    }
-                    const uint32_t bar = map_rank(smem_u32(&sh.full[s]), 0);
-                    if (rank == 0)
-                        mbar_expect_tx(&sh.full[s], (uint32_t)(2 * pair_stage_bytes<F>()));
-                    pair_load_2d(sA + s * kPairABytes, &a.ta, i * kRowBytes, m0 + 128 * rank, bar);
-                    pair_load_2d(sB + s * kPairBBytes, &a.tb, i * kRowBytes, n0 + 96 * rank, bar);
-                    pair_load_2d(sSA + s * kSf, &a.tsa, 0, sa_row + F::kSfTiles * i, bar);
-                    pair_load_2d(sSB + s * 2 * kSf, &a.tsb, 0, sb_row + F::kSfTiles * i, bar);
-                    pair_load_2d(sSB + s * 2 * kSf + kSf, &a.tsb, 0, sb_row + a.kb + F::kSfTiles * i, bar);
+        const bool elected = elect_lane();
+        const uint32_t full0 = map_rank(smem_u32(&sh.full[0]), 0);
+        Ring r;
+        uint32_t g = 0;
+        for (int t = first; t < tiles && !bad; t += step) {
+            int32_t m0, n0;
+            pair_tile(a, t, m0, n0);
+            const int32_t am = m0 + 128 * rank, bn = n0 + 96 * rank;
+            for (int i = 0; i < a.nkb; ++i) {
+                const int s = r.slot;
+                if (g >= (uint32_t)ns && !mbar_wait(&sh.empty[s], r.parity ^ 1u)) {
+                    bad = true;
+                    break;
                 }
-            }
-            // every copy issued has landed (and been read) before the CTA leaves:
-            // the stages' last uses, by the barriers this CTA has
-            for (int k = 0; k < ns && (uint32_t)k < g; ++k) {
-                // slot r.slot - 1 - k, its latest use
-                int s = r.slot - 1 - k;
-                uint32_t p = r.parity;
-                if (s < 0) {
-                    s += ns;
-                    p ^= 1u;
+                const uint32_t bar = full0 + 8 * s;
+                unsigned char *pa = sA + s * kPairABytes, *pb = sB + s * kPairBBytes;
+                unsigned char *psa = sSA + s * kSf, *psb = sSB + s * 2 * kSf;
+                if (elected) {
+                    if (rank == 0) mbar_expect_tx(&sh.full[s], (uint32_t)(2 * pair_stage_bytes<F>()));
+                    pair_load_2d(pa, &a.ta, i * kRowBytes, am, bar);
+                    pair_load_2d(pb, &a.tb, i * kRowBytes, bn, bar);
+                    pair_load_3d(psa, &a.tsa, F::kSfTiles * i, am >> 7, bar);
+                    pair_load_3d(psb, &a.tsb, F::kSfTiles * i, n0 >> 7, bar);
                 }
-                if (!mbar_wait(&sh.empty[s], p)) bad = true;
+                __syncwarp();
+                ++g;
+                r.next(ns);
             }
+        }
+        // every copy issued has landed (and been read) before the CTA leaves:
+        // the stages' last uses, by the barriers this CTA has
+        for (int k = 0; k < ns && (uint32_t)k < g; ++k) {
+            int s = r.slot - 1 - k;
+            uint32_t p = r.parity;
+            if (s < 0) {
+                s += ns;
+                p ^= 1u;
+            }
+            if (!mbar_wait(&sh.empty[s], p)) bad = true;
         }
     } else if (warp == 1) {
         if (rank == 0) {

@@ -112,11 +112,19 @@ cudaError_t rows_go(const LinearCall& c, cudaStream_t s) {
     return launch_clusters(k, clusters, best, kRowsThreads, smem, a, s);
 }
 
-// Scale tiles [tiles, 512 bytes], a box of `n` consecutive ones.
-bool scale_map(CUtensorMap* m, const uint8_t* scales, int64_t rows, int kb, int n) {
-    return matrix_map(m, CU_TENSOR_MAP_DATA_TYPE_UINT32, 4, scales, (rows + 127) / 128 * kb,
-                      kSfTileBytes, kSfTileBytes / 4, n, CU_TENSOR_MAP_SWIZZLE_NONE,
-                      CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
+// Scale tiles [row tiles, kb, 512 bytes], a box of r x n of them; tiles past
+// the ends read as zeros.
+bool scale_map(CUtensorMap* m, const uint8_t* scales, int64_t rows, int kb, int r, int n) {
+    PFN_cuTensorMapEncodeTiled_v12000 fn = encode_fn();
+    if (!fn) return false;
+    const cuuint64_t dims[3] = {kSfTileBytes / 4, (cuuint64_t)kb, (cuuint64_t)((rows + 127) / 128)};
+    const cuuint64_t strides[2] = {kSfTileBytes, (cuuint64_t)kb * kSfTileBytes};
+    const cuuint32_t box[3] = {kSfTileBytes / 4, (cuuint32_t)n, (cuuint32_t)r};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT32, 3, const_cast<uint8_t*>(scales), dims, strides, box,
+              estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // [M, N] of the output's type, box 32 rows x 128 bytes with the 128-byte swizzle.
@@ -139,8 +147,8 @@ cudaError_t pair_go(const LinearCall& c, cudaStream_t s) {
     a.kb = (int)((c.K + blk4 - 1) / blk4);
     a.nkb = (a.kb + F::kSfTiles - 1) / F::kSfTiles;
     if (!code_map(&a.ta, c.a, c.M, row_bytes, 128) || !code_map(&a.tb, c.b, c.N, row_bytes, 96) ||
-        !scale_map(&a.tsa, c.as, c.M, a.kb, F::kSfTiles) ||
-        !scale_map(&a.tsb, c.bs, c.N, a.kb, F::kSfTiles) ||
+        !scale_map(&a.tsa, c.as, c.M, a.kb, 1, F::kSfTiles) ||
+        !scale_map(&a.tsb, c.bs, c.N, a.kb, 2, F::kSfTiles) ||
         !chunk_map<OT>(&a.tout, c.ep.out, c.M, c.N) ||
         (c.ep.residual && !chunk_map<OT>(&a.tres, c.ep.residual, c.M, c.N)) ||
         (c.ep.pre && !chunk_map<OT>(&a.tpre, c.ep.pre, c.M, c.N)))
