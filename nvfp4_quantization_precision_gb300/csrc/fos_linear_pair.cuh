@@ -6,15 +6,26 @@
 // weights, rows 96 r .. 96 r + 95: the pair's MMA reads each half of b from
 // the SM that holds it, so an SM stages 16 KB of a and 12 KB of b for 128 x
 // 192 outputs where a single SM would stage 16 + 24.  Roles of a CTA's warps:
-//   warp 0     TMA producer (one thread): its halves of a and b and the scale
-//              tiles (its own of a, both of b) into a ring of stages; the
-//              bytes of both CTAs are counted by the full barrier of CTA 0
-//   warp 1     tensor memory; in CTA 0 one thread copies the scales of both
-//              CTAs (tcgen05.cp) and issues the pair's MMAs, whose completion
-//              frees the stage in both CTAs
-//   warps 2-5  epilogue of the CTA's 128 tokens, lane quadrant warp % 4
+//   warp 0     TMA producer: its halves of a and b into a ring of stages (the
+//              bytes of both CTAs are counted by the full barrier of CTA 0)
+//   warp 10    TMA producer of the scales, its own of a and both row tiles of
+//              b, by chunks of four scale tiles along K, into a ring of its own
+//   warp 1     tensor memory; in CTA 0 it issues the pair's MMAs, whose
+//              completion frees the stage in both CTAs
+//   warps 2-5  scales: shared memory to tensor memory (tcgen05.st), a chunk at
+//              a time into a ring of three buffers, lane quadrant warp % 4
+//   warps 6-9  epilogue of the CTA's 128 tokens, lane quadrant warp % 4
 // Tensor memory: two accumulators of 192 columns (the epilogue of a tile runs
-// under the MMAs of the next) and a ring of scale buffers in the other 128.
+// under the MMAs of the next) and the scale buffers of 40 columns (a: 4 per
+// scale tile, b: the 6 that its 192 rows take) in the other 128.  Copying the
+// scales with tcgen05.cp instead puts them into the tensor pipe itself, in
+// order with the MMAs, where each 512-byte tile costs about 25 cycles and
+// each batch the latency of the copy: 8192 x 4096 x 14336 took 338 us (8 bit)
+// and 232 us (NVFP4) that way.
+// All warps that issue asynchronous work run their loops converged and elect
+// the issuing lane for the instruction alone, which keeps the operands in
+// uniform registers; with a loop inside `if (lane == 0)` the issue itself was
+// the bound (513 and 492 us).
 // The epilogue goes by chunks of 32 tokens x 128 bytes of out.  A chunk's
 // residual is fetched by TMA into the very buffer its result will leave from:
 // a lane reads its 16-byte pieces, adds, and writes them back in place, so
@@ -29,34 +40,28 @@ namespace lin {
 
 constexpr int kPairM = 256, kPairN = 192;
 constexpr int kPairABytes = 128 * kRowBytes, kPairBBytes = 96 * kRowBytes;
-constexpr int kPairThreads = 192;
+constexpr int kPairThreads = 352;
 constexpr int kPairMaxStages = 8;
 constexpr int kChunkBytes = 32 * 128;
 constexpr int kPairGroupM = 8;     // tile rows per band of the tile order
 constexpr int kPairSfCol = 2 * kPairN;
 
-template <class F> constexpr int pair_sf_bytes() { return 3 * F::kSfTiles * kSfTileBytes; }
-template <class F> constexpr int pair_stage_bytes() {
-    return kPairABytes + kPairBBytes + pair_sf_bytes<F>();
-}
-// The ring of scale buffers in the 128 columns the accumulators leave: a
-// buffer holds the scales of a unit, a stage (F8) or half of one (F4); a
-// unit's copies may go once the MMAs that read its buffer are done, that is
-// those of the stage kLag before, waited for at the stage's last unit (for the
-// first unit of two, the wait of the stage before has covered it).
-template <class F> struct SfRing;
-template <> struct SfRing<F8> {
-    static constexpr int kUnits = 1, kCols = 16, kBufs = 4, kLag = 4;
-};
-template <> struct SfRing<F4> {
-    static constexpr int kUnits = 2, kCols = 24, kBufs = 5, kLag = 2;
-};
+constexpr int kPairStageBytes = kPairABytes + kPairBBytes;
+// A chunk of scales: four scale tiles along K of a's 128 rows and of b's two
+// row tiles, one stage of F4 or four of F8.
+constexpr int kSfChunkTiles = 4;
+constexpr int kSfChunkA = kSfChunkTiles * kSfTileBytes, kSfChunkBytes = 3 * kSfChunkA;
+constexpr int kSfSlots = 3;   // chunks in shared memory
+constexpr int kSfBufs = 3;    // chunks in tensor memory
+constexpr int kSfCols = 16 + 24;
+static_assert(kPairSfCol + kSfBufs * kSfCols <= (int)kAllColumns, "tensor memory");
+template <class F> constexpr int chunk_stages() { return kSfChunkTiles / F::kSfTiles; }
 
 struct PairArgs {
     CUtensorMap ta;    // a codes, box 128 bytes x 128 rows
     CUtensorMap tb;    // b codes, box 128 bytes x 96 rows
-    CUtensorMap tsa;   // a scales as [row tiles, kb, 512 bytes], box 1 x kSfTiles x 512
-    CUtensorMap tsb;   // b scales likewise, box 2 x kSfTiles x 512
+    CUtensorMap tsa;   // a scales as [row tiles, kb, 512 bytes], box 1 x 4 x 512
+    CUtensorMap tsb;   // b scales likewise, box 2 x 4 x 512
     CUtensorMap tout;  // out, residual, pre: box 128 bytes x 32 rows
     CUtensorMap tres;
     CUtensorMap tpre;
@@ -70,6 +75,7 @@ struct PairArgs {
 
 struct __align__(8) PairShared {
     uint64_t full[kPairMaxStages], empty[kPairMaxStages], acc_full[2], acc_empty[2], done;
+    uint64_t sf_full[kSfSlots], sf_empty[kSfSlots], sf_ready[kSfBufs], sf_free[kSfBufs];
     uint64_t res_full[4][4];
     uint32_t tmem;
     int fail;
@@ -88,21 +94,38 @@ __device__ __forceinline__ void pair_load_2d(void* dst, const CUtensorMap* map, 
         "[%0], [%1, {%2, %3}], [%4];" ::"r"(smem_u32(dst)),
         "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar) : "memory");
 }
-// Scale tiles (x: the whole tile, k along K, r along the rows).
-__device__ __forceinline__ void pair_load_3d(void* dst, const CUtensorMap* map, int32_t k, int32_t r,
-                                             uint32_t bar) {
+// Scale tiles k ... along K of row tile r ... into this CTA.
+__device__ __forceinline__ void sf_load_3d(void* dst, const CUtensorMap* map, int32_t k, int32_t r,
+                                           uint64_t* bar) {
     asm volatile(
-        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes "
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes "
         "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(dst)),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(k), "r"(r), "r"(bar) : "memory");
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(k), "r"(r), "r"(smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ void tmem_st_x8(uint32_t taddr, const uint32_t* v) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr),
+                 "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
 }
 __device__ __forceinline__ void pair_commit(uint64_t* bar) {
     asm volatile(
         "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
         "[%0], %1;" ::"r"(smem_u32(bar)), "h"((unsigned short)3) : "memory");
 }
+// Whether a phase has completed, without waiting.
+__device__ __forceinline__ bool mbar_ask(uint64_t* bar, uint32_t parity) {
+    uint32_t done;
+    asm volatile("{\n\t.reg .pred p;\n\t"
+                 "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+                 "selp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(done) : "r"(smem_u32(bar)), "r"(parity) : "memory");
+    return done != 0;
+}
+// Arrival at a barrier of another CTA (its cluster address).  The default
+// release is that of the CTA: what is published is in tensor memory, complete
+// and fenced.  Released to the cluster instead, each arrival took 1300 cycles.
 __device__ __forceinline__ void cluster_arrive(uint32_t bar) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&v)[32]) {
     asm volatile(
@@ -201,32 +224,15 @@ __device__ __forceinline__ void store_chunk(const CUtensorMap* map, int32_t x, i
                      map), "r"(x), "r"(y), "r"(buf) : "memory");
 }
 
-// Scale copies and MMAs of unit u of a stage (one lane): the scales of the
-// pair's 256 rows of a (each CTA its 128) and of both scale tiles of b go to
-// columns col ..., the MMAs read b's from `off` on.
+// The MMAs of a stage (one lane): nk scale tiles of it exist (F4).
 template <class F>
-__device__ __forceinline__ void pair_unit(uint32_t acc, uint32_t a0, uint32_t b0, uint32_t col,
-                                          uint32_t la, uint32_t lb, uint32_t off, int u, int nk,
-                                          uint32_t more) {
-    constexpr uint32_t kT = kSfTileBytes >> 4;
-    constexpr int kTiles = F::kSfTiles / SfRing<F>::kUnits;  // scale tiles of a unit
-    const uint32_t sfa = col, sfb = col + 4 * kTiles;
+__device__ __forceinline__ void pair_stage(uint32_t acc, uint32_t a0, uint32_t b0, uint32_t sfa,
+                                           uint32_t sfb, int nk, uint32_t more) {
 #pragma unroll
-    for (int i = 0; i < kTiles; ++i) {
-        const int kk = u * kTiles + i;
-        if (kk < nk) {
-            sf_copy<2>(sfa + 4 * i, la + kk * kT);
-            sf_copy<2>(sfb + 8 * i, lb + kk * kT);
-            sf_copy<2>(sfb + 8 * i + 4, lb + (F::kSfTiles + kk) * kT);
-        }
-    }
-    constexpr int kSteps = 4 / SfRing<F>::kUnits;
-#pragma unroll
-    for (int i = 0; i < kSteps; ++i) {
-        const int kk = u * kSteps + i;
+    for (int kk = 0; kk < 4; ++kk) {
         if (F::kGlobal && kk >= nk) break;
         mma_issue<F, 2>(acc, a0 + 2 * kk, b0 + 2 * kk, idesc<F>(kPairM, kPairN, F::kGlobal ? 0 : kk),
-                        F::kGlobal ? sfa + 4 * i : sfa, (F::kGlobal ? sfb + 8 * i : sfb) + off,
+                        F::kGlobal ? sfa + 4 * kk : sfa, F::kGlobal ? sfb + 6 * kk : sfb,
                         kk == 0 ? more : 1u);
     }
 }
@@ -237,12 +243,10 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_linear_pair(const __grid_co
     __shared__ PairShared sh;
     unsigned char* base = s_raw + ((1024u - (smem_u32(s_raw) & 1023u)) & 1023u);
     const int ns = a.stages;
-    constexpr int kSf = F::kSfTiles * kSfTileBytes;  // scale bytes of 128 rows, one stage
     unsigned char* sA = base;
     unsigned char* sB = sA + ns * kPairABytes;
     unsigned char* sC = sB + ns * kPairBBytes;       // epilogue chunks
-    unsigned char* sSA = sC + 4 * a.bufs * kChunkBytes;
-    unsigned char* sSB = sSA + ns * kSf;
+    unsigned char* sS = sC + 4 * a.bufs * kChunkBytes;  // scale chunks: a, then b's two row tiles
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = (int)cluster_rank();
     const int tiles = a.tiles_m * a.tiles_n;
@@ -255,6 +259,14 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_linear_pair(const __grid_co
         for (int b = 0; b < 2; ++b) {
             bar_init(&sh.acc_full[b], 1);
             bar_init(&sh.acc_empty[b], 8);
+        }
+        for (int b = 0; b < kSfSlots; ++b) {
+            bar_init(&sh.sf_full[b], 1);
+            bar_init(&sh.sf_empty[b], 4);
+        }
+        for (int b = 0; b < kSfBufs; ++b) {
+            bar_init(&sh.sf_ready[b], 8);
+            bar_init(&sh.sf_free[b], 1);
         }
         for (int w = 0; w < 4; ++w)
             for (int b = 0; b < 4; ++b) bar_init(&sh.res_full[w][b], 1);
@@ -292,13 +304,10 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_linear_pair(const __grid_co
                 }
                 const uint32_t bar = full0 + 8 * s;
                 unsigned char *pa = sA + s * kPairABytes, *pb = sB + s * kPairBBytes;
-                unsigned char *psa = sSA + s * kSf, *psb = sSB + s * 2 * kSf;
                 if (elected) {
-                    if (rank == 0) mbar_expect_tx(&sh.full[s], (uint32_t)(2 * pair_stage_bytes<F>()));
+                    if (rank == 0) mbar_expect_tx(&sh.full[s], (uint32_t)(2 * kPairStageBytes));
                     pair_load_2d(pa, &a.ta, i * kRowBytes, am, bar);
                     pair_load_2d(pb, &a.tb, i * kRowBytes, bn, bar);
-                    pair_load_3d(psa, &a.tsa, F::kSfTiles * i, am >> 7, bar);
-                    pair_load_3d(psb, &a.tsb, F::kSfTiles * i, n0 >> 7, bar);
                 }
                 __syncwarp();
                 ++g;
@@ -319,52 +328,40 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_linear_pair(const __grid_co
     } else if (warp == 1) {
         if (rank == 0) {
             const bool elected = elect_lane();
-            Ring r, w;      // the stage in work; the one whose scales are overwritten
-            uint32_t g = 0, buf = 0;
+            Ring r, f;      // stages; scale buffers
             int j = 0;
             for (int t = first; t < tiles && !bad; t += step, ++j) {
-                int32_t m0, n0;
-                pair_tile(a, t, m0, n0);
                 const int ab = j & 1;
                 if (j >= 2 && !mbar_wait(&sh.acc_empty[ab], (uint32_t)((j >> 1) - 1) & 1)) {
                     bad = true;
                     break;
                 }
                 const uint32_t acc = tmem + (uint32_t)(ab * kPairN);
-                const uint32_t off = (n0 & 127) ? 2u : 0u;  // b starts half-way into a scale tile
+                bool here = false;  // the stage is known to be full
                 for (int i = 0; i < a.nkb; ++i) {
-                    const int s = r.slot;
-                    if (!mbar_wait(&sh.full[s], r.parity)) {
+                    const int s = r.slot, in_chunk = i % chunk_stages<F>();
+                    if ((in_chunk == 0 && !mbar_wait(&sh.sf_ready[f.slot], f.parity)) ||
+                        (!here && !mbar_wait(&sh.full[s], r.parity))) {
                         bad = true;
                         break;
                     }
+                    // asks for the next stage now: the answer is there by the
+                    // time this stage's instructions are out
+                    r.next(ns);
+                    here = i + 1 < a.nkb && mbar_ask(&sh.full[r.slot], r.parity);
+                    tc_fence_after();
                     const int nk = min(F::kSfTiles, a.kb - F::kSfTiles * i);
-                    const uint32_t la = sf_desc_lo(smem_u32(sSA) + s * kSf);
-                    const uint32_t lb = sf_desc_lo(smem_u32(sSB) + s * 2 * kSf);
                     const uint32_t a0 = desc_lo(smem_u32(sA) + s * kPairABytes);
                     const uint32_t b0 = desc_lo(smem_u32(sB) + s * kPairBBytes);
-                    const uint32_t more = i > 0;
-                    bool ok = true;
-#pragma unroll
-                    for (int u = 0; u < SfRing<F>::kUnits; ++u) {
-                        if (u == SfRing<F>::kUnits - 1 && g >= (uint32_t)SfRing<F>::kLag) {
-                            ok = mbar_wait(&sh.empty[w.slot], w.parity);
-                            w.next(ns);
-                        }
-                        tc_fence_after();
-                        if (elected && ok)
-                            pair_unit<F>(acc, a0, b0, tmem + kPairSfCol + buf * SfRing<F>::kCols, la, lb,
-                                         off, u, nk, more);
-                        buf = buf + 1 == SfRing<F>::kBufs ? 0 : buf + 1;
+                    const uint32_t sf = tmem + kPairSfCol + f.slot * kSfCols;
+                    const bool last = in_chunk == chunk_stages<F>() - 1 || i + 1 == a.nkb;
+                    if (elected) {
+                        pair_stage<F>(acc, a0, b0, sf + 4 * in_chunk, sf + 16 + 6 * in_chunk, nk, i > 0);
+                        pair_commit(&sh.empty[s]);
+                        if (last) pair_commit(&sh.sf_free[f.slot]);
                     }
-                    if (!ok) {
-                        bad = true;
-                        break;
-                    }
-                    if (elected) pair_commit(&sh.empty[s]);
                     __syncwarp();
-                    ++g;
-                    r.next(ns);
+                    if (last) f.next(kSfBufs);
                 }
                 if (!bad && elected) pair_commit(&sh.acc_full[ab]);
                 __syncwarp();
@@ -372,8 +369,95 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_linear_pair(const __grid_co
             if (elected) pair_commit(&sh.done);
             __syncwarp();
         }
+    } else if (warp == 10) {
+        const bool elected = elect_lane();
+        Ring f;
+        uint32_t chunks = 0;
+        for (int t = first; t < tiles && !bad; t += step) {
+            int32_t m0, n0;
+            pair_tile(a, t, m0, n0);
+            const int32_t ra = (m0 + 128 * rank) >> 7, rb = n0 >> 7;
+            for (int k = 0; k < a.kb; k += kSfChunkTiles) {
+                if (chunks >= (uint32_t)kSfSlots && !mbar_wait(&sh.sf_empty[f.slot], f.parity ^ 1u)) {
+                    bad = true;
+                    break;
+                }
+                unsigned char* ps = sS + f.slot * kSfChunkBytes;
+                if (elected) {
+                    mbar_expect_tx(&sh.sf_full[f.slot], (uint32_t)kSfChunkBytes);
+                    sf_load_3d(ps, &a.tsa, k, ra, &sh.sf_full[f.slot]);
+                    sf_load_3d(ps + kSfChunkA, &a.tsb, k, rb, &sh.sf_full[f.slot]);
+                }
+                __syncwarp();
+                ++chunks;
+                f.next(kSfSlots);
+            }
+        }
+        // the chunks' last uses have landed and been read
+        for (int k = 0; k < kSfSlots && (uint32_t)k < chunks; ++k) {
+            int sl = f.slot - 1 - k;
+            uint32_t p = f.parity;
+            if (sl < 0) {
+                sl += kSfSlots;
+                p ^= 1u;
+            }
+            if (!mbar_wait(&sh.sf_empty[sl], p)) bad = true;
+        }
+    } else if (warp < 6) {
+        // scales: lane l of quadrant q writes row l of each 16-byte-wide tile,
+        // a's four words to columns 4 kk ..., of b's eight (two row tiles) the
+        // six of the tile's 192 rows to columns 16 + 6 kk ...
+        const int q = warp & 3;
+        const uint32_t lane_base = tmem + kPairSfCol + ((uint32_t)(32 * q) << 16);
+        Ring f, d;          // shared-memory slots; tensor-memory buffers
+        uint32_t chunks = 0;
+        for (int t = first; t < tiles && !bad; t += step) {
+            int32_t m0, n0;
+            pair_tile(a, t, m0, n0);
+            const bool half = (n0 & 127) != 0;  // b starts half-way into a scale tile
+            for (int i = 0; i < a.nkb; i += chunk_stages<F>()) {
+                if (!mbar_wait(&sh.sf_full[f.slot], f.parity)) {
+                    bad = true;
+                    break;
+                }
+                const unsigned char* ps = sS + f.slot * kSfChunkBytes + 16 * lane;
+                uint32_t va[16], vb[24];
+#pragma unroll
+                for (int kk = 0; kk < kSfChunkTiles; ++kk) {
+                    const uint4 x = *reinterpret_cast<const uint4*>(ps + kk * kSfTileBytes);
+                    const uint4 u = *reinterpret_cast<const uint4*>(ps + kSfChunkA + kk * kSfTileBytes);
+                    const uint4 v = *reinterpret_cast<const uint4*>(ps + 2 * kSfChunkA + kk * kSfTileBytes);
+                    va[4 * kk] = x.x; va[4 * kk + 1] = x.y; va[4 * kk + 2] = x.z; va[4 * kk + 3] = x.w;
+                    vb[6 * kk] = half ? u.z : u.x;
+                    vb[6 * kk + 1] = half ? u.w : u.y;
+                    vb[6 * kk + 2] = half ? v.x : u.z;
+                    vb[6 * kk + 3] = half ? v.y : u.w;
+                    vb[6 * kk + 4] = half ? v.z : v.x;
+                    vb[6 * kk + 5] = half ? v.w : v.y;
+                }
+                __syncwarp();
+                if (lane == 0) bar_arrive(&sh.sf_empty[f.slot]);
+                if (chunks >= (uint32_t)kSfBufs && !mbar_wait(&sh.sf_free[d.slot], d.parity ^ 1u)) {
+                    bad = true;
+                    break;
+                }
+                __syncwarp();
+                tc_fence_after();
+                const uint32_t col = lane_base + d.slot * kSfCols;
+                mma::tmem_st_x16(col, va);
+                mma::tmem_st_x16(col + 16, reinterpret_cast<uint32_t(&)[16]>(vb));
+                tmem_st_x8(col + 32, vb + 16);
+                asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) cluster_arrive(map_rank(smem_u32(&sh.sf_ready[d.slot]), 0));
+                ++chunks;
+                f.next(kSfSlots);
+                d.next(kSfBufs);
+            }
+        }
     } else {
-        const int q = warp & 3, e = warp - 2;
+        const int q = warp & 3, e = warp - 6;
         constexpr int kElt = OT == Out::F32 ? 4 : 2;
         constexpr int kCols = 128 / kElt;               // columns of a chunk
         constexpr int kChunks = kPairN / kCols;         // chunks of a tile

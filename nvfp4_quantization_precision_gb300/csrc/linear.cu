@@ -147,8 +147,8 @@ cudaError_t pair_go(const LinearCall& c, cudaStream_t s) {
     a.kb = (int)((c.K + blk4 - 1) / blk4);
     a.nkb = (a.kb + F::kSfTiles - 1) / F::kSfTiles;
     if (!code_map(&a.ta, c.a, c.M, row_bytes, 128) || !code_map(&a.tb, c.b, c.N, row_bytes, 96) ||
-        !scale_map(&a.tsa, c.as, c.M, a.kb, 1, F::kSfTiles) ||
-        !scale_map(&a.tsb, c.bs, c.N, a.kb, 2, F::kSfTiles) ||
+        !scale_map(&a.tsa, c.as, c.M, a.kb, 1, kSfChunkTiles) ||
+        !scale_map(&a.tsb, c.bs, c.N, a.kb, 2, kSfChunkTiles) ||
         !chunk_map<OT>(&a.tout, c.ep.out, c.M, c.N) ||
         (c.ep.residual && !chunk_map<OT>(&a.tres, c.ep.residual, c.M, c.N)) ||
         (c.ep.pre && !chunk_map<OT>(&a.tpre, c.ep.pre, c.M, c.N)))
@@ -158,11 +158,10 @@ cudaError_t pair_go(const LinearCall& c, cudaStream_t s) {
     a.N = c.N;
     a.tiles_m = (int)((c.M + kPairM - 1) / kPairM);
     a.tiles_n = (int)((c.N + kPairN - 1) / kPairN);
-    a.bufs = c.ep.pre ? 4 : 3;
-    const int epi = 4 * a.bufs * kChunkBytes;
-    a.stages = (kSmemLimit - 2048 - epi) / pair_stage_bytes<F>();
-    if (a.stages > kPairMaxStages) a.stages = kPairMaxStages;
-    const int smem = a.stages * pair_stage_bytes<F>() + epi + 1024;
+    a.bufs = c.ep.pre ? 4 : 2;
+    const int other = 4 * a.bufs * kChunkBytes + kSfSlots * kSfChunkBytes;
+    a.stages = (kSmemLimit - 2048 - other) / kPairStageBytes;
+    const int smem = a.stages * kPairStageBytes + other + 1024;
     auto k = k_linear_pair<F, OT>;
     cudaError_t e = allow_smem(reinterpret_cast<const void*>(k), (size_t)kSmemLimit - 1024);
     if (e != cudaSuccess) return e;
