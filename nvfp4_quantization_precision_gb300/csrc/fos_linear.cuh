@@ -173,22 +173,10 @@ __device__ __forceinline__ void store_out(void* p, int64_t i, float v) {
 template <int kN>
 __device__ __forceinline__ void act_apply(int act, float (&v)[kN]) {
     switch (static_cast<Act>(act)) {
-        case Act::RELU:
-#pragma unroll
-            for (int i = 0; i < kN; ++i) v[i] = act_value<Act::RELU>(v[i]);
-            break;
-        case Act::GELU:
-#pragma unroll
-            for (int i = 0; i < kN; ++i) v[i] = act_value<Act::GELU>(v[i]);
-            break;
-        case Act::GELU_TANH:
-#pragma unroll
-            for (int i = 0; i < kN; ++i) v[i] = act_value<Act::GELU_TANH>(v[i]);
-            break;
-        case Act::SILU:
-#pragma unroll
-            for (int i = 0; i < kN; ++i) v[i] = act_value<Act::SILU>(v[i]);
-            break;
+        case Act::RELU: act_values<Act::RELU>(v); break;
+        case Act::GELU: act_values<Act::GELU>(v); break;
+        case Act::GELU_TANH: act_values<Act::GELU_TANH>(v); break;
+        case Act::SILU: act_values<Act::SILU>(v); break;
         default: break;
     }
 }

@@ -28,9 +28,9 @@
 // the bound (513 and 492 us).
 // The epilogue goes by chunks of 32 tokens x 128 bytes of out.  A chunk's
 // residual is fetched by TMA into the very buffer its result will leave from:
-// a lane reads its 16-byte pieces, adds, and writes them back in place, so
-// three buffers a warp hold the fetch of the chunk after next, the chunk in
-// work and the store of the last.
+// a lane reads its 16-byte pieces, adds, and writes them back in place, so two
+// buffers a warp hold the chunk in work and the last one's store or the next
+// one's fetch.
 #pragma once
 
 #include "fos_linear.cuh"
@@ -70,13 +70,13 @@ struct PairArgs {
     int tiles_m, tiles_n;
     int kb, nkb;
     int stages;
-    int bufs;          // chunk buffers of an epilogue warp
+    int bufs;          // chunk buffers of an epilogue warp: 2, with pre 4
 };
 
 struct __align__(8) PairShared {
     uint64_t full[kPairMaxStages], empty[kPairMaxStages], acc_full[2], acc_empty[2], done;
     uint64_t sf_full[kSfSlots], sf_empty[kSfSlots], sf_ready[kSfBufs], sf_free[kSfBufs];
-    uint64_t res_full[4][4];
+    uint64_t res_full[4][2];
     uint32_t tmem;
     int fail;
 };
@@ -151,27 +151,16 @@ __device__ __forceinline__ void pair_tile(const PairArgs& a, int t, int32_t& m0,
     n0 = col * kPairN;
 }
 
-// 32 biases from column n (the same for every lane; columns past N are not read).
+// The biases of a tile's columns: lane l holds those of columns l, l + 32, ...
 template <Out OT>
-__device__ __forceinline__ void add_bias(const Epilogue& e, int64_t n, int64_t N, float (&v)[32]) {
+__device__ __forceinline__ void load_bias(const Epilogue& e, int64_t n0, int64_t N, int lane,
+                                          float (&b)[kPairN / 32]) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        if (n + 16 * h >= N) break;
-        if (OT == Out::F32 || e.bias32) {
-            const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(e.bias) + n + 16 * h);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float4 b = __ldg(p + i);
-                v[16 * h + 4 * i] = fadd(v[16 * h + 4 * i], b.x);
-                v[16 * h + 4 * i + 1] = fadd(v[16 * h + 4 * i + 1], b.y);
-                v[16 * h + 4 * i + 2] = fadd(v[16 * h + 4 * i + 2], b.z);
-                v[16 * h + 4 * i + 3] = fadd(v[16 * h + 4 * i + 3], b.w);
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-                v[16 * h + i] = fadd(v[16 * h + i], load_out<OT>(e.bias, n + 16 * h + i));
-        }
+    for (int i = 0; i < kPairN / 32; ++i) {
+        const int64_t n = n0 + 32 * i + lane;
+        b[i] = 0.0f;
+        if (n < N)
+            b[i] = e.bias32 ? __ldg(static_cast<const float*>(e.bias) + n) : load_out<OT>(e.bias, n);
     }
 }
 
@@ -269,7 +258,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_linear_pair(const __grid_co
             bar_init(&sh.sf_free[b], 1);
         }
         for (int w = 0; w < 4; ++w)
-            for (int b = 0; b < 4; ++b) bar_init(&sh.res_full[w][b], 1);
+            for (int b = 0; b < 2; ++b) bar_init(&sh.res_full[w][b], 1);
         bar_init(&sh.done, 1);
         sh.fail = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -462,24 +451,27 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_linear_pair(const __grid_co
         constexpr int kCols = 128 / kElt;               // columns of a chunk
         constexpr int kChunks = kPairN / kCols;         // chunks of a tile
         const bool pre = a.ep.pre != nullptr, res = a.ep.residual != nullptr;
-        const int nb = a.bufs, use = pre ? 2 : 1;       // buffers a chunk uses
-        const int ahead = nb / use - 1;                 // chunks a residual is fetched ahead
-        unsigned char* bufs = sC + e * nb * kChunkBytes;
+        // two slots of a buffer for out (and the residual) and, with pre, one for it
+        const int slot_bytes = (pre ? 2 : 1) * kChunkBytes;
+        unsigned char* bufs = sC + e * 2 * slot_bytes;
+        float* s_bias = reinterpret_cast<float*>(sS + kSfSlots * kSfChunkBytes) + e * kPairN;
         const int mine = first < tiles ? (tiles - first + step - 1) / step : 0;
         const int total = mine * kChunks;
-        // chunk c: buffer, and the coordinates of its piece of out
-        auto buf_of = [&](int c) { return (c * use) % nb; };
-        auto fetch = [&](int c) {                       // one lane
+        auto fetch = [&](int c) {                       // chunk c's residual (one lane)
             int32_t m0, n0;
             pair_tile(a, first + (c / kChunks) * step, m0, n0);
-            uint64_t* bar = &sh.res_full[e][buf_of(c)];
+            uint64_t* bar = &sh.res_full[e][c & 1];
             mbar_expect_tx(bar, kChunkBytes);
-            tma_load_2d(bufs + buf_of(c) * kChunkBytes, &a.tres, n0 + (c % kChunks) * kCols,
+            tma_load_2d(bufs + (c & 1) * slot_bytes, &a.tres, n0 + (c % kChunks) * kCols,
                         m0 + 128 * rank + 32 * q, bar);
         };
-        int fetched = 0;
-        if (res && lane == 0)
-            for (; fetched < ahead && fetched < total; ++fetched) fetch(fetched);
+        if (res && lane == 0 && total > 0) fetch(0);
+        float bias[kPairN / 32];
+        if (a.ep.bias && first < tiles) {
+            int32_t m0, n0;
+            pair_tile(a, first, m0, n0);
+            load_bias<OT>(a.ep, n0, a.N, lane, bias);
+        }
         float gb = 1.0f, ga0 = 1.0f;
         if constexpr (F::kGlobal) {
             gb = fdiv(1.0f, global_scale(a.ep.b_amax[0], a.ep.six_bound));
@@ -494,18 +486,22 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_linear_pair(const __grid_co
             if constexpr (F::kGlobal)
                 if (a.ep.a_row && mw + lane < a.M)
                     ga = fdiv(1.0f, global_scale(__ldg(a.ep.a_amax + mw + lane), a.ep.six_bound));
+            if (a.ep.bias) {  // this tile's biases to shared memory, the next one's on their way
+#pragma unroll
+                for (int i = 0; i < kPairN / 32; ++i) s_bias[32 * i + lane] = bias[i];
+                if (t + step < tiles) {
+                    int32_t mn, nn;
+                    pair_tile(a, t + step, mn, nn);
+                    load_bias<OT>(a.ep, nn, a.N, lane, bias);
+                }
+            }
             const int ab = j & 1;
             if (!bad && !mbar_wait(&sh.acc_full[ab], (uint32_t)(j >> 1) & 1)) bad = true;
             __syncwarp();
             tc_fence_after();
             for (int k = 0; k < kChunks; ++k, ++c) {
-                const int b = buf_of(c);
-                const uint32_t buf = smem_u32(bufs + b * kChunkBytes);
-                const uint32_t pbuf = smem_u32(bufs + ((b + 1) % nb) * kChunkBytes);
-                if (res) {
-                    const uint32_t use_no = (uint32_t)(c * use / nb);
-                    if (!bad && !mbar_wait(&sh.res_full[e][b], use_no & 1)) bad = true;
-                }
+                const uint32_t buf = smem_u32(bufs + (c & 1) * slot_bytes);
+                if (res && !bad && !mbar_wait(&sh.res_full[e][c & 1], (uint32_t)(c >> 1) & 1)) bad = true;
                 __syncwarp();
 #pragma unroll
                 for (int h = 0; h < kCols / 32; ++h) {
@@ -523,9 +519,18 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_linear_pair(const __grid_co
                         v[i] = __uint_as_float(u[i]);
                         if constexpr (F::kGlobal) v[i] = fmul(fmul(v[i], ga), gb);
                     }
-                    if (a.ep.bias) add_bias<OT>(a.ep, n0 + col, a.N, v);
+                    if (a.ep.bias) {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const float4 b4 = *reinterpret_cast<const float4*>(s_bias + col + 4 * i);
+                            v[4 * i] = fadd(v[4 * i], b4.x);
+                            v[4 * i + 1] = fadd(v[4 * i + 1], b4.y);
+                            v[4 * i + 2] = fadd(v[4 * i + 2], b4.z);
+                            v[4 * i + 3] = fadd(v[4 * i + 3], b4.w);
+                        }
+                    }
                     constexpr int kPieces = 32 * kElt / 16;
-                    if (pre) put_pieces<OT>(pbuf + lane * 128, lane, kPieces * h, v);
+                    if (pre) put_pieces<OT>(buf + kChunkBytes + lane * 128, lane, kPieces * h, v);
                     act_apply(a.ep.act, v);
                     if (res) add_pieces<OT>(buf + lane * 128, lane, kPieces * h, v);
                     put_pieces<OT>(buf + lane * 128, lane, kPieces * h, v);
@@ -534,14 +539,15 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_linear_pair(const __grid_co
                 __syncwarp();
                 if (lane == 0) {
                     store_chunk(&a.tout, n0 + k * kCols, mw, buf);
-                    if (pre) store_chunk(&a.tpre, n0 + k * kCols, mw, pbuf);
+                    if (pre) store_chunk(&a.tpre, n0 + k * kCols, mw, buf + kChunkBytes);
                     asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-                    // the store before this one has read its buffers: they are
-                    // the next ones to be written or fetched into
+                    // the chunk before this one has left its slot, which the
+                    // next one is fetched into and written to
                     asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
-                    if (res && fetched < total) fetch(fetched++);
+                    if (res && c + 1 < total) fetch(c + 1);
                 }
             }
+            __syncwarp();  // the biases are read before the next tile's replace them
         }
         if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
         __syncwarp();

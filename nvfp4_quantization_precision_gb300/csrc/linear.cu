@@ -159,7 +159,7 @@ cudaError_t pair_go(const LinearCall& c, cudaStream_t s) {
     a.tiles_m = (int)((c.M + kPairM - 1) / kPairM);
     a.tiles_n = (int)((c.N + kPairN - 1) / kPairN);
     a.bufs = c.ep.pre ? 4 : 2;
-    const int other = 4 * a.bufs * kChunkBytes + kSfSlots * kSfChunkBytes;
+    const int other = 4 * a.bufs * kChunkBytes + kSfSlots * kSfChunkBytes + 4 * kPairN * 4;
     a.stages = (kSmemLimit - 2048 - other) / kPairStageBytes;
     const int smem = a.stages * kPairStageBytes + other + 1024;
     auto k = k_linear_pair<F, OT>;
