@@ -150,7 +150,14 @@ def _check(rc, what):
         raise FosError(rc, what)
 
 
+# The current stream's handle without building a torch.cuda.Stream (2.2 us a
+# call on the host), where torch has it.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(t):
+    if _raw_stream is not None:
+        return _raw_stream(t.get_device())
     return ctypes.c_void_p(torch.cuda.current_stream(t.device).cuda_stream)
 
 
@@ -496,26 +503,35 @@ def _a(t):
 
 
 def _like(t, name, shape, dtype, dev):
-    """Checks an operand or a caller's output buffer: a contiguous CUDA tensor
-    of this shape, type and device."""
-    if t.dtype != dtype or t.shape != shape or t.device != dev or not t.is_contiguous():
-        raise ValueError("%s must be a contiguous %s tensor of shape %s on %s"
+    """Checks an operand or a caller's output buffer: a contiguous tensor of
+    this shape and type on CUDA device number dev."""
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev or not t.is_contiguous():
+        raise ValueError("%s must be a contiguous %s tensor of shape %s on cuda:%d"
                          % (name, dtype, tuple(shape), dev))
     return t
 
 
 def _data(t, name):
-    """Checks a rank-2 floating-point input; returns (rows, cols, type, device)."""
-    _cuda(t, name)
-    if t.dim() != 2 or t.dtype not in _DT:
+    """Checks a rank-2 floating-point input; returns (shape, type, device number)."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or not t.is_contiguous():
+        _cuda(t, name)
+    dt = _DT.get(t.dtype)
+    shape = t.shape
+    if dt is None or len(shape) != 2:
         raise ValueError("%s must be a rank-2 bf16, fp16 or fp32 tensor" % name)
-    return t.shape[0], t.shape[1], _DT[t.dtype], t.device
+    return shape, dt, t.get_device()
+
+
+def _new(shape, dtype, dev):
+    return torch.empty(shape, dtype=dtype, device=torch.device("cuda", dev))
 
 
 def _weight(w, cols, dtype, dev):
-    if not isinstance(w, torch.Tensor) or w.dtype not in (torch.float32, dtype):
+    wt = w.dtype
+    if wt is not torch.float32 and wt is not dtype:
         raise ValueError("weight must be float32 or of the input's type")
-    return _DT[_like(w, "weight", (cols,), w.dtype, dev).dtype]
+    _like(w, "weight", (cols,), wt, dev)
+    return _DT[wt]
 
 
 def _pair8(rows, cols, tiled, codes, scales, dev, names=("codes", "scales")):
@@ -524,12 +540,12 @@ def _pair8(rows, cols, tiled, codes, scales, dev, names=("codes", "scales")):
     if cols % 32:
         raise FosError(FOS_ERR_UNSUPPORTED, names[0])
     if codes is None:
-        codes = torch.empty((rows, cols), dtype=torch.uint8, device=dev)
+        codes = _new((rows, cols), torch.uint8, dev)
     else:
         _like(codes, names[0], (rows, cols), torch.uint8, dev)
     shape = ((rows + 127) // 128 * ((cols + 127) // 128) * 512,) if tiled else (rows, cols // 32)
     if scales is None:
-        scales = torch.empty(shape, dtype=torch.uint8, device=dev)
+        scales = _new(shape, torch.uint8, dev)
     else:
         _like(scales, names[1], shape, torch.uint8, dev)
     return codes, scales
@@ -549,11 +565,12 @@ def rms_norm(x, weight, residual=None, eps=1e-6, scale_tiled=True, quantized=Tru
     over the rows of x [rows, cols].  Returns (codes, scales, y, h, rstd):
     y's 8-bit codes and scales (None without quantized), y itself with
     normalized (else None), h (x itself without a residual) and rstd [rows]."""
-    R, C, dt, dev = _data(x, "x")
+    shape, dt, dev = _data(x, "x")
+    R, C = shape
     wdt = _weight(weight, C, x.dtype, dev)
     if residual is not None:
-        _like(residual, "residual", x.shape, x.dtype, dev)
-        h = torch.empty_like(x) if h is None else _like(h, "h", x.shape, x.dtype, dev)
+        _like(residual, "residual", shape, x.dtype, dev)
+        h = torch.empty_like(x) if h is None else _like(h, "h", shape, x.dtype, dev)
     elif h is not None:
         raise ValueError("h is an output of a norm with a residual")
     if quantized:
@@ -561,15 +578,15 @@ def rms_norm(x, weight, residual=None, eps=1e-6, scale_tiled=True, quantized=Tru
     else:
         codes = scales = None
     if normalized:
-        y = torch.empty_like(x) if y is None else _like(y, "y", x.shape, x.dtype, dev)
+        y = torch.empty_like(x) if y is None else _like(y, "y", shape, x.dtype, dev)
     else:
         y = None
     if rstd is None:
-        rstd = torch.empty(R, dtype=torch.float32, device=dev)
+        rstd = _new((R,), torch.float32, dev)
     else:
         _like(rstd, "rstd", (R,), torch.float32, dev)
     _check(lib().fos_rms_norm(x.data_ptr(), _a(residual), weight.data_ptr(), dt, wdt, R, C, eps,
-                              int(bool(scale_tiled)), _a(h), _a(y), _a(codes), _a(scales),
+                              1 if scale_tiled else 0, _a(h), _a(y), _a(codes), _a(scales),
                               rstd.data_ptr(), _stream(x)), "fos_rms_norm")
     return codes, scales, y, x if h is None else h, rstd
 
@@ -578,11 +595,11 @@ def _workspace(workspace, need, dev):
     if need == 0:
         return None, 0
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        workspace = _new((need,), torch.uint8, dev)
     else:
         _cuda(workspace, "workspace")
-        if workspace.dtype != torch.uint8 or workspace.device != dev:
-            raise ValueError("workspace must be a uint8 tensor on %s" % dev)
+        if workspace.dtype != torch.uint8 or workspace.get_device() != dev:
+            raise ValueError("workspace must be a uint8 tensor on cuda:%d" % dev)
     return workspace, workspace.numel()
 
 
@@ -593,17 +610,18 @@ def rms_norm_backward(dy, h, rstd, weight, dh=None, weight_grad=True, dx=None, d
     gradient dh that reaches h from elsewhere.  dx is the gradient of x and of
     the residual; dweight is fp32 (None without weight_grad).  workspace: at
     least fos_rms_norm_backward_workspace_bytes of uint8, allocated when None."""
-    R, C, dt, dev = _data(dy, "dy")
-    _like(h, "h", dy.shape, dy.dtype, dev)
+    shape, dt, dev = _data(dy, "dy")
+    R, C = shape
+    _like(h, "h", shape, dy.dtype, dev)
     _like(rstd, "rstd", (R,), torch.float32, dev)
     wdt = _weight(weight, C, dy.dtype, dev)
     if dh is not None:
-        _like(dh, "dh", dy.shape, dy.dtype, dev)
-    dx = torch.empty_like(dy) if dx is None else _like(dx, "dx", dy.shape, dy.dtype, dev)
+        _like(dh, "dh", shape, dy.dtype, dev)
+    dx = torch.empty_like(dy) if dx is None else _like(dx, "dx", shape, dy.dtype, dev)
     nws = 0
     if weight_grad:
         if dweight is None:
-            dweight = torch.empty(C, dtype=torch.float32, device=dev)
+            dweight = _new((C,), torch.float32, dev)
         else:
             _like(dweight, "dweight", (C,), torch.float32, dev)
         workspace, nws = _workspace(workspace, lib().fos_rms_norm_backward_workspace_bytes(R, C),
@@ -623,7 +641,7 @@ def quantize8(x, scale_tiled=True, rowwise=True, colwise=False, codes=None, scal
     (codes, scales, codes_t, scales_t); the first two are the rows of x (None
     without rowwise), the last two the rows of x.T padded with zeros to a
     multiple of 32 (None without colwise)."""
-    R, C, dt, dev = _data(x, "x")
+    (R, C), dt, dev = _data(x, "x")
     if rowwise:
         codes, scales = _pair8(R, C, scale_tiled, codes, scales, dev)
     else:
@@ -633,7 +651,7 @@ def quantize8(x, scale_tiled=True, rowwise=True, colwise=False, codes=None, scal
                                    ("codes_t", "scales_t"))
     else:
         codes_t = scales_t = None
-    _check(lib().fos_quantize8(x.data_ptr(), dt, R, C, int(bool(scale_tiled)), _a(codes),
+    _check(lib().fos_quantize8(x.data_ptr(), dt, R, C, 1 if scale_tiled else 0, _a(codes),
                                _a(scales), _a(codes_t), _a(scales_t), _stream(x)),
            "fos_quantize8")
     return codes, scales, codes_t, scales_t
@@ -647,10 +665,11 @@ def act_backward(dout, pre, act, scale_tiled=True, rowwise=True, colwise=True, v
     (colwise), d itself (value) and the fp32 sum of its columns (bias_grad);
     what is not asked for is None.  act: "none", "relu", "gelu", "gelu_tanh",
     "silu"; pre may be None with "none"."""
-    R, C, dt, dev = _data(dout, "dout")
+    shape, dt, dev = _data(dout, "dout")
+    R, C = shape
     a = _act(act)
     if pre is not None:
-        _like(pre, "pre", dout.shape, dout.dtype, dev)
+        _like(pre, "pre", shape, dout.dtype, dev)
     if rowwise:
         codes, scales = _pair8(R, C, scale_tiled, codes, scales, dev)
     else:
@@ -661,19 +680,19 @@ def act_backward(dout, pre, act, scale_tiled=True, rowwise=True, colwise=True, v
     else:
         codes_t = scales_t = None
     if value:
-        d = torch.empty_like(dout) if d is None else _like(d, "d", dout.shape, dout.dtype, dev)
+        d = torch.empty_like(dout) if d is None else _like(d, "d", shape, dout.dtype, dev)
     else:
         d = None
     nws = 0
     if bias_grad:
         if dbias is None:
-            dbias = torch.empty(C, dtype=torch.float32, device=dev)
+            dbias = _new((C,), torch.float32, dev)
         else:
             _like(dbias, "dbias", (C,), torch.float32, dev)
         workspace, nws = _workspace(workspace, lib().fos_act_backward_workspace_bytes(R, C), dev)
     else:
         dbias = workspace = None
-    _check(lib().fos_act_backward(dout.data_ptr(), _a(pre), dt, R, C, a, int(bool(scale_tiled)),
+    _check(lib().fos_act_backward(dout.data_ptr(), _a(pre), dt, R, C, a, 1 if scale_tiled else 0,
                                   _a(d), _a(codes), _a(scales), _a(codes_t), _a(scales_t),
                                   _a(dbias), _a(workspace), nws, _stream(dout)),
            "fos_act_backward")
@@ -683,17 +702,18 @@ def act_backward(dout, pre, act, scale_tiled=True, rowwise=True, colwise=True, v
 def _operand(codes, scales, name, blk, dev=None):
     """Checks a product operand's codes [rows, bytes] and flat tiled scales
     (blk elements per scale, 32 / blk elements per byte)."""
-    _cuda(codes, name + "_codes")
-    dev = dev or codes.device
-    if codes.dim() != 2 or codes.dtype != torch.uint8 or codes.device != dev:
-        raise ValueError("%s_codes must be a rank-2 uint8 tensor on %s" % (name, dev))
-    R, n = codes.shape
-    K = n * (32 // blk)
-    if not isinstance(scales, torch.Tensor) or scales.dtype != torch.uint8 or \
-            scales.device != dev or not scales.is_contiguous() or \
+    if not isinstance(codes, torch.Tensor) or not codes.is_cuda or not codes.is_contiguous():
+        _cuda(codes, name + "_codes")
+    on = codes.get_device()
+    shape = codes.shape
+    if len(shape) != 2 or codes.dtype is not torch.uint8 or (dev is not None and on != dev):
+        raise ValueError("%s_codes must be a rank-2 uint8 tensor on the product's device" % name)
+    R, K = shape[0], shape[1] * (32 // blk)
+    if scales.dtype is not torch.uint8 or scales.get_device() != on or \
+            not scales.is_contiguous() or \
             scales.numel() != (R + 127) // 128 * ((K + 4 * blk - 1) // (4 * blk)) * 512:
         raise ValueError("%s_scales must be the tiled uint8 scales of %s_codes" % (name, name))
-    return R, K, dev
+    return R, K, on
 
 
 def _epilogue(M, N, act, bias, residual, out_dtype, save_pre, out, pre, dev):
@@ -706,13 +726,13 @@ def _epilogue(M, N, act, bias, residual, out_dtype, save_pre, out, pre, dev):
     if residual is not None:
         _like(residual, "residual", (M, N), out_dtype, dev)
     if out is None:
-        out = torch.empty((M, N), dtype=out_dtype, device=dev)
+        out = _new((M, N), out_dtype, dev)
     else:
         _like(out, "out", (M, N), out_dtype, dev)
     if not save_pre:
         pre = None
     elif pre is None:
-        pre = torch.empty((M, N), dtype=out_dtype, device=dev)
+        pre = _new((M, N), out_dtype, dev)
     else:
         _like(pre, "pre", (M, N), out_dtype, dev)
     return FosEpilogue(_act(act), _DT[out_dtype], _DT[bias.dtype] if bias is not None else FOS_FP32,

@@ -83,11 +83,26 @@ __device__ __forceinline__ uint32_t idesc(int m, int n, int sf_id) {
            ((uint32_t)sf_id << 4) | ((uint32_t)sf_id << 29);
 }
 
+// Bounded wait of a whole converged warp: every lane gets the same answer, also
+// when the wait gives up.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
+    for (uint32_t i = 0; i < kMbarSpins; ++i) {
+        uint32_t done;
+        asm volatile("{\n\t.reg .pred p;\n\t"
+                     "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 1000;\n\t"
+                     "selp.u32 %0, 1, 0, p;\n\t}"
+                     : "=r"(done) : "r"(smem_u32(bar)), "r"(parity) : "memory");
+        if (__all_sync(0xFFFFFFFFu, done != 0)) return true;
+    }
+    return false;
+}
+
 // One lane of the warp, the same one each time: the warp's loops run converged
 // (their values stay in uniform registers, where the tensor instructions take
 // their operands from) and only the issue itself is one lane's.
 __device__ __forceinline__ bool elect_lane() {
     uint32_t p;
+    __syncwarp();  // a diverged warp would elect a lane in each part
     asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}"
                  : "=r"(p));
     return p != 0;
@@ -189,7 +204,8 @@ __device__ __forceinline__ void act_apply(int act, float (&v)[kN]) {
 // of a cluster, whose fp32 partial tiles meet in shared memory: CTA r adds
 // tokens r, r + S, ... of all S partials, read through the cluster's
 // distributed shared memory in rank order (one fixed order of the sum).
-//   warp 0    TMA producer (one thread): b tile, a tile, scale tiles of a stage
+//   warp 0    TMA producer of a stage's b tile and a tile
+//   warp 6    bulk-copy producer of its scale tiles
 //   warp 1    tensor memory; one thread copies scales and issues the MMAs
 //   warps 2-5 epilogue: lane quadrant warp % 4 of the accumulator
 // The scales of stage g go to ring buffer g % 4 of the tensor memory, after
@@ -203,7 +219,7 @@ struct RowsArgs {
     const uint8_t* sfq;  // a scales, tiled
     Epilogue ep;
     int64_t M, N;
-    int64_t tiles;       // tiles_p * tiles_q
+    int tiles;           // tiles_p * tiles_q
     int kb;              // scale tiles along K (4 blocks each)
     int nkb;             // stages along K
     int tiles_p;
@@ -212,7 +228,7 @@ struct RowsArgs {
     int stages;
 };
 
-constexpr int kRowsThreads = 192;
+constexpr int kRowsThreads = 224;
 constexpr int kMaxStages = 12;
 constexpr int kSfRing = 4;
 constexpr uint32_t kAllColumns = 512;
@@ -286,23 +302,21 @@ __device__ __forceinline__ void rows_stage(uint32_t acc, uint32_t p0, uint32_t q
     }
 }
 
-// The epilogue of kN tokens m, m + dm, ... (the first cnt of them) at weight
-// row n.
-template <class F, Out OT, int kN>
-__device__ __forceinline__ void finish_rows(const Epilogue& e, float (&v)[kN], int64_t m, int dm,
-                                            int cnt, int64_t N, int64_t n, float ga0, float gb,
-                                            float bias) {
+// The residuals of kN tokens from `at` on, dat apart (the first cnt of them).
+template <Out OT, int kN>
+__device__ __forceinline__ void load_residual(const Epilogue& e, int64_t at, int64_t dat, int cnt,
+                                              float (&r)[kN]) {
 #pragma unroll
-    for (int i = 0; i < kN; ++i) {
-        if constexpr (F::kGlobal) {
-            float ga = ga0;
-            if (e.a_row && i < cnt)
-                ga = fdiv(1.0f, global_scale(__ldg(e.a_amax + m + i * dm), e.six_bound));
-            v[i] = fmul(fmul(v[i], ga), gb);
-        }
-        v[i] = fadd(v[i], bias);
-    }
-    const int64_t at = m * N + n, dat = (int64_t)dm * N;
+    for (int i = 0; i < kN; ++i) r[i] = e.residual && i < cnt ? load_out<OT>(e.residual, at + i * dat) : 0.0f;
+}
+
+// The epilogue of kN tokens of one weight row, their scaled sums in v: stores
+// at `at`, dat apart (the first cnt of them).
+template <Out OT, int kN>
+__device__ __forceinline__ void finish_rows(const Epilogue& e, float (&v)[kN], const float (&r)[kN],
+                                            int64_t at, int64_t dat, int cnt, float bias) {
+#pragma unroll
+    for (int i = 0; i < kN; ++i) v[i] = fadd(v[i], bias);
     if (e.pre) {
 #pragma unroll
         for (int i = 0; i < kN; ++i)
@@ -310,9 +324,6 @@ __device__ __forceinline__ void finish_rows(const Epilogue& e, float (&v)[kN], i
     }
     act_apply(e.act, v);
     if (e.residual) {
-        float r[kN];
-#pragma unroll
-        for (int i = 0; i < kN; ++i) r[i] = i < cnt ? load_out<OT>(e.residual, at + i * dat) : 0.0f;
 #pragma unroll
         for (int i = 0; i < kN; ++i) v[i] = fadd(v[i], r[i]);
     }
@@ -321,10 +332,14 @@ __device__ __forceinline__ void finish_rows(const Epilogue& e, float (&v)[kN], i
         if (i < cnt) store_out<OT>(e.out, at + i * dat, v[i]);
 }
 
+// Barrier of the four epilogue warps.
+__device__ __forceinline__ void epilogue_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+
 template <class F, Out OT>
 __global__ void __launch_bounds__(kRowsThreads, 1) k_linear_rows(const __grid_constant__ RowsArgs a) {
     extern __shared__ __align__(1024) unsigned char s_raw[];
     __shared__ RowsShared sh;
+    __shared__ float s_ga[F::kGlobal ? 256 : 1];  // the tokens' decode scales
     unsigned char* base = s_raw + ((1024u - (smem_u32(s_raw) & 1023u)) & 1023u);
     const int nt = a.nt, S = a.splits, qa = rows_q_atoms<F>(nt), ns = a.stages;
     const int qbytes = nt * kRowBytes;
@@ -336,18 +351,19 @@ __global__ void __launch_bounds__(kRowsThreads, 1) k_linear_rows(const __grid_co
     float* red = reinterpret_cast<float*>(base);  // [nt][128] partial tile, over the ring
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = S > 1 ? (int)cluster_rank() : 0;
-    const int64_t first = blockIdx.x / S, step = gridDim.x / S;
+    const int first = (int)blockIdx.x / S, step = (int)gridDim.x / S;
     // this CTA's stages of every tile
-    const int k_lo = (int)((int64_t)a.nkb * rank / S), k_hi = (int)((int64_t)a.nkb * (rank + 1) / S);
-    if (threadIdx.x == 0) {
-        for (int s = 0; s < ns; ++s) {
-            bar_init(&sh.full[s], 1);
-            bar_init(&sh.empty[s], 1);
+    const int k_lo = a.nkb * rank / S, k_hi = a.nkb * (rank + 1) / S;
+    if (warp == 0) {
+        if (lane < ns) {
+            bar_init(&sh.full[lane], 2);
+            bar_init(&sh.empty[lane], 1);
+        } else if (lane == 31) {
+            bar_init(&sh.acc_full, 1);
+            bar_init(&sh.acc_empty, 4);
+            bar_init(&sh.done, 1);
+            sh.fail = 0;
         }
-        bar_init(&sh.acc_full, 1);
-        bar_init(&sh.acc_empty, 4);
-        bar_init(&sh.done, 1);
-        sh.fail = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     chain_wait();
@@ -358,50 +374,70 @@ __global__ void __launch_bounds__(kRowsThreads, 1) k_linear_rows(const __grid_co
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
     tc_fence_before();
+    __syncwarp();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = sh.tmem;
-    uint32_t g = 0;   // stages issued (warp 0) or consumed (warp 1) so far
+    uint32_t g = 0;   // stages loaded (warps 0, 6) or consumed (warp 1) so far
     Ring r, w;        // the stage in work; warp 1: the one whose scales are overwritten
     const bool elected = elect_lane();
     bool bad = false;
     int j = 0;        // tiles of this CTA so far
-    for (int64_t t = first; t < a.tiles; t += step, ++j) {
-        const int64_t n0 = (t % a.tiles_p) * 128, m0 = (t / a.tiles_p) * nt;
+    for (int t = first; t < a.tiles; t += step, ++j) {
+        const int tq = t / a.tiles_p;
+        const int n0 = (t - tq * a.tiles_p) * 128, m0 = tq * nt;
         if (warp == 0) {
-            if (lane == 0 && !bad) {
-                for (int i = k_lo; i < k_hi; ++i, ++g, r.next(ns)) {
-                    const int s = r.slot;
-                    if (g >= (uint32_t)ns && !mbar_wait(&sh.empty[s], r.parity ^ 1u)) {
-                        bad = true;
-                        break;
-                    }
-                    const int nk = min(F::kSfTiles, a.kb - F::kSfTiles * i);
-                    mbar_expect_tx(&sh.full[s], (uint32_t)(kPBytes + qbytes +
-                                                           (1 + qa) * nk * kSfTileBytes));
-                    tma_load_2d(sP + s * kPBytes, &a.tp, i * kRowBytes, (int32_t)n0, &sh.full[s]);
-                    tma_load_2d(sQ + s * qbytes, &a.tq, i * kRowBytes, (int32_t)m0, &sh.full[s]);
-                    bulk_load(sFP + s * kSfP,
-                              a.sfp + ((n0 / 128) * a.kb + F::kSfTiles * i) * kSfTileBytes,
-                              (uint32_t)(nk * kSfTileBytes), &sh.full[s]);
-                    for (int q = 0; q < qa; ++q) {
-                        // token tiles past the end of a have no scale tile: any
-                        // finite scales do (their codes are zeros)
-                        const int64_t qt = min(m0 / 128 + q, (a.M + 127) / 128 - 1);
-                        bulk_load(sFQ + (s * qa + q) * kSfP,
-                                  a.sfq + (qt * a.kb + F::kSfTiles * i) * kSfTileBytes,
-                                  (uint32_t)(nk * kSfTileBytes), &sh.full[s]);
-                    }
+            for (int i = k_lo; i < k_hi && !bad; ++i) {
+                const int s = r.slot;
+                if (g >= (uint32_t)ns && !warp_wait(&sh.empty[s], r.parity ^ 1u)) {
+                    bad = true;
+                    break;
                 }
+                unsigned char *dp = sP + s * kPBytes, *dq = sQ + s * qbytes;
+                if (elected) {
+                    mbar_expect_tx(&sh.full[s], (uint32_t)(kPBytes + qbytes));
+                    tma_load_2d(dp, &a.tp, i * kRowBytes, n0, &sh.full[s]);
+                    tma_load_2d(dq, &a.tq, i * kRowBytes, m0, &sh.full[s]);
+                }
+                __syncwarp();
+                ++g;
+                r.next(ns);
             }
-            __syncwarp();
+        } else if (warp == 6) {
+            const uint8_t* pp = a.sfp + ((int64_t)(n0 >> 7) * a.kb + F::kSfTiles * k_lo) * kSfTileBytes;
+            // token tiles past the end of a have no scale tile: any finite
+            // scales do (their codes are zeros)
+            const int last = (int)((a.M + 127) >> 7) - 1, q0 = m0 >> 7;
+            const uint8_t* pq0 = a.sfq + ((int64_t)q0 * a.kb + F::kSfTiles * k_lo) * kSfTileBytes;
+            const uint8_t* pq1 = a.sfq + ((int64_t)min(q0 + 1, last) * a.kb + F::kSfTiles * k_lo) * kSfTileBytes;
+            for (int i = k_lo; i < k_hi && !bad; ++i) {
+                const int s = r.slot;
+                if (g >= (uint32_t)ns && !warp_wait(&sh.empty[s], r.parity ^ 1u)) {
+                    bad = true;
+                    break;
+                }
+                const uint32_t bytes = (uint32_t)(min(F::kSfTiles, a.kb - F::kSfTiles * i) * kSfTileBytes);
+                unsigned char *dp = sFP + s * kSfP, *dq = sFQ + s * qa * kSfP;
+                if (elected) {
+                    mbar_expect_tx(&sh.full[s], (1 + qa) * bytes);
+                    bulk_load(dp, pp, bytes, &sh.full[s]);
+                    bulk_load(dq, pq0, bytes, &sh.full[s]);
+                    if (qa == 2) bulk_load(dq + kSfP, pq1, bytes, &sh.full[s]);
+                }
+                __syncwarp();
+                pp += kSfP;
+                pq0 += kSfP;
+                pq1 += kSfP;
+                ++g;
+                r.next(ns);
+            }
         } else if (warp == 1) {
-            if (!bad && j >= 1 && S == 1 && !mbar_wait(&sh.acc_empty, (uint32_t)(j - 1) & 1)) bad = true;
+            if (!bad && j >= 1 && S == 1 && !warp_wait(&sh.acc_empty, (uint32_t)(j - 1) & 1)) bad = true;
             tc_fence_after();
             for (int i = k_lo; i < k_hi && !bad; ++i) {
                 const int s = r.slot;
-                if (!mbar_wait(&sh.full[s], r.parity) ||
-                    (g >= (uint32_t)kSfRing && !mbar_wait(&sh.empty[w.slot], w.parity))) {
+                if (!warp_wait(&sh.full[s], r.parity) ||
+                    (g >= (uint32_t)kSfRing && !warp_wait(&sh.empty[w.slot], w.parity))) {
                     bad = true;
                     break;
                 }
@@ -430,80 +466,118 @@ __global__ void __launch_bounds__(kRowsThreads, 1) k_linear_rows(const __grid_co
             const int q = warp & 3;
             const int nl = 32 * q + lane;            // weight row of the tile
             const int64_t n = n0 + nl;
-            const int mt = (int)min((int64_t)nt, a.M - m0);
-            if (!bad && !mbar_wait(&sh.acc_full, (uint32_t)j & 1)) bad = true;
-            __syncwarp();
-            tc_fence_after();
-            const uint32_t lane_base = tmem + ((uint32_t)(32 * q) << 16);
+            const int mt = min(nt, (int)a.M - m0);
             const bool nin = n < a.N;
-            float gb = 1.0f, ga0 = 1.0f, bias = 0.0f;
-            if constexpr (F::kGlobal) {
-                gb = fdiv(1.0f, global_scale(a.ep.b_amax[0], a.ep.six_bound));
-                if (!a.ep.a_row) ga0 = fdiv(1.0f, global_scale(a.ep.a_amax[0], a.ep.six_bound));
-            }
+            float bias = 0.0f;
             if (a.ep.bias && nin)
                 bias = a.ep.bias32 ? __ldg(static_cast<const float*>(a.ep.bias) + n)
                                    : load_out<OT>(a.ep.bias, n);
-            for (int c0 = 0; c0 < mt; c0 += 16) {
-                uint32_t v[16];
-                tmem_ld16(lane_base + (uint32_t)c0, v);
-                if (S > 1) {
+            float gb = 1.0f;
+            if constexpr (F::kGlobal) {
+                // the tokens' decode scales, once per tile
+                gb = fdiv(1.0f, global_scale(a.ep.b_amax[0], a.ep.six_bound));
+                epilogue_sync();  // the tile before has read its own
+                for (int c = nl; c < mt; c += 128)
+                    s_ga[c] = fdiv(1.0f, global_scale(__ldg(a.ep.a_amax + (a.ep.a_row ? m0 + c : 0)),
+                                                      a.ep.six_bound));
+                epilogue_sync();
+            }
+            if (!bad && !warp_wait(&sh.acc_full, (uint32_t)j & 1)) bad = true;
+            __syncwarp();
+            tc_fence_after();
+            const uint32_t lane_base = tmem + ((uint32_t)(32 * q) << 16);
+            if (S > 1) {
+                for (int c0 = 0; c0 < mt; c0 += 16) {
+                    uint32_t v[16];
+                    tmem_ld16(lane_base + (uint32_t)c0, v);
 #pragma unroll
                     for (int i = 0; i < 16; ++i)
                         if (c0 + i < mt) red[(c0 + i) * 128 + nl] = __uint_as_float(v[i]);
-                } else if (nin) {
-                    float f[16];
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) f[i] = __uint_as_float(v[i]);
-                    finish_rows<F, OT>(a.ep, f, m0 + c0, 1, mt - c0, a.N, n, ga0, gb, bias);
                 }
-                __syncwarp();
-            }
-            if (S == 1) {
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) bar_arrive(&sh.acc_empty);
-            } else {
-                tc_fence_before();
                 cluster_sync();  // every partial of the tile is written
                 if (nin) {
+                    // four tokens at a time, all of their loads in flight
                     for (int c = rank; c < mt; c += 4 * S) {
-                        // four tokens at a time: 4 S loads in flight
                         const int cnt = (mt - c + S - 1) / S;
-                        float f[4];
+                        const int64_t at = (int64_t)(m0 + c) * a.N + n, dat = (int64_t)S * a.N;
+                        float f[4], rs[4], p[4][8];
+                        load_residual<OT>(a.ep, at, dat, cnt, rs);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+#pragma unroll
+                            for (int k = 0; k < 8; ++k)
+                                if (k < S && i < cnt)
+                                    p[i][k] = ld_cluster(smem_u32(red + (c + i * S) * 128 + nl), (uint32_t)k);
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
-                            const uint32_t at = smem_u32(red + (i < cnt ? c + i * S : c) * 128 + nl);
-                            f[i] = ld_cluster(at, 0u);
-                            for (int k = 1; k < S; ++k) f[i] = fadd(f[i], ld_cluster(at, (uint32_t)k));
+                            f[i] = p[i][0];
+#pragma unroll
+                            for (int k = 1; k < 8; ++k)
+                                if (k < S) f[i] = fadd(f[i], p[i][k]);
+                            if constexpr (F::kGlobal)
+                                f[i] = fmul(fmul(f[i], s_ga[i < cnt ? c + i * S : c]), gb);
                         }
-                        finish_rows<F, OT>(a.ep, f, m0 + c, S, cnt, a.N, n, ga0, gb, bias);
+                        finish_rows<OT>(a.ep, f, rs, at, dat, cnt, bias);
                     }
                 }
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 __syncwarp();
                 cluster_sync();  // every partial has been read: the ring is free again
+            } else {
+                for (int c0 = 0; c0 < mt; c0 += 16) {
+                    uint32_t v[16];
+                    tmem_ld16(lane_base + (uint32_t)c0, v);
+                    if (nin) {
+                        const int64_t at = (int64_t)(m0 + c0) * a.N + n;
+                        float f[16], rs[16];
+                        load_residual<OT>(a.ep, at, a.N, mt - c0, rs);
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            f[i] = __uint_as_float(v[i]);
+                            if constexpr (F::kGlobal)
+                                f[i] = fmul(fmul(f[i], s_ga[min(c0 + i, mt - 1)]), gb);
+                        }
+                        finish_rows<OT>(a.ep, f, rs, at, a.N, mt - c0, bias);
+                    }
+                    __syncwarp();
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) bar_arrive(&sh.acc_empty);
+                __syncwarp();
             }
         }
-        if (S > 1 && warp < 2) {
+        if (S > 1 && (warp < 2 || warp == 6)) {
+            __syncwarp();
             cluster_sync();
             cluster_sync();
             tc_fence_after();
         }
     }
     // drain: every copy and MMA issued has completed before the CTA leaves
-    if (warp == 0 && lane == 0) {
-        for (uint32_t s = 0; s < (uint32_t)ns; ++s)
-            if (g > s && !mbar_wait(&sh.full[s], ((g - 1 - s) / ns) & 1)) bad = true;
+    if (warp == 0) {
+        for (int k = 0; k < ns && (uint32_t)k < g; ++k) {
+            int sl = r.slot - 1 - k;
+            uint32_t p = r.parity;
+            if (sl < 0) {
+                sl += ns;
+                p ^= 1u;
+            }
+            if (!warp_wait(&sh.full[sl], p)) bad = true;
+        }
     } else if (warp == 1) {
         if (elected) tc_commit(&sh.done);
-        if (!mbar_wait(&sh.done, 0)) bad = true;
+        __syncwarp();  // no lane waits before the elected one has asked
+        if (!warp_wait(&sh.done, 0)) bad = true;
     }
     if (bad) sh.fail = 1;
     tc_fence_before();
+    __syncwarp();
     __syncthreads();
     if (sh.fail && threadIdx.x == 0 && first < a.tiles)
-        store_out<OT>(a.ep.out, (first / a.tiles_p) * nt * a.N + (first % a.tiles_p) * 128,
+        store_out<OT>(a.ep.out, (int64_t)(first / a.tiles_p) * nt * a.N + (first % a.tiles_p) * 128,
                       __int_as_float(0x7FC00000));
     if (warp == 1) {
         tc_fence_after();

@@ -112,14 +112,14 @@ __device__ __forceinline__ void pair_commit(uint64_t* bar) {
         "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
         "[%0], %1;" ::"r"(smem_u32(bar)), "h"((unsigned short)3) : "memory");
 }
-// Whether a phase has completed, without waiting.
+// Whether a phase has completed, without waiting (a whole converged warp).
 __device__ __forceinline__ bool mbar_ask(uint64_t* bar, uint32_t parity) {
     uint32_t done;
     asm volatile("{\n\t.reg .pred p;\n\t"
                  "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
                  "selp.u32 %0, 1, 0, p;\n\t}"
                  : "=r"(done) : "r"(smem_u32(bar)), "r"(parity) : "memory");
-    return done != 0;
+    return __all_sync(0xFFFFFFFFu, done != 0);
 }
 // Arrival at a barrier of another CTA (its cluster address).  The default
 // release is that of the CTA: what is published is in tensor memory, complete
@@ -287,7 +287,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_linear_pair(const __grid_co
             const int32_t am = m0 + 128 * rank, bn = n0 + 96 * rank;
             for (int i = 0; i < a.nkb; ++i) {
                 const int s = r.slot;
-                if (g >= (uint32_t)ns && !mbar_wait(&sh.empty[s], r.parity ^ 1u)) {
+                if (g >= (uint32_t)ns && !warp_wait(&sh.empty[s], r.parity ^ 1u)) {
                     bad = true;
                     break;
                 }
@@ -312,7 +312,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_linear_pair(const __grid_co
                 s += ns;
                 p ^= 1u;
             }
-            if (!mbar_wait(&sh.empty[s], p)) bad = true;
+            if (!warp_wait(&sh.empty[s], p)) bad = true;
         }
     } else if (warp == 1) {
         if (rank == 0) {
@@ -321,7 +321,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_linear_pair(const __grid_co
             int j = 0;
             for (int t = first; t < tiles && !bad; t += step, ++j) {
                 const int ab = j & 1;
-                if (j >= 2 && !mbar_wait(&sh.acc_empty[ab], (uint32_t)((j >> 1) - 1) & 1)) {
+                if (j >= 2 && !warp_wait(&sh.acc_empty[ab], (uint32_t)((j >> 1) - 1) & 1)) {
                     bad = true;
                     break;
                 }
@@ -329,8 +329,8 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_linear_pair(const __grid_co
                 bool here = false;  // the stage is known to be full
                 for (int i = 0; i < a.nkb; ++i) {
                     const int s = r.slot, in_chunk = i % chunk_stages<F>();
-                    if ((in_chunk == 0 && !mbar_wait(&sh.sf_ready[f.slot], f.parity)) ||
-                        (!here && !mbar_wait(&sh.full[s], r.parity))) {
+                    if ((in_chunk == 0 && !warp_wait(&sh.sf_ready[f.slot], f.parity)) ||
+                        (!here && !warp_wait(&sh.full[s], r.parity))) {
                         bad = true;
                         break;
                     }
@@ -367,7 +367,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_linear_pair(const __grid_co
             pair_tile(a, t, m0, n0);
             const int32_t ra = (m0 + 128 * rank) >> 7, rb = n0 >> 7;
             for (int k = 0; k < a.kb; k += kSfChunkTiles) {
-                if (chunks >= (uint32_t)kSfSlots && !mbar_wait(&sh.sf_empty[f.slot], f.parity ^ 1u)) {
+                if (chunks >= (uint32_t)kSfSlots && !warp_wait(&sh.sf_empty[f.slot], f.parity ^ 1u)) {
                     bad = true;
                     break;
                 }
@@ -390,7 +390,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_linear_pair(const __grid_co
                 sl += kSfSlots;
                 p ^= 1u;
             }
-            if (!mbar_wait(&sh.sf_empty[sl], p)) bad = true;
+            if (!warp_wait(&sh.sf_empty[sl], p)) bad = true;
         }
     } else if (warp < 6) {
         // scales: lane l of quadrant q writes row l of each 16-byte-wide tile,
@@ -405,7 +405,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_linear_pair(const __grid_co
             pair_tile(a, t, m0, n0);
             const bool half = (n0 & 127) != 0;  // b starts half-way into a scale tile
             for (int i = 0; i < a.nkb; i += chunk_stages<F>()) {
-                if (!mbar_wait(&sh.sf_full[f.slot], f.parity)) {
+                if (!warp_wait(&sh.sf_full[f.slot], f.parity)) {
                     bad = true;
                     break;
                 }
@@ -426,7 +426,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_linear_pair(const __grid_co
                 }
                 __syncwarp();
                 if (lane == 0) bar_arrive(&sh.sf_empty[f.slot]);
-                if (chunks >= (uint32_t)kSfBufs && !mbar_wait(&sh.sf_free[d.slot], d.parity ^ 1u)) {
+                if (chunks >= (uint32_t)kSfBufs && !warp_wait(&sh.sf_free[d.slot], d.parity ^ 1u)) {
                     bad = true;
                     break;
                 }
@@ -496,12 +496,12 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_linear_pair(const __grid_co
                 }
             }
             const int ab = j & 1;
-            if (!bad && !mbar_wait(&sh.acc_full[ab], (uint32_t)(j >> 1) & 1)) bad = true;
+            if (!bad && !warp_wait(&sh.acc_full[ab], (uint32_t)(j >> 1) & 1)) bad = true;
             __syncwarp();
             tc_fence_after();
             for (int k = 0; k < kChunks; ++k, ++c) {
                 const uint32_t buf = smem_u32(bufs + (c & 1) * slot_bytes);
-                if (res && !bad && !mbar_wait(&sh.res_full[e][c & 1], (uint32_t)(c >> 1) & 1)) bad = true;
+                if (res && !bad && !warp_wait(&sh.res_full[e][c & 1], (uint32_t)(c >> 1) & 1)) bad = true;
                 __syncwarp();
 #pragma unroll
                 for (int h = 0; h < kCols / 32; ++h) {
@@ -553,9 +553,10 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_linear_pair(const __grid_co
         __syncwarp();
     }
     // every MMA issued has completed before the tensor memory is freed
-    if (warp == 1 && !mbar_wait(&sh.done, 0)) bad = true;
+    if (warp == 1 && !warp_wait(&sh.done, 0)) bad = true;
     if (bad) sh.fail = 1;
     tc_fence_before();
+    __syncwarp();
     __syncthreads();
     cluster_sync();  // neither CTA leaves while the other may touch its memory
     if (sh.fail && threadIdx.x == 0 && first < tiles) {

@@ -85,13 +85,13 @@ cudaError_t rows_go(const LinearCall& c, cudaStream_t s) {
     a.kb = (int)((c.K + blk4 - 1) / blk4);
     a.nkb = (a.kb + F::kSfTiles - 1) / F::kSfTiles;
     a.tiles_p = (int)((c.N + 127) / 128);
-    a.tiles = (int64_t)a.tiles_p * ((c.M + a.nt - 1) / a.nt);
+    a.tiles = a.tiles_p * (int)((c.M + a.nt - 1) / a.nt);
     const int stage = rows_stage_bytes<F>(a.nt);
-    a.stages = (kSmemLimit - 2048) / stage;
+    a.stages = (kSmemLimit - 3072) / stage;
     if (a.stages > kMaxStages) a.stages = kMaxStages;
     const int smem = a.stages * stage + 1024;
     auto k = k_linear_rows<F, OT>;
-    cudaError_t e = allow_smem(reinterpret_cast<const void*>(k), (size_t)kSmemLimit - 1024);
+    cudaError_t e = allow_smem(reinterpret_cast<const void*>(k), (size_t)kSmemLimit - 2048);
     if (e != cudaSuccess) return e;
     // the split of K that needs the fewest rounds of the device, counted in
     // whole-K tiles; every CTA keeps at least two stages
@@ -108,7 +108,7 @@ cudaError_t rows_go(const LinearCall& c, cudaStream_t s) {
         }
     }
     a.splits = best;
-    if (clusters > a.tiles) clusters = (int)a.tiles;
+    if (clusters > a.tiles) clusters = a.tiles;
     return launch_clusters(k, clusters, best, kRowsThreads, smem, a, s);
 }
 
