@@ -97,6 +97,19 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
     return false;
 }
 
+// Whether a phase has completed, without waiting: asked a stage ahead, so that
+// the answer is there when it is needed (a wait for a phase long complete
+// still takes about 170 cycles, a stage's seven instructions 300).
+__device__ __forceinline__ bool mbar_ask(uint64_t* bar, uint32_t parity) {
+    uint32_t done;
+    asm volatile("{\n\t.reg .pred p;\n\t"
+                 "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+                 "selp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(done) : "r"(smem_u32(bar)), "r"(parity) : "memory");
+    return done != 0;
+}
+__device__ __forceinline__ bool warp_agrees(bool v) { return __all_sync(0xFFFFFFFFu, v); }
+
 // One lane of the warp, the same one each time: the warp's loops run converged
 // (their values stay in uniform registers, where the tensor instructions take
 // their operands from) and only the issue itself is one lane's.
@@ -382,6 +395,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1) k_linear_rows(const __grid_co
     Ring r, w;        // the stage in work; warp 1: the one whose scales are overwritten
     const bool elected = elect_lane();
     bool bad = false;
+    bool here = false, free = false;  // warp 1: the next stage is full, its scale buffer is free
     int j = 0;        // tiles of this CTA so far
     for (int t = first; t < a.tiles; t += step, ++j) {
         const int tq = t / a.tiles_p;
@@ -436,12 +450,16 @@ __global__ void __launch_bounds__(kRowsThreads, 1) k_linear_rows(const __grid_co
             tc_fence_after();
             for (int i = k_lo; i < k_hi && !bad; ++i) {
                 const int s = r.slot;
-                if (!warp_wait(&sh.full[s], r.parity) ||
-                    (g >= (uint32_t)kSfRing && !warp_wait(&sh.empty[w.slot], w.parity))) {
+                const bool over = g >= (uint32_t)kSfRing;  // a scale buffer is used again
+                if ((!warp_agrees(here) && !warp_wait(&sh.full[s], r.parity)) ||
+                    (over && !warp_agrees(free) && !warp_wait(&sh.empty[w.slot], w.parity))) {
                     bad = true;
                     break;
                 }
-                if (g >= (uint32_t)kSfRing) w.next(ns);
+                if (over) w.next(ns);
+                r.next(ns);
+                here = mbar_ask(&sh.full[r.slot], r.parity);
+                free = mbar_ask(&sh.empty[w.slot], w.parity);
                 tc_fence_after();
                 const int nk = min(F::kSfTiles, a.kb - F::kSfTiles * i);
                 const uint32_t sfp = tmem + 256 + (g % kSfRing) * 48, sfq = sfp + 4 * F::kSfTiles;
@@ -458,7 +476,6 @@ __global__ void __launch_bounds__(kRowsThreads, 1) k_linear_rows(const __grid_co
                 }
                 __syncwarp();
                 ++g;
-                r.next(ns);
             }
             if (!bad && elected) tc_commit(&sh.acc_full);
             __syncwarp();

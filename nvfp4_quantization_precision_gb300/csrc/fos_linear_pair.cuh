@@ -112,15 +112,6 @@ __device__ __forceinline__ void pair_commit(uint64_t* bar) {
         "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
         "[%0], %1;" ::"r"(smem_u32(bar)), "h"((unsigned short)3) : "memory");
 }
-// Whether a phase has completed, without waiting (a whole converged warp).
-__device__ __forceinline__ bool mbar_ask(uint64_t* bar, uint32_t parity) {
-    uint32_t done;
-    asm volatile("{\n\t.reg .pred p;\n\t"
-                 "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-                 "selp.u32 %0, 1, 0, p;\n\t}"
-                 : "=r"(done) : "r"(smem_u32(bar)), "r"(parity) : "memory");
-    return __all_sync(0xFFFFFFFFu, done != 0);
-}
 // Arrival at a barrier of another CTA (its cluster address).  The default
 // release is that of the CTA: what is published is in tensor memory, complete
 // and fenced.  Released to the cluster instead, each arrival took 1300 cycles.
@@ -318,6 +309,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_linear_pair(const __grid_co
         if (rank == 0) {
             const bool elected = elect_lane();
             Ring r, f;      // stages; scale buffers
+            bool here = false, scaled = false;  // the next stage is full, its scales are there
             int j = 0;
             for (int t = first; t < tiles && !bad; t += step, ++j) {
                 const int ab = j & 1;
@@ -326,18 +318,18 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_linear_pair(const __grid_co
                     break;
                 }
                 const uint32_t acc = tmem + (uint32_t)(ab * kPairN);
-                bool here = false;  // the stage is known to be full
                 for (int i = 0; i < a.nkb; ++i) {
                     const int s = r.slot, in_chunk = i % chunk_stages<F>();
-                    if ((in_chunk == 0 && !warp_wait(&sh.sf_ready[f.slot], f.parity)) ||
-                        (!here && !warp_wait(&sh.full[s], r.parity))) {
+                    if ((in_chunk == 0 && !warp_agrees(scaled) && !warp_wait(&sh.sf_ready[f.slot], f.parity)) ||
+                        (!warp_agrees(here) && !warp_wait(&sh.full[s], r.parity))) {
                         bad = true;
                         break;
                     }
-                    // asks for the next stage now: the answer is there by the
-                    // time this stage's instructions are out
                     r.next(ns);
-                    here = i + 1 < a.nkb && mbar_ask(&sh.full[r.slot], r.parity);
+                    here = mbar_ask(&sh.full[r.slot], r.parity);
+                    if (in_chunk == chunk_stages<F>() - 1 || i + 1 == a.nkb)
+                        scaled = mbar_ask(&sh.sf_ready[f.slot + 1 == kSfBufs ? 0 : f.slot + 1],
+                                          f.slot + 1 == kSfBufs ? f.parity ^ 1u : f.parity);
                     tc_fence_after();
                     const int nk = min(F::kSfTiles, a.kb - F::kSfTiles * i);
                     const uint32_t a0 = desc_lo(smem_u32(sA) + s * kPairABytes);
