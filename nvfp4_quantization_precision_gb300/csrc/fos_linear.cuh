@@ -108,6 +108,10 @@ __device__ __forceinline__ bool mbar_ask(uint64_t* bar, uint32_t parity) {
                  : "=r"(done) : "r"(smem_u32(bar)), "r"(parity) : "memory");
     return done != 0;
 }
+// Lane 0's value for the whole warp: the compiler then knows it is uniform and
+// keeps what follows from it (addresses, descriptors, loop counts) in uniform
+// registers, which the tensor instructions read.
+__device__ __forceinline__ uint32_t uniform(uint32_t v) { return __shfl_sync(0xFFFFFFFFu, v, 0); }
 __device__ __forceinline__ bool warp_agrees(bool v) { return __all_sync(0xFFFFFFFFu, v); }
 
 // One lane of the warp, the same one each time: the warp's loops run converged
@@ -362,8 +366,8 @@ __global__ void __launch_bounds__(kRowsThreads, 1) k_linear_rows(const __grid_co
     unsigned char* sFP = sQ + ns * qbytes;
     unsigned char* sFQ = sFP + ns * kSfP;
     float* red = reinterpret_cast<float*>(base);  // [nt][128] partial tile, over the ring
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int rank = S > 1 ? (int)cluster_rank() : 0;
+    const int warp = (int)uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
+    const int rank = S > 1 ? (int)uniform(cluster_rank()) : 0;
     const int first = (int)blockIdx.x / S, step = (int)gridDim.x / S;
     // this CTA's stages of every tile
     const int k_lo = a.nkb * rank / S, k_hi = a.nkb * (rank + 1) / S;
@@ -390,7 +394,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1) k_linear_rows(const __grid_co
     __syncwarp();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = sh.tmem;
+    const uint32_t tmem = uniform(sh.tmem);
     uint32_t g = 0;   // stages loaded (warps 0, 6) or consumed (warp 1) so far
     Ring r, w;        // the stage in work; warp 1: the one whose scales are overwritten
     const bool elected = elect_lane();

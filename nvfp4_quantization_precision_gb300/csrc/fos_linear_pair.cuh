@@ -227,8 +227,8 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_linear_pair(const __grid_co
     unsigned char* sB = sA + ns * kPairABytes;
     unsigned char* sC = sB + ns * kPairBBytes;       // epilogue chunks
     unsigned char* sS = sC + 4 * a.bufs * kChunkBytes;  // scale chunks: a, then b's two row tiles
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int rank = (int)cluster_rank();
+    const int warp = (int)uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
+    const int rank = (int)uniform(cluster_rank());
     const int tiles = a.tiles_m * a.tiles_n;
     const int first = (int)(blockIdx.x >> 1), step = (int)(gridDim.x >> 1);
     if (threadIdx.x == 0) {
@@ -265,7 +265,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_linear_pair(const __grid_co
     __syncthreads();
     cluster_sync();  // both CTAs' barriers are set up
     tc_fence_after();
-    const uint32_t tmem = sh.tmem;
+    const uint32_t tmem = uniform(sh.tmem);
     bool bad = false;
     if (warp == 0) {
         const bool elected = elect_lane();
