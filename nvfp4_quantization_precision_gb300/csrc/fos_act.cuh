@@ -10,21 +10,11 @@
 // cancellation of 1 + tanh(u) on the negative side.
 #pragma once
 
-#include "fos_device.cuh"
+#include "fos_block8.cuh"
 
 namespace fos {
 
 enum class Act : int { NONE = 0, RELU = 1, GELU = 2, GELU_TANH = 3, SILU = 4 };
-
-// 1 / (1 + exp(-z)): the reciprocal approximation and one Newton step (the
-// step is skipped where the sum has overflowed and the reciprocal is 0).
-__device__ __forceinline__ float sigmoid(float z) {
-    const float x = fadd(1.0f, expf(-z));
-    float r;
-    asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
-    const float e = __fmaf_rn(-x, r, 1.0f);
-    return x < kFltMax ? __fmaf_rn(e, r, r) : r;
-}
 
 // The epilogue's form of v * s(z), s(z) = 1 / (1 + 2^(-z log2 e)), for z = v (silu)
 // and z = 2u (gelu_tanh): the hardware's approximations of 2^x (2 ulp, and the
@@ -107,24 +97,57 @@ __device__ __forceinline__ void act_values(float (&v)[kN]) {
     }
 }
 
+__device__ __forceinline__ uint64_t pk1(float a) { return pk(a, a); }
+__device__ __forceinline__ uint64_t ex2_2(uint64_t x) {
+    float a, b;
+    upk(x, a, b);
+    return pk(ex2(a), ex2(b));
+}
+__device__ __forceinline__ uint64_t rcp_2(uint64_t x) {
+    float a, b;
+    upk(x, a, b);
+    return pk(rcp(a), rcp(b));
+}
+
+// Derivatives of two elements, on packed pairs:
+//   silu       s (1 + p (1 - s))
+//   gelu_tanh  s + p u2' s (1 - s),  s = s(u2), u2 = 2 sqrt(2/pi) (p + 0.044715 p^3)
+//   gelu       Phi(p) + p phi(p)
 template <Act A>
-__device__ __forceinline__ float act_slope(float p) {
-    if constexpr (A == Act::RELU) return p > 0.0f ? 1.0f : 0.0f;
-    if constexpr (A == Act::GELU) {
-        const float phi = fmul(kInvSqrt2Pi, expf(fmul(fmul(-0.5f, p), p)));
-        return __fmaf_rn(p, phi, fmul(0.5f, fadd(1.0f, erff(fmul(p, kSqrtHalf)))));
-    }
-    if constexpr (A == Act::GELU_TANH) {
-        const float p2 = fmul(p, p);
-        const float s = sigmoid(fmul(k2Sqrt2OverPi, __fmaf_rn(fmul(0.044715f, p2), p, p)));
-        const float du = fmul(k2Sqrt2OverPi, __fmaf_rn(0.134145f, p2, 1.0f));
-        return __fmaf_rn(fmul(p, du), fmul(s, __fsub_rn(1.0f, s)), s);
+__device__ __forceinline__ uint64_t act_slope2(uint64_t p) {
+    if constexpr (A == Act::RELU) {
+        float a, b;
+        upk(p, a, b);
+        return pk(a > 0.0f ? 1.0f : 0.0f, b > 0.0f ? 1.0f : 0.0f);
     }
     if constexpr (A == Act::SILU) {
-        const float s = sigmoid(p);
-        return fmul(s, __fmaf_rn(p, __fsub_rn(1.0f, s), 1.0f));
+        const uint64_t s = rcp_2(add2(ex2_2(mul2(p, pk1(kNegLog2e))), pk1(1.0f)));
+        return mul2(s, fma2(p, sub2(pk1(1.0f), s), pk1(1.0f)));
     }
-    return 1.0f;
+    if constexpr (A == Act::GELU_TANH) {
+        const uint64_t p2 = mul2(p, p);
+        const uint64_t z = mul2(p, fma2(p2, pk1(kNegLog2e * k2Sqrt2OverPi * 0.044715f),
+                                        pk1(kNegLog2e * k2Sqrt2OverPi)));
+        const uint64_t s = rcp_2(add2(ex2_2(z), pk1(1.0f)));
+        const uint64_t du = fma2(p2, pk1(k2Sqrt2OverPi * 0.134145f), pk1(k2Sqrt2OverPi));
+        return fma2(mul2(p, du), mul2(s, sub2(pk1(1.0f), s)), s);
+    }
+    if constexpr (A == Act::GELU) {
+        float a, b;
+        upk(p, a, b);
+        const uint64_t t = rcp_2(fma2(pk(fabsf(a), fabsf(b)), pk1(kErfP * kSqrtHalf), pk1(1.0f)));
+        const uint64_t e = ex2_2(mul2(mul2(p, p), pk1(0.5f * kNegLog2e)));
+        uint64_t q = fma2(t, pk1(0.5f * 1.061405429f), pk1(0.5f * -1.453152027f));
+        q = fma2(t, q, pk1(0.5f * 1.421413741f));
+        q = fma2(t, q, pk1(0.5f * -0.284496736f));
+        q = fma2(t, q, pk1(0.5f * 0.254829592f));
+        q = sub2(pk1(0.5f), mul2(mul2(t, q), e));  // |Phi(p) - 1/2|
+        float qa, qb;
+        upk(q, qa, qb);
+        const uint64_t cdf = add2(pk(copysignf(qa, a), copysignf(qb, b)), pk1(0.5f));
+        return fma2(mul2(p, pk1(kInvSqrt2Pi)), e, cdf);
+    }
+    return pk1(1.0f);
 }
 
 }  // namespace fos

@@ -13,14 +13,16 @@
 // Bound by HBM: e (or 2e) bytes read per element, 2 + 1/16 written, e more for
 // d itself.  A CTA takes a tile of 128 rows x 128 columns: thread t reads
 // 16-element segments (t mod 8) of rows t / 8 + 32 i, so a warp reads four
-// whole 256-byte row pieces; two neighbouring lanes hold one row block.  For
-// the columns the tile passes through shared memory in fp32 (64 KiB, three
-// CTAs an SM); lane l then takes rows 32 (l mod 4) .. + 31 of column l / 4 of
-// its warp's eight, so four lanes write the 128 code bytes of a column as one
-// line and their four scale bytes as one word.  Element (r, c) sits in 16-byte
-// chunk ((c / 4 ^ (c / 32) mod 4) + 2 (r / 32)) mod 32 of row r: the eight
-// lanes of a store phase (one row, segments 0 .. 7) and the 32 lanes of a load
-// (four row groups, eight columns) then touch every bank once.
+// whole 256-byte row pieces; two neighbouring lanes hold one row block.  (Tiles
+// of 64 columns, twice as many CTAs: 154 instead of 145 us for the case below,
+// their rows being single lines.)  For the columns the tile passes through
+// shared memory in fp32 (64 KB, three CTAs an SM); lane l then takes rows 32 (l
+// mod 4) .. + 31 of column l / 4 of its warp's eight, so four lanes write the
+// 128 code bytes of a column as one line and their four scale bytes as one
+// word.  Element (r, c) sits in 16-byte chunk ((c / 4 ^ (c / 32) mod 4) + 2 (r /
+// 32)) mod 32 of row r: the eight lanes of a store phase (one row, segments 0
+// .. 7) and the 32 lanes of a load (four row groups, eight columns) then touch
+// every bank once.
 #pragma once
 
 #include "fos_act.cuh"
@@ -44,10 +46,11 @@ struct Quant8Args {
     int tiled;
 };
 
-constexpr int kQ8Tile = 128;
+constexpr int kQ8Tile = 128;  // rows and columns of a tile
 constexpr int kQ8Threads = 256;
 constexpr size_t kQ8Smem = kQ8Tile * kQ8Tile * sizeof(float);
 
+// 16-byte chunk of column c in a row of row group rb.
 __device__ __forceinline__ int q8_chunk(int c, int rb) {
     return (((c >> 2) ^ ((c >> 5) & 3)) + 2 * rb) & 31;
 }
@@ -65,7 +68,8 @@ __global__ void __launch_bounds__(kQ8Threads, 3) k_quant8(const Quant8Args a) {
     {
         const int seg = tid & 7, rl = tid >> 3;
         const bool col_in = c0 + seg * 16 < a.cols;
-        constexpr int kAhead = (IT == In::F32) ? 1 : 4;  // segments in flight
+        // row segments in flight: what 80 registers hold
+        constexpr int kAhead = (IT == In::F32) ? 1 : (A == Act::NONE ? 4 : 2);
         Raw<IT> x[kAhead], p[kAhead];
         auto load = [&](int i, Raw<IT>& xr, Raw<IT>& pr) {
             const int64_t row = r0 + rl + 32 * i;
@@ -79,14 +83,11 @@ __global__ void __launch_bounds__(kQ8Threads, 3) k_quant8(const Quant8Args a) {
                 if constexpr (A != Act::NONE) zero_seg(pr);
             }
         };
-        if constexpr (kAhead == 4) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) load(i, x[i], p[i]);
-        }
+        for (int i = 0; i < kAhead; ++i) load(i, x[i], p[i]);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int b = i % kAhead;
-            if constexpr (kAhead == 1) load(i, x[0], p[0]);
             const int64_t row = r0 + rl + 32 * i;
             const bool in = col_in && row < a.rows;
             uint64_t d[8];
@@ -95,12 +96,9 @@ __global__ void __launch_bounds__(kQ8Threads, 3) k_quant8(const Quant8Args a) {
                 uint64_t pv[8];
                 widen<IT>(p[b], pv);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    float lo, hi;
-                    upk(pv[j], lo, hi);
-                    d[j] = mul2(d[j], pk(act_slope<A>(lo), act_slope<A>(hi)));
-                }
+                for (int j = 0; j < 8; ++j) d[j] = mul2(d[j], act_slope2<A>(pv[j]));
             }
+            if (i + kAhead < 4) load(i + kAhead, x[b], p[b]);
             if (a.codes) {
                 float m = seg_amax(d);
                 m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
