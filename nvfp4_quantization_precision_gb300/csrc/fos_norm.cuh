@@ -302,19 +302,18 @@ struct NormBwdArgs {
     int w32;
 };
 
-template <In IT>
+template <In IT, bool DH>
 __device__ __forceinline__ void load_bwd_seg(const NormBwdArgs& a, int64_t at, bool in, Raw<IT>& dy,
                                              Raw<IT>& h, Raw<IT>& dh) {
     constexpr int64_t kElt = (IT == In::F32) ? 4 : 2;
     if (in) {
         load_seg<IT, L2::FIRST>(dy, static_cast<const char*>(a.dy) + at * kElt);
         load_seg<IT, L2::FIRST>(h, static_cast<const char*>(a.h) + at * kElt);
-        if (a.dh) load_seg<IT, L2::FIRST>(dh, static_cast<const char*>(a.dh) + at * kElt);
-        else zero_seg(dh);
+        if constexpr (DH) load_seg<IT, L2::FIRST>(dh, static_cast<const char*>(a.dh) + at * kElt);
     } else {
         zero_seg(dy);
         zero_seg(h);
-        zero_seg(dh);
+        if constexpr (DH) zero_seg(dh);
     }
 }
 
@@ -324,28 +323,33 @@ __device__ __forceinline__ float warp_sum(float v) {
     return v;
 }
 
-// dx of one segment from g = dy * w: fma(g, rstd, dh) - h * c.
+// dx of one segment from g = dy * w: g rstd - h c, plus dh.
+template <bool DH>
 __device__ __forceinline__ void bwd_dx(const uint64_t (&g)[8], const uint64_t (&h)[8],
                                        const uint64_t (&dh)[8], float rstd, float c,
                                        uint64_t (&dx)[8]) {
     const uint64_t r2 = pk(rstd, rstd), c2 = pk(-c, -c);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) dx[j] = fma2(h[j], c2, fma2(g[j], r2, dh[j]));
+    for (int j = 0; j < 8; ++j) {
+        if constexpr (DH) dx[j] = fma2(h[j], c2, fma2(g[j], r2, dh[j]));
+        else dx[j] = fma2(h[j], c2, mul2(g[j], r2));
+    }
 }
 
-// A row per group of kT threads, one 16-element segment a thread; the weight
-// gradient of the thread's columns is kept in registers over all of its rows
-// and leaves as one partial row per CTA (the groups of a CTA are added in
-// order through shared memory), so the sum has one fixed order.
-template <In IT, int kT>
-__global__ void __launch_bounds__(kT < 256 ? 256 : kT) k_rms_bwd(const NormBwdArgs a) {
+// A row per group of kT threads, one 16-element segment a thread; a CTA of 512
+// threads holds 512 / kT groups.  The weight gradient of the thread's columns
+// is kept in registers over all of its rows and leaves as one partial row per
+// CTA (its groups are added in order through shared memory), so the sum has one
+// fixed order and the second kernel one partial row per SM to add.
+constexpr int kBwdThreads = 512;
+template <In IT, int kT, bool DH>
+__global__ void __launch_bounds__(kBwdThreads, 1) k_rms_bwd(const NormBwdArgs a) {
     chain_wait();
     chain_release();
-    constexpr int kCta = kT < 256 ? 256 : kT;
-    constexpr int kGroups = kCta / kT, kW = kT / 32;
-    constexpr bool kAhead = kCta <= 512 && IT != In::F32;  // next row in registers (64 or 128 of them)
-    __shared__ float s_part[2][kCta / 32];
-    __shared__ float s_dw[kGroups > 1 ? kCta * 16 : 1];
+    constexpr int kGroups = kBwdThreads / kT, kW = kT / 32;
+    constexpr bool kAhead = IT != In::F32 || !DH;  // the next row fits the registers
+    __shared__ float s_part[2][kBwdThreads / 32];
+    __shared__ float s_dw[kGroups > 1 ? kBwdThreads * 16 : 1];
     const int t = threadIdx.x % kT, g = threadIdx.x / kT;
     const bool col_in = (int64_t)t * 16 < a.cols;
     const int64_t step = (int64_t)gridDim.x * kGroups;
@@ -355,14 +359,13 @@ __global__ void __launch_bounds__(kT < 256 ? 256 : kT) k_rms_bwd(const NormBwdAr
     int64_t row = (int64_t)blockIdx.x * kGroups + g;
     Raw<IT> dy, h, dh;
     if constexpr (kAhead)
-        load_bwd_seg<IT>(a, row * a.cols + t * 16, col_in && row < a.rows, dy, h, dh);
+        load_bwd_seg<IT, DH>(a, row * a.cols + t * 16, col_in && row < a.rows, dy, h, dh);
     if (col_in) load_weight<IT>(a.w, (int64_t)t * 16, a.w32, w);
     int parity = 0;
-    for (int64_t base = (int64_t)blockIdx.x * kGroups; base < a.rows;
-         base += step, row += step, parity ^= 1) {
-        const bool in = col_in && row < a.rows;
-        if constexpr (!kAhead) load_bwd_seg<IT>(a, row * a.cols + t * 16, in, dy, h, dh);
-        const float rstd = row < a.rows ? __ldg(a.rstd + row) : 0.0f;
+    // a group runs its own rows; only its warps meet at a barrier
+    for (; row < a.rows; row += step, parity ^= 1) {
+        if constexpr (!kAhead) load_bwd_seg<IT, DH>(a, row * a.cols + t * 16, col_in, dy, h, dh);
+        const float rstd = __ldg(a.rstd + row);
         uint64_t v[8], hv[8], acc = 0;
         widen<IT>(dy, v);
         widen<IT>(h, hv);
@@ -374,44 +377,43 @@ __global__ void __launch_bounds__(kT < 256 ? 256 : kT) k_rms_bwd(const NormBwdAr
             acc = fma2(v[j], hv[j], acc);
         }
         uint64_t dhv[8];
-        widen<IT>(dh, dhv);
+        if constexpr (DH) widen<IT>(dh, dhv);
         if constexpr (kAhead)
-            load_bwd_seg<IT>(a, (row + step) * a.cols + t * 16, col_in && row + step < a.rows, dy, h,
-                             dh);
+            load_bwd_seg<IT, DH>(a, (row + step) * a.cols + t * 16, col_in && row + step < a.rows, dy,
+                                 h, dh);
         float p0, p1;
         upk(acc, p0, p1);
         float s = warp_sum(fadd(p0, p1));
         if constexpr (kW > 1) {
             if ((threadIdx.x & 31) == 0) s_part[parity][threadIdx.x >> 5] = s;
-            __syncthreads();
+            asm volatile("bar.sync %0, %1;" ::"r"(1 + g), "n"(kT) : "memory");
             s = 0.0f;
 #pragma unroll
             for (int i = 0; i < kW; ++i) s = fadd(s, s_part[parity][g * kW + i]);
         }
-        if (in) {
+        if (col_in) {
             constexpr int64_t kElt = (IT == In::F32) ? 4 : 2;
             const float c = fmul(fmul(fmul(s, rstd), fmul(a.inv_cols, rstd)), rstd);
             uint64_t dx[8];
-            bwd_dx(v, hv, dhv, rstd, c, dx);
+            bwd_dx<DH>(v, hv, dhv, rstd, c, dx);
             store_seg<IT>(static_cast<char*>(a.dx) + (row * a.cols + t * 16) * kElt, dx);
         }
     }
     if (!a.part) return;
-    float* out = a.part + (int64_t)blockIdx.x * a.cols + (int64_t)t * 16;
     if constexpr (kGroups > 1) {
         float* mine = s_dw + threadIdx.x * 16;
 #pragma unroll
         for (int j = 0; j < 8; ++j) upk(dw[j], mine[2 * j], mine[2 * j + 1]);
         __syncthreads();
         // column i of the CTA's partial: the groups in order
-        for (int64_t i = threadIdx.x; i < a.cols; i += kCta) {
+        for (int64_t i = threadIdx.x; i < a.cols; i += kBwdThreads) {
             float s = s_dw[i];
 #pragma unroll
             for (int k = 1; k < kGroups; ++k) s = fadd(s, s_dw[k * kT * 16 + i]);
             a.part[(int64_t)blockIdx.x * a.cols + i] = s;
         }
     } else if (col_in) {
-        store_seg<In::F32>(out, dw);
+        store_seg<In::F32>(a.part + (int64_t)blockIdx.x * a.cols + (int64_t)t * 16, dw);
     }
 }
 
@@ -454,14 +456,18 @@ __global__ void __launch_bounds__(512) k_rms_bwd_wide(const NormBwdArgs a) {
         for (int64_t sg = t; sg < nseg; sg += kT) {
             Raw<IT> dy, h, dh;
             uint64_t v[8], hv[8], dhv[8], w[8], dx[8];
-            load_bwd_seg<IT>(a, row * a.cols + sg * 16, true, dy, h, dh);
+            if (a.dh) load_bwd_seg<IT, true>(a, row * a.cols + sg * 16, true, dy, h, dh);
+            else {
+                load_bwd_seg<IT, false>(a, row * a.cols + sg * 16, true, dy, h, dh);
+                zero_seg(dh);
+            }
             load_weight<IT>(a.w, sg * 16, a.w32, w);
             widen<IT>(dy, v);
             widen<IT>(h, hv);
             widen<IT>(dh, dhv);
 #pragma unroll
             for (int j = 0; j < 8; ++j) v[j] = mul2(v[j], w[j]);
-            bwd_dx(v, hv, dhv, rstd, c, dx);
+            bwd_dx<true>(v, hv, dhv, rstd, c, dx);
             store_seg<IT>(static_cast<char*>(a.dx) + (row * a.cols + sg * 16) * kElt, dx);
         }
     }
@@ -497,8 +503,8 @@ __global__ void __launch_bounds__(256) k_rms_dw_wide(const NormBwdArgs a) {
 
 // ------------------------------------------------------------------ column sums
 // out[c] = sum over the `parts` partial rows, in a fixed order: a CTA takes 32
-// columns, its 32 warps every 32nd row each, and the warps' sums are added in
-// order.
+// columns, its 32 warps every 32nd row each (eight of them in flight), and the
+// warps' sums are added by one tree.
 constexpr int kSumWarps = 32;
 __global__ void __launch_bounds__(32 * kSumWarps) k_column_sums(const float* part, int64_t parts,
                                                                 int64_t cols, float* out);

@@ -14,15 +14,14 @@ __global__ void __launch_bounds__(32 * kSumWarps) k_column_sums(const float* par
     const int64_t c = (int64_t)blockIdx.x * 32 + lane;
     float s = 0.0f;
     if (c < cols) {
-        int64_t p = warp;
-        for (; p + 3 * kSumWarps < parts; p += 4 * kSumWarps) {
-            float v[4];
+        for (int64_t p = warp; p < parts; p += 8 * kSumWarps) {
+            float v[8];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) v[k] = __ldg(part + (p + k * kSumWarps) * cols + c);
+            for (int k = 0; k < 8; ++k)
+                v[k] = p + k * kSumWarps < parts ? __ldg(part + (p + k * kSumWarps) * cols + c) : 0.0f;
 #pragma unroll
-            for (int k = 0; k < 4; ++k) s = fadd(s, v[k]);
+            for (int k = 0; k < 8; ++k) s = fadd(s, v[k]);
         }
-        for (; p < parts; p += kSumWarps) s = fadd(s, __ldg(part + p * cols + c));
     }
     s_sum[warp][lane] = s;
     __syncthreads();
@@ -85,16 +84,21 @@ cudaError_t norm_by_res(const NormArgs& a, cudaStream_t s) {
     return a.res ? norm_by_width<IT, true>(a, s) : norm_by_width<IT, false>(a, s);
 }
 
-template <In IT, int kT>
-cudaError_t bwd_go(NormBwdArgs& a, float* dw, float* part, int64_t max_parts, cudaStream_t s) {
-    constexpr int cta = kT < 256 ? 256 : kT;
-    auto k = k_rms_bwd<IT, kT>;
-    int64_t grid = row_grid(k, cta, a.rows, cta / kT);
+template <In IT, int kT, bool DH>
+cudaError_t bwd_launch(NormBwdArgs& a, float* dw, float* part, int64_t max_parts, cudaStream_t s) {
+    auto k = k_rms_bwd<IT, kT, DH>;
+    int64_t grid = row_grid(k, kBwdThreads, a.rows, kBwdThreads / kT);
     if (grid > max_parts) grid = max_parts;
     a.part = !dw ? nullptr : (grid == 1 ? dw : part);  // one CTA writes the result itself
-    cudaError_t e = launch_chained(k, dim3((unsigned)grid), cta, 0, s, a);
+    cudaError_t e = launch_chained(k, dim3((unsigned)grid), kBwdThreads, 0, s, a);
     if (e != cudaSuccess || !dw || grid == 1) return e;
     return launch_column_sums(part, grid, a.cols, dw, s);
+}
+
+template <In IT, int kT>
+cudaError_t bwd_go(NormBwdArgs& a, float* dw, float* part, int64_t max_parts, cudaStream_t s) {
+    return a.dh ? bwd_launch<IT, kT, true>(a, dw, part, max_parts, s)
+                : bwd_launch<IT, kT, false>(a, dw, part, max_parts, s);
 }
 
 template <In IT>
