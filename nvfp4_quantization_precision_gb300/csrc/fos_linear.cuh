@@ -218,9 +218,11 @@ __device__ __forceinline__ void act_apply(int act, float (&v)[kN]) {
 // columns, so one token costs 16 columns of tensor work instead of 128 rows,
 // and the time is that of streaming the weights.  A CTA takes 128 weight rows
 // x nt <= 256 tokens; with few such tiles the K axis is split over the S CTAs
-// of a cluster, whose fp32 partial tiles meet in shared memory: CTA r adds
-// tokens r, r + S, ... of all S partials, read through the cluster's
-// distributed shared memory in rank order (one fixed order of the sum).
+// of a cluster.  The fp32 partial tiles are laid down in shared memory, a row
+// per token (over the ring of stages, idle by then): CTA r finishes tokens r,
+// r + S, ..., a warp a token, each lane adding four weight rows of all S
+// partials, read through the cluster's distributed shared memory in rank order
+// (one fixed order of the sum), and storing them side by side.
 //   warp 0    TMA producer of a stage's b tile and a tile
 //   warp 6    bulk-copy producer of its scale tiles
 //   warp 1    tensor memory; one thread copies scales and issues the MMAs
@@ -251,7 +253,7 @@ constexpr int kSfRing = 4;
 constexpr uint32_t kAllColumns = 512;
 
 struct __align__(8) RowsShared {
-    uint64_t full[kMaxStages], empty[kMaxStages], acc_full, acc_empty, done;
+    uint64_t full[kMaxStages], empty[kMaxStages], acc_full, done;
     uint32_t tmem;
     int fail;
 };
@@ -273,12 +275,18 @@ __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;"
                  ::: "memory");
 }
-__device__ __forceinline__ float ld_cluster(uint32_t saddr, uint32_t rank) {
-    float v;
-    asm volatile("{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %1, %2;\n\t"
-                 "ld.shared::cluster.f32 %0, [a];\n\t}"
-                 : "=f"(v) : "r"(saddr), "r"(rank) : "memory");
+__device__ __forceinline__ float4 ld_cluster4(uint32_t saddr, uint32_t rank) {
+    float4 v;
+    asm volatile("{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %4, %5;\n\t"
+                 "ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [a];\n\t}"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(saddr), "r"(rank) : "memory");
     return v;
+}
+// Barrier of all threads of the S CTAs that share a tile.
+__device__ __forceinline__ void tile_sync(int S) {
+    __syncwarp();
+    if (S > 1) cluster_sync();
+    else __syncthreads();
 }
 
 // Position in a ring of n slots: slot and the parity of its current use.
@@ -319,38 +327,100 @@ __device__ __forceinline__ void rows_stage(uint32_t acc, uint32_t p0, uint32_t q
     }
 }
 
-// The residuals of kN tokens from `at` on, dat apart (the first cnt of them).
-template <Out OT, int kN>
-__device__ __forceinline__ void load_residual(const Epilogue& e, int64_t at, int64_t dat, int cnt,
-                                              float (&r)[kN]) {
-#pragma unroll
-    for (int i = 0; i < kN; ++i) r[i] = e.residual && i < cnt ? load_out<OT>(e.residual, at + i * dat) : 0.0f;
+// Four consecutive values of the output's type at element i (a multiple of 4).
+template <Out OT>
+__device__ __forceinline__ void load4(const void* p, int64_t i, float (&v)[4]) {
+    if constexpr (OT == Out::F32) {
+        const float4 x = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(p) + i));
+        v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
+    } else {
+        const uint2 x = __ldg(reinterpret_cast<const uint2*>(static_cast<const unsigned short*>(p) + i));
+        if constexpr (OT == Out::BF16) {
+            v[0] = __uint_as_float(x.x << 16); v[1] = __uint_as_float(x.x & 0xFFFF0000u);
+            v[2] = __uint_as_float(x.y << 16); v[3] = __uint_as_float(x.y & 0xFFFF0000u);
+        } else {
+            upk(f16x2_f32x2(x.x), v[0], v[1]);
+            upk(f16x2_f32x2(x.y), v[2], v[3]);
+        }
+    }
+}
+template <Out OT>
+__device__ __forceinline__ void store4(void* p, int64_t i, const float* v) {
+    if constexpr (OT == Out::F32) {
+        const uint32_t w[4] = {__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
+                               __float_as_uint(v[3])};
+        st128(static_cast<float*>(p) + i, w);
+    } else {
+        st64(static_cast<unsigned short*>(p) + i, out_pair<OT>(pk(v[0], v[1])),
+             out_pair<OT>(pk(v[2], v[3])));
+    }
 }
 
-// The epilogue of kN tokens of one weight row, their scaled sums in v: stores
-// at `at`, dat apart (the first cnt of them).
-template <Out OT, int kN>
-__device__ __forceinline__ void finish_rows(const Epilogue& e, float (&v)[kN], const float (&r)[kN],
-                                            int64_t at, int64_t dat, int cnt, float bias) {
-#pragma unroll
-    for (int i = 0; i < kN; ++i) v[i] = fadd(v[i], bias);
-    if (e.pre) {
-#pragma unroll
-        for (int i = 0; i < kN; ++i)
-            if (i < cnt) store_out<OT>(e.pre, at + i * dat, v[i]);
-    }
-    act_apply(e.act, v);
-    if (e.residual) {
-#pragma unroll
-        for (int i = 0; i < kN; ++i) v[i] = fadd(v[i], r[i]);
-    }
-#pragma unroll
-    for (int i = 0; i < kN; ++i)
-        if (i < cnt) store_out<OT>(e.out, at + i * dat, v[i]);
-}
+// What a warp finishes of a tile: tokens m0 + c, c = first, first + 4 kS, ...
+// below mt, at weight rows n .. n + 3.
+struct Tile {
+    const float* red;
+    const float* ga;
+    int m0, mt, first, lane;
+    int64_t n, N;
+    float gb;
+};
 
-// Barrier of the four epilogue warps.
-__device__ __forceinline__ void epilogue_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+// kTok tokens at a time with all of their loads in flight.
+template <class F, Out OT, int kTok, int kS>
+__device__ __forceinline__ void finish_tokens(const Epilogue& ep, const Tile& t,
+                                              const float (&bias)[4]) {
+    for (int c0 = t.first; c0 < t.mt; c0 += 4 * kS * kTok) {
+        float4 p[kTok][kS];
+        float rs[kTok][4], f[4 * kTok];
+#pragma unroll
+        for (int i = 0; i < kTok; ++i) {
+            // tokens past the end repeat the last one's loads and are not stored
+            const int c = min(c0 + 4 * kS * i, t.mt - 1);
+            const float* at = t.red + c * 128 + 4 * t.lane;
+#pragma unroll
+            for (int k = 0; k < kS; ++k) {
+                if constexpr (kS == 1) p[i][k] = *reinterpret_cast<const float4*>(at);
+                else p[i][k] = ld_cluster4(smem_u32(at), (uint32_t)k);
+            }
+            if (ep.residual) load4<OT>(ep.residual, (int64_t)(t.m0 + c) * t.N + t.n, rs[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < kTok; ++i) {
+            const int c = c0 + 4 * kS * i;
+            float4 s = p[i][0];
+#pragma unroll
+            for (int k = 1; k < kS; ++k) {
+                s.x = fadd(s.x, p[i][k].x);
+                s.y = fadd(s.y, p[i][k].y);
+                s.z = fadd(s.z, p[i][k].z);
+                s.w = fadd(s.w, p[i][k].w);
+            }
+            if constexpr (F::kGlobal) {
+                const float ga = t.ga[min(c, t.mt - 1)];
+                s.x = fmul(fmul(s.x, ga), t.gb);
+                s.y = fmul(fmul(s.y, ga), t.gb);
+                s.z = fmul(fmul(s.z, ga), t.gb);
+                s.w = fmul(fmul(s.w, ga), t.gb);
+            }
+            f[4 * i] = fadd(s.x, bias[0]);
+            f[4 * i + 1] = fadd(s.y, bias[1]);
+            f[4 * i + 2] = fadd(s.z, bias[2]);
+            f[4 * i + 3] = fadd(s.w, bias[3]);
+            if (ep.pre && c < t.mt) store4<OT>(ep.pre, (int64_t)(t.m0 + c) * t.N + t.n, f + 4 * i);
+        }
+        act_apply(ep.act, f);
+#pragma unroll
+        for (int i = 0; i < kTok; ++i) {
+            const int c = c0 + 4 * kS * i;
+            if (ep.residual) {
+#pragma unroll
+                for (int x = 0; x < 4; ++x) f[4 * i + x] = fadd(f[4 * i + x], rs[i][x]);
+            }
+            if (c < t.mt) store4<OT>(ep.out, (int64_t)(t.m0 + c) * t.N + t.n, f + 4 * i);
+        }
+    }
+}
 
 template <class F, Out OT>
 __global__ void __launch_bounds__(kRowsThreads, 1) k_linear_rows(const __grid_constant__ RowsArgs a) {
@@ -377,7 +447,6 @@ __global__ void __launch_bounds__(kRowsThreads, 1) k_linear_rows(const __grid_co
             bar_init(&sh.empty[lane], 1);
         } else if (lane == 31) {
             bar_init(&sh.acc_full, 1);
-            bar_init(&sh.acc_empty, 4);
             bar_init(&sh.done, 1);
             sh.fail = 0;
         }
@@ -450,8 +519,6 @@ __global__ void __launch_bounds__(kRowsThreads, 1) k_linear_rows(const __grid_co
                 r.next(ns);
             }
         } else if (warp == 1) {
-            if (!bad && j >= 1 && S == 1 && !warp_wait(&sh.acc_empty, (uint32_t)(j - 1) & 1)) bad = true;
-            tc_fence_after();
             for (int i = k_lo; i < k_hi && !bad; ++i) {
                 const int s = r.slot;
                 const bool over = g >= (uint32_t)kSfRing;  // a scale buffer is used again
@@ -484,96 +551,52 @@ __global__ void __launch_bounds__(kRowsThreads, 1) k_linear_rows(const __grid_co
             if (!bad && elected) tc_commit(&sh.acc_full);
             __syncwarp();
         } else {
-            const int q = warp & 3;
-            const int nl = 32 * q + lane;            // weight row of the tile
-            const int64_t n = n0 + nl;
+            const int q = warp & 3, e = warp - 2;
             const int mt = min(nt, (int)a.M - m0);
+            // finishing, lane l has weight rows 4 l .. 4 l + 3 of the tile
+            const int64_t n = n0 + 4 * lane;
             const bool nin = n < a.N;
-            float bias = 0.0f;
-            if (a.ep.bias && nin)
-                bias = a.ep.bias32 ? __ldg(static_cast<const float*>(a.ep.bias) + n)
-                                   : load_out<OT>(a.ep.bias, n);
+            float bias[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            if (a.ep.bias && nin) {
+                if (a.ep.bias32) load4<Out::F32>(a.ep.bias, n, bias);
+                else load4<OT>(a.ep.bias, n, bias);
+            }
             float gb = 1.0f;
             if constexpr (F::kGlobal) {
                 // the tokens' decode scales, once per tile
                 gb = fdiv(1.0f, global_scale(a.ep.b_amax[0], a.ep.six_bound));
-                epilogue_sync();  // the tile before has read its own
-                for (int c = nl; c < mt; c += 128)
+                for (int c = 32 * e + lane; c < mt; c += 128)
                     s_ga[c] = fdiv(1.0f, global_scale(__ldg(a.ep.a_amax + (a.ep.a_row ? m0 + c : 0)),
                                                       a.ep.six_bound));
-                epilogue_sync();
             }
             if (!bad && !warp_wait(&sh.acc_full, (uint32_t)j & 1)) bad = true;
             __syncwarp();
             tc_fence_after();
-            const uint32_t lane_base = tmem + ((uint32_t)(32 * q) << 16);
-            if (S > 1) {
-                for (int c0 = 0; c0 < mt; c0 += 16) {
-                    uint32_t v[16];
-                    tmem_ld16(lane_base + (uint32_t)c0, v);
+            // the partial tile to shared memory, a row per token
+            for (int c0 = 0; c0 < mt; c0 += 16) {
+                uint32_t v[16];
+                tmem_ld16(tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)c0, v);
 #pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        if (c0 + i < mt) red[(c0 + i) * 128 + nl] = __uint_as_float(v[i]);
-                }
-                tc_fence_before();
-                __syncwarp();
-                cluster_sync();  // every partial of the tile is written
-                if (nin) {
-                    // four tokens at a time, all of their loads in flight
-                    for (int c = rank; c < mt; c += 4 * S) {
-                        const int cnt = (mt - c + S - 1) / S;
-                        const int64_t at = (int64_t)(m0 + c) * a.N + n, dat = (int64_t)S * a.N;
-                        float f[4], rs[4], p[4][8];
-                        load_residual<OT>(a.ep, at, dat, cnt, rs);
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-#pragma unroll
-                            for (int k = 0; k < 8; ++k)
-                                if (k < S && i < cnt)
-                                    p[i][k] = ld_cluster(smem_u32(red + (c + i * S) * 128 + nl), (uint32_t)k);
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            f[i] = p[i][0];
-#pragma unroll
-                            for (int k = 1; k < 8; ++k)
-                                if (k < S) f[i] = fadd(f[i], p[i][k]);
-                            if constexpr (F::kGlobal)
-                                f[i] = fmul(fmul(f[i], s_ga[i < cnt ? c + i * S : c]), gb);
-                        }
-                        finish_rows<OT>(a.ep, f, rs, at, dat, cnt, bias);
-                    }
-                }
-                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                __syncwarp();
-                cluster_sync();  // every partial has been read: the ring is free again
-            } else {
-                for (int c0 = 0; c0 < mt; c0 += 16) {
-                    uint32_t v[16];
-                    tmem_ld16(lane_base + (uint32_t)c0, v);
-                    if (nin) {
-                        const int64_t at = (int64_t)(m0 + c0) * a.N + n;
-                        float f[16], rs[16];
-                        load_residual<OT>(a.ep, at, a.N, mt - c0, rs);
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            f[i] = __uint_as_float(v[i]);
-                            if constexpr (F::kGlobal)
-                                f[i] = fmul(fmul(f[i], s_ga[min(c0 + i, mt - 1)]), gb);
-                        }
-                        finish_rows<OT>(a.ep, f, rs, at, a.N, mt - c0, bias);
-                    }
-                    __syncwarp();
-                }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) bar_arrive(&sh.acc_empty);
-                __syncwarp();
+                for (int i = 0; i < 16; ++i)
+                    if (c0 + i < mt) red[(c0 + i) * 128 + 32 * q + lane] = __uint_as_float(v[i]);
             }
+            tc_fence_before();
+            tile_sync(S);  // every partial of the tile is written
+            // warp e of CTA r finishes tokens r + S e, r + S (e + 4), ...
+            if (nin) {
+                const Tile t4{red, s_ga, m0, mt, rank + S * e, lane, n, a.N, gb};
+                if (S == 1) finish_tokens<F, OT, 4, 1>(a.ep, t4, bias);
+                else if (S == 2) finish_tokens<F, OT, 4, 2>(a.ep, t4, bias);
+                else if (S == 4) finish_tokens<F, OT, 2, 4>(a.ep, t4, bias);
+                else finish_tokens<F, OT, 2, 8>(a.ep, t4, bias);
+            }
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            tile_sync(S);  // every partial has been read: the ring is free again
+            tc_fence_after();
         }
-        if (S > 1 && (warp < 2 || warp == 6)) {
-            __syncwarp();
-            cluster_sync();
-            cluster_sync();
+        if (warp < 2 || warp == 6) {
+            tile_sync(S);
+            tile_sync(S);
             tc_fence_after();
         }
     }

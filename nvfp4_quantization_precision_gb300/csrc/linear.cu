@@ -68,12 +68,68 @@ cudaError_t launch_clusters(Kernel k, int clusters, int size, int threads, int s
     return cudaLaunchKernelEx(&cfg, k, a);
 }
 
+template <class F> constexpr int k_tile() { return F::kGlobal ? 64 : 128; }  // K of a scale tile
+template <class F> int k_tiles(int64_t K) { return (int)((K + k_tile<F>() - 1) / k_tile<F>()); }
+template <class F> int k_stages(int64_t K) { return (k_tiles<F>(K) + F::kSfTiles - 1) / F::kSfTiles; }
+
+// Shape of a rows launch and what it should take.
+struct RowsPlan {
+    int nt, stages, smem, splits, clusters;
+    double us;
+};
+
+// Both kernels' times by sizes, from measurements over 1 .. 1024 tokens, 1024 ..
+// 14336 weight rows and K of 4096 and 14336 (us; 8 bit, NVFP4):
+//   rows  (4.2, 4.5) + rounds (stages / S (0.32, 0.37 + 0.00043 nt) + 0.022 nt,
+//         0.034 without a split)
+//   pair  6.1 + the larger of rounds * stages (0.225, 0.29) and the weights at
+//         (5.6, 4.7) TB/s
+// E.g. 8 bit, 4096 x 14336: 64 tokens 15.7 rows, 31.0 pair; 256 tokens 22.6 and
+// 31.5.  14336 x 4096: 32 tokens 15.1 and 16.3; 256 tokens 26.5 and 17.5 (NVFP4
+// 10.6 and 13.5, 19.0 and 13.7).
 template <class F, Out OT>
-cudaError_t rows_go(const LinearCall& c, cudaStream_t s) {
+RowsPlan rows_plan(const LinearCall& c) {
+    RowsPlan p;
+    p.nt = c.M >= 256 ? 256 : (int)((c.M + 15) / 16 * 16);
+    const int stage = rows_stage_bytes<F>(p.nt);
+    p.stages = (kSmemLimit - 3072) / stage;
+    if (p.stages > kMaxStages) p.stages = kMaxStages;
+    p.smem = p.stages * stage + 1024;
+    const int nkb = k_stages<F>(c.K);
+    const int64_t tiles = (c.N + 127) / 128 * ((c.M + p.nt - 1) / p.nt);
+    // the split of K with the shortest time; every CTA keeps at least two stages
+    p.us = 1e30;
+    for (int S = 1; S <= 8 && (S == 1 || nkb / S >= 2); S *= 2) {
+        const int fit = S == 1 ? sm_count()
+                               : resident_clusters(k_linear_rows<F, OT>, kRowsThreads, p.smem, S);
+        const double stage_us = (F::kGlobal ? 0.37 : 0.32) + 0.00043 * p.nt;
+        const double us = (F::kGlobal ? 4.5 : 4.2) + (double)((tiles + fit - 1) / fit) *
+                              ((nkb + S - 1) / S * stage_us + (S > 1 ? 0.022 : 0.034) * p.nt);
+        if (us < p.us) {
+            p.us = us;
+            p.splits = S;
+            p.clusters = fit < tiles ? fit : (int)tiles;
+        }
+    }
+    return p;
+}
+
+template <class F>
+double pair_us(const LinearCall& c) {
+    const int64_t tiles = (c.M + kPairM - 1) / kPairM * ((c.N + kPairN - 1) / kPairN);
+    const int64_t pairs = sm_count() / 2;
+    const double work = (double)((tiles + pairs - 1) / pairs) * k_stages<F>(c.K) *
+                        (F::kGlobal ? 0.29 : 0.225);
+    const double weights = (double)c.N * c.K * (F::kGlobal ? 0.5625 / 4.7e6 : 1.03125 / 5.6e6);
+    return 6.1 + (work > weights ? work : weights);
+}
+
+template <class F, Out OT>
+cudaError_t rows_go(const LinearCall& c, const RowsPlan& p, cudaStream_t s) {
     RowsArgs a;
     std::memset(&a, 0, sizeof(a));
     const int64_t row_bytes = F::kGlobal ? c.K / 2 : c.K;
-    a.nt = c.M >= 256 ? 256 : (int)((c.M + 15) / 16 * 16);
+    a.nt = p.nt;
     if (!code_map(&a.tp, c.b, c.N, row_bytes, 128) || !code_map(&a.tq, c.a, c.M, row_bytes, a.nt))
         return cudaErrorInvalidValue;
     a.sfp = c.bs;
@@ -81,35 +137,13 @@ cudaError_t rows_go(const LinearCall& c, cudaStream_t s) {
     a.ep = c.ep;
     a.M = c.M;
     a.N = c.N;
-    const int blk4 = F::kGlobal ? 64 : 128;
-    a.kb = (int)((c.K + blk4 - 1) / blk4);
-    a.nkb = (a.kb + F::kSfTiles - 1) / F::kSfTiles;
+    a.kb = k_tiles<F>(c.K);
+    a.nkb = k_stages<F>(c.K);
     a.tiles_p = (int)((c.N + 127) / 128);
     a.tiles = a.tiles_p * (int)((c.M + a.nt - 1) / a.nt);
-    const int stage = rows_stage_bytes<F>(a.nt);
-    a.stages = (kSmemLimit - 3072) / stage;
-    if (a.stages > kMaxStages) a.stages = kMaxStages;
-    const int smem = a.stages * stage + 1024;
-    auto k = k_linear_rows<F, OT>;
-    cudaError_t e = allow_smem(reinterpret_cast<const void*>(k), (size_t)kSmemLimit - 2048);
-    if (e != cudaSuccess) return e;
-    // the split of K that needs the fewest rounds of the device, counted in
-    // whole-K tiles; every CTA keeps at least two stages
-    int best = 1, clusters = sm_count();
-    double cost = 1e30;
-    for (int S = 1; S <= 8; S *= 2) {
-        if (S > 1 && a.nkb / S < 2) break;
-        const int fit = S == 1 ? sm_count() : resident_clusters(k, kRowsThreads, smem, S);
-        const double t = (double)((a.tiles + fit - 1) / fit) / S;
-        if (t < 0.95 * cost) {
-            cost = t;
-            best = S;
-            clusters = fit;
-        }
-    }
-    a.splits = best;
-    if (clusters > a.tiles) clusters = a.tiles;
-    return launch_clusters(k, clusters, best, kRowsThreads, smem, a, s);
+    a.stages = p.stages;
+    a.splits = p.splits;
+    return launch_clusters(k_linear_rows<F, OT>, p.clusters, p.splits, kRowsThreads, p.smem, a, s);
 }
 
 // Scale tiles [row tiles, kb, 512 bytes], a box of r x n of them; tiles past
@@ -143,9 +177,8 @@ cudaError_t pair_go(const LinearCall& c, cudaStream_t s) {
     PairArgs a;
     std::memset(&a, 0, sizeof(a));
     const int64_t row_bytes = F::kGlobal ? c.K / 2 : c.K;
-    const int blk4 = F::kGlobal ? 64 : 128;
-    a.kb = (int)((c.K + blk4 - 1) / blk4);
-    a.nkb = (a.kb + F::kSfTiles - 1) / F::kSfTiles;
+    a.kb = k_tiles<F>(c.K);
+    a.nkb = k_stages<F>(c.K);
     if (!code_map(&a.ta, c.a, c.M, row_bytes, 128) || !code_map(&a.tb, c.b, c.N, row_bytes, 96) ||
         !scale_map(&a.tsa, c.as, c.M, a.kb, 1, kSfChunkTiles) ||
         !scale_map(&a.tsb, c.bs, c.N, a.kb, 2, kSfChunkTiles) ||
@@ -173,7 +206,11 @@ cudaError_t pair_go(const LinearCall& c, cudaStream_t s) {
 
 template <class F, Out OT>
 cudaError_t go(const LinearCall& c, cudaStream_t s) {
-    return c.M > 256 ? pair_go<F, OT>(c, s) : rows_go<F, OT>(c, s);
+    const cudaError_t e = allow_smem(reinterpret_cast<const void*>(k_linear_rows<F, OT>),
+                                     (size_t)kSmemLimit - 2048);
+    if (e != cudaSuccess) return e;
+    const RowsPlan p = rows_plan<F, OT>(c);
+    return p.us <= pair_us<F>(c) ? rows_go<F, OT>(c, p, s) : pair_go<F, OT>(c, s);
 }
 
 template <class F>
