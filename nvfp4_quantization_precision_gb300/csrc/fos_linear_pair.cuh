@@ -56,6 +56,11 @@ constexpr int kSfBufs = 3;    // chunks in tensor memory
 constexpr int kSfCols = 16 + 24;
 static_assert(kPairSfCol + kSfBufs * kSfCols <= (int)kAllColumns, "tensor memory");
 template <class F> constexpr int chunk_stages() { return kSfChunkTiles / F::kSfTiles; }
+// Where a chunk is a stage, the scale warps (four of each CTA) arrive at the
+// stage's full barrier themselves, and a stage's empty barrier also frees its
+// scale buffer: one wait and one commit a stage in the issuing warp instead of
+// two, which is what binds NVFP4 (640 cycles a stage of four MMAs with two).
+template <class F> constexpr bool chunk_is_stage() { return chunk_stages<F>() == 1; }
 
 struct PairArgs {
     CUtensorMap ta;    // a codes, box 128 bytes x 128 rows
@@ -233,7 +238,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_linear_pair(const __grid_co
     const int first = (int)(blockIdx.x >> 1), step = (int)(gridDim.x >> 1);
     if (threadIdx.x == 0) {
         for (int s = 0; s < ns; ++s) {
-            bar_init(&sh.full[s], 1);
+            bar_init(&sh.full[s], chunk_is_stage<F>() ? 9 : 1);
             bar_init(&sh.empty[s], 1);
         }
         for (int b = 0; b < 2; ++b) {
@@ -309,7 +314,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_linear_pair(const __grid_co
         if (rank == 0) {
             const bool elected = elect_lane();
             Ring r, f;      // stages; scale buffers
-            bool here = false, scaled = false;  // the next stage is full, its scales are there
+            bool here = false;  // the next stage is known to be full
             int j = 0;
             for (int t = first; t < tiles && !bad; t += step, ++j) {
                 const int ab = j & 1;
@@ -320,16 +325,12 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_linear_pair(const __grid_co
                 const uint32_t acc = tmem + (uint32_t)(ab * kPairN);
                 for (int i = 0; i < a.nkb; ++i) {
                     const int s = r.slot, in_chunk = i % chunk_stages<F>();
-                    if ((in_chunk == 0 && !warp_agrees(scaled) && !warp_wait(&sh.sf_ready[f.slot], f.parity)) ||
+                    if ((!chunk_is_stage<F>() && in_chunk == 0 && !warp_wait(&sh.sf_ready[f.slot], f.parity)) ||
                         (!warp_agrees(here) && !warp_wait(&sh.full[s], r.parity))) {
                         bad = true;
                         break;
                     }
                     r.next(ns);
-                    here = mbar_ask(&sh.full[r.slot], r.parity);
-                    if (in_chunk == chunk_stages<F>() - 1 || i + 1 == a.nkb)
-                        scaled = mbar_ask(&sh.sf_ready[f.slot + 1 == kSfBufs ? 0 : f.slot + 1],
-                                          f.slot + 1 == kSfBufs ? f.parity ^ 1u : f.parity);
                     tc_fence_after();
                     const int nk = min(F::kSfTiles, a.kb - F::kSfTiles * i);
                     const uint32_t a0 = desc_lo(smem_u32(sA) + s * kPairABytes);
@@ -339,8 +340,9 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_linear_pair(const __grid_co
                     if (elected) {
                         pair_stage<F>(acc, a0, b0, sf + 4 * in_chunk, sf + 16 + 6 * in_chunk, nk, i > 0);
                         pair_commit(&sh.empty[s]);
-                        if (last) pair_commit(&sh.sf_free[f.slot]);
+                        if (!chunk_is_stage<F>() && last) pair_commit(&sh.sf_free[f.slot]);
                     }
+                    here = mbar_ask(&sh.full[r.slot], r.parity);
                     __syncwarp();
                     if (last) f.next(kSfBufs);
                 }
@@ -390,7 +392,10 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_linear_pair(const __grid_co
         // six of the tile's 192 rows to columns 16 + 6 kk ...
         const int q = warp & 3;
         const uint32_t lane_base = tmem + kPairSfCol + ((uint32_t)(32 * q) << 16);
+        const uint32_t full0 = map_rank(smem_u32(&sh.full[0]), 0);
+        const uint32_t ready0 = map_rank(smem_u32(&sh.sf_ready[0]), 0);
         Ring f, d;          // shared-memory slots; tensor-memory buffers
+        Ring r, w;          // chunk_is_stage: its stage; the one whose buffer it takes over
         uint32_t chunks = 0;
         for (int t = first; t < tiles && !bad; t += step) {
             int32_t m0, n0;
@@ -418,11 +423,15 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_linear_pair(const __grid_co
                 }
                 __syncwarp();
                 if (lane == 0) bar_arrive(&sh.sf_empty[f.slot]);
-                if (chunks >= (uint32_t)kSfBufs && !warp_wait(&sh.sf_free[d.slot], d.parity ^ 1u)) {
-                    bad = true;
-                    break;
+                if (chunks >= (uint32_t)kSfBufs) {
+                    // the MMAs that read this buffer are done
+                    if (chunk_is_stage<F>() ? !warp_wait(&sh.empty[w.slot], w.parity)
+                                            : !warp_wait(&sh.sf_free[d.slot], d.parity ^ 1u)) {
+                        bad = true;
+                        break;
+                    }
+                    w.next(ns);
                 }
-                __syncwarp();
                 tc_fence_after();
                 const uint32_t col = lane_base + d.slot * kSfCols;
                 mma::tmem_st_x16(col, va);
@@ -431,7 +440,8 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_linear_pair(const __grid_co
                 asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) cluster_arrive(map_rank(smem_u32(&sh.sf_ready[d.slot]), 0));
+                if (lane == 0) cluster_arrive(chunk_is_stage<F>() ? full0 + 8 * r.slot : ready0 + 8 * d.slot);
+                r.next(ns);
                 ++chunks;
                 f.next(kSfSlots);
                 d.next(kSfBufs);
