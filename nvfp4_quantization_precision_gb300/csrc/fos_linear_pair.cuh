@@ -13,7 +13,9 @@
 //   warp 1     tensor memory; in CTA 0 it issues the pair's MMAs, whose
 //              completion frees the stage in both CTAs
 //   warps 2-5  scales: shared memory to tensor memory (tcgen05.st), a chunk at
-//              a time into a ring of three buffers, lane quadrant warp % 4
+//              a time into a ring of three buffers, lane quadrant warp % 4; NVFP4
+//              has a second group, warps 11-14, for every other chunk (one takes
+//              580 cycles a chunk, more than an NVFP4 stage's MMAs)
 //   warps 6-9  epilogue of the CTA's 128 tokens, lane quadrant warp % 4
 // Tensor memory: two accumulators of 192 columns (the epilogue of a tile runs
 // under the MMAs of the next) and the scale buffers of 40 columns (a: 4 per
@@ -40,7 +42,6 @@ namespace lin {
 
 constexpr int kPairM = 256, kPairN = 192;
 constexpr int kPairABytes = 128 * kRowBytes, kPairBBytes = 96 * kRowBytes;
-constexpr int kPairThreads = 352;
 constexpr int kPairMaxStages = 8;
 constexpr int kChunkBytes = 32 * 128;
 constexpr int kPairGroupM = 8;     // tile rows per band of the tile order
@@ -51,7 +52,13 @@ constexpr int kPairStageBytes = kPairABytes + kPairBBytes;
 // row tiles, one stage of F4 or four of F8.
 constexpr int kSfChunkTiles = 4;
 constexpr int kSfChunkA = kSfChunkTiles * kSfTileBytes, kSfChunkBytes = 3 * kSfChunkA;
-constexpr int kSfSlots = 3;   // chunks in shared memory
+// Groups of scale warps, and chunks in shared memory: a slot belongs to one
+// group (the slots are a multiple of the groups), so that the waits for a slot's
+// phases are all made by warps that have seen the phase before.
+template <class F> constexpr int sf_groups() { return F::kGlobal ? 2 : 1; }
+template <class F> constexpr int sf_slots() { return F::kGlobal ? 4 : 3; }
+constexpr int kSfMaxSlots = 4;
+template <class F> constexpr int pair_threads() { return 352 + 128 * (sf_groups<F>() - 1); }
 constexpr int kSfBufs = 3;    // chunks in tensor memory
 constexpr int kSfCols = 16 + 24;
 static_assert(kPairSfCol + kSfBufs * kSfCols <= (int)kAllColumns, "tensor memory");
@@ -80,7 +87,7 @@ struct PairArgs {
 
 struct __align__(8) PairShared {
     uint64_t full[kPairMaxStages], empty[kPairMaxStages], acc_full[2], acc_empty[2], done;
-    uint64_t sf_full[kSfSlots], sf_empty[kSfSlots], sf_ready[kSfBufs], sf_free[kSfBufs];
+    uint64_t sf_full[kSfMaxSlots], sf_empty[kSfMaxSlots], sf_ready[kSfBufs], sf_free[kSfBufs];
     uint64_t res_full[4][2];
     uint32_t tmem;
     int fail;
@@ -223,7 +230,7 @@ __device__ __forceinline__ void pair_stage(uint32_t acc, uint32_t a0, uint32_t b
 }
 
 template <class F, Out OT>
-__global__ void __launch_bounds__(kPairThreads, 1) k_linear_pair(const __grid_constant__ PairArgs a) {
+__global__ void __launch_bounds__(pair_threads<F>(), 1) k_linear_pair(const __grid_constant__ PairArgs a) {
     extern __shared__ __align__(1024) unsigned char s_raw[];
     __shared__ PairShared sh;
     unsigned char* base = s_raw + ((1024u - (smem_u32(s_raw) & 1023u)) & 1023u);
@@ -231,6 +238,8 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_linear_pair(const __grid_co
     unsigned char* sA = base;
     unsigned char* sB = sA + ns * kPairABytes;
     unsigned char* sC = sB + ns * kPairBBytes;       // epilogue chunks
+    static_assert(sf_slots<F>() % sf_groups<F>() == 0, "a slot belongs to one group");
+    constexpr int kSfSlots = sf_slots<F>();
     unsigned char* sS = sC + 4 * a.bufs * kChunkBytes;  // scale chunks: a, then b's two row tiles
     const int warp = (int)uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
     const int rank = (int)uniform(cluster_rank());
@@ -386,7 +395,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_linear_pair(const __grid_co
             }
             if (!warp_wait(&sh.sf_empty[sl], p)) bad = true;
         }
-    } else if (warp < 6) {
+    } else if (warp < 6 || warp > 10) {
         // scales: lane l of quadrant q writes row l of each 16-byte-wide tile,
         // a's four words to columns 4 kk ..., of b's eight (two row tiles) the
         // six of the tile's 192 rows to columns 16 + 6 kk ...
@@ -396,12 +405,21 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_linear_pair(const __grid_co
         const uint32_t ready0 = map_rank(smem_u32(&sh.sf_ready[0]), 0);
         Ring f, d;          // shared-memory slots; tensor-memory buffers
         Ring r, w;          // chunk_is_stage: its stage; the one whose buffer it takes over
+        const uint32_t mine = warp < 6 ? 0u : 1u;  // the group
         uint32_t chunks = 0;
         for (int t = first; t < tiles && !bad; t += step) {
             int32_t m0, n0;
             pair_tile(a, t, m0, n0);
             const bool half = (n0 & 127) != 0;  // b starts half-way into a scale tile
             for (int i = 0; i < a.nkb; i += chunk_stages<F>()) {
+                if (chunks % sf_groups<F>() != mine) {
+                    if (chunks >= (uint32_t)kSfBufs) w.next(ns);
+                    ++chunks;
+                    r.next(ns);
+                    f.next(kSfSlots);
+                    d.next(kSfBufs);
+                    continue;
+                }
                 if (!warp_wait(&sh.sf_full[f.slot], f.parity)) {
                     bad = true;
                     break;

@@ -192,16 +192,16 @@ cudaError_t pair_go(const LinearCall& c, cudaStream_t s) {
     a.tiles_m = (int)((c.M + kPairM - 1) / kPairM);
     a.tiles_n = (int)((c.N + kPairN - 1) / kPairN);
     a.bufs = c.ep.pre ? 4 : 2;
-    const int other = 4 * a.bufs * kChunkBytes + kSfSlots * kSfChunkBytes + 4 * kPairN * 4;
+    const int other = 4 * a.bufs * kChunkBytes + sf_slots<F>() * kSfChunkBytes + 4 * kPairN * 4;
     a.stages = (kSmemLimit - 2048 - other) / kPairStageBytes;
     const int smem = a.stages * kPairStageBytes + other + 1024;
     auto k = k_linear_pair<F, OT>;
     cudaError_t e = allow_smem(reinterpret_cast<const void*>(k), (size_t)kSmemLimit - 1024);
     if (e != cudaSuccess) return e;
     const int tiles = a.tiles_m * a.tiles_n;
-    int clusters = resident_clusters(k, kPairThreads, smem, 2);
+    int clusters = resident_clusters(k, pair_threads<F>(), smem, 2);
     if (clusters > tiles) clusters = tiles;
-    return launch_clusters(k, clusters, 2, kPairThreads, smem, a, s);
+    return launch_clusters(k, clusters, 2, pair_threads<F>(), smem, a, s);
 }
 
 template <class F, Out OT>
