@@ -522,8 +522,11 @@ def _data(t, name):
     return shape, dt, t.get_device()
 
 
+_DEVICES = [torch.device("cuda", i) for i in range(64)]
+
+
 def _new(shape, dtype, dev):
-    return torch.empty(shape, dtype=dtype, device=torch.device("cuda", dev))
+    return torch.empty(shape, dtype=dtype, device=_DEVICES[dev])
 
 
 def _weight(w, cols, dtype, dev):
@@ -624,8 +627,8 @@ def rms_norm_backward(dy, h, rstd, weight, dh=None, weight_grad=True, dx=None, d
             dweight = _new((C,), torch.float32, dev)
         else:
             _like(dweight, "dweight", (C,), torch.float32, dev)
-        workspace, nws = _workspace(workspace, lib().fos_rms_norm_backward_workspace_bytes(R, C),
-                                    dev)
+        # fos_rms_norm_backward_workspace_bytes, without the call
+        workspace, nws = _workspace(workspace, 0 if R <= 1 else min(R, 1024) * C * 4, dev)
     else:
         dweight = workspace = None
     _check(lib().fos_rms_norm_backward(dy.data_ptr(), h.data_ptr(), _a(dh), rstd.data_ptr(),
@@ -689,7 +692,8 @@ def act_backward(dout, pre, act, scale_tiled=True, rowwise=True, colwise=True, v
             dbias = _new((C,), torch.float32, dev)
         else:
             _like(dbias, "dbias", (C,), torch.float32, dev)
-        workspace, nws = _workspace(workspace, lib().fos_act_backward_workspace_bytes(R, C), dev)
+        # fos_act_backward_workspace_bytes, without the call
+        workspace, nws = _workspace(workspace, 0 if R <= 128 else (R + 127) // 128 * C * 4, dev)
     else:
         dbias = workspace = None
     _check(lib().fos_act_backward(dout.data_ptr(), _a(pre), dt, R, C, a, 1 if scale_tiled else 0,

@@ -120,7 +120,7 @@ def test_epilogues(fmt, act, dt):
 
 @pytest.mark.parametrize("fmt", [8, 4])
 @pytest.mark.parametrize("M,N,K", [(1, 256, 16384), (7, 14336, 512), (40, 4096, 14336),
-                                   (700, 4096, 4096), (2049, 2048, 1024)])
+                                   (300, 1024, 16384), (700, 4096, 4096), (2049, 2048, 1024)])
 def test_long_and_wide(fmt, M, N, K):
     _case(fmt, M, N, K, "gelu_tanh", True, True, False, row=True)
 
@@ -265,3 +265,56 @@ def test_refusals():
     w, _ = _operand(4, _rand(64, 128, 1))
     with pytest.raises(ValueError):
         fos.linear4(*q, *w)  # per-row amax without row_scaled
+
+
+@pytest.mark.parametrize("fmt", [8, 4])
+@pytest.mark.parametrize("M,N,K", [(2500, 4096, 1024), (3000, 2304, 4096), (200, 14336, 2048),
+                                   (64, 4096, 4096)])
+def test_many_calls_one_answer(fmt, M, N, K):
+    """Products of many tiles back to back, other products between them: every
+    repeat equals the first bit for bit."""
+    a, _ = _operand(fmt, _rand(M, K, 1))
+    b, _ = _operand(fmt, _rand(N, K, 2))
+    a2, _ = _operand(fmt, _rand(17, K, 3))
+    res = _rand(M, N, 4).to(BF16)
+    one = _call(fmt, a, b, act="silu", residual=res)
+    outs = []
+    for _ in range(12):
+        _call(fmt, a2, b)
+        outs.append(_call(fmt, a, b, act="silu", residual=res))
+    for o in outs:
+        assert torch.equal(one, o)
+
+
+def test_outputs_past_2_to_the_31_elements():
+    """150,000 x 14,336 outputs (2.15e9): the last rows equal those of a product
+    of the last rows alone."""
+    M, N, K = 150000, 14336, 128
+    x = _rand(M, K, 1)
+    a, _ = _operand_codes(x)
+    b, _ = _operand_codes(_rand(N, K, 2))
+    out = fos.linear8(*a, *b, act="relu", out_dtype=BF16)
+    r0 = (M - 300) // 128 * 128
+    tail, _ = _operand_codes(x[r0:].contiguous())
+    assert torch.equal(out[r0:], fos.linear8(*tail, *b, act="relu", out_dtype=BF16))
+
+
+def _operand_codes(x):
+    c, s, _, _ = fos.quantize8(x)
+    return (c, s), None
+
+
+def test_ffn_block_example():
+    """The example's training step and decode step: results of 8-bit operands
+    are within a few hundredths of the unquantized block's (an E4M3 operand is
+    off by 2^-5 at most, 0.02 to 0.03 on average; NVFP4 by about 0.1)."""
+    import importlib.util
+    import os
+    p = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "ffn_block.py")
+    spec = importlib.util.spec_from_file_location("ffn_block", p)
+    m = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(m)
+    for act, tokens in (("gelu_tanh", 333), ("silu", 64)):
+        err = m.run(tokens, 512, 1536, act)
+        for k, v in err.items():
+            assert v < (0.3 if "NVFP4" in k else 0.1), (act, k, v)

@@ -390,3 +390,21 @@ def test_refusals():
                                            ctypes.c_void_p(x.data_ptr()),
                                            ctypes.c_void_p(x.data_ptr()), None, None, None), "q")
     assert e.value.status == fos.FOS_ERR_MISALIGNED
+
+
+def test_past_2_to_the_31_elements():
+    """540,672 x 4096 (2.2e9 elements): the last rows of the norm and of both
+    quantized forms equal those of the last rows alone."""
+    R, C = 540672, 4096
+    x = torch.empty(R, C, dtype=BF16, device=DEV)
+    for r in range(0, R, 67584):
+        x[r:r + 67584] = _rand(67584, C, BF16, r)
+    w = torch.ones(C, device=DEV)
+    tail = x[R - 256:].contiguous()
+    got, one = fos.rms_norm(x, w, scale_tiled=False), fos.rms_norm(tail, w, scale_tiled=False)
+    assert torch.equal(got[0][R - 256:], one[0]) and torch.equal(got[1][R - 256:], one[1])
+    assert torch.equal(got[4][R - 256:], one[4])
+    q, p = fos.quantize8(x, scale_tiled=False, colwise=True), fos.quantize8(tail, scale_tiled=False,
+                                                                           colwise=True)
+    assert torch.equal(q[0][R - 256:], p[0]) and torch.equal(q[2][:, R - 256:], p[2])
+    assert torch.equal(q[1][R - 256:], p[1]) and torch.equal(q[3][:, (R - 256) // 32:], p[3])
