@@ -452,27 +452,38 @@ __global__ void __launch_bounds__(kRowsThreads, 1) k_linear_rows(const __grid_co
         }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    chain_wait();
-    chain_release();
-    if (warp == 1) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
-                         smem_u32(&sh.tmem)), "r"(kAllColumns) : "memory");
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-    }
-    tc_fence_before();
-    __syncwarp();
-    __syncthreads();
-    tc_fence_after();
-    const uint32_t tmem = uniform(sh.tmem);
+    // everything that needs no data of the kernel before comes before the wait
+    // for it (that kernel is still running: six stages leave room for this CTA)
+    const bool elected = elect_lane();
     uint32_t g = 0;   // stages loaded (warps 0, 6) or consumed (warp 1) so far
     Ring r, w;        // the stage in work; warp 1: the one whose scales are overwritten
-    const bool elected = elect_lane();
     bool bad = false;
     bool here = false, free = false;  // warp 1: the next stage is full, its scale buffer is free
     int j = 0;        // tiles of this CTA so far
+    int tq = first / a.tiles_p, tp = first - tq * a.tiles_p;
+    __syncwarp();
+    __syncthreads();
+    chain_wait();
+    chain_release();
+    uint32_t tmem = 0;
+    if (warp != 0 && warp != 6) {  // the producers need no tensor memory
+        if (warp == 1) {
+            asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                             smem_u32(&sh.tmem)), "r"(kAllColumns) : "memory");
+            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+        }
+        tc_fence_before();
+        __syncwarp();
+        asm volatile("bar.sync 1, 160;" ::: "memory");
+        tc_fence_after();
+        tmem = uniform(sh.tmem);
+    }
     for (int t = first; t < a.tiles; t += step, ++j) {
-        const int tq = t / a.tiles_p;
-        const int n0 = (t - tq * a.tiles_p) * 128, m0 = tq * nt;
+        if (j > 0) {
+            tq = t / a.tiles_p;
+            tp = t - tq * a.tiles_p;
+        }
+        const int n0 = tp * 128, m0 = tq * nt;
         if (warp == 0) {
             for (int i = k_lo; i < k_hi && !bad; ++i) {
                 const int s = r.slot;
@@ -570,6 +581,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1) k_linear_rows(const __grid_co
                                                       a.ep.six_bound));
             }
             if (!bad && !warp_wait(&sh.acc_full, (uint32_t)j & 1)) bad = true;
+            if (bad) sh.fail = 1;
             __syncwarp();
             tc_fence_after();
             // the partial tile to shared memory, a row per token
@@ -587,8 +599,11 @@ __global__ void __launch_bounds__(kRowsThreads, 1) k_linear_rows(const __grid_co
                 const Tile t4{red, s_ga, m0, mt, rank + S * e, lane, n, a.N, gb};
                 if (S == 1) finish_tokens<F, OT, 4, 1>(a.ep, t4, bias);
                 else if (S == 2) finish_tokens<F, OT, 4, 2>(a.ep, t4, bias);
-                else if (S == 4) finish_tokens<F, OT, 2, 4>(a.ep, t4, bias);
-                else finish_tokens<F, OT, 2, 8>(a.ep, t4, bias);
+                else if (S == 8) finish_tokens<F, OT, 2, 8>(a.ep, t4, bias);
+                // (4096 x 14336 NVFP4: 16 tokens 9.8 us two at a time, 10.4 four at
+                // a time; 48 tokens 11.5 and 11.0)
+                else if (mt <= 32) finish_tokens<F, OT, 2, 4>(a.ep, t4, bias);
+                else finish_tokens<F, OT, 4, 4>(a.ep, t4, bias);
             }
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             tile_sync(S);  // every partial has been read: the ring is free again
@@ -600,8 +615,10 @@ __global__ void __launch_bounds__(kRowsThreads, 1) k_linear_rows(const __grid_co
             tc_fence_after();
         }
     }
-    // drain: every copy and MMA issued has completed before the CTA leaves
-    if (warp == 0) {
+    // Every copy and MMA issued has completed before the CTA leaves: the epilogue
+    // has seen each tile's accumulator full, so there is something to wait for
+    // only where a wait gave up.
+    if ((bad || sh.fail) && warp == 0) {
         for (int k = 0; k < ns && (uint32_t)k < g; ++k) {
             int sl = r.slot - 1 - k;
             uint32_t p = r.parity;
@@ -611,7 +628,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1) k_linear_rows(const __grid_co
             }
             if (!warp_wait(&sh.full[sl], p)) bad = true;
         }
-    } else if (warp == 1) {
+    } else if ((bad || sh.fail) && warp == 1) {
         if (elected) tc_commit(&sh.done);
         __syncwarp();  // no lane waits before the elected one has asked
         if (!warp_wait(&sh.done, 0)) bad = true;
