@@ -44,6 +44,7 @@ struct Quant8Args {
     int64_t tiles_c;
     int64_t pc4, pc4_t;  // tiled scales: 4-block tiles per tile-row
     int tiled;
+    int wave;            // CTAs the device holds at once
 };
 
 constexpr int kQ8Tile = 128;  // rows and columns of a tile
@@ -53,6 +54,10 @@ constexpr size_t kQ8Smem = kQ8Tile * kQ8Tile * sizeof(float);
 // 16-byte chunk of column c in a row of row group rb.
 __device__ __forceinline__ int q8_chunk(int c, int rb) {
     return (((c >> 2) ^ ((c >> 5) & 3)) + 2 * rb) & 31;
+}
+
+__device__ __forceinline__ void prefetch_l2(const void* p) {
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
 }
 
 template <In IT, Act A>
@@ -123,6 +128,24 @@ __global__ void __launch_bounds__(kQ8Threads, 3) k_quant8(const Quant8Args a) {
                     upk(d[2 * k + 1], v.z, v.w);
                     *reinterpret_cast<float4*>(line + 4 * q8_chunk(seg * 16 + 4 * k, i)) = v;
                 }
+            }
+        }
+    }
+    {
+        // the tile a wave from here on its way to L2, one row's half a thread:
+        // its CTA then loads it at L2's latency (14336 x 4096 bf16: 44.6 -> 41.3
+        // us, the silu gradient of 8192 x 14336: 133 -> 122 us)
+        const int64_t nt = (int64_t)blockIdx.x + a.wave, ntr = nt / a.tiles_c, ntc = nt - ntr * a.tiles_c;
+        const int64_t row = ntr * kQ8Tile + (tid >> 1);
+        const int64_t c = ntc * kQ8Tile + (tid & 1) * (kQ8Tile / 2);
+        if (row < a.rows && c < a.cols) {
+            const int64_t at = (row * a.cols + c) * kElt;
+#pragma unroll
+            for (int l = 0; l < kElt / 2; ++l) {
+                if (c + l * (128 / kElt) >= a.cols) break;
+                prefetch_l2(static_cast<const char*>(a.x) + at + 128 * l);
+                if constexpr (A != Act::NONE)
+                    prefetch_l2(static_cast<const char*>(a.pre) + at + 128 * l);
             }
         }
     }

@@ -13,7 +13,9 @@ cudaError_t go(const Quant8Args& a, cudaStream_t s) {
     const cudaError_t e = allow_smem(reinterpret_cast<const void*>(k), kQ8Smem);
     if (e != cudaSuccess) return e;
     const int64_t tiles = (a.rows + kQ8Tile - 1) / kQ8Tile * a.tiles_c;
-    return launch_chained(k, dim3((unsigned)tiles), kQ8Threads, kQ8Smem, s, a);
+    Quant8Args b = a;
+    b.wave = sm_count() * resident_ctas_of(k, kQ8Threads, kQ8Smem);
+    return launch_chained(k, dim3((unsigned)tiles), kQ8Threads, kQ8Smem, s, b);
 }
 
 template <In IT>
