@@ -48,23 +48,28 @@ __device__ __forceinline__ void two_sum(float a, float b, float& s, float& e) {
     e = fadd(__fsub_rn(a, __fsub_rn(s, t)), __fsub_rn(b, t));
 }
 
-// Sum over a warp, every lane gets the same value: the lanes' errors are
-// carried along, so the sum is as exact as its fp32 terms.  The codes that
+// Sum over the first kLanes lanes of each such group, every lane gets the same
+// value (the sum and its error are the same in either order): the lanes' errors
+// are carried along, so the sum is as exact as its fp32 terms.  The codes that
 // follow jump by 1/16 where y crosses a rounding boundary, and every bit that
 // rstd is off moves the boundary for a whole row.
-__device__ __forceinline__ float2 warp_sum2(float hi, float lo) {
+template <int kLanes>
+__device__ __forceinline__ float2 lanes_sum2(float hi, float lo) {
 #pragma unroll
-    for (int m = 16; m >= 1; m >>= 1) {
+    for (int m = kLanes / 2; m >= 1; m >>= 1) {
         const float oh = __shfl_xor_sync(0xFFFFFFFFu, hi, m);
         const float ol = __shfl_xor_sync(0xFFFFFFFFu, lo, m);
-        float s, e;
-        // both partners add the same two numbers in the same order
-        if ((threadIdx.x & m) == 0) two_sum(hi, oh, s, e);
-        else two_sum(oh, hi, s, e);
-        hi = s;
+        float e;
+        two_sum(hi, oh, hi, e);
         lo = fadd(fadd(lo, ol), e);
     }
     return make_float2(hi, lo);
+}
+// The sum of kW warps' sums in shared memory, in every lane.
+template <int kW>
+__device__ __forceinline__ float2 parts_sum2(const float2* part) {
+    const float2 v = part[threadIdx.x & (kW - 1)];
+    return lanes_sum2<kW>(v.x, v.y);
 }
 
 // 1 / sqrt(m) as a pair: an approximation r (a few ulp) and the correction of
@@ -197,20 +202,12 @@ __global__ void __launch_bounds__(kT < 256 ? 256 : kT) k_rms_norm(const NormArgs
         float p0, p1, p2, p3;
         upk(a0, p0, p1);
         upk(a1, p2, p3);
-        float2 s = warp_sum2(fadd(fadd(p0, p1), fadd(p2, p3)), 0.0f);
+        float2 s = lanes_sum2<32>(fadd(fadd(p0, p1), fadd(p2, p3)), 0.0f);
         if constexpr (kW > 1) {
             const int wid = threadIdx.x >> 5;
             if ((threadIdx.x & 31) == 0) s_part[parity][wid] = s;
             __syncthreads();
-            float hi = 0.0f, lo = 0.0f;
-#pragma unroll
-            for (int i = 0; i < kW; ++i) {
-                const float2 o = s_part[parity][g * kW + i];
-                float e;
-                two_sum(hi, o.x, hi, e);
-                lo = fadd(lo, fadd(o.y, e));
-            }
-            s = make_float2(hi, lo);
+            s = parts_sum2<kW>(s_part[parity] + g * kW);
         }
         // mean + eps as a pair
         const float mh = fmul(s.x, a.inv_cols);
@@ -254,20 +251,13 @@ __global__ void __launch_bounds__(512) k_rms_norm_wide(const NormArgs a) {
             two_sum(hi, fadd(fadd(p0, p1), fadd(p2, p3)), hi, e);
             lo = fadd(lo, e);
         }
-        float2 s = warp_sum2(hi, lo);
+        float2 s = lanes_sum2<32>(hi, lo);
         if ((t & 31) == 0) s_part[parity][t >> 5] = s;
         __syncthreads();
-        hi = lo = 0.0f;
-#pragma unroll
-        for (int i = 0; i < kT / 32; ++i) {
-            const float2 o = s_part[parity][i];
-            float e;
-            two_sum(hi, o.x, hi, e);
-            lo = fadd(lo, fadd(o.y, e));
-        }
-        const float mh = fmul(hi, a.inv_cols);
-        float mlo = __fmaf_rn(hi, a.inv_cols, -mh);
-        mlo = __fmaf_rn(lo, a.inv_cols, mlo);
+        s = parts_sum2<kT / 32>(s_part[parity]);
+        const float mh = fmul(s.x, a.inv_cols);
+        float mlo = __fmaf_rn(s.x, a.inv_cols, -mh);
+        mlo = __fmaf_rn(s.y, a.inv_cols, mlo);
         float m, e;
         two_sum(mh, a.eps, m, e);
         const float2 rs = rsqrt2(m, fadd(e, mlo));
