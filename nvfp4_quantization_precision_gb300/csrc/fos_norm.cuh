@@ -41,48 +41,25 @@ struct NormArgs {
     int tiled;
 };
 
-// a + b with its rounding error (D. Knuth, TAOCP vol. 2, 4.2.2, theorem B).
-__device__ __forceinline__ void two_sum(float a, float b, float& s, float& e) {
-    s = fadd(a, b);
-    const float t = __fsub_rn(s, a);
-    e = fadd(__fsub_rn(a, __fsub_rn(s, t)), __fsub_rn(b, t));
-}
-
-// Sum over the first kLanes lanes of each such group, every lane gets the same
-// value (the sum and its error are the same in either order): the lanes' errors
-// are carried along, so the sum is as exact as its fp32 terms.  The codes that
-// follow jump by 1/16 where y crosses a rounding boundary, and every bit that
-// rstd is off moves the boundary for a whole row.
+// Sum over groups of kLanes lanes (a fixed tree; every lane gets it).
 template <int kLanes>
-__device__ __forceinline__ float2 lanes_sum2(float hi, float lo) {
+__device__ __forceinline__ float lanes_sum(float v) {
 #pragma unroll
-    for (int m = kLanes / 2; m >= 1; m >>= 1) {
-        const float oh = __shfl_xor_sync(0xFFFFFFFFu, hi, m);
-        const float ol = __shfl_xor_sync(0xFFFFFFFFu, lo, m);
-        float e;
-        two_sum(hi, oh, hi, e);
-        lo = fadd(fadd(lo, ol), e);
-    }
-    return make_float2(hi, lo);
+    for (int m = kLanes / 2; m >= 1; m >>= 1) v = fadd(v, __shfl_xor_sync(0xFFFFFFFFu, v, m));
+    return v;
 }
 // The sum of kW warps' sums in shared memory, in every lane.
 template <int kW>
-__device__ __forceinline__ float2 parts_sum2(const float2* part) {
-    const float2 v = part[threadIdx.x & (kW - 1)];
-    return lanes_sum2<kW>(v.x, v.y);
+__device__ __forceinline__ float parts_sum(const float* part) {
+    return lanes_sum<kW>(part[threadIdx.x & (kW - 1)]);
 }
 
-// 1 / sqrt(m) as a pair: an approximation r (a few ulp) and the correction of
-// one Newton step from the exact residual 1 - m r^2, m = mh + ml.
-__device__ __forceinline__ float2 rsqrt2(float mh, float ml) {
-    const float r = rsqrtf(mh);
-    const float t = fmul(mh, r), tl = __fmaf_rn(mh, r, -t);       // mh * r = t + tl
-    float e = __fmaf_rn(-t, r, 1.0f);                             // 1 - mh r^2
-    e = __fmaf_rn(-tl, r, e);
-    e = __fmaf_rn(-fmul(ml, r), r, e);
-    const float lo = fmul(fmul(0.5f, r), e);
+// 1 / sqrt(m): the hardware's approximation (2 ulp) and one Newton step.
+__device__ __forceinline__ float rsqrt1(float m) {
+    const float r = rsqrtf(m);
+    const float e = __fmaf_rn(-fmul(m, r), r, 1.0f);
     // a zero or infinite mean has no finite correction
-    return make_float2(r, isfinite(lo) ? lo : 0.0f);
+    return isfinite(e) ? __fmaf_rn(fmul(0.5f, r), e, r) : r;
 }
 
 // Sum of the squares of 16 values, added to two packed accumulators.
@@ -94,24 +71,22 @@ __device__ __forceinline__ void add_squares(const uint64_t (&v)[8], uint64_t& a0
     }
 }
 
-// y = h * (rstd * w) with the products' rounding errors folded into one final
-// rounding: rstd = r.x + r.y.
-__device__ __forceinline__ void normed(const uint64_t (&h)[8], const uint64_t (&w)[8], float2 r,
+// y = (h * rstd) * w, a rounding each.  (Carrying the sum's and the products'
+// rounding errors along changes 20 of 29 M codes instead of 22 against the exact
+// ones: y's own last rounding decides those, and the extra operations cost 10 %
+// of an 8192 x 4096 pass without a residual.)
+__device__ __forceinline__ void normed(const uint64_t (&h)[8], const uint64_t (&w)[8], float r,
                                        uint64_t (&y)[8]) {
-    const uint64_t rh = pk(r.x, r.x), rl = pk(r.y, r.y), neg = pk(-1.0f, -1.0f);
+    const uint64_t r2 = pk(r, r);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        const uint64_t p = mul2(w[j], rh);
-        const uint64_t q = fma2(w[j], rl, fma2(w[j], rh, mul2(p, neg)));
-        y[j] = fma2(h[j], p, mul2(h[j], q));
-    }
+    for (int j = 0; j < 8; ++j) y[j] = mul2(mul2(h[j], r2), w[j]);
 }
 
 // Outputs of one segment of a finished row; every lane of a pair takes part.
 template <In IT>
 __device__ __forceinline__ void emit_norm(const NormArgs& a, int64_t row, int64_t seg, bool in,
                                           const uint64_t (&h)[8], const uint64_t (&w)[8],
-                                          float2 r) {
+                                          float r) {
     constexpr int64_t kElt = (IT == In::F32) ? 4 : 2;
     uint64_t y[8];
     normed(h, w, r, y);
@@ -164,7 +139,7 @@ __global__ void __launch_bounds__(kT < 256 ? 256 : kT) k_rms_norm(const NormArgs
     constexpr int kCta = kT < 256 ? 256 : kT;      // threads of a CTA
     constexpr int kGroups = kCta / kT;             // rows of a CTA at a time
     constexpr int kW = kT / 32;                    // warps of a row
-    __shared__ float2 s_part[2][kCta / 32];
+    __shared__ float s_part[2][kCta / 32];
     const int t = threadIdx.x % kT, g = threadIdx.x / kT;
     const int64_t nseg = a.cols / 16;
     const int64_t step = (int64_t)gridDim.x * kGroups;
@@ -202,21 +177,15 @@ __global__ void __launch_bounds__(kT < 256 ? 256 : kT) k_rms_norm(const NormArgs
         float p0, p1, p2, p3;
         upk(a0, p0, p1);
         upk(a1, p2, p3);
-        float2 s = lanes_sum2<32>(fadd(fadd(p0, p1), fadd(p2, p3)), 0.0f);
+        float s = lanes_sum<32>(fadd(fadd(p0, p1), fadd(p2, p3)));
         if constexpr (kW > 1) {
             const int wid = threadIdx.x >> 5;
             if ((threadIdx.x & 31) == 0) s_part[parity][wid] = s;
             __syncthreads();
-            s = parts_sum2<kW>(s_part[parity] + g * kW);
+            s = parts_sum<kW>(s_part[parity] + g * kW);
         }
-        // mean + eps as a pair
-        const float mh = fmul(s.x, a.inv_cols);
-        float mlo = __fmaf_rn(s.x, a.inv_cols, -mh);
-        mlo = __fmaf_rn(s.y, a.inv_cols, mlo);
-        float m, e;
-        two_sum(mh, a.eps, m, e);
-        const float2 rs = rsqrt2(m, fadd(e, mlo));
-        if (t == 0 && a.rstd && row < a.rows) a.rstd[row] = fadd(rs.x, rs.y);
+        const float rs = rsqrt1(__fmaf_rn(s, a.inv_cols, a.eps));
+        if (t == 0 && a.rstd && row < a.rows) a.rstd[row] = rs;
 #pragma unroll
         for (int k = 0; k < kSeg; ++k)
             emit_norm<IT>(a, row, t + k * kT, in[k] && row < a.rows, h[k], w[k], rs);
@@ -230,7 +199,7 @@ __global__ void __launch_bounds__(512) k_rms_norm_wide(const NormArgs a) {
     chain_wait();
     chain_release();
     constexpr int kT = 512;
-    __shared__ float2 s_part[2][kT / 32];
+    __shared__ float s_part[2][kT / 32];
     const int t = threadIdx.x;
     const int64_t nseg = a.cols / 16;
     if (a.tiled && a.codes)
@@ -238,30 +207,23 @@ __global__ void __launch_bounds__(512) k_rms_norm_wide(const NormArgs a) {
                         gridDim.x * kT);
     int parity = 0;
     for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, parity ^= 1) {
-        float hi = 0.0f, lo = 0.0f;
+        uint64_t a0 = 0, a1 = 0;
         for (int64_t sg = t; sg < nseg; sg += kT) {
             Raw<IT> x, r;
-            uint64_t h[8], a0 = 0, a1 = 0;
+            uint64_t h[8];
             load_row_seg<IT, RES>(a, row, sg, true, x, r);
             row_values<IT, RES>(x, r, h);
             add_squares(h, a0, a1);
-            float p0, p1, p2, p3, e;
-            upk(a0, p0, p1);
-            upk(a1, p2, p3);
-            two_sum(hi, fadd(fadd(p0, p1), fadd(p2, p3)), hi, e);
-            lo = fadd(lo, e);
         }
-        float2 s = lanes_sum2<32>(hi, lo);
+        float p0, p1, p2, p3;
+        upk(a0, p0, p1);
+        upk(a1, p2, p3);
+        float s = lanes_sum<32>(fadd(fadd(p0, p1), fadd(p2, p3)));
         if ((t & 31) == 0) s_part[parity][t >> 5] = s;
         __syncthreads();
-        s = parts_sum2<kT / 32>(s_part[parity]);
-        const float mh = fmul(s.x, a.inv_cols);
-        float mlo = __fmaf_rn(s.x, a.inv_cols, -mh);
-        mlo = __fmaf_rn(s.y, a.inv_cols, mlo);
-        float m, e;
-        two_sum(mh, a.eps, m, e);
-        const float2 rs = rsqrt2(m, fadd(e, mlo));
-        if (t == 0 && a.rstd) a.rstd[row] = fadd(rs.x, rs.y);
+        s = parts_sum<kT / 32>(s_part[parity]);
+        const float rs = rsqrt1(__fmaf_rn(s, a.inv_cols, a.eps));
+        if (t == 0 && a.rstd) a.rstd[row] = rs;
         for (int64_t base = 0; base < nseg; base += kT) {  // whole warps for the block shuffles
             const int64_t sg = base + t;
             const bool in = sg < nseg;
@@ -305,12 +267,6 @@ __device__ __forceinline__ void load_bwd_seg(const NormBwdArgs& a, int64_t at, b
         zero_seg(h);
         if constexpr (DH) zero_seg(dh);
     }
-}
-
-__device__ __forceinline__ float warp_sum(float v) {
-#pragma unroll
-    for (int m = 16; m >= 1; m >>= 1) v = fadd(v, __shfl_xor_sync(0xFFFFFFFFu, v, m));
-    return v;
 }
 
 // dx of one segment from g = dy * w: g rstd - h c, plus dh.
@@ -373,7 +329,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) k_rms_bwd(const NormBwdArgs a)
                                  h, dh);
         float p0, p1;
         upk(acc, p0, p1);
-        float s = warp_sum(fadd(p0, p1));
+        float s = lanes_sum<32>(fadd(p0, p1));
         if constexpr (kW > 1) {
             if ((threadIdx.x & 31) == 0) s_part[parity][threadIdx.x >> 5] = s;
             asm volatile("bar.sync %0, %1;" ::"r"(1 + g), "n"(kT) : "memory");
@@ -436,7 +392,7 @@ __global__ void __launch_bounds__(512) k_rms_bwd_wide(const NormBwdArgs a) {
         }
         float p0, p1;
         upk(acc, p0, p1);
-        float s = warp_sum(fadd(p0, p1));
+        float s = lanes_sum<32>(fadd(p0, p1));
         if ((t & 31) == 0) s_part[parity][t >> 5] = s;
         __syncthreads();
         s = 0.0f;

@@ -27,7 +27,7 @@ __global__ void __launch_bounds__(32 * kSumWarps) k_column_sums(const float* par
     __syncthreads();
     // warp w adds the 32 partial sums of column w (a fixed tree)
     float v = s_sum[lane][warp];
-    v = warp_sum(v);
+    v = lanes_sum<32>(v);
     const int64_t cw = (int64_t)blockIdx.x * 32 + warp;
     if (lane == 0 && cw < cols) out[cw] = v;
 }
@@ -72,14 +72,7 @@ cudaError_t norm_by_width(const NormArgs& a, cudaStream_t s) {
     if (nseg <= 32) return norm_go<IT, RES, 32, 1>(a, s);
     if (nseg <= 64) return norm_go<IT, RES, 32, 2>(a, s);
     if (nseg <= 128) return norm_go<IT, RES, 128, 1>(a, s);
-    if (nseg <= 256) {
-        // without a residual the reduction is most of a row's work: two segments
-        // a thread halve it (8192 x 4096 bf16: 26.9 -> 24.3 us; with a residual
-        // 40.2 -> 43.2).  The variant goes by the width alone, so that a row's
-        // result does not depend on the rows beside it.
-        if constexpr (RES) return norm_go<IT, RES, 256, 1>(a, s);
-        else return norm_go<IT, RES, 128, 2>(a, s);
-    }
+    if (nseg <= 256) return norm_go<IT, RES, 256, 1>(a, s);
     if (nseg <= 512) return norm_go<IT, RES, 256, 2>(a, s);
     if (nseg <= 1024) return norm_go<IT, RES, 512, 2>(a, s);
     auto k = k_rms_norm_wide<IT, RES>;
