@@ -6,16 +6,27 @@
 //   backward  g = dy * w; dx = rstd * g - h * (rstd^3 * mean(g * h)) + dh;
 //             dw[c] = sum over rows of dy * h * rstd
 //
-// Both are bound by HBM: forward 2 * e bytes read (x, residual), e + 1 + 1/32
-// written per element of e bytes (e with the residual), backward 2e or 3e read
-// and e written.  So a row is read once and lives in registers: a group of
-// kT threads owns a row, thread t the 16-element segments t, t + kT, ..., the
-// row's sum crosses the group by shuffles and one barrier, and the next row's
-// loads are issued before the current row is finished.  Two neighbouring lanes
-// hold one 32-element block.  kT is the smallest group that leaves at most two
-// segments (one in the backward pass, whose weight gradient takes 16 more
-// registers a segment) to a thread; rows of up to 1024 elements go one to a
-// warp, without a barrier.
+// Both are bound by HBM: forward e bytes read per element of e bytes (2 e with
+// the residual) and 1 + 1/32 written (e more for h), backward 2e or 3e read and
+// e written.  So a row is read once and lives in registers: a group of kT
+// threads owns a row, thread t the 16-element segments t, t + kT, ..., the row's
+// sum crosses the group by shuffles and one barrier, and the next row's loads are
+// issued before the current row is finished.  Two neighbouring lanes hold one
+// 32-element block.  A thread holds one or two segments (one in the backward
+// pass, whose weight gradient takes 16 more registers a segment); rows of up to
+// 1024 elements go one to a warp, without a barrier.
+//
+// Measured, against a device copy's 6.78 TB/s (bf16 unless named):
+//   forward   16384 x 7168 with residual, h, codes, scales: 127.5 us, 6.47 TB/s
+//             (95 %); 8192 x 4096 without residual and h: 19.4 us
+//   backward  8192 x 4096 with dh and dw: 44.9 us, 5.98 TB/s (88 %);
+//             1021 x 7168 fp32 without dh: 18.5 us, 4.77 TB/s (70 %; 6.7 rows a
+//             CTA, then 2.5 us for the sum of the weight gradient's partial rows)
+//   one row of 4096: 2.1 us, the chain of a launch, two reads of memory and a
+//             barrier
+// The variant goes by the row's width alone, so that a row's result does not
+// depend on how many others are with it.
+
 #pragma once
 
 #include "fos_block8.cuh"
@@ -71,15 +82,17 @@ __device__ __forceinline__ void add_squares(const uint64_t (&v)[8], uint64_t& a0
     }
 }
 
-// y = (h * rstd) * w, a rounding each.  (Carrying the sum's and the products'
-// rounding errors along changes 20 of 29 M codes instead of 22 against the exact
-// ones: y's own last rounding decides those, and the extra operations cost 10 %
-// of an 8192 x 4096 pass without a residual.)
+// y = (h * w) * rstd.  In this order the first product of 16-bit h and w is exact
+// in 32 bits, so that y carries rstd's error and one rounding of its own; h * rstd
+// first would round twice.  h * w leaves the range of 32 bits only where the row's
+// sum of squares already has, or with weights beyond 10^19.  (Carrying the sum's and the products' rounding errors
+// along as well saves 2 of 22 changed codes in 29 M and costs 10 % of an 8192 x 4096
+// pass without a residual.)
 __device__ __forceinline__ void normed(const uint64_t (&h)[8], const uint64_t (&w)[8], float r,
                                        uint64_t (&y)[8]) {
     const uint64_t r2 = pk(r, r);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) y[j] = mul2(mul2(h[j], r2), w[j]);
+    for (int j = 0; j < 8; ++j) y[j] = mul2(mul2(h[j], w[j]), r2);
 }
 
 // Outputs of one segment of a finished row; every lane of a pair takes part.
@@ -104,6 +117,12 @@ __device__ __forceinline__ void emit_norm(const NormArgs& a, int64_t row, int64_
         if ((seg & 1) == 0)
             st8(a.scales + scale8_at(a.tiled, row, seg >> 1, a.cols / 32, a.pc4), sc);
     }
+}
+
+// `bytes` from p on (both multiples of 16) on their way to L2.
+__device__ __forceinline__ void fetch_l2(const void* p, int64_t bytes) {
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"((uint32_t)bytes)
+                 : "memory");
 }
 
 template <In IT, bool RES>
@@ -131,7 +150,13 @@ __device__ __forceinline__ void row_values(const Raw<IT>& x, const Raw<IT>& r, u
     }
 }
 
-// A row per warp (kT = 32) or per CTA (kT = 64 .. 512 threads).
+// A row per warp (kT = 32) or per group of 64 .. 512 threads, CTAs of at least 256
+// threads.  Without a residual a row is small against the memory's latency (what
+// the next row's loads keep in flight is 24 KB an SM, and 5.3 TB/s with 800 ns take
+// 28), so the row after it is fetched to L2 as well (33.5 M elements without / with:
+// bf16, 2048 wide 25.8 / 22.4 us, 4096 21.5 / 19.4, 16384 21.9 / 20.3; fp32, 2048
+// wide 31.7 / 28.7, where rows of 4096 and more lose 0.4 to 1.3 us by it, as a
+// residual does: bf16 16384 x 7168 127 / 136).
 template <In IT, bool RES, int kT, int kSeg>
 __global__ void __launch_bounds__(kT < 256 ? 256 : kT) k_rms_norm(const NormArgs a) {
     chain_wait();
@@ -139,6 +164,7 @@ __global__ void __launch_bounds__(kT < 256 ? 256 : kT) k_rms_norm(const NormArgs
     constexpr int kCta = kT < 256 ? 256 : kT;      // threads of a CTA
     constexpr int kGroups = kCta / kT;             // rows of a CTA at a time
     constexpr int kW = kT / 32;                    // warps of a row
+    constexpr bool kFar = !RES && (IT != In::F32 || kT < 256);
     __shared__ float s_part[2][kCta / 32];
     const int t = threadIdx.x % kT, g = threadIdx.x / kT;
     const int64_t nseg = a.cols / 16;
@@ -174,6 +200,12 @@ __global__ void __launch_bounds__(kT < 256 ? 256 : kT) k_rms_norm(const NormArgs
             load_row_seg<IT, RES>(a, row + step, t + k * kT, in[k] && row + step < a.rows, x[k],
                                   r[k]);
         }
+        if constexpr (kFar) {
+            constexpr int kElt = (IT == In::F32) ? 4 : 2;
+            const int64_t far = row + 2 * step;
+            if (t == 0 && far < a.rows)
+                fetch_l2(static_cast<const char*>(a.x) + far * a.cols * kElt, a.cols * kElt);
+        }
         float p0, p1, p2, p3;
         upk(a0, p0, p1);
         upk(a1, p2, p3);
@@ -192,8 +224,9 @@ __global__ void __launch_bounds__(kT < 256 ? 256 : kT) k_rms_norm(const NormArgs
     }
 }
 
-// Rows of more than 16384 elements: a CTA per row reads it twice, the second
-// time from L2 (a row of x and residual is at most a few MB).
+// Rows of more than 16384 elements, which no longer fit a CTA's registers: a CTA
+// per row reads it twice, the second time from L2 (a row of x and residual is at
+// most a few MB).
 template <In IT, bool RES>
 __global__ void __launch_bounds__(512) k_rms_norm_wide(const NormArgs a) {
     chain_wait();
@@ -286,7 +319,10 @@ __device__ __forceinline__ void bwd_dx(const uint64_t (&g)[8], const uint64_t (&
 // threads holds 512 / kT groups.  The weight gradient of the thread's columns
 // is kept in registers over all of its rows and leaves as one partial row per
 // CTA (its groups are added in order through shared memory), so the sum has one
-// fixed order and the second kernel one partial row per SM to add.
+// fixed order and the second kernel one partial row per SM to add (CTAs of one
+// group, four an SM with a partial row each: 46.8 instead of 45.0 us for 8192 x
+// 4096).  512 threads because dw and a row in flight next to the row in work take
+// 128 registers a thread.
 constexpr int kBwdThreads = 512;
 template <In IT, int kT, bool DH>
 __global__ void __launch_bounds__(kBwdThreads, 1) k_rms_bwd(const NormBwdArgs a) {
@@ -450,7 +486,8 @@ __global__ void __launch_bounds__(256) k_rms_dw_wide(const NormBwdArgs a) {
 // ------------------------------------------------------------------ column sums
 // out[c] = sum over the `parts` partial rows, in a fixed order: a CTA takes 32
 // columns, its 32 warps every 32nd row each (eight of them in flight), and the
-// warps' sums are added by one tree.
+// warps' sums are added by one tree.  Bound by latency: 152 rows of 7168 (4.4 MB,
+// in L2) take about 2.5 us, started ahead of the kernel before's end.
 constexpr int kSumWarps = 32;
 __global__ void __launch_bounds__(32 * kSumWarps) k_column_sums(const float* part, int64_t parts,
                                                                 int64_t cols, float* out);

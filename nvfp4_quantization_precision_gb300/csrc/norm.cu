@@ -68,9 +68,13 @@ cudaError_t norm_go(const NormArgs& a, cudaStream_t s) {
 
 template <In IT, bool RES>
 cudaError_t norm_by_width(const NormArgs& a, cudaStream_t s) {
+    // 33.5 M elements, bf16 with a residual, this group and another (us): 512 wide
+    // 43.8 and 52.1 (64 threads, half of them idle); 1024 wide 40.9 and 43.9 (32, two
+    // segments); 2048 wide 40.5 and 43.0 (64, two); 4096 wide 38.6 and 42.5 (128,
+    // two); 8192 wide 38.8 and 40.5 (512, one); 16384 wide 39.1 and 40.9 (1024, one)
     const int64_t nseg = a.cols / 16;
     if (nseg <= 32) return norm_go<IT, RES, 32, 1>(a, s);
-    if (nseg <= 64) return norm_go<IT, RES, 32, 2>(a, s);
+    if (nseg <= 64) return norm_go<IT, RES, 64, 1>(a, s);
     if (nseg <= 128) return norm_go<IT, RES, 128, 1>(a, s);
     if (nseg <= 256) return norm_go<IT, RES, 256, 1>(a, s);
     if (nseg <= 512) return norm_go<IT, RES, 256, 2>(a, s);

@@ -4,9 +4,9 @@ ragged row counts, both scale layouts and special values; repeat calls bit
 for bit; refusals.
 
 Bounds (u = unit roundoff of the stored type, e = 2^-24 of fp32):
-  rstd   relative 2^-22: the sum of squares carries its rounding errors along
-         (per-thread chains of at most 16 terms in fp32, gamma_16 e = 2^-20
-         worst case, random in sign; 2^-22 is a quarter of that)
+  rstd   relative 2^-22: the sum of squares in fp32 (per-thread chains of at
+         most 16 terms and a tree, gamma_16 e = 2^-20 worst case, random in
+         sign; 2^-22 is a quarter of that)
   y      relative 2^-21 before its rounding: rstd's bound and three roundings
   dx     u |dx| + 2^-21 (|g rstd| + |h c| + |dh|) + the sum's error: at most
          C e per unit of sum |g h|, rstd^3 |h| / C times that
