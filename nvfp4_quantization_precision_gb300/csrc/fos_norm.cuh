@@ -322,13 +322,18 @@ __device__ __forceinline__ void bwd_dx(const uint64_t (&g)[8], const uint64_t (&
 // fixed order and the second kernel one partial row per SM to add (CTAs of one
 // group, four an SM with a partial row each: 46.8 instead of 45.0 us for 8192 x
 // 4096).  512 threads because dw and a row in flight next to the row in work take
-// 128 registers a thread.
+// 128 registers a thread.  Where one group takes the whole CTA, an SM has one row in
+// work and one in flight, and the row after that is fetched to L2 (4681 x 7168
+// without / with: bf16 52.8 / 38.4 us, with dh 47.4 / 45.0; fp32 with dh 92.6 /
+// 84.7; narrower rows, of which an SM has more, lose by it: 8192 x 4096 45.2 /
+// 46.6).
 constexpr int kBwdThreads = 512;
 template <In IT, int kT, bool DH>
 __global__ void __launch_bounds__(kBwdThreads, 1) k_rms_bwd(const NormBwdArgs a) {
     chain_wait();
     chain_release();
     constexpr int kGroups = kBwdThreads / kT, kW = kT / 32;
+    constexpr bool kFar = kGroups == 1;
     constexpr bool kAhead = IT != In::F32 || !DH;  // the next row fits the registers
     __shared__ float s_part[2][kBwdThreads / 32];
     __shared__ float s_dw[kGroups > 1 ? kBwdThreads * 16 : 1];
@@ -363,6 +368,14 @@ __global__ void __launch_bounds__(kBwdThreads, 1) k_rms_bwd(const NormBwdArgs a)
         if constexpr (kAhead)
             load_bwd_seg<IT, DH>(a, (row + step) * a.cols + t * 16, col_in && row + step < a.rows, dy,
                                  h, dh);
+        if constexpr (kFar) {
+            constexpr int kElt = (IT == In::F32) ? 4 : 2;
+            const int64_t far = row + 2 * step;
+            if (t < (DH ? 3 : 2) && far < a.rows) {
+                const void* p = t == 0 ? a.dy : (t == 1 ? a.h : a.dh);
+                fetch_l2(static_cast<const char*>(p) + far * a.cols * kElt, a.cols * kElt);
+            }
+        }
         float p0, p1;
         upk(acc, p0, p1);
         float s = lanes_sum<32>(fadd(p0, p1));
