@@ -17,6 +17,16 @@
 //              has a second group, warps 11-14, for every other chunk (one takes
 //              580 cycles a chunk, more than an NVFP4 stage's MMAs)
 //   warps 6-9  epilogue of the CTA's 128 tokens, lane quadrant warp % 4
+// Measured, 8192 x 4096 x 14336 without an epilogue: 8 bit 284 us, 3.39 PFLOP/s
+// (1.78 times the bf16 rate of a library product), at the clock that the power
+// limit leaves 388 cycles a stage of four MMAs where the MMAs themselves take 384:
+// bound by the tensor pipe.  NVFP4 154 us, 6.27 PFLOP/s (3.3 times): 520 cycles a
+// stage of 34 KB an SM, together 17.9 TB/s out of L2, which is the bound: tiles of
+// 256 x 128 (30 KB a stage, two thirds of the MMAs' time) take 436 cycles a stage,
+// 180 us in all, and neither 6 instead of 3 scale buffers there nor 2 here (160 us)
+// change that much.  With bias, gelu_tanh and the pre-activation kept, 8192 x
+// 14336 x 4096: 306 .. 312 us in a burst, 360 after a second under load; 5003 x
+// 4096 x 14336 NVFP4 with bias, gelu and residual 107 .. 121 us.
 // Tensor memory: two accumulators of 192 columns (the epilogue of a tile runs
 // under the MMAs of the next) and the scale buffers of 40 columns (a: 4 per
 // scale tile, b: the 6 that its 192 rows take) in the other 128.  Copying the
@@ -59,7 +69,10 @@ template <class F> constexpr int sf_groups() { return F::kGlobal ? 2 : 1; }
 template <class F> constexpr int sf_slots() { return F::kGlobal ? 4 : 3; }
 constexpr int kSfMaxSlots = 4;
 template <class F> constexpr int pair_threads() { return 352 + 128 * (sf_groups<F>() - 1); }
-constexpr int kSfBufs = 3;    // chunks in tensor memory
+// Chunks in tensor memory.  Where a chunk is a stage, no more than the ring has
+// stages: the wait for the stage that used a buffer last may look back one turn of
+// the ring at most, or its phase is mistaken for a later one.
+constexpr int kSfBufs = 3;
 constexpr int kSfCols = 16 + 24;
 static_assert(kPairSfCol + kSfBufs * kSfCols <= (int)kAllColumns, "tensor memory");
 template <class F> constexpr int chunk_stages() { return kSfChunkTiles / F::kSfTiles; }

@@ -193,6 +193,8 @@ cudaError_t pair_go(const LinearCall& c, cudaStream_t s) {
     a.tiles_n = (int)((c.N + kPairN - 1) / kPairN);
     a.bufs = c.ep.pre ? 4 : 2;
     const int other = 4 * a.bufs * kChunkBytes + sf_slots<F>() * kSfChunkBytes + 4 * kPairN * 4;
+    static_assert((kSmemLimit - 2048 - 16 * kChunkBytes - kSfMaxSlots * kSfChunkBytes - 16 * kPairN) /
+                          kPairStageBytes >= kSfBufs, "stages");
     a.stages = (kSmemLimit - 2048 - other) / kPairStageBytes;
     const int smem = a.stages * kPairStageBytes + other + 1024;
     auto k = k_linear_pair<F, OT>;
