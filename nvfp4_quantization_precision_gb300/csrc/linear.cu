@@ -92,7 +92,7 @@ RowsPlan rows_plan(const LinearCall& c) {
     RowsPlan p;
     p.nt = c.M >= 256 ? 256 : (int)((c.M + 15) / 16 * 16);
     const int stage = rows_stage_bytes<F>(p.nt);
-    p.stages = (kSmemLimit - 3072) / stage;
+    p.stages = (kSmemLimit - 3 * 1024) / stage;
     if (p.stages > kMaxStages) p.stages = kMaxStages;
     p.smem = p.stages * stage + 1024;
     const int nkb = k_stages<F>(c.K);
