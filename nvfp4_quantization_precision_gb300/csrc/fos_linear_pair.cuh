@@ -25,7 +25,7 @@
 // 256 x 128 (30 KB a stage, two thirds of the MMAs' time) take 436 cycles a stage,
 // 180 us in all, and neither 6 instead of 3 scale buffers there nor 2 here (160 us)
 // change that much.  With bias, gelu_tanh and the pre-activation kept, 8192 x
-// 14336 x 4096: 306 .. 312 us in a burst, 360 after a second under load; 5003 x
+// 14336 x 4096: 306 .. 330 us in a burst, 355 after a second under load; 5003 x
 // 4096 x 14336 NVFP4 with bias, gelu and residual 107 .. 121 us.
 // Tensor memory: two accumulators of 192 columns (the epilogue of a tile runs
 // under the MMAs of the next) and the scale buffers of 40 columns (a: 4 per
@@ -54,7 +54,6 @@ constexpr int kPairM = 256, kPairN = 192;
 constexpr int kPairABytes = 128 * kRowBytes, kPairBBytes = 96 * kRowBytes;
 constexpr int kPairMaxStages = 8;
 constexpr int kChunkBytes = 32 * 128;
-constexpr int kPairGroupM = 8;     // tile rows per band of the tile order
 constexpr int kPairSfCol = 2 * kPairN;
 
 constexpr int kPairStageBytes = kPairABytes + kPairBBytes;
@@ -93,6 +92,7 @@ struct PairArgs {
     Epilogue ep;
     int64_t M, N;
     int tiles_m, tiles_n;
+    int band;          // tile rows of a band of the tile order
     int kb, nkb;
     int stages;
     int bufs;          // chunk buffers of an epilogue warp: 2, with pre 4
@@ -156,14 +156,14 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&v)[32]) {
     asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
 
-// Tile order: bands of kPairGroupM tile rows, down the rows first, so that the
-// tiles in work at one time share a and b tiles in L2.
+// Tile order: bands of a.band tile rows, down the rows first, so that the tiles in
+// work at one time share a and b tiles in L2.
 __device__ __forceinline__ void pair_tile(const PairArgs& a, int t, int32_t& m0, int32_t& n0) {
-    const int per_band = kPairGroupM * a.tiles_n;
+    const int per_band = a.band * a.tiles_n;
     const int band = t / per_band, r = t - band * per_band;
-    const int rows = min(kPairGroupM, a.tiles_m - band * kPairGroupM);
+    const int rows = min(a.band, a.tiles_m - band * a.band);
     const int col = r / rows;
-    m0 = (band * kPairGroupM + r - col * rows) * kPairM;
+    m0 = (band * a.band + r - col * rows) * kPairM;
     n0 = col * kPairN;
 }
 
