@@ -28,6 +28,7 @@ Entry points (names follow the C ABI):
 """
 import ctypes
 import os
+import threading
 from dataclasses import dataclass
 
 import torch
@@ -594,15 +595,31 @@ def rms_norm(x, weight, residual=None, eps=1e-6, scale_tiled=True, quantized=Tru
     return codes, scales, y, x if h is None else h, rstd
 
 
+# Workspaces of calls that bring none, one per thread, device and stream: two
+# threads may interleave the launches of their calls on one stream, and calls on
+# different streams overlap.  (An allocation in every call costs 5 to 6 of 16 to
+# 27 us on the host.)  Larger ones and those of a captured graph, which may be
+# replayed on any stream, are allocated by the call.
+_KEPT_MOST = 16 << 20
+_kept = threading.local()
+
+
 def _workspace(workspace, need, dev):
     if need == 0:
         return None, 0
     if workspace is None:
-        workspace = _new((need,), torch.uint8, dev)
-    else:
-        _cuda(workspace, "workspace")
-        if workspace.dtype != torch.uint8 or workspace.get_device() != dev:
-            raise ValueError("workspace must be a uint8 tensor on cuda:%d" % dev)
+        if need > _KEPT_MOST or _raw_stream is None or torch.cuda.current_device() != dev or \
+                torch.cuda.is_current_stream_capturing():
+            return _new((need,), torch.uint8, dev), need
+        key = (dev, _raw_stream(dev))
+        mine = _kept.__dict__
+        workspace = mine.get(key)
+        if workspace is None or workspace.numel() < need:
+            mine[key] = workspace = _new((need,), torch.uint8, dev)
+        return workspace, need
+    _cuda(workspace, "workspace")
+    if workspace.dtype != torch.uint8 or workspace.get_device() != dev:
+        raise ValueError("workspace must be a uint8 tensor on cuda:%d" % dev)
     return workspace, workspace.numel()
 
 
@@ -612,7 +629,8 @@ def rms_norm_backward(dy, h, rstd, weight, dh=None, weight_grad=True, dx=None, d
     output, the h and rstd the forward call returned, and optionally the
     gradient dh that reaches h from elsewhere.  dx is the gradient of x and of
     the residual; dweight is fp32 (None without weight_grad).  workspace: at
-    least fos_rms_norm_backward_workspace_bytes of uint8, allocated when None."""
+    least fos_rms_norm_backward_workspace_bytes of uint8; when None, one that the
+    binding keeps for this thread and stream (up to 16 MB, else allocated)."""
     shape, dt, dev = _data(dy, "dy")
     R, C = shape
     _like(h, "h", shape, dy.dtype, dev)
@@ -667,7 +685,8 @@ def act_backward(dout, pre, act, scale_tiled=True, rowwise=True, colwise=True, v
     scales_t, d, dbias): its 8-bit rows (rowwise), its 8-bit columns
     (colwise), d itself (value) and the fp32 sum of its columns (bias_grad);
     what is not asked for is None.  act: "none", "relu", "gelu", "gelu_tanh",
-    "silu"; pre may be None with "none"."""
+    "silu"; pre may be None with "none".  workspace: as in rms_norm_backward
+    (fos_act_backward_workspace_bytes)."""
     shape, dt, dev = _data(dout, "dout")
     R, C = shape
     a = _act(act)

@@ -15,6 +15,7 @@ Bounds (u = unit roundoff of the stored type, e = 2^-24 of fp32):
          |p| < 17, exp and erf within 2 ulp)
 """
 import ctypes
+import threading
 
 import pytest
 import torch
@@ -352,6 +353,57 @@ def test_graph_capture():
     torch.cuda.synchronize()
     for p, q in zip([t for t in out if t is not None], want):
         assert torch.equal(p, q)
+
+
+def test_kept_workspaces():
+    """Calls without a workspace: any order of sizes gives what a workspace of
+    the caller's gives; streams, threads and captured graphs do not share one."""
+    gen = torch.Generator(device=DEV)
+    gen.manual_seed(9)
+    args = []
+    for rows, cols in ((300, 512), (2000, 4096), (130, 64), (2000, 4096)):
+        dy, h = (torch.randn(rows, cols, generator=gen, device=DEV).to(BF16) for _ in range(2))
+        args.append((dy, h, torch.rand(rows, generator=gen, device=DEV) + 0.5,
+                     torch.randn(cols, generator=gen, device=DEV)))
+    give = [torch.empty(64 << 20, dtype=torch.uint8, device=DEV) for _ in args]
+
+    def calls(ws):
+        out = []
+        for (dy, h, rstd, w), x in zip(args, ws):
+            out += fos.rms_norm_backward(dy, h, rstd, w, workspace=x)
+            out.append(fos.act_backward(dy, h, "silu", rowwise=False, colwise=False, workspace=x)[5])
+        return out
+
+    want = calls(give)
+    none = [None] * len(args)
+    assert all(torch.equal(p, q) for p, q in zip(calls(none), want))
+    mine = dict(fos._kept.__dict__)
+    assert len({v.data_ptr() for v in mine.values()}) == len(mine) and max(
+        v.numel() for v in mine.values()) <= 16 << 20
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got = {}
+    with torch.cuda.stream(side):
+        got["stream"] = calls(none)
+
+    def other():
+        got["thread"] = calls(none)
+        got["kept"] = {v.data_ptr() for v in fos._kept.__dict__.values()}
+
+    th = threading.Thread(target=other)
+    th.start()
+    got["main"] = calls(none)
+    th.join()
+    both = {v.data_ptr() for v in fos._kept.__dict__.values()}
+    assert len(both) > len(mine) and not both & got["kept"]
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        got["graph"] = calls(none)
+    assert {v.data_ptr() for v in fos._kept.__dict__.values()} == both
+    g.replay()
+    torch.cuda.synchronize()
+    for k in ("stream", "thread", "main", "graph"):
+        assert all(torch.equal(p, q) for p, q in zip(got[k], want)), k
 
 
 def test_refusals():
