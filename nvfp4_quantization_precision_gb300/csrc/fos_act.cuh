@@ -146,10 +146,14 @@ __device__ __forceinline__ uint64_t act_slope2(uint64_t p) {
         q = fma2(t, q, pk1(kTail3));
         q = fma2(t, q, pk1(kTail2));
         q = fma2(t, q, pk1(kTail1));
-        q = sub2(pk1(0.5f), mul2(mul2(t, q), e));  // |Phi(p) - 1/2|
-        float qa, qb;
-        upk(q, qa, qb);
-        const uint64_t cdf = add2(pk(copysignf(qa, a), copysignf(qb, b)), pk1(0.5f));
+        // Phi(-|p|) as it is for negative p, where the slope is small: by way of
+        // Phi - 1/2 an 8192 x 14336 gradient takes 135 instead of 139 us, but as many
+        // of its codes as a plain form's differ from the exact ones, not 60 % of them
+        const uint64_t tail = mul2(mul2(t, q), e);
+        float ta, tb, ua, ub;
+        upk(tail, ta, tb);
+        upk(sub2(pk1(1.0f), tail), ua, ub);
+        const uint64_t cdf = pk(a < 0.0f ? ta : ua, b < 0.0f ? tb : ub);
         return fma2(mul2(p, pk1(kInvSqrt2Pi)), e, cdf);
     }
     return pk1(1.0f);
