@@ -474,7 +474,8 @@ enum { FOS_ACT_NONE = 0, FOS_ACT_RELU = 1, FOS_ACT_GELU = 2, FOS_ACT_GELU_TANH =
  * (for the input gradient's product), its 8-bit columns (for the weight
  * gradient's), and dbias [cols] fp32, the sum of its columns.  dbias over
  * more than 128 rows needs fos_act_backward_workspace_bytes(rows, cols)
- * bytes of workspace.  relu'(0) = 0.
+ * bytes of workspace.  relu'(0) = 0.  Every finite pre has its derivative (0 or 1
+ * far out); an infinite or NaN pre gives NaN, with relu 1, 0 and 0.
  */
 FOS_API size_t fos_act_backward_workspace_bytes(int64_t rows, int64_t cols);
 FOS_API fos_status fos_act_backward(const void* dout, const void* pre, fos_dtype dt, int64_t rows,

@@ -117,6 +117,8 @@ __device__ __forceinline__ uint64_t rcp_2(uint64_t x) {
 //   silu       s (1 + p (1 - s))
 //   gelu_tanh  s + p u2' s (1 - s),  s = s(u2), u2 = 2 sqrt(2/pi) (p + 0.044715 p^3)
 //   gelu       Phi(p) + p phi(p)
+// For every finite p, up to the type's largest; infinities end in inf * 0 = NaN, as
+// these forms do (relu: 1 and 0).
 template <Act A>
 __device__ __forceinline__ uint64_t act_slope2(uint64_t p) {
     if constexpr (A == Act::RELU) {
@@ -129,12 +131,17 @@ __device__ __forceinline__ uint64_t act_slope2(uint64_t p) {
         return mul2(s, fma2(p, sub2(pk1(1.0f), s), pk1(1.0f)));
     }
     if constexpr (A == Act::GELU_TANH) {
-        const uint64_t p2 = mul2(p, p);
+        // p^2 no larger than 512, past which s is 0 or 1: p s (1 - s) u2' then has no
+        // factor that overflows, and the one that vanishes comes first
+        const uint64_t pp = mul2(p, p);
+        float a, b;
+        upk(pp, a, b);
+        const uint64_t p2 = pk(fminf(a, 512.0f), fminf(b, 512.0f));
         const uint64_t z = mul2(p, fma2(p2, pk1(kNegLog2e * k2Sqrt2OverPi * 0.044715f),
                                         pk1(kNegLog2e * k2Sqrt2OverPi)));
         const uint64_t s = rcp_2(add2(ex2_2(z), pk1(1.0f)));
         const uint64_t du = fma2(p2, pk1(k2Sqrt2OverPi * 0.134145f), pk1(k2Sqrt2OverPi));
-        return fma2(mul2(p, du), mul2(s, sub2(pk1(1.0f), s)), s);
+        return fma2(mul2(p, mul2(s, sub2(pk1(1.0f), s))), du, s);
     }
     if constexpr (A == Act::GELU) {
         float a, b;
