@@ -436,7 +436,7 @@ FOS_API fos_status fos_rms_norm(const void* x, const void* residual, const void*
 
 /*
  * fos_rms_norm_backward -- with g = dy * weight:
- *   dx = rstd * g - h * rstd^3 * mean(g * h) + dh
+ *   dx = rstd * (g - h * (rstd * mean(g * h * rstd))) + dh
  *   dweight[c] = sum over rows of dy * h * rstd            (fp32)
  * dy, h, dx are of type dt; dh (the gradient that reaches h past the norm)
  * may be NULL; dx is the gradient of x and, the same, of the residual.

@@ -3,8 +3,8 @@
 //
 //   forward   h = x + residual; rstd = 1 / sqrt(mean(h^2) + eps);
 //             y = h * rstd * w; codes and scales of y's rows (fos_block8.cuh)
-//   backward  g = dy * w; dx = rstd * g - h * (rstd^3 * mean(g * h)) + dh;
-//             dw[c] = sum over rows of dy * h * rstd
+//   backward  g = dy * w; xh = h * rstd; dx = rstd * (g - h * (rstd * mean(g * xh))) + dh;
+//             dw[c] = sum over rows of dy * xh
 //
 // Both are bound by HBM: forward e bytes read per element of e bytes (2 e with
 // the residual) and 1 + 1/32 written (e more for h), backward 2e or 3e read and
@@ -305,7 +305,9 @@ __device__ __forceinline__ void load_bwd_seg(const NormBwdArgs& a, int64_t at, b
     }
 }
 
-// dx of one segment from g = dy * w: g rstd - h c, plus dh.
+// dx of one segment from g = dy * w and c = rstd mean(g xh): (g - h c) rstd, plus dh.
+// In this order every step is of g's or of dx's size, also where rows are so small
+// (1e-20, with eps = 0) that rstd^3 leaves fp32's range.
 template <bool DH>
 __device__ __forceinline__ void bwd_dx(const uint64_t (&g)[8], const uint64_t (&h)[8],
                                        const uint64_t (&dh)[8], float rstd, float c,
@@ -313,8 +315,9 @@ __device__ __forceinline__ void bwd_dx(const uint64_t (&g)[8], const uint64_t (&
     const uint64_t r2 = pk(rstd, rstd), c2 = pk(-c, -c);
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-        if constexpr (DH) dx[j] = fma2(h[j], c2, fma2(g[j], r2, dh[j]));
-        else dx[j] = fma2(h[j], c2, mul2(g[j], r2));
+        const uint64_t t = fma2(h[j], c2, g[j]);
+        if constexpr (DH) dx[j] = fma2(t, r2, dh[j]);
+        else dx[j] = mul2(t, r2);
     }
 }
 
@@ -362,9 +365,10 @@ __global__ void __launch_bounds__(kBwdThreads, 1) k_rms_bwd(const NormBwdArgs a)
         const uint64_t r2 = pk(rstd, rstd);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            dw[j] = fma2(v[j], mul2(hv[j], r2), dw[j]);
+            const uint64_t xh = mul2(hv[j], r2);
+            dw[j] = fma2(v[j], xh, dw[j]);
             v[j] = mul2(v[j], w[j]);
-            acc = fma2(v[j], hv[j], acc);
+            acc = fma2(v[j], xh, acc);
         }
         uint64_t dhv[8];
         if constexpr (DH) widen<IT>(dh, dhv);
@@ -391,7 +395,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) k_rms_bwd(const NormBwdArgs a)
         }
         if (col_in) {
             constexpr int64_t kElt = (IT == In::F32) ? 4 : 2;
-            const float c = fmul(fmul(fmul(s, rstd), fmul(a.inv_cols, rstd)), rstd);
+            const float c = fmul(fmul(s, a.inv_cols), rstd);
             uint64_t dx[8];
             bwd_dx<DH>(v, hv, dhv, rstd, c, dx);
             store_seg<IT>(static_cast<char*>(a.dx) + (row * a.cols + t * 16) * kElt, dx);
@@ -429,6 +433,7 @@ __global__ void __launch_bounds__(512) k_rms_bwd_wide(const NormBwdArgs a) {
     int parity = 0;
     for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, parity ^= 1) {
         const float rstd = __ldg(a.rstd + row);
+        const uint64_t r2 = pk(rstd, rstd);
         uint64_t acc = 0;
         for (int64_t sg = t; sg < nseg; sg += kT) {
             Raw<IT> dy, h;
@@ -440,7 +445,7 @@ __global__ void __launch_bounds__(512) k_rms_bwd_wide(const NormBwdArgs a) {
             widen<IT>(dy, v);
             widen<IT>(h, hv);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) acc = fma2(mul2(v[j], w[j]), hv[j], acc);
+            for (int j = 0; j < 8; ++j) acc = fma2(mul2(v[j], w[j]), mul2(hv[j], r2), acc);
         }
         float p0, p1;
         upk(acc, p0, p1);
@@ -450,7 +455,7 @@ __global__ void __launch_bounds__(512) k_rms_bwd_wide(const NormBwdArgs a) {
         s = 0.0f;
 #pragma unroll
         for (int i = 0; i < kT / 32; ++i) s = fadd(s, s_part[parity][i]);
-        const float c = fmul(fmul(fmul(s, rstd), fmul(a.inv_cols, rstd)), rstd);
+        const float c = fmul(fmul(s, a.inv_cols), rstd);
         for (int64_t sg = t; sg < nseg; sg += kT) {
             Raw<IT> dy, h, dh;
             uint64_t v[8], hv[8], dhv[8], w[8], dx[8];

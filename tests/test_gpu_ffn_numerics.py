@@ -106,3 +106,30 @@ def test_act_backward_of_infinities_and_nan(act, dt):
     for k in at:
         d[k] = d[0, 0]
     assert (d == d[0, 0]).all() and torch.isfinite(d).all()
+
+
+@pytest.mark.parametrize("dt", [F32, BF16])
+@pytest.mark.parametrize("cols", [64, 1024, 4096, 8192, 8224, 16416])
+def test_rms_norm_backward_of_tiny_rows(cols, dt):
+    """Rows of about 1e-20 and 1e-21 with the rstd that eps = 0 gives them (up to
+    1e21), gradients of ordinary and of small size: dx is in range, and so is
+    every step to it.  Bounds as for ordinary rows: e per rounding and per unit
+    of the terms' sizes, the sum's error 40 e (a chain of 16 terms and a tree)."""
+    g = torch.Generator(device=DEV)
+    g.manual_seed(cols)
+    rows = 24
+    size = torch.tensor([1e-20, 1e-21, 1.0], device=DEV).repeat(8).unsqueeze(1)
+    h = (torch.randn(rows, cols, generator=g, device=DEV) * size).to(dt)
+    rstd = (1 / h.to(D).square().mean(1).sqrt()).float()
+    up = torch.tensor([1.0, 1e-3, 1e-18], device=DEV).repeat_interleave(8).unsqueeze(1)
+    dy = (torch.randn(rows, cols, generator=g, device=DEV) * up).to(dt)
+    w = 1 + 0.1 * torch.randn(cols, generator=g, device=DEV)
+    for dh in (None, dy.flip(0).contiguous()):
+        dx, dw = fos.rms_norm_backward(dy, h, rstd, w, dh)
+        gr, xh, r = dy.to(D) * w.to(D), h.to(D) * rstd.to(D).unsqueeze(1), rstd.to(D).unsqueeze(1)
+        want = r * (gr - xh * (gr * xh).mean(1, keepdim=True)) + (dh.to(D) if dh is not None else 0)
+        size = r * (gr.abs() + xh.abs() * (gr * xh).abs().mean(1, keepdim=True) * 40)
+        bound = want.abs() * ref.U[dt] + (size + want.abs()) * 8 * E + ref.TINY[dt]
+        ref.near(dx, want, bound, "dx")
+        t = dy.to(D) * xh
+        ref.near(dw, t.sum(0), t.abs().sum(0) * (rows + 8) * E, "dweight")
