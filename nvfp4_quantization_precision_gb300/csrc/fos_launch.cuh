@@ -4,6 +4,8 @@
 
 #include <cuda_runtime.h>
 
+#include <functional>
+#include <initializer_list>
 #include <mutex>
 #include <unordered_map>
 
@@ -27,32 +29,47 @@ inline int sm_count() {
     return cache[dev];
 }
 
-// Resident CTAs per SM of a kernel at a dynamic shared-memory size (cached:
-// the occupancy query costs host time on every launch otherwise).
-inline int resident_ctas(const void* kernel, size_t dyn_smem) {
-    struct Key {
-        const void* k;
-        size_t smem;
-        int dev;
-        bool operator==(const Key& o) const { return k == o.k && smem == o.smem && dev == o.dev; }
-    };
-    struct Hash {
-        size_t operator()(const Key& k) const {
-            return std::hash<const void*>()(k.k) ^ (k.smem * 1315423911u) ^ (size_t)k.dev;
-        }
-    };
-    static std::mutex mu;
-    static std::unordered_map<Key, int, Hash> cache;
+// What an occupancy or a function attribute depends on: the kernel, the device (both
+// belong to a device's context), the CTA's threads and dynamic shared memory, and the
+// cluster's size.  A cache whose value does not depend on one of them leaves it 0.
+struct LaunchKey {
+    const void* kernel;
+    int dev;
+    int threads;
+    size_t smem;
+    int cluster;
+    bool operator==(const LaunchKey& o) const {
+        return kernel == o.kernel && dev == o.dev && threads == o.threads && smem == o.smem &&
+               cluster == o.cluster;
+    }
+};
+struct LaunchKeyHash {
+    size_t operator()(const LaunchKey& k) const {
+        size_t h = std::hash<const void*>()(k.kernel);
+        for (size_t v : {(size_t)k.dev, (size_t)k.threads, k.smem, (size_t)k.cluster})
+            h = h * 1000003u ^ v;
+        return h;
+    }
+};
+inline int current_device() {
     int dev = 0;
     cudaGetDevice(&dev);
-    const Key key{kernel, dyn_smem, dev};
+    return dev;
+}
+
+// Resident CTAs per SM of a kernel (cached: the occupancy query costs host
+// time on every launch otherwise).
+inline int resident_ctas(const void* kernel, size_t dyn_smem, int threads = kThreads) {
+    static std::mutex mu;
+    static std::unordered_map<LaunchKey, int, LaunchKeyHash> cache;
+    const LaunchKey key{kernel, current_device(), threads, dyn_smem, 0};
     {
         std::lock_guard<std::mutex> g(mu);
         auto it = cache.find(key);
         if (it != cache.end()) return it->second;
     }
     int occ = 1;
-    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, kernel, kThreads, dyn_smem) !=
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, kernel, threads, dyn_smem) !=
             cudaSuccess || occ < 1) {
         cudaGetLastError();
         occ = 1;
@@ -73,18 +90,19 @@ inline int persistent_grid(Kernel kernel, int64_t units, size_t dyn_smem) {
     return (int)(g < 1 ? 1 : g);
 }
 
-// Raises a kernel's dynamic shared-memory limit when it needs more than the
-// default 48 KiB (once per kernel and size).
+// Raises a kernel's dynamic shared-memory limit on the current device when it
+// needs more than the default 48 KiB (once per kernel, device and size).
 inline cudaError_t allow_smem(const void* kernel, size_t bytes) {
     if (bytes <= 48 * 1024) return cudaSuccess;
     static std::mutex mu;
-    static std::unordered_map<const void*, size_t> done;
+    static std::unordered_map<LaunchKey, size_t, LaunchKeyHash> done;
+    const LaunchKey key{kernel, current_device(), 0, 0, 0};
     std::lock_guard<std::mutex> g(mu);
-    auto it = done.find(kernel);
+    auto it = done.find(key);
     if (it != done.end() && it->second >= bytes) return cudaSuccess;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          (int)bytes);
-    if (e == cudaSuccess) done[kernel] = bytes;
+    if (e == cudaSuccess) done[key] = bytes;
     return e;
 }
 

@@ -14,29 +14,6 @@ struct Quant8Args;
 struct LinearCall;
 enum class Act : int;
 
-// Resident CTAs per SM of a kernel with `threads` threads (cached per kernel,
-// size and device: the query costs host time on every launch otherwise).
-template <class Kernel>
-inline int resident_ctas_of(Kernel kernel, int threads, size_t smem) {
-    static std::mutex mu;
-    static std::unordered_map<const void*, int> cache[16];
-    int dev = 0;
-    cudaGetDevice(&dev);
-    const void* key = reinterpret_cast<const void*>(kernel);
-    std::lock_guard<std::mutex> g(mu);
-    auto& c = cache[dev & 15];
-    auto it = c.find(key);
-    if (it != c.end()) return it->second;
-    int occ = 1;
-    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, kernel, threads, smem) != cudaSuccess ||
-        occ < 1) {
-        cudaGetLastError();
-        occ = 1;
-    }
-    c[key] = occ;
-    return occ;
-}
-
 // A launch that may be placed while the previous kernel of the stream drains
 // (every kernel waits for it before its first global access).
 template <class Kernel, class... Args>

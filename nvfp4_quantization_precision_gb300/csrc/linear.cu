@@ -18,14 +18,12 @@ bool code_map(CUtensorMap* m, const uint8_t* codes, int64_t rows, int64_t row_by
                       box_rows, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
 }
 
-// Clusters of `size` CTAs the device holds at once (cached per kernel and size).
+// Clusters of `size` CTAs the device holds at once (cached).
 template <class Kernel>
 int resident_clusters(Kernel k, int threads, int smem, int size) {
     static std::mutex mu;
-    static std::unordered_map<uint64_t, int> cache;
-    int dev = 0;
-    cudaGetDevice(&dev);
-    const uint64_t key = reinterpret_cast<uint64_t>(k) * 64 + (uint64_t)size + ((uint64_t)dev << 56);
+    static std::unordered_map<LaunchKey, int, LaunchKeyHash> cache;
+    const LaunchKey key{reinterpret_cast<const void*>(k), current_device(), threads, (size_t)smem, size};
     std::lock_guard<std::mutex> g(mu);
     auto it = cache.find(key);
     if (it != cache.end()) return it->second;

@@ -2,7 +2,6 @@
 // the persistent block-scaled NVFP4 kernel (fos_mma.cuh) with its three TMA
 // descriptors (a codes, b codes, out).
 #include <cstring>
-#include <mutex>
 
 #include "fos_launch.cuh"
 #include "fos_mma.cuh"
@@ -72,12 +71,10 @@ int run_mm(const uint8_t* a_codes, const uint8_t* a_scales, const float* a_amax,
     const int64_t tiles = a.tiles_m * a.tiles_n;
     auto kernel = mma::k_mm_nvfp4<kMmEpi, kMmBufs>;
     constexpr int smem = mma::smem_bytes<kMmEpi, kMmBufs>();
-    static std::once_flag once;
-    static cudaError_t attr = cudaSuccess;
-    std::call_once(once, [&] {
-        attr = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    });
-    if (attr != cudaSuccess) return 2;
+    if (allow_smem(reinterpret_cast<const void*>(kernel), smem) != cudaSuccess) {
+        cudaGetLastError();
+        return 2;
+    }
     // persistent: one CTA per SM (the tensor memory and shared memory of a
     // CTA take an SM), never more CTAs than tiles
     const int64_t sms = sm_count();

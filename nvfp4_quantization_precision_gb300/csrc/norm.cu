@@ -43,7 +43,8 @@ namespace {
 // Grid of a row kernel: the resident CTAs, no more than the rows need.
 template <class Kernel>
 int row_grid(Kernel k, int threads, int64_t rows, int groups) {
-    const int64_t full = (int64_t)sm_count() * resident_ctas_of(k, threads, 0);
+    const int64_t full = (int64_t)sm_count() *
+                         resident_ctas(reinterpret_cast<const void*>(k), 0, threads);
     const int64_t need = (rows + groups - 1) / groups;
     return (int)(need < full ? need : full);
 }

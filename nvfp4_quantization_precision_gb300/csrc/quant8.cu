@@ -14,7 +14,7 @@ cudaError_t go(const Quant8Args& a, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     const int64_t tiles = (a.rows + kQ8Tile - 1) / kQ8Tile * a.tiles_c;
     Quant8Args b = a;
-    b.wave = sm_count() * resident_ctas_of(k, kQ8Threads, kQ8Smem);
+    b.wave = sm_count() * resident_ctas(reinterpret_cast<const void*>(k), kQ8Smem, kQ8Threads);
     return launch_chained(k, dim3((unsigned)tiles), kQ8Threads, kQ8Smem, s, b);
 }
 
