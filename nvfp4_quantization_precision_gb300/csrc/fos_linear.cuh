@@ -83,15 +83,28 @@ __device__ __forceinline__ uint32_t idesc(int m, int n, int sf_id) {
            ((uint32_t)sf_id << 4) | ((uint32_t)sf_id << 29);
 }
 
+// What a wait orders.  CTA: memory of this CTA's own arrivals and copies.  CLUSTER:
+// the same for arrivals and copies of the other CTA of a pair as well.  TENSOR:
+// tensor memory alone, whichever CTA arrives: its completed accesses (wait::ld,
+// wait::st, a commit) are ordered by the tcgen05 fences on both sides of the
+// barrier, which itself only has to order the two threads' execution.
+enum class Sync { CTA, CLUSTER, TENSOR };
+
+#define FOS_MBAR_TEST(op, sem, hint)                                              \
+    asm volatile("{\n\t.reg .pred p;\n\t"                                       \
+                 "mbarrier." op ".parity" sem ".shared::cta.b64 p, [%1], %2" hint ";\n\t" \
+                 "selp.u32 %0, 1, 0, p;\n\t}"                                    \
+                 : "=r"(done) : "r"(smem_u32(bar)), "r"(parity) : "memory")
+
 // Bounded wait of a whole converged warp: every lane gets the same answer, also
 // when the wait gives up.
+template <Sync S = Sync::CTA>
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
     for (uint32_t i = 0; i < kMbarSpins; ++i) {
         uint32_t done;
-        asm volatile("{\n\t.reg .pred p;\n\t"
-                     "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 1000;\n\t"
-                     "selp.u32 %0, 1, 0, p;\n\t}"
-                     : "=r"(done) : "r"(smem_u32(bar)), "r"(parity) : "memory");
+        if constexpr (S == Sync::CTA) FOS_MBAR_TEST("try_wait", ".acquire.cta", ", 1000");
+        else if constexpr (S == Sync::CLUSTER) FOS_MBAR_TEST("try_wait", ".acquire.cluster", ", 1000");
+        else FOS_MBAR_TEST("try_wait", ".relaxed.cluster", ", 1000");
         if (__all_sync(0xFFFFFFFFu, done != 0)) return true;
     }
     return false;
@@ -100,14 +113,15 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
 // Whether a phase has completed, without waiting: asked a stage ahead, so that
 // the answer is there when it is needed (a wait for a phase long complete
 // still takes about 170 cycles, a stage's seven instructions 300).
+template <Sync S = Sync::CTA>
 __device__ __forceinline__ bool mbar_ask(uint64_t* bar, uint32_t parity) {
     uint32_t done;
-    asm volatile("{\n\t.reg .pred p;\n\t"
-                 "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-                 "selp.u32 %0, 1, 0, p;\n\t}"
-                 : "=r"(done) : "r"(smem_u32(bar)), "r"(parity) : "memory");
+    if constexpr (S == Sync::CTA) FOS_MBAR_TEST("test_wait", ".acquire.cta", "");
+    else if constexpr (S == Sync::CLUSTER) FOS_MBAR_TEST("test_wait", ".acquire.cluster", "");
+    else FOS_MBAR_TEST("test_wait", ".relaxed.cluster", "");
     return done != 0;
 }
+#undef FOS_MBAR_TEST
 // Lane 0's value for the whole warp: the compiler then knows it is uniform and
 // keeps what follows from it (addresses, descriptors, loop counts) in uniform
 // registers, which the tensor instructions read.

@@ -137,11 +137,11 @@ __device__ __forceinline__ void pair_commit(uint64_t* bar) {
         "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
         "[%0], %1;" ::"r"(smem_u32(bar)), "h"((unsigned short)3) : "memory");
 }
-// Arrival at a barrier of another CTA (its cluster address).  The default
-// release is that of the CTA: what is published is in tensor memory, complete
-// and fenced.  Released to the cluster instead, each arrival took 1300 cycles.
+// Arrival at a barrier of CTA 0 from either CTA of the pair, for accesses to tensor
+// memory that have completed: the fences around the barrier order them (see Sync),
+// so the arrival is relaxed, at the scope that holds both CTAs.
 __device__ __forceinline__ void cluster_arrive(uint32_t bar) {
-    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&v)[32]) {
     asm volatile(
@@ -305,7 +305,7 @@ __global__ void __launch_bounds__(pair_threads<F>(), 1) k_linear_pair(const __gr
             const int32_t am = m0 + 128 * rank, bn = n0 + 96 * rank;
             for (int i = 0; i < a.nkb; ++i) {
                 const int s = r.slot;
-                if (g >= (uint32_t)ns && !warp_wait(&sh.empty[s], r.parity ^ 1u)) {
+                if (g >= (uint32_t)ns && !warp_wait<Sync::CLUSTER>(&sh.empty[s], r.parity ^ 1u)) {
                     bad = true;
                     break;
                 }
@@ -330,7 +330,7 @@ __global__ void __launch_bounds__(pair_threads<F>(), 1) k_linear_pair(const __gr
                 s += ns;
                 p ^= 1u;
             }
-            if (!warp_wait(&sh.empty[s], p)) bad = true;
+            if (!warp_wait<Sync::CLUSTER>(&sh.empty[s], p)) bad = true;
         }
     } else if (warp == 1) {
         if (rank == 0) {
@@ -340,15 +340,15 @@ __global__ void __launch_bounds__(pair_threads<F>(), 1) k_linear_pair(const __gr
             int j = 0;
             for (int t = first; t < tiles && !bad; t += step, ++j) {
                 const int ab = j & 1;
-                if (j >= 2 && !warp_wait(&sh.acc_empty[ab], (uint32_t)((j >> 1) - 1) & 1)) {
+                if (j >= 2 && !warp_wait<Sync::TENSOR>(&sh.acc_empty[ab], (uint32_t)((j >> 1) - 1) & 1)) {
                     bad = true;
                     break;
                 }
                 const uint32_t acc = tmem + (uint32_t)(ab * kPairN);
                 for (int i = 0; i < a.nkb; ++i) {
                     const int s = r.slot, in_chunk = i % chunk_stages<F>();
-                    if ((!chunk_is_stage<F>() && in_chunk == 0 && !warp_wait(&sh.sf_ready[f.slot], f.parity)) ||
-                        (!warp_agrees(here) && !warp_wait(&sh.full[s], r.parity))) {
+                    if ((!chunk_is_stage<F>() && in_chunk == 0 && !warp_wait<Sync::TENSOR>(&sh.sf_ready[f.slot], f.parity)) ||
+                        (!warp_agrees(here) && !warp_wait<Sync::CLUSTER>(&sh.full[s], r.parity))) {
                         bad = true;
                         break;
                     }
@@ -364,7 +364,7 @@ __global__ void __launch_bounds__(pair_threads<F>(), 1) k_linear_pair(const __gr
                         pair_commit(&sh.empty[s]);
                         if (!chunk_is_stage<F>() && last) pair_commit(&sh.sf_free[f.slot]);
                     }
-                    here = mbar_ask(&sh.full[r.slot], r.parity);
+                    here = mbar_ask<Sync::CLUSTER>(&sh.full[r.slot], r.parity);
                     __syncwarp();
                     if (last) f.next(kSfBufs);
                 }
@@ -456,8 +456,8 @@ __global__ void __launch_bounds__(pair_threads<F>(), 1) k_linear_pair(const __gr
                 if (lane == 0) bar_arrive(&sh.sf_empty[f.slot]);
                 if (chunks >= (uint32_t)kSfBufs) {
                     // the MMAs that read this buffer are done
-                    if (chunk_is_stage<F>() ? !warp_wait(&sh.empty[w.slot], w.parity)
-                                            : !warp_wait(&sh.sf_free[d.slot], d.parity ^ 1u)) {
+                    if (chunk_is_stage<F>() ? !warp_wait<Sync::TENSOR>(&sh.empty[w.slot], w.parity)
+                                            : !warp_wait<Sync::TENSOR>(&sh.sf_free[d.slot], d.parity ^ 1u)) {
                         bad = true;
                         break;
                     }
@@ -529,7 +529,7 @@ __global__ void __launch_bounds__(pair_threads<F>(), 1) k_linear_pair(const __gr
                 }
             }
             const int ab = j & 1;
-            if (!bad && !warp_wait(&sh.acc_full[ab], (uint32_t)(j >> 1) & 1)) bad = true;
+            if (!bad && !warp_wait<Sync::TENSOR>(&sh.acc_full[ab], (uint32_t)(j >> 1) & 1)) bad = true;
             __syncwarp();
             tc_fence_after();
             for (int k = 0; k < kChunks; ++k, ++c) {
@@ -586,7 +586,7 @@ __global__ void __launch_bounds__(pair_threads<F>(), 1) k_linear_pair(const __gr
         __syncwarp();
     }
     // every MMA issued has completed before the tensor memory is freed
-    if (warp == 1 && !warp_wait(&sh.done, 0)) bad = true;
+    if (warp == 1 && !warp_wait<Sync::TENSOR>(&sh.done, 0)) bad = true;
     if (bad) sh.fail = 1;
     tc_fence_before();
     __syncwarp();
