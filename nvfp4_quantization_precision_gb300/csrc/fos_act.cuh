@@ -17,13 +17,17 @@ namespace fos {
 enum class Act : int { NONE = 0, RELU = 1, GELU = 2, GELU_TANH = 3, SILU = 4 };
 
 // The epilogue's form of v * s(z), s(z) = 1 / (1 + 2^(-z log2 e)), for z = v (silu)
-// and z = 2u (gelu_tanh): the hardware's approximations of 2^x (2 ulp, and the
-// argument's rounding, a relative |z| 2^-24) and of the reciprocal (1 ulp).
-// That is a relative error of a few 2^-24 where s is not negligible, below
-// every stored type's rounding but fp32's, at 5 and 7 instructions instead of
-// 18 and 20 with expf and a refined reciprocal: 32 columns of gelu_tanh took
-// 1800 cycles of the product's epilogue that way.  A zero or infinite sum ends
-// in the right limit (2^x = inf gives s = 0).
+// and z = 2u (gelu_tanh): the hardware's approximations of 2^x (relative error
+// 2^-22) and of the reciprocal (2^-23), at 5 and 7 instructions instead of 18 and 20
+// with expf and a refined reciprocal: 32 columns of gelu_tanh took 1800 cycles of the
+// product's epilogue that way.  The rounding of the argument adds a relative error
+// that grows in the negative tail, and there is one of the result:
+//   silu       (9 + |z|) 2^-24, up to 2^-17 at z = -87, where a result is below 2^-118
+//              and the next ones are 0.  Beneath a 16-bit output's own rounding (2^-11,
+//              2^-8); for 32-bit outputs silu_values takes a closer form.
+//   gelu_tanh  (9 + 3.5 |z|) 2^-24, for every output: v = -10 gives |z| = 87 and the
+//              range's end.  (1 + tanh(u), the formula as it stands, has no correct
+//              digit below v = -6.)
 __device__ __forceinline__ float ex2(float x) {
     float r;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
@@ -36,6 +40,8 @@ __device__ __forceinline__ float rcp(float x) {
 }
 
 constexpr float kNegLog2e = -1.4426950408889634f;
+constexpr float kNegLog2eLo = -1.9259630e-8f;  // what kNegLog2e rounds off
+constexpr float kLn2 = 0.69314718f;
 constexpr float kInvSqrt2Pi = 0.39894228040143268f;
 constexpr float k2Sqrt2OverPi = 1.5957691216057308f;  // 2 sqrt(2 / pi)
 
@@ -55,6 +61,32 @@ __device__ __forceinline__ float tail_poly(float t) {
     q = __fmaf_rn(t, q, kTail2);
     q = __fmaf_rn(t, q, kTail1);
     return fmul(t, q);
+}
+
+// silu for 32-bit outputs, kN elements in place: the argument's rounding put back to
+// first order, 2^(t + lo) = 2^t (1 + lo ln 2), within 10 * 2^-24 of the result.  For
+// |v| > 80, where 1 + exp(-v) is 1 or exp(-v) in fp32: v exp(v), by halves because
+// exp(v) leaves fp32's range before the product does (at -87 and -92).
+template <int kN>
+__device__ __forceinline__ void silu_values(float (&v)[kN]) {
+    float y[kN], most = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kN; ++i) {
+        const float x = v[i], t = fmul(x, kNegLog2e);
+        const float lo = __fmaf_rn(x, kNegLog2eLo, __fmaf_rn(x, kNegLog2e, -t));
+        y[i] = fmul(x, rcp(__fmaf_rn(ex2(t), __fmaf_rn(lo, kLn2, 1.0f), 1.0f)));
+        most = fmaxf(most, fabsf(x));
+    }
+    if (most > 80.0f) {
+#pragma unroll
+        for (int i = 0; i < kN; ++i) {
+            const float x = v[i], h = expf(0.5f * x);
+            if (x > 80.0f) y[i] = x;
+            if (x < -80.0f) y[i] = fmul(fmul(x, h), h);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < kN; ++i) v[i] = y[i];
 }
 
 // Values of kN elements in place, step by step over groups of eight so that

@@ -216,13 +216,16 @@ __device__ __forceinline__ void store_out(void* p, int64_t i, float v) {
     else st16(static_cast<unsigned short*>(p) + i, out_pair<OT>(pk(v, 0.0f)));
 }
 
-template <int kN>
+template <Out OT, int kN>
 __device__ __forceinline__ void act_apply(int act, float (&v)[kN]) {
     switch (static_cast<Act>(act)) {
         case Act::RELU: act_values<Act::RELU>(v); break;
         case Act::GELU: act_values<Act::GELU>(v); break;
         case Act::GELU_TANH: act_values<Act::GELU_TANH>(v); break;
-        case Act::SILU: act_values<Act::SILU>(v); break;
+        case Act::SILU:
+            if constexpr (OT == Out::F32) silu_values(v);
+            else act_values<Act::SILU>(v);
+            break;
         default: break;
     }
 }
@@ -431,7 +434,7 @@ __device__ __forceinline__ void finish_tokens(const Epilogue& ep, const Tile& t,
             f[4 * i + 3] = fadd(s.w, bias[3]);
             if (ep.pre && c < t.mt) store4<OT>(ep.pre, (int64_t)(t.m0 + c) * t.N + t.n, f + 4 * i);
         }
-        act_apply(ep.act, f);
+        act_apply<OT>(ep.act, f);
 #pragma unroll
         for (int i = 0; i < kTok; ++i) {
             const int c = c0 + 4 * kS * i;

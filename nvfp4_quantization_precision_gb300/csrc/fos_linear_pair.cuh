@@ -564,7 +564,7 @@ __global__ void __launch_bounds__(pair_threads<F>(), 1) k_linear_pair(const __gr
                     }
                     constexpr int kPieces = 32 * kElt / 16;
                     if (pre) put_pieces<OT>(buf + kChunkBytes + lane * 128, lane, kPieces * h, v);
-                    act_apply(a.ep.act, v);
+                    act_apply<OT>(a.ep.act, v);
                     if (res) add_pieces<OT>(buf + lane * 128, lane, kPieces * h, v);
                     put_pieces<OT>(buf + lane * 128, lane, kPieces * h, v);
                 }

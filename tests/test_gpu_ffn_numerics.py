@@ -133,3 +133,106 @@ def test_rms_norm_backward_of_tiny_rows(cols, dt):
         ref.near(dx, want, bound, "dx")
         t = dy.to(D) * xh
         ref.near(dw, t.sum(0), t.abs().sum(0) * (rows + 8) * E, "dweight")
+
+
+def _sweep(v, act, dt, rows):
+    """The epilogue's activation at the values v (a multiple of 16 of them), as
+    (outputs, pre-activations) of a product of zeros with v as the bias."""
+    n = v.numel()
+    a = fos.quantize8(torch.zeros(rows, 32, device=DEV))
+    b = fos.quantize8(torch.zeros(n, 32, device=DEV))
+    out, pre = fos.linear8(a[0], a[1], b[0], b[1], act=act, bias=v, out_dtype=dt, save_pre=True)
+    bits = lambda t: t.view({4: torch.int32, 2: torch.int16}[t.element_size()])  # noqa: E731
+    assert all(torch.equal(bits(t), bits(t[:1]).expand_as(t)) for t in (out, pre))
+    return out[0], pre[0]
+
+
+def _rel(act, v):
+    """Relative error of the factor that the activation multiplies v by, where v < 0:
+    silu       9 e: 2^x 4, its argument's remainder 1, the sum 1, the reciprocal 2,
+               the product 1 (below -80: expf twice 4, two products 2)
+    gelu_tanh  8 e, and the argument z = 2u of the exponential with 3.5 e |z|: two
+               squares' and sums' roundings, two constants, the product
+    gelu       tail: the polynomial's fit 1 e, its evaluation 4.1 e, t with 3 e and a
+               sensitivity of at most 1, 2^x 4, two products 2; the exponential's
+               argument v^2 / 2 with 2.5 e of itself; the last rounding 1"""
+    if act == "silu":
+        return torch.full_like(v, 10 * E)
+    if act == "gelu_tanh":
+        return E * (9 + 3.5 * (2 * math.sqrt(2 / math.pi) * (v + 0.044715 * v ** 3)).abs())
+    return E * (15.2 + 1.25 * v * v)
+
+
+@pytest.mark.parametrize("act", ["relu", "gelu_tanh", "silu"])
+@pytest.mark.parametrize("rows", [1, 3, 700])
+def test_activation_relative_to_its_result(act, rows):
+    """fp32 outputs over -100 .. 100 and out to the type's ends, from the kernel for
+    few tokens and the one for many: the error is relative to the result, also
+    in the negative tail, down to results of 2^-110."""
+    lin = torch.linspace(-12, 12, 4096 * 3, device=DEV)
+    wide = torch.linspace(-100, 100, 4096, device=DEV)
+    far = torch.exp2(torch.linspace(-120, 127.9, 1024, device=DEV))
+    v = torch.cat((lin, wide, far, -far))
+    out, pre = _sweep(v, act, F32, rows)
+    assert torch.equal(pre, v)
+    v = v.to(D)
+    want = _act64(v, act)
+    if act == "relu":
+        assert torch.equal(out.to(D), want)
+        return
+    r = _rel(act, v)
+    neg = want.abs() * r
+    # v > 0: v - |v| tail(v), or v times a factor of which 1 - s is off by what the
+    # negative side's is, with the sum's, the reciprocal's and the product's roundings
+    pos = want.abs() * 4 * E + (_act64(-v, act)).abs() * r
+    bound = torch.where(v < 0, neg, pos) + 2.0 ** -110
+    ref.near(out, want, bound, act)
+
+
+def test_silu_below_the_range_of_the_exponential():
+    """silu down to -103, where exp(-v) leaves fp32's range at -88.7 and the result
+    itself only below -92: relative to the result, to a subnormal's spacing."""
+    v = torch.linspace(-103.9, -70, 4096, device=DEV)
+    for rows in (1, 700):
+        out, _ = _sweep(v, "silu", F32, rows)
+        want = _act64(v.to(D), "silu")
+        ref.near(out, want, want.abs() * 10 * E + 2.0 ** -149, "silu")
+
+
+def test_activations_of_infinities_and_nan():
+    """As the formulas give them: inf, and inf * 0 = NaN on the negative side."""
+    v = torch.tensor([math.inf, -math.inf, math.nan, 1.0] * 4, device=DEV)
+    for rows in (1, 700):
+        for act in ("relu", "gelu", "gelu_tanh", "silu"):
+            out, _ = _sweep(v, act, F32, rows)
+            assert out[0].item() == math.inf and math.isnan(out[2].item())
+            assert out[1].item() == 0 if act == "relu" else math.isnan(out[1].item())
+            assert math.isfinite(out[3].item())
+
+
+@pytest.mark.parametrize("act", ["gelu_tanh", "silu"])
+def test_derivative_relative_to_its_terms(act):
+    """act_backward in fp32 with dout = 1 over -30 .. 30: the error is relative to
+    the sizes of the derivative's terms, which vanish in the negative tail.
+      gelu       Phi + p phi: Phi's tail as in _rel, phi with 4 e (2^x), 2.5 e of its
+                 argument and 3 e of products; the sum's rounding
+      the others s + p z' s (1 - s) with s of relative error r = 9 e + 3.5 e |z|
+                 (silu z = p: 1.5 e |z|): r s (1 - s) from the exponential and 3 e s from the
+                 rest in each s, 1 - s with e more, products 4 e"""
+    p = torch.cat((torch.linspace(-12, 12, 16384, device=DEV), torch.linspace(-30, 30, 4096, device=DEV)))
+    d = fos.act_backward(torch.ones(64, 320, device=DEV), p.view(64, 320).contiguous(), act,
+                         rowwise=False, colwise=False, value=True, bias_grad=False)[4].view(-1)
+    p = p.to(D)
+    want = _slope64(p, act)
+    if act == "gelu":
+        phi = torch.exp(-p * p / 2) / math.sqrt(2 * math.pi)
+        tail = 0.5 * torch.erfc(p.abs() / math.sqrt(2))
+        bound = (tail * E * (15.2 + 1.25 * p * p) + (p > 0) * E
+                 + p.abs() * phi * E * (7.5 + 1.25 * p * p) + want.abs() * E)
+    else:
+        c = 2 * math.sqrt(2 / math.pi)
+        z, dz = (p, 1) if act == "silu" else (c * (p + 0.044715 * p ** 3), c * (1 + 0.134145 * p * p))
+        s, r = torch.sigmoid(z), torch.sigmoid(-z)
+        es = s * r * E * (4 + (1.5 if act == "silu" else 3.5) * z.abs()) + s * 3 * E
+        bound = es + (p * dz).abs() * (es * r + s * (es + r * E) + s * r * 4 * E) + want.abs() * 2 * E
+    ref.near(d, want, bound * 1.02 + 2.0 ** -110, act)
