@@ -45,22 +45,50 @@ constexpr float kLn2 = 0.69314718f;
 constexpr float kInvSqrt2Pi = 0.39894228040143268f;
 constexpr float k2Sqrt2OverPi = 1.5957691216057308f;  // 2 sqrt(2 / pi)
 
-// 1 - Phi(|x|) = q(t) exp(-x^2 / 2) with t = 1 / (1 + 0.28 |x|) and q the polynomial
-// of degree 6 without constant term that is nearest to it over x = 0 .. 9 (a
-// Lawson iteration of weighted least squares; within 1e-8, 3e-8 root mean square
-// once evaluated in fp32, half of what the five-term form of Abramowitz and
-// Stegun 7.1.26 leaves).  Written on |x|, it has no cancellation on the negative
-// side.
+// 1 - Phi(|x|) = q(t) exp(-x^2 / 2) with t = 1 / (1 + 0.28 |x|) and q a polynomial
+// without constant term, fitted by a Lawson iteration of weighted least squares.
+// Written on |x|, it has no cancellation on the negative side, where gelu is |x| times
+// it.  Two of them:
+//   degree 6, nearest in absolute distance over x = 0 .. 9: 3e-8 (4e-8 evaluated in
+//     fp32); of the tail itself 5e-6 at 3, 1e-4 at 6, 1e-3 at 9, 4e-3 at 14.  For 16-bit
+//     data, whose rounding (2^-11 down to 1e-8, that is x = 6; 2^-8) lies above.
+//   degree 9, nearest in relative distance over x = 0 .. 14.4, where the product
+//     leaves fp32's range: 6e-8, evaluated in fp32 4e-7; with the rounded argument
+//     of the exponential the tail is within (15 + 1.25 x^2) 2^-24 of itself.  For
+//     32-bit data; with 16-bit ones it would take an 8192 x 14336 gradient from 139
+//     to 145 us and a product of that size with gelu from 351 to 361.
 constexpr float kTailT = 0.28f;
-constexpr float kTail1 = 0.116520897f, kTail2 = 0.0674960166f, kTail3 = 0.268912017f;
-constexpr float kTail4 = -0.236995801f, kTail5 = 0.389875442f, kTail6 = -0.105808601f;
+template <bool kFine>
+__host__ __device__ constexpr int tail_degree() { return kFine ? 9 : 6; }
+// Coefficient of t^(i + 1).
+template <bool kFine>
+__host__ __device__ constexpr float tail_coef(int i) {
+    if constexpr (kFine) {
+        constexpr float c[9] = {0.11168936f, 0.11195968f, 0.10117771f, 0.09112499f, 0.055468258f,
+                                0.017690117f, 0.07250024f, -0.08466628f, 0.023055973f};
+        return c[i];
+    } else {
+        constexpr float c[6] = {0.116520897f, 0.0674960166f, 0.268912017f,
+                                -0.236995801f, 0.389875442f, -0.105808601f};
+        return c[i];
+    }
+}
+template <bool kFine>
 __device__ __forceinline__ float tail_poly(float t) {
-    float q = __fmaf_rn(t, kTail6, kTail5);
-    q = __fmaf_rn(t, q, kTail4);
-    q = __fmaf_rn(t, q, kTail3);
-    q = __fmaf_rn(t, q, kTail2);
-    q = __fmaf_rn(t, q, kTail1);
+    constexpr int kD = tail_degree<kFine>();
+    float q = tail_coef<kFine>(kD - 1);
+#pragma unroll
+    for (int i = kD - 2; i >= 0; --i) q = __fmaf_rn(t, q, tail_coef<kFine>(i));
     return fmul(t, q);
+}
+template <bool kFine>
+__device__ __forceinline__ uint64_t tail_poly2(uint64_t t) {
+    constexpr int kD = tail_degree<kFine>();
+    uint64_t q = pk(tail_coef<kFine>(kD - 1), tail_coef<kFine>(kD - 1));
+#pragma unroll
+    for (int i = kD - 2; i >= 0; --i)
+        q = fma2(t, q, pk(tail_coef<kFine>(i), tail_coef<kFine>(i)));
+    return mul2(t, q);
 }
 
 // silu for 32-bit outputs, kN elements in place: the argument's rounding put back to
@@ -90,8 +118,8 @@ __device__ __forceinline__ void silu_values(float (&v)[kN]) {
 }
 
 // Values of kN elements in place, step by step over groups of eight so that
-// eight independent chains are in flight.
-template <Act A, int kN>
+// eight independent chains are in flight.  kFine: for 32-bit outputs.
+template <Act A, bool kFine, int kN>
 __device__ __forceinline__ void act_values(float (&v)[kN]) {
     constexpr int kG = kN < 8 ? kN : 8;
 #pragma unroll
@@ -119,7 +147,7 @@ __device__ __forceinline__ void act_values(float (&v)[kN]) {
             for (int i = 0; i < kG; ++i)
                 e[i] = ex2(fmul(fmul(v[g + i], v[g + i]), 0.5f * kNegLog2e));
 #pragma unroll
-            for (int i = 0; i < kG; ++i) t[i] = fmul(tail_poly(t[i]), e[i]);
+            for (int i = 0; i < kG; ++i) t[i] = fmul(tail_poly<kFine>(t[i]), e[i]);
         }
 #pragma unroll
         for (int i = 0; i < kG; ++i) {
@@ -150,8 +178,8 @@ __device__ __forceinline__ uint64_t rcp_2(uint64_t x) {
 //   gelu_tanh  s + p u2' s (1 - s),  s = s(u2), u2 = 2 sqrt(2/pi) (p + 0.044715 p^3)
 //   gelu       Phi(p) + p phi(p)
 // For every finite p, up to the type's largest; infinities end in inf * 0 = NaN, as
-// these forms do (relu: 1 and 0).
-template <Act A>
+// these forms do (relu: 1 and 0).  kFine: for 32-bit data.
+template <Act A, bool kFine>
 __device__ __forceinline__ uint64_t act_slope2(uint64_t p) {
     if constexpr (A == Act::RELU) {
         float a, b;
@@ -180,15 +208,10 @@ __device__ __forceinline__ uint64_t act_slope2(uint64_t p) {
         upk(p, a, b);
         const uint64_t t = rcp_2(fma2(pk(fabsf(a), fabsf(b)), pk1(kTailT), pk1(1.0f)));
         const uint64_t e = ex2_2(mul2(mul2(p, p), pk1(0.5f * kNegLog2e)));
-        uint64_t q = fma2(t, pk1(kTail6), pk1(kTail5));
-        q = fma2(t, q, pk1(kTail4));
-        q = fma2(t, q, pk1(kTail3));
-        q = fma2(t, q, pk1(kTail2));
-        q = fma2(t, q, pk1(kTail1));
         // Phi(-|p|) as it is for negative p, where the slope is small: by way of
         // Phi - 1/2 an 8192 x 14336 gradient takes 135 instead of 139 us, but as many
         // of its codes as a plain form's differ from the exact ones, not 60 % of them
-        const uint64_t tail = mul2(mul2(t, q), e);
+        const uint64_t tail = mul2(tail_poly2<kFine>(t), e);
         float ta, tb, ua, ub;
         upk(tail, ta, tb);
         upk(sub2(pk1(1.0f), tail), ua, ub);

@@ -218,13 +218,14 @@ __device__ __forceinline__ void store_out(void* p, int64_t i, float v) {
 
 template <Out OT, int kN>
 __device__ __forceinline__ void act_apply(int act, float (&v)[kN]) {
+    constexpr bool kFine = OT == Out::F32;
     switch (static_cast<Act>(act)) {
-        case Act::RELU: act_values<Act::RELU>(v); break;
-        case Act::GELU: act_values<Act::GELU>(v); break;
-        case Act::GELU_TANH: act_values<Act::GELU_TANH>(v); break;
+        case Act::RELU: act_values<Act::RELU, kFine>(v); break;
+        case Act::GELU: act_values<Act::GELU, kFine>(v); break;
+        case Act::GELU_TANH: act_values<Act::GELU_TANH, kFine>(v); break;
         case Act::SILU:
-            if constexpr (OT == Out::F32) silu_values(v);
-            else act_values<Act::SILU>(v);
+            if constexpr (kFine) silu_values(v);
+            else act_values<Act::SILU, kFine>(v);
             break;
         default: break;
     }

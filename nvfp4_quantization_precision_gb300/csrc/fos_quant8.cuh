@@ -104,7 +104,7 @@ __global__ void __launch_bounds__(kQ8Threads, 3) k_quant8(const Quant8Args a) {
                 uint64_t pv[8];
                 widen<IT>(p[b], pv);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) d[j] = mul2(d[j], act_slope2<A>(pv[j]));
+                for (int j = 0; j < 8; ++j) d[j] = mul2(d[j], act_slope2<A, IT == In::F32>(pv[j]));
             }
             if (i + kAhead < 4) load(i + kAhead, x[b], p[b]);
             if (a.codes) {

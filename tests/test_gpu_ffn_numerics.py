@@ -163,7 +163,7 @@ def _rel(act, v):
     return E * (15.2 + 1.25 * v * v)
 
 
-@pytest.mark.parametrize("act", ["relu", "gelu_tanh", "silu"])
+@pytest.mark.parametrize("act", ["relu", "gelu", "gelu_tanh", "silu"])
 @pytest.mark.parametrize("rows", [1, 3, 700])
 def test_activation_relative_to_its_result(act, rows):
     """fp32 outputs over -100 .. 100 and out to the type's ends, from the kernel for
@@ -189,6 +189,30 @@ def test_activation_relative_to_its_result(act, rows):
     ref.near(out, want, bound, act)
 
 
+@pytest.mark.parametrize("dt", [BF16, F16])
+@pytest.mark.parametrize("act", ["relu", "gelu", "gelu_tanh", "silu"])
+def test_activation_of_16_bit_outputs(act, dt):
+    """16-bit outputs over -80 .. 80: the type's rounding, and of the shorter forms silu's
+    argument (1.5 e |v|: its rounding and the constant's) and gelu's tail (5.5e-6
+    of itself to 3, 1.1e-4 to 6, 1.1e-3 to 9, 5e-3 beyond)."""
+    v = torch.cat((torch.linspace(-12, 12, 4096 * 3, device=DEV), torch.linspace(-80, 80, 4096, device=DEV)))
+    for rows in (1, 700):
+        out, _ = _sweep(v, act, dt, rows)
+        x = v.to(D)
+        want = _act64(x, act)
+        if act == "relu":
+            r = torch.zeros_like(x)
+        elif act == "silu":
+            r = E * (10 + 1.5 * x.abs())
+        else:
+            r = _rel(act, x)
+        if act == "gelu":
+            a = x.abs()
+            r = r + torch.where(a <= 3, 5.5e-6, torch.where(a <= 6, 1.1e-4, torch.where(a <= 9, 1.1e-3, 5e-3)))
+        bound = torch.where(x < 0, want.abs() * r, want.abs() * 4 * E + _act64(-x, act).abs() * r)
+        ref.near(out, want, bound * 1.01 + want.abs() * ref.U[dt] * (1 + 2.0 ** -7) + ref.TINY[dt] + 2.0 ** -117, act)
+
+
 def test_silu_below_the_range_of_the_exponential():
     """silu down to -103, where exp(-v) leaves fp32's range at -88.7 and the result
     itself only below -92: relative to the result, to a subnormal's spacing."""
@@ -210,7 +234,7 @@ def test_activations_of_infinities_and_nan():
             assert math.isfinite(out[3].item())
 
 
-@pytest.mark.parametrize("act", ["gelu_tanh", "silu"])
+@pytest.mark.parametrize("act", ["gelu", "gelu_tanh", "silu"])
 def test_derivative_relative_to_its_terms(act):
     """act_backward in fp32 with dout = 1 over -30 .. 30: the error is relative to
     the sizes of the derivative's terms, which vanish in the negative tail.
