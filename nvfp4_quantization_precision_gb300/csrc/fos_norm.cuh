@@ -46,7 +46,8 @@ struct NormArgs {
     int64_t rows;
     int64_t cols;
     int64_t pc4;        // tiled scales: 4-block tiles per tile-row
-    float inv_cols;     // 1 / cols
+    float inv_cols;     // 1 / cols, rounded, and
+    float inv_cols_lo;  // what the rounding leaves out
     float eps;
     int w32;            // weight is fp32 (else the data's type)
     int tiled;
@@ -63,6 +64,13 @@ __device__ __forceinline__ float lanes_sum(float v) {
 template <int kW>
 __device__ __forceinline__ float parts_sum(const float* part) {
     return lanes_sum<kW>(part[threadIdx.x & (kW - 1)]);
+}
+
+// s / cols + add.  1 / cols rounded to fp32 is off by the same 2^-25 or less in every
+// row (7168: 4.5e-8, half of it in rstd, as much as all roundings of the row together),
+// which one more multiply-add takes out (of a finite sum: an infinite one stays that).
+__device__ __forceinline__ float row_mean(float s, float inv, float inv_lo, float add) {
+    return __fmaf_rn(s, inv, __fmaf_rn(fmaxf(fminf(s, kFltMax), -kFltMax), inv_lo, add));
 }
 
 // 1 / sqrt(m): the hardware's approximation (2 ulp) and one Newton step, whose
@@ -219,7 +227,7 @@ __global__ void __launch_bounds__(kT < 256 ? 256 : kT) k_rms_norm(const NormArgs
             __syncthreads();
             s = parts_sum<kW>(s_part[parity] + g * kW);
         }
-        const float rs = rsqrt1(__fmaf_rn(s, a.inv_cols, a.eps));
+        const float rs = rsqrt1(row_mean(s, a.inv_cols, a.inv_cols_lo, a.eps));
         if (t == 0 && a.rstd && row < a.rows) a.rstd[row] = rs;
 #pragma unroll
         for (int k = 0; k < kSeg; ++k)
@@ -258,7 +266,7 @@ __global__ void __launch_bounds__(512) k_rms_norm_wide(const NormArgs a) {
         if ((t & 31) == 0) s_part[parity][t >> 5] = s;
         __syncthreads();
         s = parts_sum<kT / 32>(s_part[parity]);
-        const float rs = rsqrt1(__fmaf_rn(s, a.inv_cols, a.eps));
+        const float rs = rsqrt1(row_mean(s, a.inv_cols, a.inv_cols_lo, a.eps));
         if (t == 0 && a.rstd) a.rstd[row] = rs;
         for (int64_t base = 0; base < nseg; base += kT) {  // whole warps for the block shuffles
             const int64_t sg = base + t;
@@ -286,7 +294,8 @@ struct NormBwdArgs {
     void* dx;
     float* part;          // [gridDim.x, cols] partial weight gradients, or null
     int64_t rows, cols;
-    float inv_cols;
+    float inv_cols;       // as in NormArgs
+    float inv_cols_lo;
     int w32;
 };
 
@@ -395,7 +404,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) k_rms_bwd(const NormBwdArgs a)
         }
         if (col_in) {
             constexpr int64_t kElt = (IT == In::F32) ? 4 : 2;
-            const float c = fmul(fmul(s, a.inv_cols), rstd);
+            const float c = fmul(row_mean(s, a.inv_cols, a.inv_cols_lo, 0.0f), rstd);
             uint64_t dx[8];
             bwd_dx<DH>(v, hv, dhv, rstd, c, dx);
             store_seg<IT>(static_cast<char*>(a.dx) + (row * a.cols + t * 16) * kElt, dx);
@@ -455,7 +464,7 @@ __global__ void __launch_bounds__(512) k_rms_bwd_wide(const NormBwdArgs a) {
         s = 0.0f;
 #pragma unroll
         for (int i = 0; i < kT / 32; ++i) s = fadd(s, s_part[parity][i]);
-        const float c = fmul(fmul(s, a.inv_cols), rstd);
+        const float c = fmul(row_mean(s, a.inv_cols, a.inv_cols_lo, 0.0f), rstd);
         for (int64_t sg = t; sg < nseg; sg += kT) {
             Raw<IT> dy, h, dh;
             uint64_t v[8], hv[8], dhv[8], w[8], dx[8];

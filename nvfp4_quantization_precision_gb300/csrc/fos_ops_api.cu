@@ -186,6 +186,7 @@ fos_status fos_rms_norm(const void* x, const void* residual, const void* weight,
     a.cols = cols;
     a.pc4 = pc4_of(cols);
     a.inv_cols = 1.0f / (float)cols;
+    a.inv_cols_lo = (float)(1.0 / (double)cols - (double)a.inv_cols);
     a.eps = eps;
     a.w32 = weight_dt == FOS_FP32;
     a.tiled = scale_layout == FOS_SCALES_TILED;
@@ -233,6 +234,7 @@ fos_status fos_rms_norm_backward(const void* dy, const void* h, const void* dh, 
     a.rows = rows;
     a.cols = cols;
     a.inv_cols = 1.0f / (float)cols;
+    a.inv_cols_lo = (float)(1.0 / (double)cols - (double)a.inv_cols);
     a.w32 = weight_dt == FOS_FP32;
     return cuda_status(launch_rms_bwd(in_of(dt), a, dweight, static_cast<float*>(workspace),
                                       rows < kMaxParts ? rows : kMaxParts, s));

@@ -260,3 +260,22 @@ def test_derivative_relative_to_its_terms(act):
         es = s * r * E * (4 + (1.5 if act == "silu" else 3.5) * z.abs()) + s * 3 * E
         bound = es + (p * dz).abs() * (es * r + s * (es + r * E) + s * r * 4 * E) + want.abs() * 2 * E
     ref.near(d, want, bound * 1.02 + 2.0 ** -110, act)
+
+
+@pytest.mark.parametrize("cols", [32 * 49, 32 * 41, 2080, 7168, 7456, 8224, 14336, 16416])
+def test_rstd_has_no_bias(cols):
+    """Rows of small integers, whose sums of squares are exact: what is left in rstd
+    are roundings of either sign, at most 2 e in each row, so their mean over n
+    rows is within 5 * 2 e / sqrt(3 n) (five standard deviations of uniform errors),
+    for widths that are no power of two as well.  1 / cols rounded to fp32 has one
+    error in every row."""
+    g = torch.Generator(device=DEV)
+    g.manual_seed(cols)
+    n = 20000
+    x = torch.randint(-3, 4, (n, cols), generator=g, device=DEV).to(BF16)
+    x[:, 0] = 1
+    rstd = fos.rms_norm(x, torch.ones(cols, device=DEV), eps=0.0, quantized=False)[4]
+    want = 1 / x.float().square().sum(1).to(D).div(cols).sqrt()
+    off = rstd.to(D) / want - 1
+    assert off.abs().max() < 2 * E
+    assert abs(off.mean().item()) < 10 * E / math.sqrt(3 * n), off.mean().item() / E
