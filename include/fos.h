@@ -412,12 +412,14 @@ FOS_API fos_status fos_quantize_grouped(const void* x, fos_dtype dt, int64_t row
  *
  * Sums, the norm's statistics and every step before the one rounding to the
  * output's type are fp32.  Sums have a fixed order: equal calls give equal
- * bits.  Outputs must not overlap inputs or one another.  rows and cols below
- * 2^30.  Tensors 32-byte, codes 16-byte (codes_t 32-byte), tiled scales
- * 4-byte, workspaces 256-byte aligned.  Errors: FOS_ERR_INVALID_ARG (bad
- * enum, negative size, missing pointer, codes without scales, pointers on
- * different devices, a workspace too small), FOS_ERR_UNSUPPORTED (cols % 32,
- * sizes above the limits), FOS_ERR_MISALIGNED.
+ * bits.  Outputs must not overlap inputs or one another, except that an output
+ * may be the very tensor of an input where its call says "in the place of".
+ * rows and cols below 2^30.  Tensors 32-byte, codes 16-byte (codes_t
+ * 32-byte), tiled scales 4-byte, workspaces 256-byte aligned.  Errors:
+ * FOS_ERR_INVALID_ARG (bad enum, negative size, missing pointer, codes
+ * without scales, pointers on different devices, a workspace too small, an
+ * overlap), FOS_ERR_UNSUPPORTED (cols % 32, sizes above the limits),
+ * FOS_ERR_MISALIGNED.
  */
 FOS_API int64_t fos_scales8_bytes(int64_t rows, int64_t cols, int scale_layout);
 
@@ -427,7 +429,8 @@ FOS_API int64_t fos_scales8_bytes(int64_t rows, int64_t cols, int scale_layout);
  * of these is given: h and y rounded to dt, the 8-bit codes and scales of
  * the unrounded y, rstd [rows] fp32 (what the backward pass reads).  weight
  * [cols] is fp32 or of type dt.  eps finite and >= 0.  A row with an infinity
- * has rstd 0; a NaN spreads over its row.  cols == 0 is refused.
+ * has rstd 0; a NaN spreads over its row.  cols == 0 is refused.  h may be in
+ * the place of x or of residual.
  */
 FOS_API fos_status fos_rms_norm(const void* x, const void* residual, const void* weight,
                                 fos_dtype dt, fos_dtype weight_dt, int64_t rows, int64_t cols,
@@ -439,7 +442,8 @@ FOS_API fos_status fos_rms_norm(const void* x, const void* residual, const void*
  *   dx = rstd * (g - h * (rstd * mean(g * h * rstd))) + dh
  *   dweight[c] = sum over rows of dy * h * rstd            (fp32)
  * dy, h, dx are of type dt; dh (the gradient that reaches h past the norm)
- * may be NULL; dx is the gradient of x and, the same, of the residual.
+ * may be NULL; dx is the gradient of x and, the same, of the residual; it may be
+ * in the place of dy, h or dh.
  * dweight may be NULL.  With dweight, workspace holds
  * fos_rms_norm_backward_workspace_bytes(rows, cols) bytes of device memory.
  */
@@ -475,7 +479,8 @@ enum { FOS_ACT_NONE = 0, FOS_ACT_RELU = 1, FOS_ACT_GELU = 2, FOS_ACT_GELU_TANH =
  * gradient's), and dbias [cols] fp32, the sum of its columns.  dbias over
  * more than 128 rows needs fos_act_backward_workspace_bytes(rows, cols)
  * bytes of workspace.  relu'(0) = 0.  Every finite pre has its derivative (0 or 1
- * far out); an infinite or NaN pre gives NaN, with relu 1, 0 and 0.
+ * far out); an infinite or NaN pre gives NaN, with relu 1, 0 and 0.  d may be in
+ * the place of dout or of pre.
  */
 FOS_API size_t fos_act_backward_workspace_bytes(int64_t rows, int64_t cols);
 FOS_API fos_status fos_act_backward(const void* dout, const void* pre, fos_dtype dt, int64_t rows,
@@ -499,7 +504,7 @@ typedef struct {
  * fos_linear8 -- out [M, N] = act(a . b^T + bias) + residual from operands in
  * the 8-bit block format: a [M, K] (tokens) and b [N, K] (weights), codes
  * [M, K] and [N, K], scales tiled.  N % 16 == 0, K % 32 == 0, K > 0; M any
- * number from 0, one token included.
+ * number from 0, one token included.  out may be in the place of the residual.
  * fos_linear4 -- the same from NVFP4 operands as fos_mm takes them (1x16
  * codes [M, K/2] and [N, K/2], tiled scales, amaxes; cfg->granularity
  * FOS_SCALE_ROW: a_amax [M]); the product is (D * g_a(m)) * g_b as in fos_mm.

@@ -568,7 +568,8 @@ def rms_norm(x, weight, residual=None, eps=1e-6, scale_tiled=True, quantized=Tru
     """fos_rms_norm: h = x + residual, y = h / sqrt(mean(h^2) + eps) * weight
     over the rows of x [rows, cols].  Returns (codes, scales, y, h, rstd):
     y's 8-bit codes and scales (None without quantized), y itself with
-    normalized (else None), h (x itself without a residual) and rstd [rows]."""
+    normalized (else None), h (x itself without a residual) and rstd [rows].
+    h may be passed as x or as residual, to be written in its place."""
     shape, dt, dev = _data(x, "x")
     R, C = shape
     wdt = _weight(weight, C, x.dtype, dev)
@@ -628,7 +629,7 @@ def rms_norm_backward(dy, h, rstd, weight, dh=None, weight_grad=True, dx=None, d
     """fos_rms_norm_backward: (dx, dweight) from the gradient dy of the norm's
     output, the h and rstd the forward call returned, and optionally the
     gradient dh that reaches h from elsewhere.  dx is the gradient of x and of
-    the residual; dweight is fp32 (None without weight_grad).  workspace: at
+    the residual, and may be passed as dy, h or dh; dweight is fp32 (None without weight_grad).  workspace: at
     least fos_rms_norm_backward_workspace_bytes of uint8; when None, one that the
     binding keeps for this thread and stream (up to 16 MB, else allocated)."""
     shape, dt, dev = _data(dy, "dy")
@@ -685,8 +686,8 @@ def act_backward(dout, pre, act, scale_tiled=True, rowwise=True, colwise=True, v
     scales_t, d, dbias): its 8-bit rows (rowwise), its 8-bit columns
     (colwise), d itself (value) and the fp32 sum of its columns (bias_grad);
     what is not asked for is None.  act: "none", "relu", "gelu", "gelu_tanh",
-    "silu"; pre may be None with "none".  workspace: as in rms_norm_backward
-    (fos_act_backward_workspace_bytes)."""
+    "silu"; pre may be None with "none".  d may be passed as dout or as pre.
+    workspace: as in rms_norm_backward (fos_act_backward_workspace_bytes)."""
     shape, dt, dev = _data(dout, "dout")
     R, C = shape
     a = _act(act)
@@ -766,9 +767,9 @@ def linear8(a_codes, a_scales, b_codes, b_scales, act="none", bias=None, residua
             out_dtype=torch.bfloat16, save_pre=False, out=None, pre=None):
     """fos_linear8: act(a . b^T + bias) + residual from 8-bit block operands a
     [M, K] and b [N, K] (codes, tiled scales).  bias [N] is fp32 or of the
-    output's type, residual [M, N] of the output's type.  Returns out, or (out,
-    pre) with save_pre: pre is the value before the activation, which
-    act_backward reads."""
+    output's type, residual [M, N] of the output's type; out may be the residual
+    itself.  Returns out, or (out, pre) with save_pre: pre is the value before
+    the activation, which act_backward reads."""
     M, K, dev = _operand(a_codes, a_scales, "a", 32)
     N, Kb, _ = _operand(b_codes, b_scales, "b", 32, dev)
     if K != Kb:

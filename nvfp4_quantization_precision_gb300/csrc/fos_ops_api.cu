@@ -52,6 +52,36 @@ int device_of_given(std::initializer_list<const void*> ptrs) {
     return dev;
 }
 
+// One tensor of a call.  An output (`may` given) may not touch another tensor, but
+// for the inputs named in `may` (a bit each, by position in the list), whose place
+// it may take whole: there each element is read before the one thread that reads
+// it writes it.
+struct Region {
+    const void* p;
+    int64_t bytes;
+    int may = -1;  // -1: an input
+};
+
+// Whether the outputs of a call keep apart from its other tensors.
+bool keep_apart(std::initializer_list<Region> all) {
+    const Region* r = all.begin();
+    const int n = (int)all.size();
+    for (int i = 0; i < n; ++i) {
+        if (r[i].may < 0 || !r[i].p || r[i].bytes <= 0) continue;
+        const uintptr_t a = reinterpret_cast<uintptr_t>(r[i].p), a1 = a + (uintptr_t)r[i].bytes;
+        for (int j = 0; j < n; ++j) {
+            if (j == i || !r[j].p || r[j].bytes <= 0 || (r[j].may >= 0 && j < i)) continue;
+            const uintptr_t b = reinterpret_cast<uintptr_t>(r[j].p), b1 = b + (uintptr_t)r[j].bytes;
+            if (a >= b1 || b >= a1) continue;
+            const bool place = r[j].may < 0 && (r[i].may >> j & 1) && a == b && a1 == b1;
+            if (!place) return false;
+        }
+    }
+    return true;
+}
+
+int64_t elt_of(int dt) { return dt == FOS_FP32 ? 4 : 2; }
+
 cudaStream_t stream_of(fos_stream_t s) { return reinterpret_cast<cudaStream_t>(s); }
 
 int64_t q8_tiles(int64_t rows) { return (rows + kQ8Tile - 1) / kQ8Tile; }
@@ -83,6 +113,15 @@ fos_status run_quant8(const void* x, const void* pre, fos_dtype dt, int64_t rows
         if (!aligned(workspace, 256)) return FOS_ERR_MISALIGNED;
     }
     if (rows == 0 && !dbias) return FOS_OK;
+    const int64_t nb = rows * cols * elt_of(dt), rows_pad = (rows + 31) / 32 * 32;
+    if (!keep_apart({{x, nb}, {act != FOS_ACT_NONE ? pre : nullptr, nb}, {d, nb, 3},
+                     {codes, rows * cols, 0}, {scales, fos_scales8_bytes(rows, cols, layout), 0},
+                     {codes_t, cols * rows_pad, 0},
+                     {scales_t, codes_t ? fos_scales8_bytes(cols, rows_pad, layout) : 0, 0},
+                     {dbias, cols * 4, 0},
+                     {sums ? workspace : nullptr,
+                      (int64_t)fos_act_backward_workspace_bytes(rows, cols), 0}}))
+        return FOS_ERR_INVALID_ARG;
     const int dev = device_of_given({x, act != FOS_ACT_NONE ? pre : nullptr, d, codes, scales,
                                      codes_t, scales_t, dbias, sums ? workspace : nullptr});
     if (dev < 0) return FOS_ERR_INVALID_ARG;
@@ -100,7 +139,7 @@ fos_status run_quant8(const void* x, const void* pre, fos_dtype dt, int64_t rows
     a.part = dbias ? (sums ? static_cast<float*>(workspace) : dbias) : nullptr;
     a.rows = rows;
     a.cols = cols;
-    a.rows_pad = (rows + 31) / 32 * 32;
+    a.rows_pad = rows_pad;
     a.tiles_c = tiles_c;
     a.pc4 = pc4_of(cols);
     a.pc4_t = pc4_of(a.rows_pad);
@@ -127,6 +166,13 @@ fos_status run_linear(LinearCall c, const fos_epilogue* e, void* out, cudaStream
         !aligned(out, 16) || !aligned(e->residual, 16) || !aligned(e->pre, 16) ||
         !aligned(e->bias, 16))
         return FOS_ERR_MISALIGNED;
+    const int64_t blk = c.fmt4 ? 16 : 32, half = c.fmt4 ? 2 : 1, no = c.M * c.N * elt_of(e->out_dt);
+    auto tiles = [&](int64_t rows) { return (rows + 127) / 128 * ((c.K + 4 * blk - 1) / (4 * blk)) * 512; };
+    if (!keep_apart({{e->residual, no}, {c.a, c.M * c.K / half}, {c.as, tiles(c.M)},
+                     {c.b, c.N * c.K / half}, {c.bs, tiles(c.N)},
+                     {c.ep.a_amax, 4 * (c.ep.a_row ? c.M : 1)}, {c.ep.b_amax, 4},
+                     {e->bias, c.N * elt_of(e->bias_dt)}, {out, no, 1}, {e->pre, no, 0}}))
+        return FOS_ERR_INVALID_ARG;
     const int dev = device_of_given({c.a, c.as, c.b, c.bs, c.ep.a_amax, c.ep.b_amax, e->bias,
                                      e->residual, e->pre, out});
     if (dev < 0) return FOS_ERR_INVALID_ARG;
@@ -169,6 +215,11 @@ fos_status fos_rms_norm(const void* x, const void* residual, const void* weight,
         return FOS_ERR_MISALIGNED;
     st = check_pair(codes, scales, 16, scale_layout == FOS_SCALES_TILED);
     if (st) return st;
+    const int64_t nb = rows * cols * elt_of(dt);
+    if (!keep_apart({{x, nb}, {residual, nb}, {weight, cols * elt_of(weight_dt)}, {h, nb, 3}, {y, nb, 0},
+                     {codes, rows * cols, 0}, {scales, fos_scales8_bytes(rows, cols, scale_layout), 0},
+                     {rstd, rows * 4, 0}}))
+        return FOS_ERR_INVALID_ARG;
     const int dev = device_of_given({x, residual, weight, h, y, codes, scales, rstd});
     if (dev < 0) return FOS_ERR_INVALID_ARG;
     DeviceScope scope(dev);
@@ -216,6 +267,10 @@ fos_status fos_rms_norm_backward(const void* dy, const void* h, const void* dh, 
         if (!workspace || workspace_bytes < need) return FOS_ERR_INVALID_ARG;
         if (!aligned(workspace, 256)) return FOS_ERR_MISALIGNED;
     }
+    const int64_t nb = rows * cols * elt_of(dt);
+    if (!keep_apart({{dy, nb}, {h, nb}, {dh, nb}, {rstd, rows * 4}, {weight, cols * elt_of(weight_dt)},
+                     {dx, nb, 7}, {dweight, cols * 4, 0}, {need ? workspace : nullptr, (int64_t)need, 0}}))
+        return FOS_ERR_INVALID_ARG;
     const int dev = rows > 0 ? device_of_given({dy, h, dh, rstd, weight, dx, dweight,
                                                 need ? workspace : nullptr})
                              : device_of(dweight);

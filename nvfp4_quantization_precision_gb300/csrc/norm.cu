@@ -116,14 +116,23 @@ cudaError_t bwd_by_width(NormBwdArgs& a, float* dw, float* part, int64_t max_par
     if (nseg <= 256) return bwd_go<IT, 256>(a, dw, part, max_parts, s);
     if (nseg <= 512) return bwd_go<IT, 512>(a, dw, part, max_parts, s);
     auto k = k_rms_bwd_wide<IT>;
-    cudaError_t e = launch_chained(k, dim3((unsigned)row_grid(k, 512, a.rows, 1)), 512, 0, s, a);
-    if (e != cudaSuccess || !dw) return e;
+    auto input_grad = [&] {
+        return launch_chained(k, dim3((unsigned)row_grid(k, 512, a.rows, 1)), 512, 0, s, a);
+    };
+    if (!dw) return input_grad();
     const int64_t strips = (a.cols + 4095) / 4096;
     int64_t parts = (2 * sm_count() + strips - 1) / strips;
     if (parts > a.rows) parts = a.rows;
     if (parts > max_parts) parts = max_parts;
     a.part = parts == 1 ? dw : part;
-    e = launch_chained(k_rms_dw_wide<IT>, dim3((unsigned)strips, (unsigned)parts), 256, 0, s, a);
+    auto weight_grad = [&] {
+        return launch_chained(k_rms_dw_wide<IT>, dim3((unsigned)strips, (unsigned)parts), 256, 0, s, a);
+    };
+    // the weight gradient reads dy and h as well, so it goes first where dx takes
+    // their place (2048 x 16384 bf16 with dh: 90.7 us, the other way 88.1)
+    const bool replaced = a.dx == a.dy || a.dx == a.h;
+    cudaError_t e = replaced ? weight_grad() : input_grad();
+    if (e == cudaSuccess) e = replaced ? input_grad() : weight_grad();
     if (e != cudaSuccess || parts == 1) return e;
     return launch_column_sums(part, parts, a.cols, dw, s);
 }

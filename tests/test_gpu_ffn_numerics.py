@@ -279,3 +279,99 @@ def test_rstd_has_no_bias(cols):
     off = rstd.to(D) / want - 1
     assert off.abs().max() < 2 * E
     assert abs(off.mean().item()) < 10 * E / math.sqrt(3 * n), off.mean().item() / E
+
+
+def _rand(rows, cols, dt, seed):
+    g = torch.Generator(device=DEV)
+    g.manual_seed(seed)
+    return torch.randn(rows, cols, generator=g, device=DEV).to(dt)
+
+
+@pytest.mark.parametrize("cols", [64, 2048, 4096, 16384, 16416])
+@pytest.mark.parametrize("dt", [BF16, F32])
+def test_norm_in_place(cols, dt):
+    """h in the place of the residual or of x."""
+    for rows in (1, 700):
+        x, r, w = _rand(rows, cols, dt, 1), _rand(rows, cols, dt, 2), torch.ones(cols, device=DEV)
+        want = fos.rms_norm(x, w, r, normalized=True)
+        for which in (0, 1):
+            a, b = x.clone(), r.clone()
+            got = fos.rms_norm(a, w, b, normalized=True, h=(a, b)[which])
+            assert got[3] is (a, b)[which]
+            assert all(torch.equal(p, q) for p, q in zip(got, want))
+            assert torch.equal((a, b)[1 - which], (x, r)[1 - which])
+
+
+@pytest.mark.parametrize("cols", [64, 4096, 8192, 8224])
+@pytest.mark.parametrize("dt", [BF16, F32])
+def test_norm_backward_in_place(cols, dt):
+    """dx in the place of dy, h or dh."""
+    for rows in (1, 700):
+        dy, h, dh = (_rand(rows, cols, dt, k) for k in (1, 2, 3))
+        rstd, w = torch.rand(rows, device=DEV) + 0.5, torch.rand(cols, device=DEV) + 0.5
+        want = fos.rms_norm_backward(dy, h, rstd, w, dh)
+        for which in range(3):
+            t = [dy.clone(), h.clone(), dh.clone()]
+            got = fos.rms_norm_backward(t[0], t[1], rstd, w, t[2], dx=t[which])
+            assert all(torch.equal(p, q) for p, q in zip(got, want))
+
+
+def test_act_backward_in_place():
+    """d in the place of dout or of pre."""
+    for dt in (BF16, F32):
+        dout, pre = _rand(517, 1088, dt, 1), _rand(517, 1088, dt, 2)
+        want = fos.act_backward(dout, pre, "silu", value=True)
+        for which in (0, 1):
+            t = [dout.clone(), pre.clone()]
+            got = fos.act_backward(*t, "silu", value=True, d=t[which])
+            assert all(torch.equal(p, q) for p, q in zip(got, want))
+
+
+@pytest.mark.parametrize("fmt", [8, 4])
+@pytest.mark.parametrize("dt", [BF16, F32])
+def test_linear_in_place(fmt, dt):
+    """out in the place of the residual: a residual stream updated where it is."""
+    for M, N, K in ((1, 16, 64), (5, 16, 64), (48, 4096, 1024), (300, 48, 4096), (1500, 2064, 256)):
+        a, b, r = _rand(M, K, BF16, 1), _rand(N, K, BF16, 2), _rand(M, N, dt, 3)
+        if fmt == 8:
+            (ac, as_, _, _), (bc, bs, _, _) = fos.quantize8(a), fos.quantize8(b)
+            call = lambda res, **kw: fos.linear8(ac, as_, bc, bs, residual=res, out_dtype=dt, **kw)  # noqa: E731
+        else:
+            cfg = fos.Config(scale_tiled=True)
+            qa, qb = fos.quantize(a, cfg), fos.quantize(b, cfg)
+            call = lambda res, **kw: fos.linear4(*qa, *qb, residual=res, out_dtype=dt, **kw)  # noqa: E731
+        want, t = call(r), r.clone()
+        assert call(t, out=t) is t and torch.equal(t, want)
+
+
+def test_overlaps_are_refused():
+    """An output may be the same tensor as the inputs named in the header; any
+    other overlap is refused before a launch."""
+    buf = torch.zeros(4 * 64 * 64, dtype=BF16, device=DEV)
+    at = lambda o, r=64, c=64: buf[o:o + r * c].view(r, c)  # noqa: E731
+    x, res, w = at(0), at(4096), torch.ones(64, device=DEV)
+    rstd = torch.ones(64, device=DEV)
+    u8 = buf.view(torch.uint8)
+    bad = [
+        lambda: fos.rms_norm(x, w, res, h=at(64)),
+        lambda: fos.rms_norm(x, w, res, h=at(4096 - 64)),
+        lambda: fos.rms_norm(x, w, normalized=True, y=x),
+        lambda: fos.rms_norm(x, w, res, normalized=True, y=at(12288), h=at(12288)),
+        lambda: fos.rms_norm(x, w, codes=u8[:4096].view(64, 64)),
+        lambda: fos.rms_norm_backward(x, res, rstd, w, dx=at(4096 + 64)),
+        lambda: fos.rms_norm_backward(x, res, rstd, w, dweight=rstd),
+        lambda: fos.act_backward(x, res, "silu", value=True, d=at(64)),
+        lambda: fos.quantize8(x, codes=u8[:4096].view(64, 64)),
+        lambda: fos.act_backward(at(0, 256), at(0, 256), "silu", dbias=buf.view(F32)[:64]),
+    ]
+    for f in bad:
+        with pytest.raises(fos.FosError) as e:
+            f()
+        assert e.value.status == fos.FOS_ERR_INVALID_ARG
+    ac, as_, _, _ = fos.quantize8(x)
+    r2 = at(4096)
+    for kw in (dict(residual=r2, out=at(4096 + 64)), dict(out=at(0), pre=at(0), save_pre=True),
+               dict(residual=r2, pre=r2, save_pre=True), dict(bias=r2[0], out=r2)):
+        with pytest.raises(fos.FosError) as e:
+            fos.linear8(ac, as_, ac, as_, **kw)
+        assert e.value.status == fos.FOS_ERR_INVALID_ARG
