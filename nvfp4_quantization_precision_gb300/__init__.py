@@ -25,6 +25,7 @@ Entry points (names follow the C ABI):
   linear8(a_codes, a_scales, b_codes, b_scales, ...) -> act(a . b^T + bias) + residual
   linear4(a_codes, a_scales, a_amax, b_codes, b_scales, b_amax, ...) -> the same, NVFP4
   act_backward(dout, pre, act, ...)         -> (codes, scales, codes_t, scales_t, d, dbias)
+  release_workspaces()                      -> what the backward calls keep for this thread
 """
 import ctypes
 import os
@@ -600,8 +601,11 @@ def rms_norm(x, weight, residual=None, eps=1e-6, scale_tiled=True, quantized=Tru
 # threads may interleave the launches of their calls on one stream, and calls on
 # different streams overlap.  (An allocation in every call costs 5 to 6 of 16 to
 # 27 us on the host.)  Larger ones and those of a captured graph, which may be
-# replayed on any stream, are allocated by the call.
+# replayed on any stream, are allocated by the call.  A thread keeps those of the
+# streams it used last; what it gives up or leaves behind goes back to the
+# allocator of the stream that used it, which orders its next use.
 _KEPT_MOST = 16 << 20
+_KEPT_STREAMS = 8
 _kept = threading.local()
 
 
@@ -614,14 +618,24 @@ def _workspace(workspace, need, dev):
             return _new((need,), torch.uint8, dev), need
         key = (dev, _raw_stream(dev))
         mine = _kept.__dict__
-        workspace = mine.get(key)
+        workspace = mine.pop(key, None)
         if workspace is None or workspace.numel() < need:
-            mine[key] = workspace = _new((need,), torch.uint8, dev)
+            workspace = _new((need,), torch.uint8, dev)
+        mine[key] = workspace  # the latest one last
+        if len(mine) > _KEPT_STREAMS:
+            del mine[next(iter(mine))]
         return workspace, need
     _cuda(workspace, "workspace")
     if workspace.dtype != torch.uint8 or workspace.get_device() != dev:
         raise ValueError("workspace must be a uint8 tensor on cuda:%d" % dev)
     return workspace, workspace.numel()
+
+
+def release_workspaces():
+    """Gives back the workspaces that the binding keeps for the calling thread
+    (up to 16 MB for each of the eight streams it used last; a thread's go with
+    it when it ends)."""
+    _kept.__dict__.clear()
 
 
 def rms_norm_backward(dy, h, rstd, weight, dh=None, weight_grad=True, dx=None, dweight=None,
@@ -631,7 +645,8 @@ def rms_norm_backward(dy, h, rstd, weight, dh=None, weight_grad=True, dx=None, d
     gradient dh that reaches h from elsewhere.  dx is the gradient of x and of
     the residual, and may be passed as dy, h or dh; dweight is fp32 (None without weight_grad).  workspace: at
     least fos_rms_norm_backward_workspace_bytes of uint8; when None, one that the
-    binding keeps for this thread and stream (up to 16 MB, else allocated)."""
+    binding keeps for this thread and stream (up to 16 MB, else allocated; see
+    release_workspaces)."""
     shape, dt, dev = _data(dy, "dy")
     R, C = shape
     _like(h, "h", shape, dy.dtype, dev)

@@ -375,3 +375,28 @@ def test_overlaps_are_refused():
         with pytest.raises(fos.FosError) as e:
             fos.linear8(ac, as_, ac, as_, **kw)
         assert e.value.status == fos.FOS_ERR_INVALID_ARG
+
+
+def test_kept_workspaces_are_bounded_and_released():
+    """A thread keeps the workspaces of the streams that it used last, at most
+    eight, and gives them back when asked."""
+    dy, h = _rand(300, 512, BF16, 1), _rand(300, 512, BF16, 2)
+    rstd, w = torch.ones(300, device=DEV), torch.ones(512, device=DEV)
+    want = fos.rms_norm_backward(dy, h, rstd, w)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(12)]
+    for s in streams + streams[:3]:
+        s.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(s):
+            got = fos.rms_norm_backward(dy, h, rstd, w)
+        s.synchronize()
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+        assert len(fos._kept.__dict__) <= 8
+        assert list(fos._kept.__dict__)[-1] == (dy.get_device(), s.cuda_stream)
+    torch.cuda.synchronize()
+    before = torch.cuda.memory_allocated()
+    held = sum(v.numel() for v in fos._kept.__dict__.values())
+    fos.release_workspaces()
+    assert not fos._kept.__dict__ and before - torch.cuda.memory_allocated() >= held > 0
+    got = fos.rms_norm_backward(dy, h, rstd, w)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
