@@ -408,7 +408,9 @@ FOS_API fos_status fos_quantize_grouped(const void* x, fos_dtype dt, int64_t row
  * plain [rows, cols/32] (FOS_SCALES_PLAIN) or in the tiled layout of
  * fos_swizzle_scales applied to that matrix (FOS_SCALES_TILED, padding
  * zeroed by the call, what the products read): fos_scales8_bytes gives their
- * size, -1 for negative sizes, cols % 32 != 0 or a bad layout.
+ * size, -1 for negative sizes, sizes above 2^30, cols % 32 != 0 or a bad
+ * layout.  The workspace sizes below are 0 where a call needs none, and for
+ * sizes that it refuses.
  *
  * Sums, the norm's statistics and every step before the one rounding to the
  * output's type are fp32.  Sums have a fixed order: equal calls give equal

@@ -193,7 +193,9 @@ fos_status run_linear(LinearCall c, const fos_epilogue* e, void* out, cudaStream
 extern "C" {
 
 int64_t fos_scales8_bytes(int64_t rows, int64_t cols, int scale_layout) {
+    // of a column-wise form too, whose rows padded to 32 may reach 2^30
     if (rows < 0 || cols < 0 || cols % 32 != 0 || !valid_layout(scale_layout)) return -1;
+    if (rows > (INT64_C(1) << 30) || cols > (INT64_C(1) << 30)) return -1;
     if (scale_layout == FOS_SCALES_PLAIN) return rows * (cols / 32);
     return (rows + 127) / 128 * 128 * (pc4_of(cols) * 4);
 }
@@ -245,7 +247,7 @@ fos_status fos_rms_norm(const void* x, const void* residual, const void* weight,
 }
 
 size_t fos_rms_norm_backward_workspace_bytes(int64_t rows, int64_t cols) {
-    if (rows <= 1 || cols <= 0) return 0;
+    if (rows <= 1 || cols <= 0 || check_shape8(rows, cols)) return 0;
     return (size_t)(rows < kMaxParts ? rows : kMaxParts) * (size_t)cols * sizeof(float);
 }
 
@@ -303,7 +305,7 @@ fos_status fos_quantize8(const void* x, fos_dtype dt, int64_t rows, int64_t cols
 }
 
 size_t fos_act_backward_workspace_bytes(int64_t rows, int64_t cols) {
-    if (rows <= kQ8Tile || cols <= 0) return 0;
+    if (rows <= kQ8Tile || cols <= 0 || check_shape8(rows, cols)) return 0;
     return (size_t)q8_tiles(rows) * (size_t)cols * sizeof(float);
 }
 
