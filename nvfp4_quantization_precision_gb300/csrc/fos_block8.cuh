@@ -45,6 +45,18 @@ __device__ __forceinline__ void encode8(const uint64_t (&v)[8], float inv, uint3
     for (int k = 0; k < 4; ++k) w[k] = e4m3x4(v[2 * k], v[2 * k + 1], inv2);
 }
 
+// One value of data that the kernel before may have written (volatile like load_seg,
+// which orders it with the other loads).  Not __ldg: that promises data constant from the
+// kernel's start, and this kernel starts while the one before still runs, so the
+// compiler may move it past the wait, and L1 may hold its line from before the wait.
+// load_seg's lines are not kept in L1; of an output in the place of an input, each
+// element's store takes its value from the element's load, and nothing reads it after.
+__device__ __forceinline__ float ld_f32(const float* p) {
+    float v;
+    asm volatile("ld.global.f32 %0, [%1];" : "=f"(v) : "l"(p));
+    return v;
+}
+
 // Rounds 16 values to the storage type and stores them.
 template <In IT>
 __device__ __forceinline__ void store_seg(void* p, const uint64_t (&v)[8]) {

@@ -202,13 +202,13 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&v)[16]) {
 template <Out OT>
 __device__ __forceinline__ float load_out(const void* p, int64_t i) {
     if constexpr (OT == Out::BF16)
-        return __uint_as_float((uint32_t)__ldg(static_cast<const unsigned short*>(p) + i) << 16);
+        return __uint_as_float((uint32_t)static_cast<const unsigned short*>(p)[i] << 16);
     else if constexpr (OT == Out::F16) {
         float f;
-        asm("cvt.f32.f16 %0, %1;" : "=f"(f) : "h"(__ldg(static_cast<const unsigned short*>(p) + i)));
+        asm("cvt.f32.f16 %0, %1;" : "=f"(f) : "h"(static_cast<const unsigned short*>(p)[i]));
         return f;
     } else
-        return __ldg(static_cast<const float*>(p) + i);
+        return static_cast<const float*>(p)[i];
 }
 template <Out OT>
 __device__ __forceinline__ void store_out(void* p, int64_t i, float v) {
@@ -357,10 +357,10 @@ __device__ __forceinline__ void rows_stage(uint32_t acc, uint32_t p0, uint32_t q
 template <Out OT>
 __device__ __forceinline__ void load4(const void* p, int64_t i, float (&v)[4]) {
     if constexpr (OT == Out::F32) {
-        const float4 x = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(p) + i));
+        const float4 x = *reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
         v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
     } else {
-        const uint2 x = __ldg(reinterpret_cast<const uint2*>(static_cast<const unsigned short*>(p) + i));
+        const uint2 x = *reinterpret_cast<const uint2*>(static_cast<const unsigned short*>(p) + i);
         if constexpr (OT == Out::BF16) {
             v[0] = __uint_as_float(x.x << 16); v[1] = __uint_as_float(x.x & 0xFFFF0000u);
             v[2] = __uint_as_float(x.y << 16); v[3] = __uint_as_float(x.y & 0xFFFF0000u);
@@ -603,7 +603,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1) k_linear_rows(const __grid_co
                 // the tokens' decode scales, once per tile
                 gb = fdiv(1.0f, global_scale(a.ep.b_amax[0], a.ep.six_bound));
                 for (int c = 32 * e + lane; c < mt; c += 128)
-                    s_ga[c] = fdiv(1.0f, global_scale(__ldg(a.ep.a_amax + (a.ep.a_row ? m0 + c : 0)),
+                    s_ga[c] = fdiv(1.0f, global_scale(a.ep.a_amax[a.ep.a_row ? m0 + c : 0],
                                                       a.ep.six_bound));
             }
             if (!bad && !warp_wait(&sh.acc_full, (uint32_t)j & 1)) bad = true;

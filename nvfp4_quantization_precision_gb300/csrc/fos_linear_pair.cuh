@@ -176,7 +176,7 @@ __device__ __forceinline__ void load_bias(const Epilogue& e, int64_t n0, int64_t
         const int64_t n = n0 + 32 * i + lane;
         b[i] = 0.0f;
         if (n < N)
-            b[i] = e.bias32 ? __ldg(static_cast<const float*>(e.bias) + n) : load_out<OT>(e.bias, n);
+            b[i] = e.bias32 ? static_cast<const float*>(e.bias)[n] : load_out<OT>(e.bias, n);
     }
 }
 
@@ -518,7 +518,7 @@ __global__ void __launch_bounds__(pair_threads<F>(), 1) k_linear_pair(const __gr
             float ga = ga0;
             if constexpr (F::kGlobal)
                 if (a.ep.a_row && mw + lane < a.M)
-                    ga = fdiv(1.0f, global_scale(__ldg(a.ep.a_amax + mw + lane), a.ep.six_bound));
+                    ga = fdiv(1.0f, global_scale(a.ep.a_amax[mw + lane], a.ep.six_bound));
             if (a.ep.bias) {  // this tile's biases to shared memory, the next one's on their way
 #pragma unroll
                 for (int i = 0; i < kPairN / 32; ++i) s_bias[32 * i + lane] = bias[i];

@@ -362,12 +362,13 @@ __global__ void __launch_bounds__(kBwdThreads, 1) k_rms_bwd(const NormBwdArgs a)
     Raw<IT> dy, h, dh;
     if constexpr (kAhead)
         load_bwd_seg<IT, DH>(a, row * a.cols + t * 16, col_in && row < a.rows, dy, h, dh);
+    float rstd_next = kAhead && row < a.rows ? ld_f32(a.rstd + row) : 0.0f;
     if (col_in) load_weight<IT>(a.w, (int64_t)t * 16, a.w32, w);
     int parity = 0;
     // a group runs its own rows; only its warps meet at a barrier
     for (; row < a.rows; row += step, parity ^= 1) {
         if constexpr (!kAhead) load_bwd_seg<IT, DH>(a, row * a.cols + t * 16, col_in, dy, h, dh);
-        const float rstd = __ldg(a.rstd + row);
+        const float rstd = kAhead ? rstd_next : ld_f32(a.rstd + row);
         uint64_t v[8], hv[8], acc = 0;
         widen<IT>(dy, v);
         widen<IT>(h, hv);
@@ -381,9 +382,11 @@ __global__ void __launch_bounds__(kBwdThreads, 1) k_rms_bwd(const NormBwdArgs a)
         }
         uint64_t dhv[8];
         if constexpr (DH) widen<IT>(dh, dhv);
-        if constexpr (kAhead)
+        if constexpr (kAhead) {
             load_bwd_seg<IT, DH>(a, (row + step) * a.cols + t * 16, col_in && row + step < a.rows, dy,
                                  h, dh);
+            if (row + step < a.rows) rstd_next = ld_f32(a.rstd + row + step);
+        }
         if constexpr (kFar) {
             constexpr int kElt = (IT == In::F32) ? 4 : 2;
             const int64_t far = row + 2 * step;
@@ -441,7 +444,7 @@ __global__ void __launch_bounds__(512) k_rms_bwd_wide(const NormBwdArgs a) {
     const int64_t nseg = a.cols / 16;
     int parity = 0;
     for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, parity ^= 1) {
-        const float rstd = __ldg(a.rstd + row);
+        const float rstd = ld_f32(a.rstd + row);
         const uint64_t r2 = pk(rstd, rstd);
         uint64_t acc = 0;
         for (int64_t sg = t; sg < nseg; sg += kT) {
@@ -498,7 +501,7 @@ __global__ void __launch_bounds__(256) k_rms_dw_wide(const NormBwdArgs a) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) dw[j] = 0;
     for (int64_t row = blockIdx.y; row < a.rows; row += gridDim.y) {
-        const float rstd = __ldg(a.rstd + row);
+        const float rstd = ld_f32(a.rstd + row);
         const uint64_t r2 = pk(rstd, rstd);
         Raw<IT> dy, h;
         uint64_t v[8], hv[8];

@@ -18,7 +18,7 @@ __global__ void __launch_bounds__(32 * kSumWarps) k_column_sums(const float* par
             float v[8];
 #pragma unroll
             for (int k = 0; k < 8; ++k)
-                v[k] = p + k * kSumWarps < parts ? __ldg(part + (p + k * kSumWarps) * cols + c) : 0.0f;
+                v[k] = p + k * kSumWarps < parts ? ld_f32(part + (p + k * kSumWarps) * cols + c) : 0.0f;
 #pragma unroll
             for (int k = 0; k < 8; ++k) s = fadd(s, v[k]);
         }
