@@ -11,10 +11,11 @@
 // g the global decode scales).  Both keep 128 code bytes of a row per K stage
 // (the 128-byte swizzle) and take four MMAs of 32 bytes each; their scales
 // come as the 512-byte tiles of the tiled layout, one tile per 128 rows and 4
-// scale blocks, copied from shared to tensor memory by tcgen05.cp in the very
-// form the MMA reads them: scale j of row 32 i + l in byte j of column i of
-// lane l, for every quadrant of lanes.  F4 takes one tile per MMA (its four
-// 16-element blocks), F8 one tile per stage, the MMA choosing byte j.
+// scale blocks, and go from shared to tensor memory (k_linear_rows by
+// tcgen05.cp, k_linear_pair through registers) in the very form the MMA reads
+// them: scale j of row 32 i + l in byte j of column i of lane l, for every
+// quadrant of lanes.  F4 takes one tile per MMA (its four 16-element blocks), F8
+// one tile per stage, the MMA choosing byte j.
 #pragma once
 
 #include <cuda.h>
@@ -61,12 +62,10 @@ struct LinearCall {
 namespace lin {
 
 struct F8 {
-    static constexpr int kStageK = 128;   // K elements of a stage
     static constexpr int kSfTiles = 1;    // scale tiles of a stage, per 128 rows
     static constexpr bool kGlobal = false;
 };
 struct F4 {
-    static constexpr int kStageK = 256;
     static constexpr int kSfTiles = 4;
     static constexpr bool kGlobal = true;
 };
@@ -176,16 +175,10 @@ __device__ __forceinline__ void mma_issue(uint32_t acc, uint32_t alo, uint32_t b
 #undef FOS_MMA_TEXT
 
 // One scale tile from shared (low descriptor word) to tensor memory.
-template <int kPair>
 __device__ __forceinline__ void sf_copy(uint32_t taddr, uint32_t lo) {
-    if constexpr (kPair == 1)
-        asm volatile("{\n\t.reg .b64 d;\n\tmov.b64 d, {%1, %2};\n\t"
-                     "tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], d;\n\t}" ::"r"(taddr), "r"(lo),
-                     "r"(kSfDescHi) : "memory");
-    else
-        asm volatile("{\n\t.reg .b64 d;\n\tmov.b64 d, {%1, %2};\n\t"
-                     "tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], d;\n\t}" ::"r"(taddr), "r"(lo),
-                     "r"(kSfDescHi) : "memory");
+    asm volatile("{\n\t.reg .b64 d;\n\tmov.b64 d, {%1, %2};\n\t"
+                 "tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], d;\n\t}" ::"r"(taddr), "r"(lo),
+                 "r"(kSfDescHi) : "memory");
 }
 
 __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&v)[16]) {
@@ -337,10 +330,10 @@ __device__ __forceinline__ void rows_stage(uint32_t acc, uint32_t p0, uint32_t q
 #pragma unroll
     for (int kk = 0; kk < F::kSfTiles; ++kk) {
         if (kk < nk) {
-            sf_copy<1>(sfp + 4 * kk, lp + kk * kT);
+            sf_copy(sfp + 4 * kk, lp + kk * kT);
 #pragma unroll
             for (int q = 0; q < kQ; ++q)
-                sf_copy<1>(sfq + 4 * (kk * kQ + q), lq + (q * F::kSfTiles + kk) * kT);
+                sf_copy(sfq + 4 * (kk * kQ + q), lq + (q * F::kSfTiles + kk) * kT);
         }
     }
 #pragma unroll

@@ -87,6 +87,10 @@ struct RowsPlan {
 // 10.6 and 13.5, 19.0 and 13.7).
 template <class F, Out OT>
 RowsPlan rows_plan(const LinearCall& c) {
+    // The wait for the stage that used a scale buffer last may look back one turn
+    // of the ring at most (a full tile of tokens has the fewest stages).
+    static_assert((kSmemLimit - 3 * 1024) / rows_stage_bytes<F>(256) >= kSfRing && kMaxStages >= kSfRing,
+                  "stages");
     RowsPlan p;
     p.nt = c.M >= 256 ? 256 : (int)((c.M + 15) / 16 * 16);
     const int stage = rows_stage_bytes<F>(p.nt);
