@@ -45,50 +45,52 @@ constexpr float kLn2 = 0.69314718f;
 constexpr float kInvSqrt2Pi = 0.39894228040143268f;
 constexpr float k2Sqrt2OverPi = 1.5957691216057308f;  // 2 sqrt(2 / pi)
 
-// 1 - Phi(|x|) = q(t) exp(-x^2 / 2) with t = 1 / (1 + 0.28 |x|) and q a polynomial
-// without constant term, fitted by a Lawson iteration of weighted least squares.
-// Written on |x|, it has no cancellation on the negative side, where gelu is |x| times
-// it.  Two of them:
-//   degree 6, nearest in absolute distance over x = 0 .. 9: 3e-8 (4e-8 evaluated in
-//     fp32); of the tail itself 5e-6 at 3, 1e-4 at 6, 1e-3 at 9, 4e-3 at 14.  For 16-bit
-//     data, whose rounding (2^-11 down to 1e-8, that is x = 6; 2^-8) lies above.
-//   degree 9, nearest in relative distance over x = 0 .. 14.4, where the product
-//     leaves fp32's range: 6e-8, evaluated in fp32 4e-7; with the rounded argument
-//     of the exponential the tail is within (15 + 1.25 x^2) 2^-24 of itself.  For
-//     32-bit data; with 16-bit ones it would take an 8192 x 14336 gradient from 139
-//     to 145 us and a product of that size with gelu from 351 to 361.
-constexpr float kTailT = 0.28f;
+// 1 - Phi(|x|) = q(s) exp(-x^2 / 2) with s = |x| / (1 + c |x|) and q a polynomial whose
+// constant term is 1/2, fitted by a Lawson iteration of weighted least squares.  Written
+// on |x|, it has no cancellation on the negative side, where gelu is |x| times it;
+// in s, which is 0 with x, the reciprocal's rounding vanishes where q is large (a
+// polynomial in 1 / (1 + c |x|) is off by 4e-8 root mean square over 0 .. 1, this by 1.2e-8).
+// Two of them, their errors evaluated in fp32:
+//   degree 6, c = 0.38: 4e-9 of 1; of the tail itself 1.3e-6 to 3, 6e-5 to 6, 3e-4 to
+//     9, 3e-3 to 14.  For 16-bit data, whose rounding (2^-11 down to 1e-8, that is x =
+//     6; 2^-8) lies above.
+//   degree 9, c = 0.45, for 32-bit data: 1.8e-6 of the tail itself to 14.4, where the
+//     product leaves fp32's range.
+// Either way the exponential adds its own error, 4 * 2^-24, and its argument's, 1.25 x^2
+// 2^-24.
 template <bool kFine>
 __host__ __device__ constexpr int tail_degree() { return kFine ? 9 : 6; }
-// Coefficient of t^(i + 1).
+template <bool kFine>
+__host__ __device__ constexpr float tail_c() { return kFine ? 0.45f : 0.38f; }
+// Coefficient of s^(i + 1).
 template <bool kFine>
 __host__ __device__ constexpr float tail_coef(int i) {
     if constexpr (kFine) {
-        constexpr float c[9] = {0.11168936f, 0.11195968f, 0.10117771f, 0.09112499f, 0.055468258f,
-                                0.017690117f, 0.07250024f, -0.08466628f, 0.023055973f};
+        constexpr float c[9] = {-0.3989421f, 0.07047819f, 0.011195586f, -0.0013211702f, -0.0013286442f,
+                                0.00042060253f, -0.00041844323f, 0.0002011633f, -0.000029093711f};
         return c[i];
     } else {
-        constexpr float c[6] = {0.116520897f, 0.0674960166f, 0.268912017f,
-                                -0.236995801f, 0.389875442f, -0.105808601f};
+        constexpr float c[6] = {-0.3989426f, 0.0984082f, -0.0006266588f,
+                                -0.002581888f, -0.00040525946f, 0.00016812574f};
         return c[i];
     }
 }
 template <bool kFine>
-__device__ __forceinline__ float tail_poly(float t) {
+__device__ __forceinline__ float tail_poly(float s) {
     constexpr int kD = tail_degree<kFine>();
     float q = tail_coef<kFine>(kD - 1);
 #pragma unroll
-    for (int i = kD - 2; i >= 0; --i) q = __fmaf_rn(t, q, tail_coef<kFine>(i));
-    return fmul(t, q);
+    for (int i = kD - 2; i >= 0; --i) q = __fmaf_rn(s, q, tail_coef<kFine>(i));
+    return __fmaf_rn(s, q, 0.5f);
 }
 template <bool kFine>
-__device__ __forceinline__ uint64_t tail_poly2(uint64_t t) {
+__device__ __forceinline__ uint64_t tail_poly2(uint64_t s) {
     constexpr int kD = tail_degree<kFine>();
     uint64_t q = pk(tail_coef<kFine>(kD - 1), tail_coef<kFine>(kD - 1));
 #pragma unroll
     for (int i = kD - 2; i >= 0; --i)
-        q = fma2(t, q, pk(tail_coef<kFine>(i), tail_coef<kFine>(i)));
-    return mul2(t, q);
+        q = fma2(s, q, pk(tail_coef<kFine>(i), tail_coef<kFine>(i)));
+    return fma2(s, q, pk(0.5f, 0.5f));
 }
 
 // silu for 32-bit outputs, kN elements in place: the argument's rounding put back to
@@ -129,7 +131,8 @@ __device__ __forceinline__ void act_values(float (&v)[kN]) {
         for (int i = 0; i < kG; ++i) {
             const float x = v[g + i];
             if constexpr (A == Act::RELU) t[i] = x < 0.0f ? 0.0f : x;
-            if constexpr (A == Act::GELU) t[i] = rcp(__fmaf_rn(fabsf(x), kTailT, 1.0f));
+            if constexpr (A == Act::GELU)
+                t[i] = fmul(fabsf(x), rcp(__fmaf_rn(fabsf(x), tail_c<kFine>(), 1.0f)));
             if constexpr (A == Act::GELU_TANH)
                 t[i] = fmul(x, __fmaf_rn(kNegLog2e * k2Sqrt2OverPi * 0.044715f, fmul(x, x),
                                          kNegLog2e * k2Sqrt2OverPi));
@@ -176,7 +179,7 @@ __device__ __forceinline__ uint64_t rcp_2(uint64_t x) {
 // Derivatives of two elements, on packed pairs:
 //   silu       s (1 + p (1 - s))
 //   gelu_tanh  s + p u2' s (1 - s),  s = s(u2), u2 = 2 sqrt(2/pi) (p + 0.044715 p^3)
-//   gelu       Phi(p) + p phi(p)
+//   gelu       Phi(p) + p phi(p), Phi(-p) = q exp(-p^2 / 2)
 // For every finite p, up to the type's largest; infinities end in inf * 0 = NaN, as
 // these forms do (relu: 1 and 0).  kFine: for 32-bit data.
 template <Act A, bool kFine>
@@ -191,32 +194,33 @@ __device__ __forceinline__ uint64_t act_slope2(uint64_t p) {
         return mul2(s, fma2(p, sub2(pk1(1.0f), s), pk1(1.0f)));
     }
     if constexpr (A == Act::GELU_TANH) {
-        // p^2 no larger than 512, past which s is 0 or 1: p s (1 - s) u2' then has no
-        // factor that overflows, and the one that vanishes comes first
-        const uint64_t pp = mul2(p, p);
-        float a, b;
-        upk(pp, a, b);
-        const uint64_t p2 = pk(fminf(a, 512.0f), fminf(b, 512.0f));
-        const uint64_t z = mul2(p, fma2(p2, pk1(kNegLog2e * k2Sqrt2OverPi * 0.044715f),
-                                        pk1(kNegLog2e * k2Sqrt2OverPi)));
-        const uint64_t s = rcp_2(add2(ex2_2(z), pk1(1.0f)));
-        const uint64_t du = fma2(p2, pk1(k2Sqrt2OverPi * 0.134145f), pk1(k2Sqrt2OverPi));
-        return fma2(mul2(p, mul2(s, sub2(pk1(1.0f), s))), du, s);
-    }
-    if constexpr (A == Act::GELU) {
+        // 1 - s as E s, E = exp(-u2), without the cancellation (which for p = 2 .. 6 leaves
+        // an error of 3.6e-7 instead of 6e-8).  For u2 and its derivative p is held within
+        // 16, where E is 0, and -10.05, where E is finite and its reciprocal 0: no
+        // factor overflows, and the one that vanishes meets p first.
         float a, b;
         upk(p, a, b);
-        const uint64_t t = rcp_2(fma2(pk(fabsf(a), fabsf(b)), pk1(kTailT), pk1(1.0f)));
+        const uint64_t x = pk(fmaxf(fminf(a, 16.0f), -10.05f), fmaxf(fminf(b, 16.0f), -10.05f));
+        const uint64_t x2 = mul2(x, x);
+        const uint64_t e = ex2_2(mul2(x, fma2(x2, pk1(kNegLog2e * k2Sqrt2OverPi * 0.044715f),
+                                              pk1(kNegLog2e * k2Sqrt2OverPi))));
+        const uint64_t s = rcp_2(add2(e, pk1(1.0f)));
+        const uint64_t du = fma2(x2, pk1(k2Sqrt2OverPi * 0.134145f), pk1(k2Sqrt2OverPi));
+        return fma2(mul2(p, mul2(mul2(e, s), s)), du, s);
+    }
+    if constexpr (A == Act::GELU) {
+        // the negative side's slope exp(-p^2 / 2) (q - |p| / sqrt(2 pi)), the positive
+        // side's 1 minus that
+        float a, b;
+        upk(p, a, b);
+        const uint64_t x = pk(fabsf(a), fabsf(b));
+        const uint64_t t = mul2(x, rcp_2(fma2(x, pk1(tail_c<kFine>()), pk1(1.0f))));
         const uint64_t e = ex2_2(mul2(mul2(p, p), pk1(0.5f * kNegLog2e)));
-        // Phi(-|p|) as it is for negative p, where the slope is small: by way of
-        // Phi - 1/2 an 8192 x 14336 gradient takes 135 instead of 139 us, but as many
-        // of its codes as a plain form's differ from the exact ones, not 60 % of them
-        const uint64_t tail = mul2(tail_poly2<kFine>(t), e);
-        float ta, tb, ua, ub;
-        upk(tail, ta, tb);
-        upk(sub2(pk1(1.0f), tail), ua, ub);
-        const uint64_t cdf = pk(a < 0.0f ? ta : ua, b < 0.0f ? tb : ub);
-        return fma2(mul2(p, pk1(kInvSqrt2Pi)), e, cdf);
+        const uint64_t neg = mul2(fma2(x, pk1(-kInvSqrt2Pi), tail_poly2<kFine>(t)), e);
+        float na, nb, ua, ub;
+        upk(neg, na, nb);
+        upk(sub2(pk1(1.0f), neg), ua, ub);
+        return pk(a < 0.0f ? na : ua, b < 0.0f ? nb : ub);
     }
     return pk1(1.0f);
 }

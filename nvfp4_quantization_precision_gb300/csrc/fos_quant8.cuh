@@ -13,7 +13,7 @@
 // Bound by HBM: e (or 2e) bytes read per element, 2 + 1/16 written, e more for
 // d itself.  Measured (bf16, a device copy reaches 6.78 TB/s): 14336 x 4096, both
 // directions, 41.1 us, 5.8 TB/s (86 %); silu gradient with its column sums, 8192 x
-// 14336, 122 us, 5.8 TB/s (86 %; relu 119, gelu_tanh 125, gelu 139 us); 1000 x
+// 14336, 122 us, 5.8 TB/s (86 %; relu 119, gelu_tanh 128, gelu 139 us); 1000 x
 // 2048 f16 10.0 us, two launches and one tile's latency.
 // A CTA takes a tile of 128 rows x 128 columns: thread t reads 16-element
 // segments (t mod 8) of rows t / 8 + 32 i, so a warp reads four whole 256-byte
