@@ -22,7 +22,7 @@ enum class Act : int { NONE = 0, RELU = 1, GELU = 2, GELU_TANH = 3, SILU = 4 };
 // with expf and a refined reciprocal: 32 columns of gelu_tanh took 1800 cycles of the
 // product's epilogue that way.  The rounding of the argument adds a relative error
 // that grows in the negative tail, and there is one of the result:
-//   silu       (9 + |z|) 2^-24, up to 2^-17 at z = -87, where a result is below 2^-118
+//   silu       (9 + 1.3 |z|) 2^-24, up to 2^-17 at z = -87, where a result is below 2^-118
 //              and the next ones are 0.  Beneath a 16-bit output's own rounding (2^-11,
 //              2^-8); for 32-bit outputs silu_values takes a closer form.
 //   gelu_tanh  (9 + 3.5 |z|) 2^-24, for every output: v = -10 gives |z| = 87 and the
@@ -51,8 +51,8 @@ constexpr float k2Sqrt2OverPi = 1.5957691216057308f;  // 2 sqrt(2 / pi)
 // in s, which is 0 with x, the reciprocal's rounding vanishes where q is large (a
 // polynomial in 1 / (1 + c |x|) is off by 4e-8 root mean square over 0 .. 1, this by 1.2e-8).
 // Two of them, their errors evaluated in fp32:
-//   degree 6, c = 0.38: 4e-9 of 1; of the tail itself 1.3e-6 to 3, 6e-5 to 6, 3e-4 to
-//     9, 3e-3 to 14.  For 16-bit data, whose rounding (2^-11 down to 1e-8, that is x =
+//   degree 6, c = 0.38, fitted within 8e-9 in all and of the tail itself, as it is
+//     evaluated, 1.3e-6 to 3, 6e-5 to 6, 3e-4 to 9, 3e-3 to 14.  For 16-bit data, whose rounding (2^-11 down to 1e-8, that is x =
 //     6; 2^-8) lies above.
 //   degree 9, c = 0.45, for 32-bit data: 1.8e-6 of the tail itself to 14.4, where the
 //     product leaves fp32's range.

@@ -244,8 +244,8 @@ __device__ __forceinline__ void act_apply(int act, float (&v)[kN]) {
 // bounded; a CTA whose wait gave up writes NaN into the first element of its
 // output.
 // Measured, the weights' bytes over the time against a device copy's 6.78 TB/s:
-// 8 bit 14336 x 4096 (60.6 MB) 1 token 13.8 us, 4.4 TB/s (65 %); NVFP4 4096 x
-// 14336 (33 MB) 48 tokens 11.0 us, 3.1 TB/s (46 %).  Of those times 4.2 .. 4.5 us
+// 8 bit 14336 x 4096 (60.6 MB) 1 token 13.5 us, 4.5 TB/s (66 %); NVFP4 4096 x
+// 14336 (33 MB) 48 tokens 10.9 us, 3.1 TB/s (46 %).  Of those times 4.2 .. 4.5 us
 // are the launch, the first stage's way through memory and the last one's through
 // the epilogue, which do not shrink with the weights; in between a CTA takes a
 // stage every 0.32 us (8 bit; NVFP4 0.37), one warp issuing its four MMAs and

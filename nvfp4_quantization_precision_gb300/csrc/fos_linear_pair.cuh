@@ -25,8 +25,8 @@
 // 256 x 128 (30 KB a stage, two thirds of the MMAs' time) take 436 cycles a stage,
 // 180 us in all, and neither 6 instead of 3 scale buffers there nor 2 here (160 us)
 // change that much.  With bias, gelu_tanh and the pre-activation kept, 8192 x
-// 14336 x 4096: 306 .. 330 us in a burst, 355 after a second under load; 5003 x
-// 4096 x 14336 NVFP4 with bias, gelu and residual 107 .. 121 us.
+// 14336 x 4096: 311 .. 335 us in a burst, 345 .. 355 under load; 5003 x 4096 x 14336
+// NVFP4 with bias, gelu and residual 107 .. 110 us, 95.5 without an epilogue.
 // Tensor memory: two accumulators of 192 columns (the epilogue of a tile runs
 // under the MMAs of the next) and the scale buffers of 40 columns (a: 4 per
 // scale tile, b: the 6 that its 192 rows take) in the other 128.  Copying the

@@ -18,9 +18,9 @@
 //
 // Measured, against a device copy's 6.78 TB/s (bf16 unless named):
 //   forward   16384 x 7168 with residual, h, codes, scales: 127.5 us, 6.47 TB/s
-//             (95 %); 8192 x 4096 without residual and h: 19.4 us
-//   backward  8192 x 4096 with dh and dw: 44.9 us, 5.98 TB/s (88 %);
-//             1021 x 7168 fp32 without dh: 18.5 us, 4.77 TB/s (70 %; 6.7 rows a
+//             (95 %); 8192 x 4096 without residual and h: 19.0 us
+//   backward  8192 x 4096 with dh and dw: 45.0 us, 5.97 TB/s (88 %);
+//             1021 x 7168 fp32 without dh: 18.8 us, 4.69 TB/s (69 %; 6.7 rows a
 //             CTA, then 2.5 us for the sum of the weight gradient's partial rows)
 //   one row of 4096: 2.1 us, the chain of a launch, two reads of memory and a
 //             barrier
