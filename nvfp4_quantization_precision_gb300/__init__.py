@@ -643,8 +643,9 @@ def rms_norm_backward(dy, h, rstd, weight, dh=None, weight_grad=True, dx=None, d
     """fos_rms_norm_backward: (dx, dweight) from the gradient dy of the norm's
     output, the h and rstd the forward call returned, and optionally the
     gradient dh that reaches h from elsewhere.  dx is the gradient of x and of
-    the residual, and may be passed as dy, h or dh; dweight is fp32 (None without weight_grad).  workspace: at
-    least fos_rms_norm_backward_workspace_bytes of uint8; when None, one that the
+    the residual, and may be passed as dy, h or dh; dweight is fp32 (None
+    without weight_grad).  workspace: at least
+    fos_rms_norm_backward_workspace_bytes of uint8; when None, one that the
     binding keeps for this thread and stream (up to 16 MB, else allocated; see
     release_workspaces)."""
     shape, dt, dev = _data(dy, "dy")

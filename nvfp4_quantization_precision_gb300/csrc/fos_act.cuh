@@ -52,8 +52,8 @@ constexpr float k2Sqrt2OverPi = 1.5957691216057308f;  // 2 sqrt(2 / pi)
 // polynomial in 1 / (1 + c |x|) is off by 4e-8 root mean square over 0 .. 1, this by 1.2e-8).
 // Two of them, their errors evaluated in fp32:
 //   degree 6, c = 0.38, fitted within 8e-9 in all and of the tail itself, as it is
-//     evaluated, 1.3e-6 to 3, 6e-5 to 6, 3e-4 to 9, 3e-3 to 14.  For 16-bit data, whose rounding (2^-11 down to 1e-8, that is x =
-//     6; 2^-8) lies above.
+//     evaluated, 1.3e-6 to 3, 6e-5 to 6, 3e-4 to 9, 3e-3 to 14.  For 16-bit data,
+//     whose rounding (2^-11 down to 1e-8, that is x = 6; 2^-8) lies above.
 //   degree 9, c = 0.45, for 32-bit data: 1.8e-6 of the tail itself to 14.4, where the
 //     product leaves fp32's range.
 // Either way the exponential adds its own error, 4 * 2^-24, and its argument's, 1.25 x^2

@@ -347,7 +347,8 @@ __global__ void __launch_bounds__(pair_threads<F>(), 1) k_linear_pair(const __gr
                 const uint32_t acc = tmem + (uint32_t)(ab * kPairN);
                 for (int i = 0; i < a.nkb; ++i) {
                     const int s = r.slot, in_chunk = i % chunk_stages<F>();
-                    if ((!chunk_is_stage<F>() && in_chunk == 0 && !warp_wait<Sync::TENSOR>(&sh.sf_ready[f.slot], f.parity)) ||
+                    if ((!chunk_is_stage<F>() && in_chunk == 0 &&
+                         !warp_wait<Sync::TENSOR>(&sh.sf_ready[f.slot], f.parity)) ||
                         (!warp_agrees(here) && !warp_wait<Sync::CLUSTER>(&sh.full[s], r.parity))) {
                         bad = true;
                         break;
