@@ -190,6 +190,9 @@ __device__ __forceinline__ uint64_t act_slope2(uint64_t p) {
         return pk(a > 0.0f ? 1.0f : 0.0f, b > 0.0f ? 1.0f : 0.0f);
     }
     if constexpr (A == Act::SILU) {
+        // (1 - s as E s, like below, halves the error from p = 3 on, but the roundings of s no
+        // longer cancel below: of 123 M codes of fp16 gradients 194 instead of 153 differ
+        // from the exact ones, and 8192 x 14336 takes 123.7 instead of 121.8 us)
         const uint64_t s = rcp_2(add2(ex2_2(mul2(p, pk1(kNegLog2e))), pk1(1.0f)));
         return mul2(s, fma2(p, sub2(pk1(1.0f), s), pk1(1.0f)));
     }
