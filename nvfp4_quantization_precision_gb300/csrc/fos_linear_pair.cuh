@@ -453,8 +453,6 @@ __global__ void __launch_bounds__(pair_threads<F>(), 1) k_linear_pair(const __gr
                     vb[6 * kk + 4] = half ? v.z : v.x;
                     vb[6 * kk + 5] = half ? v.w : v.y;
                 }
-                __syncwarp();
-                if (lane == 0) bar_arrive(&sh.sf_empty[f.slot]);
                 if (chunks >= (uint32_t)kSfBufs) {
                     // the MMAs that read this buffer are done
                     if (chunk_is_stage<F>() ? !warp_wait<Sync::TENSOR>(&sh.empty[w.slot], w.parity)
@@ -472,7 +470,13 @@ __global__ void __launch_bounds__(pair_threads<F>(), 1) k_linear_pair(const __gr
                 asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) cluster_arrive(chunk_is_stage<F>() ? full0 + 8 * r.slot : ready0 + 8 * d.slot);
+                if (lane == 0) {
+                    cluster_arrive(chunk_is_stage<F>() ? full0 + 8 * r.slot : ready0 + 8 * d.slot);
+                    // The slot is free once its values are in tensor memory: freed before
+                    // the stores that use them, its last loads were found moved behind the
+                    // arrival and took the slot's next chunk.
+                    bar_arrive(&sh.sf_empty[f.slot]);
+                }
                 r.next(ns);
                 ++chunks;
                 f.next(kSfSlots);
