@@ -525,6 +525,108 @@ FOS_API fos_status fos_linear4(const uint8_t* a_codes, const uint8_t* a_scales_t
                                int64_t N, int64_t K, const fos_config* cfg,
                                const fos_epilogue* epilogue, void* out, fos_stream_t stream);
 
+/*
+ * ------------------------------------------------------------------------
+ * The experts' part of a feed-forward block.  Rows (tokens) are packed by
+ * expert: offs (device int32 [G]) holds the cumulative ends, read as
+ * fos_quantize_grouped reads them: expert e has rows [end_{e-1}, end_e),
+ * end_e = clamp(offs[e], end_{e-1}, rows).  Any expert may be empty.  The ends
+ * are read on the device, so one captured graph serves every routing.  Rows at
+ * or past the last end are not read, and what an output holds for them is left
+ * as it was.  1 <= G <= FOS_LINEAR_MAX_GROUPS.  Conventions, formats and errors
+ * are those of the feed-forward operators above; sizes, and products of two of
+ * them, as there (rows x N, G x N x K and so on up to 2^40, G x N below 2^31).
+ */
+#define FOS_LINEAR_MAX_GROUPS 1024
+
+/*
+ * fos_linear8_grouped, fos_linear4_grouped -- fos_linear8 / fos_linear4 with the
+ * weights of each row's expert:
+ *   out[m] = act(a[m] . b[e]^T + bias[e]) + residual[m],  e the expert of row m.
+ *   a_codes [rows, K] ([rows, K/2]) with PLAIN scales [rows, K/32] ([rows, K/16]):
+ *     what fos_rms_norm, fos_quantize8, fos_act_backward with FOS_SCALES_PLAIN
+ *     (fos_quantize_grouped, fos_quantize) write for the packed rows;
+ *   b_codes [G, N, K] ([G, N, K/2]), b_scales_tiled: each expert's tiled scales,
+ *     one after the other (with N % 128 == 0 that is one quantize call's output for
+ *     the weights [G * N, K]);
+ *   a_amax [G] (FOS_SCALE_TENSOR: what fos_quantize_grouped returns) or [rows]
+ *     (FOS_SCALE_ROW); b_amax [G].
+ *   epilogue: bias [G, N]; residual, pre and out [rows, N].
+ * N % 16 == 0; K a multiple of 128 (64).  With the weights' column-wise form as b
+ * the 8-bit call is also the input gradient.  Waits are bounded as in fos_linear8.
+ */
+FOS_API fos_status fos_linear8_grouped(const uint8_t* a_codes, const uint8_t* a_scales,
+                                       const uint8_t* b_codes, const uint8_t* b_scales_tiled,
+                                       const int32_t* offs, int G, int64_t rows, int64_t N,
+                                       int64_t K, const fos_epilogue* epilogue, void* out,
+                                       fos_stream_t stream);
+FOS_API fos_status fos_linear4_grouped(const uint8_t* a_codes, const uint8_t* a_scales,
+                                       const float* a_amax, const uint8_t* b_codes,
+                                       const uint8_t* b_scales_tiled, const float* b_amax,
+                                       const int32_t* offs, int G, int64_t rows, int64_t N,
+                                       int64_t K, const fos_config* cfg,
+                                       const fos_epilogue* epilogue, void* out,
+                                       fos_stream_t stream);
+
+/*
+ * fos_quantize8_grouped, fos_act_backward_grouped -- fos_quantize8 / fos_act_backward
+ * of packed rows.  codes, scales (plain) and d are as there.  The column-wise form
+ * has P = fos_grouped_cols(rows, G) columns: expert e's rows are columns p_e ...,
+ * p_0 = 0, p_{e+1} = p_e + 128 ceil(n_e / 128), with zeros up to p_{e+1}, so that each
+ * expert's part is an operand by itself; codes_t [cols, P], scales_t the tiled scales
+ * of a [cols, P] tensor.  What they hold past the last expert's part is left as it
+ * was.  dbias [G, cols] fp32: the sum of each expert's rows (0 for an empty one); it
+ * needs fos_act_backward_grouped_workspace_bytes(rows, cols, G) bytes of workspace.
+ * fos_grouped_cols returns -1 for negative rows or a G out of range.
+ */
+FOS_API int64_t fos_grouped_cols(int64_t rows, int G);
+FOS_API fos_status fos_quantize8_grouped(const void* x, fos_dtype dt, int64_t rows, int64_t cols,
+                                         const int32_t* offs, int G, uint8_t* codes,
+                                         uint8_t* scales, uint8_t* codes_t, uint8_t* scales_t,
+                                         fos_stream_t stream);
+FOS_API size_t fos_act_backward_grouped_workspace_bytes(int64_t rows, int64_t cols, int G);
+FOS_API fos_status fos_act_backward_grouped(const void* dout, const void* pre, fos_dtype dt,
+                                            int64_t rows, int64_t cols, const int32_t* offs, int G,
+                                            int act, void* d, uint8_t* codes, uint8_t* scales,
+                                            uint8_t* codes_t, uint8_t* scales_t, float* dbias,
+                                            void* workspace, size_t workspace_bytes,
+                                            fos_stream_t stream);
+
+/*
+ * fos_linear8_grouped_wgrad -- the experts' weight gradients,
+ *   out[e] = d_t[:, e] . z_t[:, e]^T + residual[e]          [G, N, K]
+ * from the column-wise forms of the gradient behind the product (d_codes_t [N, P],
+ * d_scales_t tiled) and of its input (z_codes_t [K, P], z_scales_t tiled) for the same
+ * offs, P = fos_grouped_cols(rows, G).  An expert without rows gets its residual, or
+ * zeros.  out and residual (may be NULL; out may be in its place) are of out_dt, 16-byte
+ * aligned.  N % 16 == 0, K % 16 == 0, K > 0.
+ */
+FOS_API fos_status fos_linear8_grouped_wgrad(const uint8_t* d_codes_t, const uint8_t* d_scales_t,
+                                             const uint8_t* z_codes_t, const uint8_t* z_scales_t,
+                                             const int32_t* offs, int G, int64_t rows, int64_t N,
+                                             int64_t K, const void* residual, fos_dtype out_dt,
+                                             void* out, fos_stream_t stream);
+
+/*
+ * fos_matvec4 -- few rows of x, not quantized, with NVFP4 weights:
+ *   out[p] = act(x[p / (M / x_rows)] . b[e]^T + bias[e]) + residual[p],  e = ids[p]
+ * x [x_rows, K] of dt; ids (device int32 [M]) or NULL (e = 0, G = 1); x_rows divides M:
+ * the experts of one token stand next to one another, or every row has its own x.
+ * b_codes [G, N, K/2], b_scales_tiled (scale bytes 0x00 .. 0x7E, as the quantizer writes
+ * them) and b_amax [G] as in fos_linear4_grouped; cfg->granularity is not read.  epilogue
+ * bias [G, N]; residual and out [M, N] (out may be in the residual's place); pre must be
+ * NULL.  A row whose id is outside 0 .. G - 1 is left as it was.  Weights are decoded
+ * exactly and products summed in fp32; an expert's weights are read once for up to eight
+ * rows (two of fp32 x).  M <= FOS_MATVEC_MAX_ROWS; N % 16 == 0; K % 32 == 0, K > 0.
+ * x, codes, scales and the epilogue's tensors 16-byte aligned.
+ */
+#define FOS_MATVEC_MAX_ROWS 1024
+FOS_API fos_status fos_matvec4(const void* x, fos_dtype dt, int64_t x_rows, const int32_t* ids,
+                               const uint8_t* b_codes, const uint8_t* b_scales_tiled,
+                               const float* b_amax, int64_t M, int64_t N, int64_t K, int G,
+                               const fos_config* cfg, const fos_epilogue* epilogue, void* out,
+                               fos_stream_t stream);
+
 /* Static, human-readable name of a status code. */
 FOS_API const char* fos_status_string(fos_status s);
 

@@ -25,6 +25,12 @@ Entry points (names follow the C ABI):
   linear8(a_codes, a_scales, b_codes, b_scales, ...) -> act(a . b^T + bias) + residual
   linear4(a_codes, a_scales, a_amax, b_codes, b_scales, b_amax, ...) -> the same, NVFP4
   act_backward(dout, pre, act, ...)         -> (codes, scales, codes_t, scales_t, d, dbias)
+  linear8_grouped(a_codes, a_scales, b_codes, b_scales, offs, ...) -> linear8 of rows packed by expert
+  linear4_grouped(a_codes, a_scales, a_amax, b_codes, b_scales, b_amax, offs, ...) -> the same, NVFP4
+  quantize8_grouped(x, offs, ...)           -> (codes, scales, codes_t, scales_t), columns by expert
+  act_backward_grouped(dout, pre, act, offs, ...) -> act_backward likewise, dbias [G, cols]
+  linear8_grouped_wgrad(d_codes_t, d_scales_t, z_codes_t, z_scales_t, offs, rows) -> [G, N, K]
+  matvec4(x, b_codes, b_scales, b_amax, ids, ...) -> few unquantized rows times NVFP4 weights
   release_workspaces()                      -> what the backward calls keep for this thread
 """
 import ctypes
@@ -42,6 +48,8 @@ LIB_PATH = os.path.join(_HERE, "libfos.so")
 FOS_BF16, FOS_FP16, FOS_FP32 = 0, 1, 2
 QDQ_MAX_LIST = 64
 GROUPED_MAX_GROUPS = 8192
+LINEAR_MAX_GROUPS = 1024
+MATVEC_MAX_ROWS = 1024
 
 _DT = {torch.bfloat16: FOS_BF16, torch.float16: FOS_FP16, torch.float32: FOS_FP32}
 _NAMES = ("fos_amax", "fos_quantize", "fos_quantize_list", "fos_quantize_overlap",
@@ -136,6 +144,20 @@ def lib():
         for n in ("fos_rms_norm_backward_workspace_bytes", "fos_act_backward_workspace_bytes"):
             getattr(L, n).argtypes = [I64, I64]
             getattr(L, n).restype = ctypes.c_size_t
+        L.fos_linear8_grouped.argtypes = [P, P, P, P, P, I, I64, I64, I64, EP, P, P]
+        L.fos_linear4_grouped.argtypes = [P, P, P, P, P, P, P, I, I64, I64, I64, CFG, EP, P, P]
+        L.fos_quantize8_grouped.argtypes = [P, I, I64, I64, P, I, P, P, P, P, P]
+        L.fos_act_backward_grouped.argtypes = [P, P, I, I64, I64, P, I, I, P, P, P, P, P, P, P,
+                                               ctypes.c_size_t, P]
+        L.fos_linear8_grouped_wgrad.argtypes = [P, P, P, P, P, I, I64, I64, I64, P, I, P, P]
+        L.fos_matvec4.argtypes = [P, I, I64, P, P, P, P, I64, I64, I64, I, CFG, EP, P, P]
+        for n in ("fos_linear8_grouped", "fos_linear4_grouped", "fos_quantize8_grouped",
+                  "fos_act_backward_grouped", "fos_linear8_grouped_wgrad", "fos_matvec4"):
+            getattr(L, n).restype = ctypes.c_int
+        L.fos_grouped_cols.argtypes = [I64, I]
+        L.fos_grouped_cols.restype = ctypes.c_int64
+        L.fos_act_backward_grouped_workspace_bytes.argtypes = [I64, I64, I]
+        L.fos_act_backward_grouped_workspace_bytes.restype = ctypes.c_size_t
         L.fos_status_string.argtypes = [I]
         L.fos_status_string.restype = ctypes.c_char_p
         L.fos_version.restype = ctypes.c_int
@@ -815,6 +837,219 @@ def linear4(a_codes, a_scales, a_amax, b_codes, b_scales, b_amax, act="none", bi
                              ctypes.byref(cc), ctypes.byref(ep), out.data_ptr(),
                              _stream(a_codes)), "fos_linear4")
     return (out, pre) if save_pre else out
+
+
+# ------------------------------------------------------------------ by expert
+def _ends(offs, dev, name="offs"):
+    """Checks the experts' cumulative ends (or the rows' experts); returns their number."""
+    if not isinstance(offs, torch.Tensor) or offs.dtype is not torch.int32 or offs.dim() != 1 or \
+            offs.get_device() != dev or not offs.is_contiguous():
+        raise ValueError("%s must be a contiguous int32 vector on cuda:%d" % (name, dev))
+    return offs.shape[0]
+
+
+def _experts(codes, scales, name, G, blk, dev):
+    """Checks the experts' weights: codes [G, N, bytes] and each one's flat tiled
+    scales one after the other; returns (N, K)."""
+    if not isinstance(codes, torch.Tensor) or codes.dtype is not torch.uint8 or codes.dim() != 3 or \
+            codes.shape[0] != G or codes.get_device() != dev or not codes.is_contiguous():
+        raise ValueError("%s_codes must be a contiguous uint8 tensor [%d, N, bytes] on cuda:%d"
+                         % (name, G, dev))
+    N, K = codes.shape[1], codes.shape[2] * (32 // blk)
+    if scales.dtype is not torch.uint8 or scales.get_device() != dev or not scales.is_contiguous() or \
+            scales.numel() != G * ((N + 127) // 128) * ((K + 4 * blk - 1) // (4 * blk)) * 512:
+        raise ValueError("%s_scales must be the tiled uint8 scales of every expert's %s_codes"
+                         % (name, name))
+    return N, K
+
+
+def _packed(codes, scales, blk):
+    """Checks packed rows' codes [rows, bytes] and plain scales; returns (rows, K, device)."""
+    if not isinstance(codes, torch.Tensor) or not codes.is_cuda or not codes.is_contiguous():
+        _cuda(codes, "a_codes")
+    dev = codes.get_device()
+    if codes.dim() != 2 or codes.dtype is not torch.uint8:
+        raise ValueError("a_codes must be a rank-2 uint8 tensor")
+    R, K = codes.shape[0], codes.shape[1] * (32 // blk)
+    _like(scales, "a_scales", (R, K // blk), torch.uint8, dev)
+    return R, K, dev
+
+
+def _grouped_epilogue(G, M, N, act, bias, residual, out_dtype, save_pre, out, pre, dev):
+    """_epilogue() with a bias row an expert."""
+    if bias is not None:
+        if bias.dtype not in (torch.float32, out_dtype):
+            raise ValueError("bias must be float32 or of the output's type")
+        _like(bias, "bias", (G, N), bias.dtype, dev)
+    ep, out, pre = _epilogue(M, N, act, None, residual, out_dtype, save_pre, out, pre, dev)
+    if bias is not None:
+        ep.bias_dt, ep.bias = _DT[bias.dtype], bias.data_ptr()
+    return ep, out, pre
+
+
+def linear8_grouped(a_codes, a_scales, b_codes, b_scales, offs, act="none", bias=None, residual=None,
+                    out_dtype=torch.bfloat16, save_pre=False, out=None, pre=None):
+    """fos_linear8_grouped: act(a . b[e]^T + bias[e]) + residual, e the expert of
+    each row of a.  a: packed rows' codes [M, K] and plain scales [M, K/32];
+    b: the experts' codes [G, N, K] and their tiled scales; offs: int32 [G],
+    cumulative ends.  bias [G, N], residual [M, N]; out may be the residual itself.
+    Rows past the last end keep what out (and pre) hold.  Returns out, or (out,
+    pre) with save_pre."""
+    M, K, dev = _packed(a_codes, a_scales, 32)
+    G = _ends(offs, dev)
+    N, Kb = _experts(b_codes, b_scales, "b", G, 32, dev)
+    if K != Kb:
+        raise ValueError("a and b must have the same K")
+    ep, out, pre = _grouped_epilogue(G, M, N, act, bias, residual, out_dtype, save_pre, out, pre, dev)
+    _check(lib().fos_linear8_grouped(a_codes.data_ptr(), a_scales.data_ptr(), b_codes.data_ptr(),
+                                     b_scales.data_ptr(), offs.data_ptr(), G, M, N, K,
+                                     ctypes.byref(ep), out.data_ptr(), _stream(a_codes)),
+           "fos_linear8_grouped")
+    return (out, pre) if save_pre else out
+
+
+def linear4_grouped(a_codes, a_scales, a_amax, b_codes, b_scales, b_amax, offs, act="none", bias=None,
+                    residual=None, out_dtype=torch.bfloat16, save_pre=False, cfg=Config(), out=None,
+                    pre=None):
+    """fos_linear4_grouped: linear8_grouped for NVFP4 operands: what
+    quantize_grouped returns for the packed rows (a_amax [G]; [M] with
+    cfg.row_scaled), the experts' codes [G, N, K/2], their tiled scales and
+    b_amax [G]."""
+    M, K, dev = _packed(a_codes, a_scales, 16)
+    G = _ends(offs, dev)
+    N, Kb = _experts(b_codes, b_scales, "b", G, 16, dev)
+    if K != Kb:
+        raise ValueError("a and b must have the same K")
+    _like(a_amax, "a_amax", (M if cfg.row_scaled else G,), torch.float32, dev)
+    _like(b_amax, "b_amax", (G,), torch.float32, dev)
+    ep, out, pre = _grouped_epilogue(G, M, N, act, bias, residual, out_dtype, save_pre, out, pre, dev)
+    cc = cfg.c(True)
+    _check(lib().fos_linear4_grouped(a_codes.data_ptr(), a_scales.data_ptr(), a_amax.data_ptr(),
+                                     b_codes.data_ptr(), b_scales.data_ptr(), b_amax.data_ptr(),
+                                     offs.data_ptr(), G, M, N, K, ctypes.byref(cc),
+                                     ctypes.byref(ep), out.data_ptr(), _stream(a_codes)),
+           "fos_linear4_grouped")
+    return (out, pre) if save_pre else out
+
+
+def grouped_cols(rows, groups):
+    """Columns of the column-wise form of `rows` packed rows: every expert's part
+    padded to a multiple of 128, for any routing."""
+    n = lib().fos_grouped_cols(int(rows), int(groups))
+    if n < 0:
+        raise ValueError("bad number of rows or experts")
+    return n
+
+
+def quantize8_grouped(x, offs, rowwise=True, colwise=True, codes=None, scales=None, codes_t=None,
+                      scales_t=None):
+    """fos_quantize8_grouped: packed rows x [rows, cols] in the 8-bit block format.
+    Returns (codes, scales, codes_t, scales_t): the rows with plain scales [rows,
+    cols/32] (None without rowwise) and, with grouped_cols(rows, G) columns, the
+    rows of x.T, each expert's part padded with zeros to a multiple of 128, with
+    tiled scales (None without colwise)."""
+    (R, C), dt, dev = _data(x, "x")
+    G = _ends(offs, dev)
+    codes, scales = _pair8(R, C, False, codes, scales, dev) if rowwise else (None, None)
+    codes_t, scales_t = _pair8(C, grouped_cols(R, G), True, codes_t, scales_t, dev,
+                               ("codes_t", "scales_t")) if colwise else (None, None)
+    _check(lib().fos_quantize8_grouped(x.data_ptr(), dt, R, C, offs.data_ptr(), G, _a(codes),
+                                       _a(scales), _a(codes_t), _a(scales_t), _stream(x)),
+           "fos_quantize8_grouped")
+    return codes, scales, codes_t, scales_t
+
+
+def act_backward_grouped(dout, pre, act, offs, rowwise=True, colwise=True, value=False,
+                         bias_grad=True, codes=None, scales=None, codes_t=None, scales_t=None,
+                         d=None, dbias=None, workspace=None):
+    """fos_act_backward_grouped: act_backward of packed rows, as (codes, scales,
+    codes_t, scales_t, d, dbias): the 8-bit forms as in quantize8_grouped, d with
+    value, and dbias [G, cols], the sum of each expert's rows.  d may be passed as
+    dout or as pre.  workspace: as in rms_norm_backward
+    (fos_act_backward_grouped_workspace_bytes)."""
+    shape, dt, dev = _data(dout, "dout")
+    R, C = shape
+    a = _act(act)
+    G = _ends(offs, dev)
+    if pre is not None:
+        _like(pre, "pre", shape, dout.dtype, dev)
+    P = grouped_cols(R, G)
+    codes, scales = _pair8(R, C, False, codes, scales, dev) if rowwise else (None, None)
+    codes_t, scales_t = _pair8(C, P, True, codes_t, scales_t, dev,
+                               ("codes_t", "scales_t")) if colwise else (None, None)
+    if value:
+        d = torch.empty_like(dout) if d is None else _like(d, "d", shape, dout.dtype, dev)
+    else:
+        d = None
+    nws = 0
+    if bias_grad:
+        if dbias is None:
+            dbias = _new((G, C), torch.float32, dev)
+        else:
+            _like(dbias, "dbias", (G, C), torch.float32, dev)
+        # fos_act_backward_grouped_workspace_bytes, without the call
+        workspace, nws = _workspace(workspace, 0 if R == 0 else 4 * (P // 128 * C + G + 1), dev)
+    else:
+        dbias = workspace = None
+    _check(lib().fos_act_backward_grouped(dout.data_ptr(), _a(pre), dt, R, C, offs.data_ptr(), G, a,
+                                          _a(d), _a(codes), _a(scales), _a(codes_t), _a(scales_t),
+                                          _a(dbias), _a(workspace), nws, _stream(dout)),
+           "fos_act_backward_grouped")
+    return codes, scales, codes_t, scales_t, d, dbias
+
+
+def linear8_grouped_wgrad(d_codes_t, d_scales_t, z_codes_t, z_scales_t, offs, rows, residual=None,
+                          out_dtype=torch.float32, out=None):
+    """fos_linear8_grouped_wgrad: the experts' weight gradients [G, N, K], d^T . z
+    over each expert's rows (+ residual), from the column-wise forms of d [rows, N]
+    and z [rows, K] that quantize8_grouped and act_backward_grouped return for the
+    same offs.  An expert without rows gets its residual, or zeros.  out may be the
+    residual itself."""
+    N, P, dev = _operand(d_codes_t, d_scales_t, "d", 32)
+    K, Pz, _ = _operand(z_codes_t, z_scales_t, "z", 32, dev)
+    G = _ends(offs, dev)
+    if P != Pz or P != grouped_cols(rows, G):
+        raise ValueError("d and z must have grouped_cols(rows, %d) columns" % G)
+    if out_dtype not in _DT:
+        raise ValueError("out_dtype must be bf16, fp16 or fp32")
+    if residual is not None:
+        _like(residual, "residual", (G, N, K), out_dtype, dev)
+    out = _new((G, N, K), out_dtype, dev) if out is None else _like(out, "out", (G, N, K), out_dtype, dev)
+    _check(lib().fos_linear8_grouped_wgrad(d_codes_t.data_ptr(), d_scales_t.data_ptr(),
+                                           z_codes_t.data_ptr(), z_scales_t.data_ptr(),
+                                           offs.data_ptr(), G, rows, N, K, _a(residual),
+                                           _DT[out_dtype], out.data_ptr(), _stream(d_codes_t)),
+           "fos_linear8_grouped_wgrad")
+    return out
+
+
+def matvec4(x, b_codes, b_scales, b_amax, ids=None, act="none", bias=None, residual=None,
+            out_dtype=None, cfg=Config(), out=None):
+    """fos_matvec4: act(x . b[e]^T + bias[e]) + residual for few rows x [X, K] that
+    stay in bf16, fp16 or fp32, with NVFP4 weights.  Without ids b is one matrix
+    (codes [N, K/2], tiled scales, amax [1], bias [N]); with ids (int32 [M], M a
+    multiple of X) row p takes x[p // (M / X)] and expert ids[p] of codes [G, N,
+    K/2], their tiled scales, amax [G], bias [G, N]; a row with an id outside 0 ..
+    G - 1 keeps what out holds.  out and residual [M, N] are of out_dtype (x's own
+    by default); out may be the residual itself."""
+    (X, K), dt, dev = _data(x, "x")
+    out_dtype = x.dtype if out_dtype is None else out_dtype
+    if ids is None:
+        M, G = X, 1
+        N, Kb, _ = _operand(b_codes, b_scales, "b", 16, dev)
+        ep, out, _ = _epilogue(M, N, act, bias, residual, out_dtype, False, out, None, dev)
+    else:
+        M, G = _ends(ids, dev, "ids"), b_codes.shape[0]
+        N, Kb = _experts(b_codes, b_scales, "b", G, 16, dev)
+        ep, out, _ = _grouped_epilogue(G, M, N, act, bias, residual, out_dtype, False, out, None, dev)
+    if K != Kb:
+        raise ValueError("x and b must have the same K")
+    _like(b_amax, "b_amax", (G,), torch.float32, dev)
+    cc = cfg.c(True)
+    _check(lib().fos_matvec4(x.data_ptr(), dt, X, _a(ids), b_codes.data_ptr(), b_scales.data_ptr(),
+                             b_amax.data_ptr(), M, N, K, G, ctypes.byref(cc), ctypes.byref(ep),
+                             out.data_ptr(), _stream(x)), "fos_matvec4")
+    return out
 
 
 DIAG_E2M1_ENCODE, DIAG_E2M1_DECODE, DIAG_E4M3_ENCODE, DIAG_E4M3_DECODE = 0, 1, 2, 3

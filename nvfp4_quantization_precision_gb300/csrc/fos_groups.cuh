@@ -1,0 +1,87 @@
+// fos_groups.cuh -- rows packed by group (expert), read from cumulative ends on
+// the device: group g has rows [end_{g-1}, end_g), end_g = clamp(offs[g],
+// end_{g-1}, rows), and its rows are cut into tiles of 2^kShift rows that belong
+// to it alone (its last one may be short).
+//
+// The host does not know the ends, so each CTA forms the table of groups itself,
+// one warp over at most 1024 ends: entry g holds group g's first row and the
+// number of its first tile, entry G the last end and the number of tiles.
+#pragma once
+
+#include "fos_block8.cuh"
+
+namespace fos {
+
+struct Group {
+    int32_t row, tile;
+};
+constexpr int kMaxGroups = 1024;  // FOS_LINEAR_MAX_GROUPS
+inline __host__ __device__ constexpr size_t group_table_bytes(int G) {
+    return ((size_t)(G + 1) * sizeof(Group) + 15) / 16 * 16;
+}
+// Tiles of 2^shift rows that G groups of together `rows` rows can have at most:
+// every group with rows adds up to 2^shift - 1 to be a whole number of tiles.
+inline __host__ __device__ constexpr int64_t group_tiles_max(int64_t rows, int64_t G, int shift) {
+    const int64_t most = G < rows ? G : rows;
+    return (rows + most * ((INT64_C(1) << shift) - 1)) >> shift;
+}
+
+__device__ __forceinline__ int32_t ld_s32(const int32_t* p) {
+    int32_t v;
+    asm volatile("ld.global.s32 %0, [%1];" : "=r"(v) : "l"(p));
+    return v;
+}
+
+// The table by one converged warp; lane l takes ceil(G / 32) neighbouring groups.
+template <int kShift>
+__device__ __forceinline__ void group_table(Group* t, const int32_t* offs, int G, int32_t rows,
+                                            int lane) {
+    const int per = (G + 31) >> 5, lo = min(G, lane * per), hi = min(G, lo + per);
+    int32_t most = 0;
+#pragma unroll 4
+    for (int i = lo; i < hi; ++i) {
+        most = max(most, ld_s32(offs + i));
+        t[i + 1].row = most;
+    }
+    int32_t before = most;  // largest end of the lanes up to this one
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int32_t o = __shfl_up_sync(0xFFFFFFFFu, before, d);
+        if (lane >= d) before = max(before, o);
+    }
+    before = __shfl_up_sync(0xFFFFFFFFu, before, 1);
+    if (lane == 0) before = 0;
+    int32_t row = min(rows, before), tiles = 0;
+    for (int i = lo; i < hi; ++i) {
+        const int32_t end = min(rows, max(before, t[i + 1].row));
+        tiles += (end - row + (1 << kShift) - 1) >> kShift;
+        t[i + 1] = Group{end, tiles};
+        row = end;
+    }
+    int32_t sum = tiles;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int32_t o = __shfl_up_sync(0xFFFFFFFFu, sum, d);
+        if (lane >= d) sum += o;
+    }
+    sum -= tiles;
+    for (int i = lo; i < hi; ++i) t[i + 1].tile += sum;
+    if (lane == 0) t[0] = Group{0, 0};
+    __syncwarp();
+}
+
+// The group of tile `tile` (below t[G].tile): `g`, where the caller's walk stands, or
+// the one after it, else by bisection (runs of empty groups).
+__device__ __forceinline__ int group_of(const Group* t, int G, int tile, int g) {
+    if (t[g + 1].tile > tile && t[g].tile <= tile) return g;
+    if (g + 2 <= G && t[g + 2].tile > tile && t[g + 1].tile <= tile) return g + 1;
+    int lo = 0, hi = G;  // t[lo].tile <= tile < t[hi].tile
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (t[mid].tile <= tile) lo = mid;
+        else hi = mid;
+    }
+    return lo;
+}
+
+}  // namespace fos

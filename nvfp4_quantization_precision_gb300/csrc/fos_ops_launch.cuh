@@ -11,7 +11,10 @@ namespace fos {
 struct NormArgs;
 struct NormBwdArgs;
 struct Quant8Args;
+struct GroupedQuant8Args;
 struct LinearCall;
+struct MatvecArgs;
+struct GroupedCall;
 enum class Act : int;
 
 // A launch that may be placed while the previous kernel of the stream drains
@@ -42,5 +45,8 @@ cudaError_t launch_rms_bwd(In, NormBwdArgs, float* dw, float* part, int64_t max_
                            cudaStream_t);
 cudaError_t launch_linear(const LinearCall&, cudaStream_t);
 cudaError_t launch_quant8(In, Act, const Quant8Args&, cudaStream_t);
+cudaError_t launch_quant8_grouped(In, Act, const GroupedQuant8Args&, float* sums, cudaStream_t);
+cudaError_t launch_matvec4(In, const MatvecArgs&, cudaStream_t);
+cudaError_t launch_grouped(const GroupedCall&, cudaStream_t);
 
 }  // namespace fos

@@ -30,6 +30,7 @@
 
 #include "fos_act.cuh"
 #include "fos_block8.cuh"
+#include "fos_groups.cuh"
 
 namespace fos {
 
@@ -46,7 +47,7 @@ struct Quant8Args {
     int64_t rows_pad;    // rows rounded up to a multiple of 32
     int64_t tiles_c;
     int64_t pc4, pc4_t;  // tiled scales: 4-block tiles per tile-row
-    int tiled;
+    int tiled, tiled_t;  // layout of scales, of scales_t
     int wave;            // CTAs the device holds at once
 };
 
@@ -63,15 +64,20 @@ __device__ __forceinline__ void prefetch_l2(const void* p) {
     asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
 }
 
-template <In IT, Act A>
-__global__ void __launch_bounds__(kQ8Threads, 3) k_quant8(const Quant8Args a) {
-    chain_wait();
-    chain_release();
-    extern __shared__ __align__(16) float s_tile[];
+// A tile and what its rows are, as both kernels name it.
+struct Q8Tile {
+    int64_t r0, row_end;     // first row; rows from row_end on count as zeros
+    int64_t c0;              // first column
+    int64_t t0, t_end;       // first column of codes_t, and where they end
+    int64_t part_row;        // row of `part`
+};
+
+template <In IT, Act A, class Ahead>
+__device__ __forceinline__ void quant8_tile(const Quant8Args& a, const Q8Tile& q, float* s_tile,
+                                            Ahead fetch_ahead) {
     constexpr int64_t kElt = (IT == In::F32) ? 4 : 2;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int64_t tr = blockIdx.x / a.tiles_c, tc = blockIdx.x - tr * a.tiles_c;
-    const int64_t r0 = tr * kQ8Tile, c0 = tc * kQ8Tile;
+    const int64_t r0 = q.r0, c0 = q.c0;
     const bool cols_wanted = a.codes_t || a.part;
     {
         const int seg = tid & 7, rl = tid >> 3;
@@ -81,7 +87,7 @@ __global__ void __launch_bounds__(kQ8Threads, 3) k_quant8(const Quant8Args a) {
         Raw<IT> x[kAhead], p[kAhead];
         auto load = [&](int i, Raw<IT>& xr, Raw<IT>& pr) {
             const int64_t row = r0 + rl + 32 * i;
-            if (col_in && row < a.rows) {
+            if (col_in && row < q.row_end) {
                 const int64_t at = (row * a.cols + c0 + seg * 16) * kElt;
                 load_seg<IT, L2::FIRST>(xr, static_cast<const char*>(a.x) + at);
                 if constexpr (A != Act::NONE)
@@ -97,7 +103,7 @@ __global__ void __launch_bounds__(kQ8Threads, 3) k_quant8(const Quant8Args a) {
         for (int i = 0; i < 4; ++i) {
             const int b = i % kAhead;
             const int64_t row = r0 + rl + 32 * i;
-            const bool in = col_in && row < a.rows;
+            const bool in = col_in && row < q.row_end;
             uint64_t d[8];
             widen<IT>(x[b], d);
             if constexpr (A != Act::NONE) {
@@ -134,33 +140,11 @@ __global__ void __launch_bounds__(kQ8Threads, 3) k_quant8(const Quant8Args a) {
             }
         }
     }
-    {
-        // the tile a wave from here on its way to L2, one row's half a thread:
-        // its CTA then loads it at L2's latency (14336 x 4096 bf16: 44.6 -> 41.0
-        // us, the silu gradient of 8192 x 14336: 133 -> 122 us)
-        const int64_t nt = (int64_t)blockIdx.x + a.wave, ntr = nt / a.tiles_c, ntc = nt - ntr * a.tiles_c;
-        const int64_t row = ntr * kQ8Tile + (tid >> 1);
-        const int64_t c = ntc * kQ8Tile + (tid & 1) * (kQ8Tile / 2);
-        if (row < a.rows && c < a.cols) {
-            const int64_t at = (row * a.cols + c) * kElt;
-#pragma unroll
-            for (int l = 0; l < kElt / 2; ++l) {
-                if (c + l * (128 / kElt) >= a.cols) break;
-                prefetch_l2(static_cast<const char*>(a.x) + at + 128 * l);
-                if constexpr (A != Act::NONE)
-                    prefetch_l2(static_cast<const char*>(a.pre) + at + 128 * l);
-            }
-        }
-    }
-    if (a.tiled) {
-        const uint32_t t = blockIdx.x * kQ8Threads + tid, n = gridDim.x * kQ8Threads;
-        if (a.codes) clear_tiled_pad(a.scales, a.rows, a.cols / 32, a.pc4, t, n);
-        if (a.codes_t) clear_tiled_pad(a.scales_t, a.cols, a.rows_pad / 32, a.pc4_t, t, n);
-    }
+    fetch_ahead();
     if (!cols_wanted) return;
     __syncthreads();
     const int rb = lane & 3;
-    const int64_t rblk = r0 + 32 * rb;
+    const int64_t rblk = q.t0 + 32 * rb;
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
         const int cl = half * 64 + warp * 8 + (lane >> 2);
@@ -170,7 +154,7 @@ __global__ void __launch_bounds__(kQ8Threads, 3) k_quant8(const Quant8Args a) {
 #pragma unroll
         for (int i = 0; i < 16; ++i)
             v[i >> 3][i & 7] = pk(col[(2 * i) * kQ8Tile], col[(2 * i + 1) * kQ8Tile]);
-        if (a.codes_t && c < a.cols && rblk < a.rows_pad) {
+        if (a.codes_t && c < a.cols && rblk < q.t_end) {
             const uint32_t sc = scale8_code(fmaxf(seg_amax(v[0]), seg_amax(v[1])));
             const float inv = scale8_inv(sc);
             uint32_t w[2][4];
@@ -179,7 +163,7 @@ __global__ void __launch_bounds__(kQ8Threads, 3) k_quant8(const Quant8Args a) {
             const uint32_t o[8] = {w[0][0], w[0][1], w[0][2], w[0][3],
                                    w[1][0], w[1][1], w[1][2], w[1][3]};
             st256(a.codes_t + c * a.rows_pad + rblk, o);
-            st8(a.scales_t + scale8_at(a.tiled, c, rblk >> 5, a.rows_pad / 32, a.pc4_t), sc);
+            st8(a.scales_t + scale8_at(a.tiled_t, c, rblk >> 5, a.rows_pad / 32, a.pc4_t), sc);
         }
         if (a.part) {
             uint64_t s2 = add2(v[0][0], v[1][0]);
@@ -190,8 +174,98 @@ __global__ void __launch_bounds__(kQ8Threads, 3) k_quant8(const Quant8Args a) {
             s = fadd(s, t);
             s = fadd(s, __shfl_xor_sync(0xFFFFFFFFu, s, 1));
             s = fadd(s, __shfl_xor_sync(0xFFFFFFFFu, s, 2));
-            if (rb == 0 && c < a.cols) a.part[tr * a.cols + c] = s;
+            if (rb == 0 && c < a.cols) a.part[q.part_row * a.cols + c] = s;
         }
+    }
+}
+
+// One row's half of a tile on its way to L2.
+template <In IT, Act A>
+__device__ __forceinline__ void prefetch_tile(const Quant8Args& a, int64_t r0, int64_t row_end,
+                                              int64_t c0) {
+    constexpr int64_t kElt = (IT == In::F32) ? 4 : 2;
+    const int tid = threadIdx.x;
+    const int64_t row = r0 + (tid >> 1), c = c0 + (tid & 1) * (kQ8Tile / 2);
+    if (row < row_end && c < a.cols) {
+        const int64_t at = (row * a.cols + c) * kElt;
+#pragma unroll
+        for (int l = 0; l < kElt / 2; ++l) {
+            if (c + l * (128 / kElt) >= a.cols) break;
+            prefetch_l2(static_cast<const char*>(a.x) + at + 128 * l);
+            if constexpr (A != Act::NONE)
+                prefetch_l2(static_cast<const char*>(a.pre) + at + 128 * l);
+        }
+    }
+}
+
+template <In IT, Act A>
+__global__ void __launch_bounds__(kQ8Threads, 3) k_quant8(const Quant8Args a) {
+    chain_wait();
+    chain_release();
+    extern __shared__ __align__(16) float s_tile[];
+    const int64_t tr = blockIdx.x / a.tiles_c, tc = blockIdx.x - tr * a.tiles_c;
+    const int64_t r0 = tr * kQ8Tile;
+    quant8_tile<IT, A>(a, Q8Tile{r0, a.rows, tc * kQ8Tile, r0, a.rows_pad, tr}, s_tile, [&] {
+        // the tile a wave from here on its way to L2, one row's half a thread:
+        // its CTA then loads it at L2's latency (14336 x 4096 bf16: 44.6 -> 41.0
+        // us, the silu gradient of 8192 x 14336: 133 -> 122 us)
+        const int64_t nt = (int64_t)blockIdx.x + a.wave, ntr = nt / a.tiles_c, ntc = nt - ntr * a.tiles_c;
+        prefetch_tile<IT, A>(a, ntr * kQ8Tile, a.rows, ntc * kQ8Tile);
+        if (a.tiled) {
+            const uint32_t t = blockIdx.x * kQ8Threads + threadIdx.x, n = gridDim.x * kQ8Threads;
+            if (a.codes) clear_tiled_pad(a.scales, a.rows, a.cols / 32, a.pc4, t, n);
+            if (a.codes_t) clear_tiled_pad(a.scales_t, a.cols, a.rows_pad / 32, a.pc4_t, t, n);
+        }
+    });
+}
+
+// The same for rows packed by group: a tile's rows are of one group, whose columns
+// of codes_t start at 128 times its first tile's number, so that a group's part of
+// the column-wise form is a whole number of 128 columns, zeros past its rows: an
+// operand of the group's own product.  Row-wise scales are plain, column-wise ones
+// tiled; part has a row a tile, and `bounds` [G + 1] gets the groups' first tiles.
+// Persistent, three CTAs an SM, so that each reads the ends and forms the table of
+// groups once.
+struct GroupedQuant8Args {
+    Quant8Args q;        // rows_pad: columns of codes_t; wave unused
+    const int32_t* offs;
+    int G;
+    int32_t* bounds;     // with part
+};
+
+template <In IT, Act A>
+__global__ void __launch_bounds__(kQ8Threads, 3) k_quant8_grouped(const __grid_constant__ GroupedQuant8Args b) {
+    chain_wait();
+    chain_release();
+    extern __shared__ __align__(16) float s_tile[];
+    Group* s_groups = reinterpret_cast<Group*>(s_tile + kQ8Tile * kQ8Tile);
+    const Quant8Args& a = b.q;
+    const int tid = threadIdx.x;
+    if (tid < 32) group_table<7>(s_groups, b.offs, b.G, (int32_t)a.rows, tid);
+    __syncthreads();
+    const int tiles_c = (int)a.tiles_c, total = s_groups[b.G].tile * tiles_c;
+    if (a.part && blockIdx.x == 0)
+        for (int g = tid; g <= b.G; g += kQ8Threads) b.bounds[g] = s_groups[g].tile;
+    if (a.codes_t)
+        clear_tiled_pad(a.scales_t, a.cols, a.rows_pad / 32, a.pc4_t,
+                        blockIdx.x * kQ8Threads + tid, gridDim.x * kQ8Threads);
+    int g = 0;
+    for (int t = blockIdx.x; t < total; t += gridDim.x) {
+        const int tr = t / tiles_c, tc = t - tr * tiles_c;
+        g = group_of(s_groups, b.G, tr, g);
+        const int64_t r0 = s_groups[g].row + (int64_t)(tr - s_groups[g].tile) * kQ8Tile;
+        const int64_t t0 = (int64_t)tr * kQ8Tile;
+        quant8_tile<IT, A>(a, Q8Tile{r0, s_groups[g + 1].row, (int64_t)tc * kQ8Tile, t0, t0 + kQ8Tile, tr},
+                           s_tile, [&] {
+            const int nt = t + (int)gridDim.x;
+            if (nt < total) {
+                const int ntr = nt / tiles_c;
+                const int ng = group_of(s_groups, b.G, ntr, g);
+                prefetch_tile<IT, A>(a, s_groups[ng].row + (int64_t)(ntr - s_groups[ng].tile) * kQ8Tile,
+                                     s_groups[ng + 1].row, (int64_t)(nt - ntr * tiles_c) * kQ8Tile);
+            }
+        });
+        __syncthreads();  // the tile has been read
     }
 }
 
