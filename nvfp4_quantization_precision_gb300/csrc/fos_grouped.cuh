@@ -1,31 +1,9 @@
 // fos_grouped.cuh -- products of rows packed by group (expert) with the groups'
-// own weights, and the weights' gradients, on pairs of SMs (tcgen05
-// cta_group::2, M = 256).
-//
-//   kW false  out[m] = act(a[m] . b[e]^T + bias[e]) + residual[m], e the group of
-//             row m: tiles of 256 rows of one group x 192 weight rows; the groups'
-//             rows are ragged, every tile's K is K.
-//   kW true   out[e] = a[:, e] . b[:, e]^T + residual[e], a and b column-wise 8-bit
-//             forms whose columns are the tokens, each group's part a whole number
-//             of 128: tiles of 256 x 192 of out[e], K the group's columns (none:
-//             the product is 0).
-//
-// The host knows neither the groups' sizes nor the number of tiles: every CTA reads
-// the ends (fos_groups.cuh) and walks tiles t, t + pairs, ... of the groups one
-// after the other, each role for itself.  Roles, rings, tensor memory and the
-// epilogue's chunks are those of k_linear_pair; what differs:
-//   rows of a   a tile's last rows may be another group's: boxes of 32 rows fetch
-//               what the group has (with one row an expert, 4 KB a stage instead
-//               of 16 per SM: the weights are then all that streams), and the rest of
-//               the stage keeps what it held.  Those rows of the accumulator are
-//               nobody's: a row of the product depends on its own row of a alone.
-//   scales of a are plain, [rows, K / 16 or K / 32] as the quantizers write packed rows:
-//               a tile starts at any row, and a 128-row tile of scales could not
-//               start there.  Warp 10 copies 16 bytes (four scale tiles along K) a
-//               row by cp.async, and the lanes that hold rows l, 32 + l, 64 + l, 96 +
-//               l read them as they are.
-//   rows of out a chunk of 32 rows that the group fills leaves by TMA; one that it
-//               ends in is copied row by row.
+// own weights, and the weights' gradients, on pairs of SMs (tcgen05 cta_group::2, M =
+// 256).  The host knows neither the groups' sizes nor the number of tiles: every CTA
+// reads the ends (fos_groups.cuh) and walks tiles t, t + pairs, ... of the groups one
+// after the other, each role for itself.  Roles, rings, tensor memory and the waits
+// are those of k_linear_pair.
 #pragma once
 
 #include "fos_groups.cuh"
@@ -39,7 +17,7 @@ struct GroupedCall {
     const int32_t* offs;
     int G;
     int64_t rows;                    // packed rows
-    int64_t M, N, K;                 // rows of a tile grid (weight gradient), columns of out, K
+    int64_t M, N, K;                 // rows of out[e] (weight gradient), columns of out, K
     Epilogue ep;
     In out;
     bool fmt4, wgrad;
@@ -47,81 +25,80 @@ struct GroupedCall {
 
 namespace lin {
 
+// The pair's halves of a stage: 128 rows of the first operand, up to 96 of the second.
+static_assert(kPairABytes == 128 * kRowBytes && kPairBBytes == 96 * kRowBytes, "stage");
+
+// ------------------------------------------------------------------ out = act(a . b[e]^T ...)
+// k_grouped: the weights are the MMA's 256 rows and a group's rows (tokens) its
+// columns, as in k_linear_rows, so that a tile that the group ends in costs what it has:
+// tiles of 256 weight rows x 192 tokens, the last one of a group as many as it
+// needs, rounded up to 32.  (With tokens as the 256 rows, groups of 255 rows on average
+// fill 60 % of their tiles: 16084 x 2048 x 7168 NVFP4 over 63 groups 182 us.)
+// CTA r of a pair holds weight rows 128 r .. + 127 of the tile and its half of the
+// tokens; each CTA's tensor memory has the products of its weight rows and all of
+// the tokens.  What differs from k_linear_pair besides:
+//   tokens     a tile starts at any row: a last tile's are fetched by boxes of 16 rows,
+//              which may hold another group's behind the end: their columns of the
+//              product are nobody's
+//   scales     of the weights are tiled, of the tokens plain, [rows, K / 16 or K / 32],
+//              as the quantizers write packed rows (a 128-row tile of scales could not
+//              start at any row): warp 10 copies 16 bytes (four scale tiles along K) a
+//              token by cp.async, and the lanes that hold tokens l, 32 + l, ... read them
+//              as they are
+//   epilogue   a lane has one weight row: its 32 neighbours' results of a token are 64
+//              or 128 contiguous bytes of out, stored (and the residual loaded) as
+//              they are, without a way through shared memory
+
+constexpr int kTokTile = 192;                    // tokens of a tile
+constexpr int kTokStep = 32;                     // an MMA's columns come in steps of these
+constexpr int kTokBox = 16;                      // tokens of a small box
+constexpr int kTokSfBytes = kTokTile * 16;       // a chunk of their scales
+constexpr int kGrpSfBytes = kSfChunkA + kTokSfBytes;
+
 struct GroupedArgs {
-    CUtensorMap ta;    // a codes, box 128 bytes x 128 rows
-    CUtensorMap ta32;  // the same, 32 rows (kW false)
-    CUtensorMap tb;    // b codes, box 128 bytes x 96 rows, the groups' weights below one another
-    CUtensorMap tsa;   // kW: a's tiled scales, box 1 x 4 x 512
-    CUtensorMap tsb;   // b's tiled scales, box 2 x 4 x 512
-    CUtensorMap tout;  // out, residual, pre: box 128 bytes x 32 rows
-    CUtensorMap tres;
-    CUtensorMap tpre;
+    CUtensorMap tw;    // weights' codes, box 128 bytes x 128 rows, the groups' below one another
+    CUtensorMap tt;    // tokens' codes, box 128 bytes x 96 rows
+    CUtensorMap tt16;  // the same, 16 rows
+    CUtensorMap tsw;   // weights' tiled scales, box 1 x 4 x 512
     Epilogue ep;
-    const uint8_t* sa;     // plain scales of a
-    int64_t sa_pitch;      // bytes of a row of them
-    int sa_wide;           // rows of them are whole 16-byte pieces
+    const uint8_t* ts;     // plain scales of the tokens
+    int64_t ts_pitch;      // bytes of a row of them
+    int ts_wide;           // rows of them are whole 16-byte pieces
     const int32_t* offs;
     int G;
     int rows;              // packed rows
-    int M;                 // kW: rows of out[e]
-    int N;                 // columns of out
-    int tiles_m;           // kW: row tiles of out[e]
+    int N;                 // weight rows of a group
     int tiles_n;
-    int band;
-    int kb, nkb;           // kW false: scale tiles and stages along K
-    int row_tiles_b;       // kW false: scale row tiles of one group's weights
-    int stages, bufs;
+    int band;              // token tiles of a band of the tile order
+    int kb, nkb;           // scale tiles and stages along K
+    int row_tiles;         // scale row tiles of a group's weights
+    int stages;
 };
 
 // One tile of the walk.
 struct GroupedTile {
     int g;
-    int32_t m0, m_end;   // rows of a (and of out, from out_row) and where they end
+    int32_t t0, live;  // first token, tokens of the group in it
+    int32_t cols;      // the same, rounded up to kTokStep
     int32_t n0;
-    int32_t k0, nkb;     // first stage of a's columns, stages
-    int32_t out_row;     // out's row of a's row 0
 };
 
-template <bool kW>
-__device__ __forceinline__ int grouped_tiles(const GroupedArgs& a, const Group* t) {
-    return (kW ? a.G * a.tiles_m : t[a.G].tile) * a.tiles_n;
-}
-// Within a group, bands of a.band tile rows, down the rows first (pair_tile()).
-template <bool kW>
+// Within a group, bands of a.band token tiles, down the tokens first (pair_tile()).
 __device__ __forceinline__ void grouped_tile(const GroupedArgs& a, const Group* t, int tile,
                                              GroupedTile& w) {
-    const int q = tile / a.tiles_n;
-    const int g = kW ? q / a.tiles_m : group_of(t, a.G, q, w.g);
-    const int base = kW ? g * a.tiles_m : t[g].tile;
-    const int all = kW ? a.tiles_m : t[g + 1].tile - base;
-    const int r0 = tile - base * a.tiles_n;
+    const int g = group_of(t, a.G, tile / a.tiles_n, w.g);
+    const int all = t[g + 1].tile - t[g].tile;
+    const int r0 = tile - t[g].tile * a.tiles_n;
     const int per_band = a.band * a.tiles_n;
     const int band = r0 / per_band, r = r0 - band * per_band;
     const int rows = min(a.band, all - band * a.band);
     const int col = r / rows;
-    const int m = (band * a.band + r - col * rows) * kPairM;
     w.g = g;
-    w.n0 = col * kPairN;
-    if constexpr (kW) {
-        w.m0 = m;
-        w.m_end = a.M;
-        w.k0 = t[g].tile;
-        w.nkb = t[g + 1].tile - w.k0;
-        w.out_row = g * a.M;
-    } else {
-        w.m0 = t[g].row + m;
-        w.m_end = t[g + 1].row;
-        w.k0 = 0;
-        w.nkb = a.nkb;
-        w.out_row = 0;
-    }
+    w.t0 = t[g].row + (band * a.band + r - col * rows) * kTokTile;
+    w.live = min(kTokTile, t[g + 1].row - w.t0);
+    w.cols = (w.live + kTokStep - 1) / kTokStep * kTokStep;
+    w.n0 = col * kPairM;
 }
-// Rows of the tile that CTA `rank` of the pair has.
-__device__ __forceinline__ int rank_rows(const GroupedTile& w, int rank) {
-    return max(0, min(128, w.m_end - w.m0 - 128 * rank));
-}
-// Boxes of 32 rows that fetch them (more than three: one box of 128).
-__device__ __forceinline__ int a_boxes(int rows) { return (rows + 31) >> 5; }
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
@@ -132,6 +109,460 @@ __device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
 // This thread's arrival at `bar` once its copies so far have landed.
 __device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
+// The MMAs of a stage (one lane) of a tile whose instruction descriptor is `id`: nk
+// scale tiles of it exist (F4).
+template <class F>
+__device__ __forceinline__ void grouped_stage(uint32_t acc, uint32_t a0, uint32_t b0, uint32_t id,
+                                              uint32_t sfa, uint32_t sfb, int nk, uint32_t more) {
+#pragma unroll
+    for (int kk = 0; kk < 4; ++kk) {
+        if (F::kGlobal && kk >= nk) break;
+        mma_issue<F, 2>(acc, a0 + 2 * kk, b0 + 2 * kk,
+                        F::kGlobal ? id : id | ((uint32_t)kk << 4) | ((uint32_t)kk << 29),
+                        F::kGlobal ? sfa + 4 * kk : sfa, F::kGlobal ? sfb + 6 * kk : sfb,
+                        kk == 0 ? more : 1u);
+    }
+}
+
+// One value of the output's type as it is stored: a load that the stores of the
+// same thread may not overtake (out may be in the residual's place).
+template <Out OT>
+__device__ __forceinline__ uint32_t ld_raw(const void* p, int64_t i) {
+    uint32_t v;
+    if constexpr (OT == Out::F32)
+        asm volatile("ld.global.b32 %0, [%1];" : "=r"(v) : "l"(static_cast<const float*>(p) + i) : "memory");
+    else
+        asm volatile("{\n\t.reg .b16 h;\n\tld.global.b16 h, [%1];\n\tcvt.u32.u16 %0, h;\n\t}"
+                     : "=r"(v) : "l"(static_cast<const unsigned short*>(p) + i) : "memory");
+    return v;
+}
+template <Out OT>
+__device__ __forceinline__ float raw_value(uint32_t v) {
+    if constexpr (OT == Out::F32) return __uint_as_float(v);
+    else if constexpr (OT == Out::BF16) return __uint_as_float(v << 16);
+    else {
+        float f;
+        asm("{\n\t.reg .b16 h;\n\tcvt.u16.u32 h, %1;\n\tcvt.f32.f16 %0, h;\n\t}" : "=f"(f) : "r"(v));
+        return f;
+    }
+}
+// 32 values of a lane's column n to rows 0 .. of `p` (at row 0, column n) below `rows`.
+template <Out OT>
+__device__ __forceinline__ void store_column(void* p, int64_t N, const float (&v)[32], int rows) {
+    if constexpr (OT == Out::F32) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+            if (i < rows) st32(static_cast<float*>(p) + i * N, __float_as_uint(v[i]));
+    } else {
+#pragma unroll
+        for (int i = 0; i < 32; i += 2) {
+            const uint32_t w = out_pair<OT>(pk(v[i], v[i + 1]));
+            if (i < rows) st16(static_cast<unsigned short*>(p) + i * N, w);
+            if (i + 1 < rows) st16(static_cast<unsigned short*>(p) + (i + 1) * N, w >> 16);
+        }
+    }
+}
+
+template <class F, Out OT>
+__global__ void __launch_bounds__(pair_threads<F>(), 1) k_grouped(const __grid_constant__ GroupedArgs a) {
+    extern __shared__ __align__(1024) unsigned char s_raw[];
+    __shared__ PairShared sh;
+    __shared__ __align__(16) float s_ga[F::kGlobal ? 4 : 1][kTokTile];  // the tokens' decode scales
+    unsigned char* base = s_raw + ((1024u - (smem_u32(s_raw) & 1023u)) & 1023u);
+    const int ns = a.stages;
+    constexpr int kSfSlots = sf_slots<F>();
+    unsigned char* sA = base;
+    unsigned char* sB = sA + ns * kPairABytes;
+    unsigned char* sS = sB + ns * kPairBBytes;  // scale chunks: the weights', then the tokens'
+    Group* groups = reinterpret_cast<Group*>(sS + kSfSlots * kGrpSfBytes);
+    const int warp = (int)uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
+    const int rank = (int)uniform(cluster_rank());
+    const int first = (int)(blockIdx.x >> 1), step = (int)(gridDim.x >> 1);
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < ns; ++s) {
+            bar_init(&sh.full[s], chunk_is_stage<F>() ? 9 : 1);
+            bar_init(&sh.empty[s], 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            bar_init(&sh.acc_full[b], 1);
+            bar_init(&sh.acc_empty[b], 8);
+        }
+        for (int b = 0; b < kSfSlots; ++b) {
+            bar_init(&sh.sf_full[b], 33);  // the TMA copy's, and each lane's of warp 10
+            bar_init(&sh.sf_empty[b], 4);
+        }
+        for (int b = 0; b < kSfBufs; ++b) {
+            bar_init(&sh.sf_ready[b], 8);
+            bar_init(&sh.sf_free[b], 1);
+        }
+        bar_init(&sh.done, 1);
+        sh.fail = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    chain_wait();
+    chain_release();
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                         smem_u32(&sh.tmem)), "r"(kAllColumns) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    } else if (warp == 2) {
+        group_table<kTokTile>(groups, a.offs, a.G, a.rows, lane);
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();  // both CTAs' barriers are set up
+    tc_fence_after();
+    const uint32_t tmem = uniform(sh.tmem);
+    const int tiles = groups[a.G].tile * a.tiles_n;
+    GroupedTile w;
+    w.g = 0;
+    bool bad = false;
+    if (warp == 0) {
+        const bool elected = elect_lane();
+        const uint32_t full0 = map_rank(smem_u32(&sh.full[0]), 0);
+        Ring r;
+        uint32_t g = 0;
+        for (int t = first; t < tiles && !bad; t += step) {
+            grouped_tile(a, groups, t, w);
+            const int half = w.cols >> 1;  // tokens of this CTA
+            const int32_t bt = w.t0 + half * rank, an = w.g * a.N + w.n0 + 128 * rank;
+            const uint32_t bytes = (uint32_t)(2 * (kPairABytes + half * kRowBytes));
+            for (int i = 0; i < a.nkb; ++i) {
+                const int s = r.slot;
+                if (g >= (uint32_t)ns && !warp_wait<Sync::CLUSTER>(&sh.empty[s], r.parity ^ 1u)) {
+                    bad = true;
+                    break;
+                }
+                const uint32_t bar = full0 + 8 * s;
+                unsigned char *pa = sA + s * kPairABytes, *pb = sB + s * kPairBBytes;
+                if (elected) {
+                    if (rank == 0) mbar_expect_tx(&sh.full[s], bytes);
+                    pair_load_2d(pa, &a.tw, i * kRowBytes, an, bar);
+                    if (half == kTokTile / 2) {
+                        pair_load_2d(pb, &a.tt, i * kRowBytes, bt, bar);
+                    } else {
+                        for (int j = 0; j < half; j += kTokBox)
+                            pair_load_2d(pb + j * kRowBytes, &a.tt16, i * kRowBytes, bt + j, bar);
+                    }
+                }
+                __syncwarp();
+                ++g;
+                r.next(ns);
+            }
+        }
+        // every copy issued has landed (and been read) before the CTA leaves:
+        // the stages' last uses, by the barriers this CTA has
+        for (int k = 0; k < ns && (uint32_t)k < g; ++k) {
+            int s = r.slot - 1 - k;
+            uint32_t p = r.parity;
+            if (s < 0) {
+                s += ns;
+                p ^= 1u;
+            }
+            if (!warp_wait<Sync::CLUSTER>(&sh.empty[s], p)) bad = true;
+        }
+    } else if (warp == 1) {
+        if (rank == 0) {
+            const bool elected = elect_lane();
+            Ring r, f;          // stages; scale buffers
+            bool here = false;  // the next stage is known to be full
+            int j = 0;
+            for (int t = first; t < tiles && !bad; t += step, ++j) {
+                grouped_tile(a, groups, t, w);
+                const uint32_t id = idesc<F>(kPairM, (int)uniform(w.cols), 0);
+                const int ab = j & 1;
+                if (j >= 2 && !warp_wait<Sync::TENSOR>(&sh.acc_empty[ab], (uint32_t)((j >> 1) - 1) & 1)) {
+                    bad = true;
+                    break;
+                }
+                const uint32_t acc = tmem + (uint32_t)(ab * kTokTile);
+                for (int i = 0; i < a.nkb; ++i) {
+                    const int s = r.slot, in_chunk = i % chunk_stages<F>();
+                    if ((!chunk_is_stage<F>() && in_chunk == 0 &&
+                         !warp_wait<Sync::TENSOR>(&sh.sf_ready[f.slot], f.parity)) ||
+                        (!warp_agrees(here) && !warp_wait<Sync::CLUSTER>(&sh.full[s], r.parity))) {
+                        bad = true;
+                        break;
+                    }
+                    r.next(ns);
+                    tc_fence_after();
+                    const int nk = min(F::kSfTiles, a.kb - F::kSfTiles * i);
+                    const uint32_t a0 = desc_lo(smem_u32(sA) + s * kPairABytes);
+                    const uint32_t b0 = desc_lo(smem_u32(sB) + s * kPairBBytes);
+                    const uint32_t sf = tmem + kPairSfCol + f.slot * kSfCols;
+                    const bool last = in_chunk == chunk_stages<F>() - 1 || i + 1 == a.nkb;
+                    if (elected) {
+                        grouped_stage<F>(acc, a0, b0, id, sf + 4 * in_chunk, sf + 16 + 6 * in_chunk, nk, i > 0);
+                        pair_commit(&sh.empty[s]);
+                        if (!chunk_is_stage<F>() && last) pair_commit(&sh.sf_free[f.slot]);
+                    }
+                    here = mbar_ask<Sync::CLUSTER>(&sh.full[r.slot], r.parity);
+                    __syncwarp();
+                    if (last) f.next(kSfBufs);
+                }
+                if (!bad && elected) pair_commit(&sh.acc_full[ab]);
+                __syncwarp();
+            }
+            if (elected) pair_commit(&sh.done);
+            __syncwarp();
+        }
+    } else if (warp == 10) {
+        const bool elected = elect_lane();
+        Ring f;
+        uint32_t chunks = 0;
+        for (int t = first; t < tiles && !bad; t += step) {
+            grouped_tile(a, groups, t, w);
+            const int32_t ra = w.g * a.row_tiles + (w.n0 >> 7) + rank;
+            const uint8_t* src = a.ts + w.t0 * a.ts_pitch;
+            for (int k = 0; k < a.kb; k += kSfChunkTiles) {
+                if (chunks >= (uint32_t)kSfSlots && !warp_wait(&sh.sf_empty[f.slot], f.parity ^ 1u)) {
+                    bad = true;
+                    break;
+                }
+                unsigned char* ps = sS + f.slot * kGrpSfBytes;
+                uint64_t* bar = &sh.sf_full[f.slot];
+                if (elected) {
+                    mbar_expect_tx(bar, (uint32_t)kSfChunkA);
+                    sf_load_3d(ps, &a.tsw, k, ra, bar);
+                }
+                __syncwarp();
+                for (int r = lane; r < w.live; r += 32) {
+                    const uint8_t* p = src + r * a.ts_pitch + 4 * k;
+                    const uint32_t d = smem_u32(ps) + kSfChunkA + 16 * r;
+                    if (a.ts_wide) {
+                        cp_async16(d, p);
+                    } else {
+                        for (int j = 0; j < min(kSfChunkTiles, a.kb - k); ++j) cp_async4(d + 4 * j, p + 4 * j);
+                    }
+                }
+                cp_async_arrive(bar);
+                __syncwarp();
+                ++chunks;
+                f.next(kSfSlots);
+            }
+        }
+        // the chunks' last uses have landed and been read
+        for (int k = 0; k < kSfSlots && (uint32_t)k < chunks; ++k) {
+            int sl = f.slot - 1 - k;
+            uint32_t p = f.parity;
+            if (sl < 0) {
+                sl += kSfSlots;
+                p ^= 1u;
+            }
+            if (!warp_wait(&sh.sf_empty[sl], p)) bad = true;
+        }
+    } else if (warp < 6 || warp > 10) {
+        // scales: lane l of quadrant q writes the weights' (rows l, 32 + l, .. in the words
+        // of tile kk) to columns 4 kk ..., the tokens' (token 32 i + l, tiles in the words)
+        // to columns 16 + 6 kk ...
+        const int q = warp & 3;
+        const uint32_t lane_base = tmem + kPairSfCol + ((uint32_t)(32 * q) << 16);
+        const uint32_t full0 = map_rank(smem_u32(&sh.full[0]), 0);
+        const uint32_t ready0 = map_rank(smem_u32(&sh.sf_ready[0]), 0);
+        Ring f, d;          // shared-memory slots; tensor-memory buffers
+        Ring r, u;          // chunk_is_stage: its stage; the one whose buffer it takes over
+        const uint32_t mine = warp < 6 ? 0u : 1u;  // the group of scale warps
+        uint32_t chunks = 0;
+        for (int t = first; t < tiles && !bad; t += step) {
+            for (int i = 0; i < a.nkb; i += chunk_stages<F>()) {
+                if (chunks % sf_groups<F>() != mine) {
+                    if (chunks >= (uint32_t)kSfBufs) u.next(ns);
+                    ++chunks;
+                    r.next(ns);
+                    f.next(kSfSlots);
+                    d.next(kSfBufs);
+                    continue;
+                }
+                if (!warp_wait(&sh.sf_full[f.slot], f.parity)) {
+                    bad = true;
+                    break;
+                }
+                const unsigned char* ps = sS + f.slot * kGrpSfBytes + 16 * lane;
+                uint32_t va[16], vb[24];
+#pragma unroll
+                for (int kk = 0; kk < kSfChunkTiles; ++kk) {
+                    const uint4 x = *reinterpret_cast<const uint4*>(ps + kk * kSfTileBytes);
+                    va[4 * kk] = x.x; va[4 * kk + 1] = x.y; va[4 * kk + 2] = x.z; va[4 * kk + 3] = x.w;
+                }
+#pragma unroll
+                for (int j = 0; j < 6; ++j) {
+                    const uint4 x = *reinterpret_cast<const uint4*>(ps + kSfChunkA + j * 512);
+                    vb[j] = x.x; vb[6 + j] = x.y; vb[12 + j] = x.z; vb[18 + j] = x.w;
+                }
+                if (chunks >= (uint32_t)kSfBufs) {
+                    // the MMAs that read this buffer are done
+                    if (chunk_is_stage<F>() ? !warp_wait<Sync::TENSOR>(&sh.empty[u.slot], u.parity)
+                                            : !warp_wait<Sync::TENSOR>(&sh.sf_free[d.slot], d.parity ^ 1u)) {
+                        bad = true;
+                        break;
+                    }
+                    u.next(ns);
+                }
+                tc_fence_after();
+                const uint32_t col = lane_base + d.slot * kSfCols;
+                mma::tmem_st_x16(col, va);
+                mma::tmem_st_x16(col + 16, reinterpret_cast<uint32_t(&)[16]>(vb));
+                tmem_st_x8(col + 32, vb + 16);
+                asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    cluster_arrive(chunk_is_stage<F>() ? full0 + 8 * r.slot : ready0 + 8 * d.slot);
+                    // behind the stores that use its values (k_linear_pair)
+                    bar_arrive(&sh.sf_empty[f.slot]);
+                }
+                r.next(ns);
+                ++chunks;
+                f.next(kSfSlots);
+                d.next(kSfBufs);
+            }
+        }
+    } else {
+        const int q = warp & 3, e = warp - 6;
+        const bool pre = a.ep.pre != nullptr, res = a.ep.residual != nullptr;
+        int j = 0;
+        for (int t = first; t < tiles; t += step, ++j) {
+            grouped_tile(a, groups, t, w);
+            const int n = w.n0 + 128 * rank + 32 * q + lane;
+            const bool in = n < a.N;
+            // column n of the tile's rows; rows of this lane (none past the weights)
+            const int64_t at = (int64_t)w.t0 * a.N + n;
+            const int live = in ? w.live : 0;
+            float bias = 0.0f, gb = 1.0f, ga0 = 1.0f;
+            if (a.ep.bias && in) {
+                const int64_t i = (int64_t)w.g * a.N + n;
+                bias = a.ep.bias32 ? static_cast<const float*>(a.ep.bias)[i] : load_out<OT>(a.ep.bias, i);
+            }
+            uint32_t rs[32];
+            auto fetch = [&](int c0) {  // the residual of tokens c0 .. c0 + 31
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                    if (c0 + i < live) rs[i] = ld_raw<OT>(a.ep.residual, at + (int64_t)(c0 + i) * a.N);
+            };
+            if (res) fetch(0);
+            if constexpr (F::kGlobal) {
+                gb = fdiv(1.0f, global_scale(a.ep.b_amax[w.g], a.ep.six_bound));
+                if (a.ep.a_row) {
+                    for (int c = lane; c < w.live; c += 32)
+                        s_ga[e][c] = fdiv(1.0f, global_scale(a.ep.a_amax[w.t0 + c], a.ep.six_bound));
+                } else {
+                    ga0 = fdiv(1.0f, global_scale(a.ep.a_amax[w.g], a.ep.six_bound));
+                }
+            }
+            const int ab = j & 1;
+            if (!bad && !warp_wait<Sync::TENSOR>(&sh.acc_full[ab], (uint32_t)(j >> 1) & 1)) bad = true;
+            __syncwarp();
+            tc_fence_after();
+            for (int c0 = 0; c0 < w.cols; c0 += 32) {
+                uint32_t u[32];
+                tmem_ld32(tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(ab * kTokTile + c0), u);
+                if (c0 + 32 == w.cols) {  // this warp has read the accumulator
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) cluster_arrive(map_rank(smem_u32(&sh.acc_empty[ab]), 0));
+                }
+                float v[32];
+#pragma unroll
+                for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(u[i]);
+                if constexpr (F::kGlobal) {
+                    if (a.ep.a_row) {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const float4 ga = *reinterpret_cast<const float4*>(&s_ga[e][c0 + 4 * i]);
+                            v[4 * i] = fmul(fmul(v[4 * i], ga.x), gb);
+                            v[4 * i + 1] = fmul(fmul(v[4 * i + 1], ga.y), gb);
+                            v[4 * i + 2] = fmul(fmul(v[4 * i + 2], ga.z), gb);
+                            v[4 * i + 3] = fmul(fmul(v[4 * i + 3], ga.w), gb);
+                        }
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) v[i] = fmul(fmul(v[i], ga0), gb);
+                    }
+                }
+                if (a.ep.bias) {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) v[i] = fadd(v[i], bias);
+                }
+                constexpr int kElt = OT == Out::F32 ? 4 : 2;
+                const int64_t to = (at + (int64_t)c0 * a.N) * kElt;
+                if (pre) store_column<OT>(static_cast<char*>(a.ep.pre) + to, a.N, v, live - c0);
+                act_apply<OT>(a.ep.act, v);
+                if (res) {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) v[i] = fadd(v[i], raw_value<OT>(rs[i]));
+                    fetch(c0 + 32);
+                }
+                store_column<OT>(static_cast<char*>(a.ep.out) + to, a.N, v, live - c0);
+            }
+            __syncwarp();  // the decode scales are read before the next tile's replace them
+        }
+    }
+    // every MMA issued has completed before the tensor memory is freed
+    if (warp == 1 && !warp_wait<Sync::TENSOR>(&sh.done, 0)) bad = true;
+    if (bad) sh.fail = 1;
+    tc_fence_before();
+    __syncwarp();
+    __syncthreads();
+    cluster_sync();  // neither CTA leaves while the other may touch its memory
+    if (sh.fail && threadIdx.x == 0 && first < tiles) {
+        grouped_tile(a, groups, first, w);
+        store_out<OT>(a.ep.out, (int64_t)w.t0 * a.N + w.n0, __int_as_float(0x7FC00000));
+    }
+    if (warp == 1) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem),
+                     "r"(kAllColumns) : "memory");
+    }
+}
+
+// ------------------------------------------------------------------ out[e] = a[:, e] . b[:, e]^T
+// k_grouped_wgrad: a and b are column-wise 8-bit forms whose columns are the tokens,
+// each group's part a whole number of 128 (a stage, a scale tile); tiles of 256 x 192 of
+// out[e] with as many stages as the group has columns / 128, none for an empty
+// group, whose product is 0.  The rest is k_linear_pair's, but for the last rows of
+// out[e], behind which the next group's lie: a chunk of 32 rows that ends there is
+// copied row by row.
+struct WgradArgs {
+    CUtensorMap ta;    // a codes, box 128 bytes x 128 rows
+    CUtensorMap tb;    // b codes, box 128 bytes x 96 rows
+    CUtensorMap tsa;   // tiled scales, box 1 x 4 x 512
+    CUtensorMap tsb;   // box 2 x 4 x 512
+    CUtensorMap tout;  // out, residual [G * M, N]: box 128 bytes x 32 rows
+    CUtensorMap tres;
+    Epilogue ep;       // residual, out
+    const int32_t* offs;
+    int G;
+    int rows;              // packed rows
+    int M, N;              // of out[e]
+    int tiles_m, tiles_n;
+    int band;
+    int stages;
+};
+
+struct WgradTile {
+    int g;
+    int32_t m0, m_end;   // rows of a, and of out from out_row; where they end
+    int32_t n0;
+    int32_t k0, nkb;     // first stage of the columns, stages
+    int32_t out_row;
+};
+
+__device__ __forceinline__ void wgrad_tile(const WgradArgs& a, const Group* t, int tile, WgradTile& w) {
+    const int per_group = a.tiles_m * a.tiles_n;
+    const int g = tile / per_group, r0 = tile - g * per_group;
+    const int per_band = a.band * a.tiles_n;
+    const int band = r0 / per_band, r = r0 - band * per_band;
+    const int rows = min(a.band, a.tiles_m - band * a.band);
+    const int col = r / rows;
+    w.g = g;
+    w.m0 = (band * a.band + r - col * rows) * kPairM;
+    w.m_end = a.M;
+    w.n0 = col * kPairN;
+    w.k0 = t[g].tile;
+    w.nkb = t[g + 1].tile - w.k0;
+    w.out_row = g * a.M;
 }
 
 // The first `rows` rows of a 32-row chunk to `dst` [.., N] at (row, col): eight
@@ -151,8 +582,9 @@ __device__ __forceinline__ void copy_rows(uint32_t buf, void* dst, int64_t row, 
     }
 }
 
-template <class F, Out OT, bool kW>
-__global__ void __launch_bounds__(pair_threads<F>(), 1) k_grouped(const __grid_constant__ GroupedArgs a) {
+template <Out OT>
+__global__ void __launch_bounds__(pair_threads<F8>(), 1) k_grouped_wgrad(const __grid_constant__ WgradArgs a) {
+    using F = F8;
     extern __shared__ __align__(1024) unsigned char s_raw[];
     __shared__ PairShared sh;
     unsigned char* base = s_raw + ((1024u - (smem_u32(s_raw) & 1023u)) & 1023u);
@@ -161,15 +593,14 @@ __global__ void __launch_bounds__(pair_threads<F>(), 1) k_grouped(const __grid_c
     unsigned char* sA = base;
     unsigned char* sB = sA + ns * kPairABytes;
     unsigned char* sC = sB + ns * kPairBBytes;          // epilogue chunks
-    unsigned char* sS = sC + 4 * a.bufs * kChunkBytes;  // scale chunks: a, then b's two row tiles
-    float* sBias = reinterpret_cast<float*>(sS + kSfSlots * kSfChunkBytes);
-    Group* groups = reinterpret_cast<Group*>(sBias + 4 * kPairN);
+    unsigned char* sS = sC + 8 * kChunkBytes;  // scale chunks: a, then b's two row tiles
+    Group* groups = reinterpret_cast<Group*>(sS + kSfSlots * kSfChunkBytes);
     const int warp = (int)uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
     const int rank = (int)uniform(cluster_rank());
     const int first = (int)(blockIdx.x >> 1), step = (int)(gridDim.x >> 1);
     if (threadIdx.x == 0) {
         for (int s = 0; s < ns; ++s) {
-            bar_init(&sh.full[s], chunk_is_stage<F>() ? 9 : 1);
+            bar_init(&sh.full[s], 1);
             bar_init(&sh.empty[s], 1);
         }
         for (int b = 0; b < 2; ++b) {
@@ -177,7 +608,7 @@ __global__ void __launch_bounds__(pair_threads<F>(), 1) k_grouped(const __grid_c
             bar_init(&sh.acc_empty[b], 8);
         }
         for (int b = 0; b < kSfSlots; ++b) {
-            bar_init(&sh.sf_full[b], kW ? 1 : 33);  // and each lane's copies of a's scales
+            bar_init(&sh.sf_full[b], 1);
             bar_init(&sh.sf_empty[b], 4);
         }
         for (int b = 0; b < kSfBufs; ++b) {
@@ -197,15 +628,15 @@ __global__ void __launch_bounds__(pair_threads<F>(), 1) k_grouped(const __grid_c
                          smem_u32(&sh.tmem)), "r"(kAllColumns) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
     } else if (warp == 2) {
-        group_table<kW ? 7 : 8>(groups, a.offs, a.G, a.rows, lane);
+        group_table<kRowBytes>(groups, a.offs, a.G, a.rows, lane);
     }
     tc_fence_before();
     __syncthreads();
     cluster_sync();  // both CTAs' barriers are set up
     tc_fence_after();
     const uint32_t tmem = uniform(sh.tmem);
-    const int tiles = grouped_tiles<kW>(a, groups);
-    GroupedTile w;
+    const int tiles = a.G * a.tiles_m * a.tiles_n;
+    WgradTile w;
     w.g = 0;
     bool bad = false;
     if (warp == 0) {
@@ -214,13 +645,9 @@ __global__ void __launch_bounds__(pair_threads<F>(), 1) k_grouped(const __grid_c
         Ring r;
         uint32_t g = 0;
         for (int t = first; t < tiles && !bad; t += step) {
-            grouped_tile<kW>(a, groups, t, w);
+            wgrad_tile(a, groups, t, w);
             const int32_t am = w.m0 + 128 * rank;
-            const int32_t bn = (kW ? 0 : w.g * a.N) + w.n0 + 96 * rank;
-            // the pair's rows, in boxes; past the last row a weight gradient's boxes read zeros
-            const int mine = kW ? 4 : a_boxes(rank_rows(w, rank));
-            const int both = kW ? 8 : a_boxes(rank_rows(w, 0)) + a_boxes(rank_rows(w, 1));
-            const uint32_t bytes = (uint32_t)(2 * kPairBBytes + both * (kPairABytes / 4));
+            const int32_t bn = w.n0 + 96 * rank;
             for (int i = 0; i < w.nkb; ++i) {
                 const int s = r.slot;
                 if (g >= (uint32_t)ns && !warp_wait<Sync::CLUSTER>(&sh.empty[s], r.parity ^ 1u)) {
@@ -231,13 +658,8 @@ __global__ void __launch_bounds__(pair_threads<F>(), 1) k_grouped(const __grid_c
                 const int32_t x = (w.k0 + i) * kRowBytes;
                 unsigned char *pa = sA + s * kPairABytes, *pb = sB + s * kPairBBytes;
                 if (elected) {
-                    if (rank == 0) mbar_expect_tx(&sh.full[s], bytes);
-                    if (mine == 4) {
-                        pair_load_2d(pa, &a.ta, x, am, bar);
-                    } else {
-                        for (int j = 0; j < mine; ++j)
-                            pair_load_2d(pa + j * (kPairABytes / 4), &a.ta32, x, am + 32 * j, bar);
-                    }
+                    if (rank == 0) mbar_expect_tx(&sh.full[s], (uint32_t)(2 * kPairStageBytes));
+                    pair_load_2d(pa, &a.ta, x, am, bar);
                     pair_load_2d(pb, &a.tb, x, bn, bar);
                 }
                 __syncwarp();
@@ -263,8 +685,8 @@ __global__ void __launch_bounds__(pair_threads<F>(), 1) k_grouped(const __grid_c
             bool here = false;  // the next stage is known to be full
             int j = 0;          // accumulators used
             for (int t = first; t < tiles && !bad; t += step) {
-                grouped_tile<kW>(a, groups, t, w);
-                if (kW && w.nkb == 0) continue;  // no accumulator: the epilogue takes zeros
+                wgrad_tile(a, groups, t, w);
+                if (w.nkb == 0) continue;  // no accumulator: the epilogue takes zeros
                 const int ab = j & 1;
                 if (j >= 2 && !warp_wait<Sync::TENSOR>(&sh.acc_empty[ab], (uint32_t)((j >> 1) - 1) & 1)) {
                     bad = true;
@@ -272,26 +694,23 @@ __global__ void __launch_bounds__(pair_threads<F>(), 1) k_grouped(const __grid_c
                 }
                 ++j;
                 const uint32_t acc = tmem + (uint32_t)(ab * kPairN);
-                const int kb = kW ? w.nkb : a.kb;
                 for (int i = 0; i < w.nkb; ++i) {
                     const int s = r.slot, in_chunk = i % chunk_stages<F>();
-                    if ((!chunk_is_stage<F>() && in_chunk == 0 &&
-                         !warp_wait<Sync::TENSOR>(&sh.sf_ready[f.slot], f.parity)) ||
+                    if ((in_chunk == 0 && !warp_wait<Sync::TENSOR>(&sh.sf_ready[f.slot], f.parity)) ||
                         (!warp_agrees(here) && !warp_wait<Sync::CLUSTER>(&sh.full[s], r.parity))) {
                         bad = true;
                         break;
                     }
                     r.next(ns);
                     tc_fence_after();
-                    const int nk = min(F::kSfTiles, kb - F::kSfTiles * i);
                     const uint32_t a0 = desc_lo(smem_u32(sA) + s * kPairABytes);
                     const uint32_t b0 = desc_lo(smem_u32(sB) + s * kPairBBytes);
                     const uint32_t sf = tmem + kPairSfCol + f.slot * kSfCols;
                     const bool last = in_chunk == chunk_stages<F>() - 1 || i + 1 == w.nkb;
                     if (elected) {
-                        pair_stage<F>(acc, a0, b0, sf + 4 * in_chunk, sf + 16 + 6 * in_chunk, nk, i > 0);
+                        pair_stage<F>(acc, a0, b0, sf + 4 * in_chunk, sf + 16 + 6 * in_chunk, 1, i > 0);
                         pair_commit(&sh.empty[s]);
-                        if (!chunk_is_stage<F>() && last) pair_commit(&sh.sf_free[f.slot]);
+                        if (last) pair_commit(&sh.sf_free[f.slot]);
                     }
                     here = mbar_ask<Sync::CLUSTER>(&sh.full[r.slot], r.parity);
                     __syncwarp();
@@ -308,13 +727,9 @@ __global__ void __launch_bounds__(pair_threads<F>(), 1) k_grouped(const __grid_c
         Ring f;
         uint32_t chunks = 0;
         for (int t = first; t < tiles && !bad; t += step) {
-            grouped_tile<kW>(a, groups, t, w);
-            const int32_t ra = (w.m0 + 128 * rank) >> 7;
-            const int32_t rb = (kW ? 0 : w.g * a.row_tiles_b) + (w.n0 >> 7);
-            const int mine = rank_rows(w, rank);
-            const uint8_t* src = kW ? nullptr : a.sa + (int64_t)(w.m0 + 128 * rank) * a.sa_pitch;
-            const int kb = kW ? w.nkb : a.kb;
-            for (int k = 0; k < kb; k += kSfChunkTiles) {
+            wgrad_tile(a, groups, t, w);
+            const int32_t ra = (w.m0 + 128 * rank) >> 7, rb = w.n0 >> 7;
+            for (int k = 0; k < w.nkb; k += kSfChunkTiles) {
                 if (chunks >= (uint32_t)kSfSlots && !warp_wait(&sh.sf_empty[f.slot], f.parity ^ 1u)) {
                     bad = true;
                     break;
@@ -322,24 +737,11 @@ __global__ void __launch_bounds__(pair_threads<F>(), 1) k_grouped(const __grid_c
                 unsigned char* ps = sS + f.slot * kSfChunkBytes;
                 uint64_t* bar = &sh.sf_full[f.slot];
                 if (elected) {
-                    mbar_expect_tx(bar, (uint32_t)(kW ? kSfChunkBytes : kSfChunkBytes - kSfChunkA));
-                    if (kW) sf_load_3d(ps, &a.tsa, w.k0 + k, ra, bar);
+                    mbar_expect_tx(bar, (uint32_t)kSfChunkBytes);
+                    sf_load_3d(ps, &a.tsa, w.k0 + k, ra, bar);
                     sf_load_3d(ps + kSfChunkA, &a.tsb, w.k0 + k, rb, bar);
                 }
                 __syncwarp();
-                if constexpr (!kW) {
-                    for (int r = lane; r < mine; r += 32) {
-                        const uint8_t* p = src + r * a.sa_pitch + 4 * k;
-                        const uint32_t d = smem_u32(ps) + 16 * r;
-                        if (a.sa_wide) {
-                            cp_async16(d, p);
-                        } else {
-                            for (int j = 0; j < min(kSfChunkTiles, kb - k); ++j) cp_async4(d + 4 * j, p + 4 * j);
-                        }
-                    }
-                    cp_async_arrive(bar);
-                    __syncwarp();
-                }
                 ++chunks;
                 f.next(kSfSlots);
             }
@@ -354,30 +756,18 @@ __global__ void __launch_bounds__(pair_threads<F>(), 1) k_grouped(const __grid_c
             }
             if (!warp_wait(&sh.sf_empty[sl], p)) bad = true;
         }
-    } else if (warp < 6 || warp > 10) {
-        // scales: lane l of quadrant q writes a's of rows l, 32 + l, 64 + l, 96 + l to
-        // columns 4 kk ..., of b's eight words (two row tiles) the six of the tile's
-        // 192 rows to columns 16 + 6 kk ...
+    } else if (warp < 6) {
+        // scales: lane l of quadrant q writes row l of each 16-byte-wide tile, as in
+        // k_linear_pair
         const int q = warp & 3;
         const uint32_t lane_base = tmem + kPairSfCol + ((uint32_t)(32 * q) << 16);
-        const uint32_t full0 = map_rank(smem_u32(&sh.full[0]), 0);
         const uint32_t ready0 = map_rank(smem_u32(&sh.sf_ready[0]), 0);
         Ring f, d;          // shared-memory slots; tensor-memory buffers
-        Ring r, u;          // chunk_is_stage: its stage; the one whose buffer it takes over
-        const uint32_t mine = warp < 6 ? 0u : 1u;  // the group of scale warps
         uint32_t chunks = 0;
         for (int t = first; t < tiles && !bad; t += step) {
-            grouped_tile<kW>(a, groups, t, w);
+            wgrad_tile(a, groups, t, w);
             const bool half = (w.n0 & 127) != 0;  // b starts half-way into a scale tile
             for (int i = 0; i < w.nkb; i += chunk_stages<F>()) {
-                if (chunks % sf_groups<F>() != mine) {
-                    if (chunks >= (uint32_t)kSfBufs) u.next(ns);
-                    ++chunks;
-                    r.next(ns);
-                    f.next(kSfSlots);
-                    d.next(kSfBufs);
-                    continue;
-                }
                 if (!warp_wait(&sh.sf_full[f.slot], f.parity)) {
                     bad = true;
                     break;
@@ -386,13 +776,10 @@ __global__ void __launch_bounds__(pair_threads<F>(), 1) k_grouped(const __grid_c
                 uint32_t va[16], vb[24];
 #pragma unroll
                 for (int kk = 0; kk < kSfChunkTiles; ++kk) {
-                    // kW: tile kk, rows l ... in its words; else rows 32 kk + l, tiles in the words
                     const uint4 x = *reinterpret_cast<const uint4*>(ps + kk * kSfTileBytes);
                     const uint4 y = *reinterpret_cast<const uint4*>(ps + kSfChunkA + kk * kSfTileBytes);
                     const uint4 z = *reinterpret_cast<const uint4*>(ps + 2 * kSfChunkA + kk * kSfTileBytes);
-                    constexpr int kA = kW ? 1 : 4;
-                    const int a0 = kW ? 4 * kk : kk;
-                    va[a0] = x.x; va[a0 + kA] = x.y; va[a0 + 2 * kA] = x.z; va[a0 + 3 * kA] = x.w;
+                    va[4 * kk] = x.x; va[4 * kk + 1] = x.y; va[4 * kk + 2] = x.z; va[4 * kk + 3] = x.w;
                     vb[6 * kk] = half ? y.z : y.x;
                     vb[6 * kk + 1] = half ? y.w : y.y;
                     vb[6 * kk + 2] = half ? z.x : y.z;
@@ -402,12 +789,10 @@ __global__ void __launch_bounds__(pair_threads<F>(), 1) k_grouped(const __grid_c
                 }
                 if (chunks >= (uint32_t)kSfBufs) {
                     // the MMAs that read this buffer are done
-                    if (chunk_is_stage<F>() ? !warp_wait<Sync::TENSOR>(&sh.empty[u.slot], u.parity)
-                                            : !warp_wait<Sync::TENSOR>(&sh.sf_free[d.slot], d.parity ^ 1u)) {
+                    if (!warp_wait<Sync::TENSOR>(&sh.sf_free[d.slot], d.parity ^ 1u)) {
                         bad = true;
                         break;
                     }
-                    u.next(ns);
                 }
                 tc_fence_after();
                 const uint32_t col = lane_base + d.slot * kSfCols;
@@ -418,13 +803,10 @@ __global__ void __launch_bounds__(pair_threads<F>(), 1) k_grouped(const __grid_c
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) {
-                    cluster_arrive(chunk_is_stage<F>() ? full0 + 8 * r.slot : ready0 + 8 * d.slot);
-                    // The slot is free once its values are in tensor memory: freed before
-                    // the stores that use them, its last loads were found moved behind the
-                    // arrival and took the slot's next chunk.
+                    cluster_arrive(ready0 + 8 * d.slot);
+                    // behind the stores that use its values (k_linear_pair)
                     bar_arrive(&sh.sf_empty[f.slot]);
                 }
-                r.next(ns);
                 ++chunks;
                 f.next(kSfSlots);
                 d.next(kSfBufs);
@@ -435,39 +817,21 @@ __global__ void __launch_bounds__(pair_threads<F>(), 1) k_grouped(const __grid_c
         constexpr int kElt = OT == Out::F32 ? 4 : 2;
         constexpr int kCols = 128 / kElt;               // columns of a chunk
         constexpr int kChunks = kPairN / kCols;         // chunks of a tile
-        const bool pre = !kW && a.ep.pre != nullptr, res = a.ep.residual != nullptr;
-        const bool has_bias = !kW && a.ep.bias != nullptr;
-        // two slots of a buffer for out (and the residual) and, with pre, one for it
-        const int slot_bytes = (pre ? 2 : 1) * kChunkBytes;
-        unsigned char* bufs = sC + e * 2 * slot_bytes;
-        float* s_bias = sBias + e * kPairN;
+        const bool res = a.ep.residual != nullptr;
+        unsigned char* bufs = sC + e * 2 * kChunkBytes;  // two slots, for out and the residual
         int c = 0, j = 0;  // chunks of this warp, accumulators used
         for (int t = first; t < tiles; t += step) {
-            grouped_tile<kW>(a, groups, t, w);
+            wgrad_tile(a, groups, t, w);
             const int32_t mw = w.m0 + 128 * rank + 32 * q;           // first row of this warp
             const int live = max(0, min(32, w.m_end - mw));          // rows of the group
             const int32_t orow = w.out_row + mw;
             auto fetch = [&](int k) {                                // chunk k's residual (one lane)
                 uint64_t* bar = &sh.res_full[e][c & 1];
                 mbar_expect_tx(bar, kChunkBytes);
-                tma_load_2d(bufs + (c & 1) * slot_bytes, &a.tres, w.n0 + k * kCols, orow, bar);
+                tma_load_2d(bufs + (c & 1) * kChunkBytes, &a.tres, w.n0 + k * kCols, orow, bar);
             };
             if (res && live > 0 && lane == 0) fetch(0);
-            float ga = 1.0f, gb = 1.0f;
-            if constexpr (F::kGlobal) {
-                gb = fdiv(1.0f, global_scale(a.ep.b_amax[w.g], a.ep.six_bound));
-                if (lane < live)
-                    ga = fdiv(1.0f, global_scale(a.ep.a_amax[a.ep.a_row ? mw + lane : w.g], a.ep.six_bound));
-            }
-            if (has_bias && live > 0) {
-                float bias[kPairN / 32];
-                Epilogue ep = a.ep;
-                ep.bias = static_cast<const char*>(a.ep.bias) + (int64_t)w.g * a.N * (a.ep.bias32 ? 4 : kElt);
-                load_bias<OT>(ep, w.n0, a.N, lane, bias);
-#pragma unroll
-                for (int i = 0; i < kPairN / 32; ++i) s_bias[32 * i + lane] = bias[i];
-            }
-            const bool sum = !kW || w.nkb > 0;  // there is a product
+            const bool sum = w.nkb > 0;  // there is a product
             const int ab = j & 1;
             if (sum) {
                 if (!bad && !warp_wait<Sync::TENSOR>(&sh.acc_full[ab], (uint32_t)(j >> 1) & 1)) bad = true;
@@ -484,7 +848,7 @@ __global__ void __launch_bounds__(pair_threads<F>(), 1) k_grouped(const __grid_c
                 continue;
             }
             for (int k = 0; k < kChunks; ++k, ++c) {
-                const uint32_t buf = smem_u32(bufs + (c & 1) * slot_bytes);
+                const uint32_t buf = smem_u32(bufs + (c & 1) * kChunkBytes);
                 if (res && !bad && !warp_wait(&sh.res_full[e][c & 1], (uint32_t)(c >> 1) & 1)) bad = true;
                 __syncwarp();
 #pragma unroll
@@ -504,23 +868,8 @@ __global__ void __launch_bounds__(pair_threads<F>(), 1) k_grouped(const __grid_c
                     }
                     float v[32];
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) {
-                        v[i] = __uint_as_float(u[i]);
-                        if constexpr (F::kGlobal) v[i] = fmul(fmul(v[i], ga), gb);
-                    }
-                    if (has_bias) {
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const float4 b4 = *reinterpret_cast<const float4*>(s_bias + col + 4 * i);
-                            v[4 * i] = fadd(v[4 * i], b4.x);
-                            v[4 * i + 1] = fadd(v[4 * i + 1], b4.y);
-                            v[4 * i + 2] = fadd(v[4 * i + 2], b4.z);
-                            v[4 * i + 3] = fadd(v[4 * i + 3], b4.w);
-                        }
-                    }
+                    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(u[i]);
                     constexpr int kPieces = 32 * kElt / 16;
-                    if (pre) put_pieces<OT>(buf + kChunkBytes + lane * 128, lane, kPieces * h, v);
-                    if constexpr (!kW) act_apply<OT>(a.ep.act, v);
                     if (res) add_pieces<OT>(buf + lane * 128, lane, kPieces * h, v);
                     put_pieces<OT>(buf + lane * 128, lane, kPieces * h, v);
                 }
@@ -528,15 +877,11 @@ __global__ void __launch_bounds__(pair_threads<F>(), 1) k_grouped(const __grid_c
                 if (live < 32) {  // the rows below are another group's
                     __syncwarp();
                     copy_rows<OT>(buf, a.ep.out, orow, n, a.N, live, lane);
-                    if (pre) copy_rows<OT>(buf + kChunkBytes, a.ep.pre, orow, n, a.N, live, lane);
                 }
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 __syncwarp();
                 if (lane == 0) {
-                    if (live == 32) {
-                        store_chunk(&a.tout, n, orow, buf);
-                        if (pre) store_chunk(&a.tpre, n, orow, buf + kChunkBytes);
-                    }
+                    if (live == 32) store_chunk(&a.tout, n, orow, buf);
                     asm volatile("cp.async.bulk.commit_group;" ::: "memory");
                     // the chunk before this one has left its slot, which the
                     // next one is fetched into and written to
@@ -544,11 +889,10 @@ __global__ void __launch_bounds__(pair_threads<F>(), 1) k_grouped(const __grid_c
                     if (res && k + 1 < kChunks) {
                         uint64_t* bar = &sh.res_full[e][(c + 1) & 1];
                         mbar_expect_tx(bar, kChunkBytes);
-                        tma_load_2d(bufs + ((c + 1) & 1) * slot_bytes, &a.tres, n + kCols, orow, bar);
+                        tma_load_2d(bufs + ((c + 1) & 1) * kChunkBytes, &a.tres, n + kCols, orow, bar);
                     }
                 }
             }
-            __syncwarp();  // the biases are read before the next tile's replace them
         }
         if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
         __syncwarp();
@@ -561,7 +905,7 @@ __global__ void __launch_bounds__(pair_threads<F>(), 1) k_grouped(const __grid_c
     __syncthreads();
     cluster_sync();  // neither CTA leaves while the other may touch its memory
     if (sh.fail && threadIdx.x == 0 && first < tiles) {
-        grouped_tile<kW>(a, groups, first, w);
+        wgrad_tile(a, groups, first, w);
         store_out<OT>(a.ep.out, (int64_t)(w.out_row + w.m0) * a.N + w.n0, __int_as_float(0x7FC00000));
     }
     if (warp == 1) {

@@ -1,7 +1,7 @@
 // fos_groups.cuh -- rows packed by group (expert), read from cumulative ends on
 // the device: group g has rows [end_{g-1}, end_g), end_g = clamp(offs[g],
-// end_{g-1}, rows), and its rows are cut into tiles of 2^kShift rows that belong
-// to it alone (its last one may be short).
+// end_{g-1}, rows), and its rows are cut into tiles of kUnit rows that belong to it
+// alone (its last one may be short).
 //
 // The host does not know the ends, so each CTA forms the table of groups itself,
 // one warp over at most 1024 ends: entry g holds group g's first row and the
@@ -19,11 +19,11 @@ constexpr int kMaxGroups = 1024;  // FOS_LINEAR_MAX_GROUPS
 inline __host__ __device__ constexpr size_t group_table_bytes(int G) {
     return ((size_t)(G + 1) * sizeof(Group) + 15) / 16 * 16;
 }
-// Tiles of 2^shift rows that G groups of together `rows` rows can have at most:
-// every group with rows adds up to 2^shift - 1 to be a whole number of tiles.
-inline __host__ __device__ constexpr int64_t group_tiles_max(int64_t rows, int64_t G, int shift) {
+// Tiles of `unit` rows that G groups of together `rows` rows can have at most: every
+// group with rows adds up to unit - 1 to be a whole number of tiles.
+inline __host__ __device__ constexpr int64_t group_tiles_max(int64_t rows, int64_t G, int unit) {
     const int64_t most = G < rows ? G : rows;
-    return (rows + most * ((INT64_C(1) << shift) - 1)) >> shift;
+    return (rows + most * (unit - 1)) / unit;
 }
 
 __device__ __forceinline__ int32_t ld_s32(const int32_t* p) {
@@ -33,7 +33,7 @@ __device__ __forceinline__ int32_t ld_s32(const int32_t* p) {
 }
 
 // The table by one converged warp; lane l takes ceil(G / 32) neighbouring groups.
-template <int kShift>
+template <int kUnit>
 __device__ __forceinline__ void group_table(Group* t, const int32_t* offs, int G, int32_t rows,
                                             int lane) {
     const int per = (G + 31) >> 5, lo = min(G, lane * per), hi = min(G, lo + per);
@@ -54,7 +54,7 @@ __device__ __forceinline__ void group_table(Group* t, const int32_t* offs, int G
     int32_t row = min(rows, before), tiles = 0;
     for (int i = lo; i < hi; ++i) {
         const int32_t end = min(rows, max(before, t[i + 1].row));
-        tiles += (end - row + (1 << kShift) - 1) >> kShift;
+        tiles += (end - row + kUnit - 1) / kUnit;
         t[i + 1] = Group{end, tiles};
         row = end;
     }

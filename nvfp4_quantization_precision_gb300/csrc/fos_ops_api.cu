@@ -536,7 +536,7 @@ fos_status fos_linear4_grouped(const uint8_t* a_codes, const uint8_t* a_scales, 
 
 int64_t fos_grouped_cols(int64_t rows, int G) {
     if (rows < 0 || rows > kMost || check_groups(G)) return -1;
-    return 128 * group_tiles_max(rows, G, 7);
+    return kQ8Tile * group_tiles_max(rows, G, kQ8Tile);
 }
 
 fos_status fos_quantize8_grouped(const void* x, fos_dtype dt, int64_t rows, int64_t cols,
@@ -548,7 +548,7 @@ fos_status fos_quantize8_grouped(const void* x, fos_dtype dt, int64_t rows, int6
 
 size_t fos_act_backward_grouped_workspace_bytes(int64_t rows, int64_t cols, int G) {
     if (rows <= 0 || cols <= 0 || check_shape8(rows, cols) || check_groups(G)) return 0;
-    const int64_t tiles = group_tiles_max(rows, G, 7);
+    const int64_t tiles = group_tiles_max(rows, G, kQ8Tile);
     return within(tiles, cols) ? (size_t)(tiles * cols + G + 1) * sizeof(float) : 0;
 }
 

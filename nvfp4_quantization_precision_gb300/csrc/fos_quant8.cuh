@@ -241,7 +241,7 @@ __global__ void __launch_bounds__(kQ8Threads, 3) k_quant8_grouped(const __grid_c
     Group* s_groups = reinterpret_cast<Group*>(s_tile + kQ8Tile * kQ8Tile);
     const Quant8Args& a = b.q;
     const int tid = threadIdx.x;
-    if (tid < 32) group_table<7>(s_groups, b.offs, b.G, (int32_t)a.rows, tid);
+    if (tid < 32) group_table<kQ8Tile>(s_groups, b.offs, b.G, (int32_t)a.rows, tid);
     __syncthreads();
     const int tiles_c = (int)a.tiles_c, total = s_groups[b.G].tile * tiles_c;
     if (a.part && blockIdx.x == 0)

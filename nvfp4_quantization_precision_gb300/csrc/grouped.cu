@@ -9,29 +9,67 @@ namespace lin {
 
 namespace {
 
-template <class F, Out OT, bool kW>
+// Tile rows of a band: their rows of the operand that stays in L2 take at most 30 MB, a
+// quarter of it (pair_go()).
+int band_rows(int64_t tile_bytes) {
+    const int64_t fit = 30000000 / tile_bytes;
+    return (int)(fit < 1 ? 1 : fit > 4096 ? 4096 : fit);
+}
+
+template <class Kernel, class Args>
+cudaError_t launch_pairs(Kernel k, int threads, int64_t tiles, int smem, const Args& a, cudaStream_t s) {
+    const cudaError_t e = allow_smem(reinterpret_cast<const void*>(k), (size_t)kSmemLimit - 4096);
+    if (e != cudaSuccess) return e;
+    int64_t clusters = resident_clusters(k, threads, smem, 2);
+    if (clusters > tiles) clusters = tiles;
+    return launch_clusters(k, (int)clusters, 2, threads, smem, a, s);
+}
+
+template <class F, Out OT>
 cudaError_t go(const GroupedCall& c, cudaStream_t s) {
     GroupedArgs a;
     std::memset(&a, 0, sizeof(a));
-    // bytes of a row of codes; of a weight gradient's columns they are the tokens
     const int64_t row_bytes = F::kGlobal ? c.K / 2 : c.K;
-    const int64_t rows_a = kW ? c.M : c.rows, rows_b = kW ? c.N : c.G * c.N;
-    const int64_t rows_out = kW ? c.G * c.M : c.rows;
     a.kb = k_tiles<F>(c.K);
     a.nkb = k_stages<F>(c.K);
-    a.row_tiles_b = (int)((c.N + 127) / 128);
-    if (!code_map(&a.ta, c.a, rows_a, row_bytes, 128) || !code_map(&a.tb, c.b, rows_b, row_bytes, 96) ||
-        (!kW && !code_map(&a.ta32, c.a, rows_a, row_bytes, 32)) ||
-        (kW && !scale_map(&a.tsa, c.as, rows_a, a.kb, 1, kSfChunkTiles)) ||
-        !scale_map(&a.tsb, c.bs, kW ? rows_b : (int64_t)c.G * a.row_tiles_b * 128, a.kb, 2, kSfChunkTiles) ||
-        !chunk_map<OT>(&a.tout, c.ep.out, rows_out, c.N) ||
-        (c.ep.residual && !chunk_map<OT>(&a.tres, c.ep.residual, rows_out, c.N)) ||
-        (c.ep.pre && !chunk_map<OT>(&a.tpre, c.ep.pre, rows_out, c.N)))
+    a.row_tiles = (int)((c.N + 127) / 128);
+    if (!code_map(&a.tw, c.b, c.G * c.N, row_bytes, 128) || !code_map(&a.tt, c.a, c.rows, row_bytes, kTokTile / 2) ||
+        !code_map(&a.tt16, c.a, c.rows, row_bytes, kTokBox) ||
+        !scale_map(&a.tsw, c.bs, (int64_t)c.G * a.row_tiles * 128, a.kb, 1, kSfChunkTiles))
         return cudaErrorInvalidValue;
     a.ep = c.ep;
-    a.sa = c.as;
-    a.sa_pitch = F::kGlobal ? c.K / 16 : c.K / 32;
-    a.sa_wide = a.sa_pitch % 16 == 0;
+    a.ts = c.as;
+    a.ts_pitch = F::kGlobal ? c.K / 16 : c.K / 32;
+    a.ts_wide = a.ts_pitch % 16 == 0;
+    a.offs = c.offs;
+    a.G = c.G;
+    a.rows = (int)c.rows;
+    a.N = (int)c.N;
+    a.tiles_n = (int)((c.N + kPairM - 1) / kPairM);
+    a.band = band_rows(kTokTile * row_bytes);
+    // 4 KB for the kernel's own shared memory and 1 KB to align the stages
+    constexpr int kFixed = 4096 + 1024 + sf_slots<F>() * kGrpSfBytes;
+    static_assert((kSmemLimit - kFixed - (int)group_table_bytes(kMaxGroups)) / kPairStageBytes >= kSfBufs, "stages");
+    const int table = (int)group_table_bytes(c.G);
+    a.stages = (kSmemLimit - kFixed - table) / kPairStageBytes;
+    if (a.stages > kPairMaxStages) a.stages = kPairMaxStages;
+    const int smem = a.stages * kPairStageBytes + sf_slots<F>() * kGrpSfBytes + table + 1024;
+    return launch_pairs(k_grouped<F, OT>, pair_threads<F>(), group_tiles_max(c.rows, c.G, kTokTile) * a.tiles_n,
+                        smem, a, s);
+}
+
+template <Out OT>
+cudaError_t go_wgrad(const GroupedCall& c, cudaStream_t s) {
+    WgradArgs a;
+    std::memset(&a, 0, sizeof(a));
+    const int kb = k_tiles<F8>(c.K);  // K: the padded tokens
+    if (!code_map(&a.ta, c.a, c.M, c.K, 128) || !code_map(&a.tb, c.b, c.N, c.K, 96) ||
+        !scale_map(&a.tsa, c.as, c.M, kb, 1, kSfChunkTiles) ||
+        !scale_map(&a.tsb, c.bs, c.N, kb, 2, kSfChunkTiles) ||
+        !chunk_map<OT>(&a.tout, c.ep.out, c.G * c.M, c.N) ||
+        (c.ep.residual && !chunk_map<OT>(&a.tres, c.ep.residual, c.G * c.M, c.N)))
+        return cudaErrorInvalidValue;
+    a.ep = c.ep;
     a.offs = c.offs;
     a.G = c.G;
     a.rows = (int)c.rows;
@@ -39,34 +77,32 @@ cudaError_t go(const GroupedCall& c, cudaStream_t s) {
     a.N = (int)c.N;
     a.tiles_m = (int)((c.M + kPairM - 1) / kPairM);
     a.tiles_n = (int)((c.N + kPairN - 1) / kPairN);
-    // Bands of tile rows whose rows of a take at most 30 MB, a quarter of L2 (pair_go());
-    // of a weight gradient's columns a group has its share.
-    const int64_t band_bytes = kPairM * (kW ? row_bytes / c.G + 1 : row_bytes);
-    const int64_t fit = 30000000 / band_bytes;
-    a.band = (int)(fit < 1 ? 1 : fit > 4096 ? 4096 : fit);
-    a.bufs = c.ep.pre ? 4 : 2;
+    a.band = band_rows(kPairM * (c.K / c.G + 1));  // a group's share of the columns
+    constexpr int kOther = 8 * kChunkBytes + sf_slots<F8>() * kSfChunkBytes;
+    static_assert((kSmemLimit - 4096 - 1024 - kOther - (int)group_table_bytes(kMaxGroups)) / kPairStageBytes >=
+                      kSfBufs, "stages");
     const int table = (int)group_table_bytes(c.G);
-    const int other = 4 * a.bufs * kChunkBytes + sf_slots<F>() * kSfChunkBytes + 4 * kPairN * 4 + table;
-    static_assert((kSmemLimit - 2048 - 16 * kChunkBytes - kSfMaxSlots * kSfChunkBytes - 16 * kPairN -
-                   (int)group_table_bytes(kMaxGroups)) / kPairStageBytes >= kSfBufs, "stages");
-    a.stages = (kSmemLimit - 2048 - other) / kPairStageBytes;
+    a.stages = (kSmemLimit - 4096 - 1024 - kOther - table) / kPairStageBytes;
     if (a.stages > kPairMaxStages) a.stages = kPairMaxStages;
-    const int smem = a.stages * kPairStageBytes + other + 1024;
-    auto k = k_grouped<F, OT, kW>;
-    cudaError_t e = allow_smem(reinterpret_cast<const void*>(k), (size_t)kSmemLimit - 1024);
-    if (e != cudaSuccess) return e;
-    const int64_t tiles = (kW ? (int64_t)c.G * a.tiles_m : group_tiles_max(c.rows, c.G, 8)) * a.tiles_n;
-    int64_t clusters = resident_clusters(k, pair_threads<F>(), smem, 2);
-    if (clusters > tiles) clusters = tiles;
-    return launch_clusters(k, (int)clusters, 2, pair_threads<F>(), smem, a, s);
+    const int smem = a.stages * kPairStageBytes + kOther + table + 1024;
+    return launch_pairs(k_grouped_wgrad<OT>, pair_threads<F8>(), (int64_t)c.G * a.tiles_m * a.tiles_n, smem, a, s);
 }
 
-template <class F, bool kW>
+template <class F>
 cudaError_t by_out(const GroupedCall& c, cudaStream_t s) {
     switch (c.out) {
-        case In::BF16: return go<F, Out::BF16, kW>(c, s);
-        case In::F16: return go<F, Out::F16, kW>(c, s);
-        case In::F32: return go<F, Out::F32, kW>(c, s);
+        case In::BF16: return go<F, Out::BF16>(c, s);
+        case In::F16: return go<F, Out::F16>(c, s);
+        case In::F32: return go<F, Out::F32>(c, s);
+    }
+    return cudaErrorInvalidValue;
+}
+
+cudaError_t wgrad_by_out(const GroupedCall& c, cudaStream_t s) {
+    switch (c.out) {
+        case In::BF16: return go_wgrad<Out::BF16>(c, s);
+        case In::F16: return go_wgrad<Out::F16>(c, s);
+        case In::F32: return go_wgrad<Out::F32>(c, s);
     }
     return cudaErrorInvalidValue;
 }
@@ -75,8 +111,8 @@ cudaError_t by_out(const GroupedCall& c, cudaStream_t s) {
 }  // namespace lin
 
 cudaError_t launch_grouped(const GroupedCall& c, cudaStream_t s) {
-    if (c.wgrad) return lin::by_out<lin::F8, true>(c, s);
-    return c.fmt4 ? lin::by_out<lin::F4, false>(c, s) : lin::by_out<lin::F8, false>(c, s);
+    if (c.wgrad) return lin::wgrad_by_out(c, s);
+    return c.fmt4 ? lin::by_out<lin::F4>(c, s) : lin::by_out<lin::F8>(c, s);
 }
 
 }  // namespace fos

@@ -45,7 +45,7 @@ cudaError_t go_grouped(const GroupedQuant8Args& b, float* sums, cudaStream_t s) 
     const size_t smem = kQ8Smem + group_table_bytes(b.G);
     cudaError_t e = allow_smem(reinterpret_cast<const void*>(k), kQ8Smem + group_table_bytes(kMaxGroups));
     if (e != cudaSuccess) return e;
-    const int64_t most = group_tiles_max(b.q.rows, b.G, 7) * b.q.tiles_c;
+    const int64_t most = group_tiles_max(b.q.rows, b.G, kQ8Tile) * b.q.tiles_c;
     const int64_t wave = (int64_t)sm_count() *
                          resident_ctas(reinterpret_cast<const void*>(k), smem, kQ8Threads);
     e = launch_chained(k, dim3((unsigned)(most < wave ? most : wave)), kQ8Threads, smem, s, b);
