@@ -32,7 +32,8 @@ static_assert(kPairABytes == 128 * kRowBytes && kPairBBytes == 96 * kRowBytes, "
 // k_grouped: the weights are the MMA's 256 rows and a group's rows (tokens) its
 // columns, as in k_linear_rows, so that a tile that the group ends in costs what it has:
 // tiles of 256 weight rows x 192 tokens, the last one of a group as many as it
-// needs, rounded up to 32.  (With tokens as the 256 rows, groups of 255 rows on average
+// needs, rounded up to 32 (a group's tokens in even parts: prefill of 16384 tokens over
+// 63 experts 140 us instead of 127).  (With tokens as the 256 rows, groups of 255 rows on average
 // fill 60 % of their tiles: 16084 x 2048 x 7168 NVFP4 over 63 groups 182 us.)
 // CTA r of a pair holds weight rows 128 r .. + 127 of the tile and its half of the
 // tokens; each CTA's tensor memory has the products of its weight rows and all of
@@ -54,16 +55,29 @@ constexpr int kTokStep = 32;                     // an MMA's columns come in ste
 constexpr int kTokBox = 16;                      // tokens of a small box
 constexpr int kTokSfBytes = kTokTile * 16;       // a chunk of their scales
 constexpr int kGrpSfBytes = kSfChunkA + kTokSfBytes;
+// Chunks of scales in shared memory: of NVFP4, whose chunk is a stage, two are held by
+// the groups of scale warps while they wait for a buffer in tensor memory, and the
+// others have to cover the copies' latency.
+template <class F> constexpr int grp_slots() { return F::kGlobal ? 8 : 3; }
+
+struct __align__(8) GroupedShared {
+    uint64_t full[kPairMaxStages], empty[kPairMaxStages], acc_full[2], acc_empty[2], done;
+    uint64_t sf_full[8], sf_empty[8], sf_ready[kSfBufs], sf_free[kSfBufs];
+    uint32_t tmem;
+    int fail;
+};
 
 struct GroupedArgs {
     CUtensorMap tw;    // weights' codes, box 128 bytes x 128 rows, the groups' below one another
     CUtensorMap tt;    // tokens' codes, box 128 bytes x 96 rows
     CUtensorMap tt16;  // the same, 16 rows
     CUtensorMap tsw;   // weights' tiled scales, box 1 x 4 x 512
+    CUtensorMap tst;   // ts_wide: the tokens' plain scales, box 16 bytes x 192 rows
+    CUtensorMap tst32; // the same, 32 rows
     Epilogue ep;
     const uint8_t* ts;     // plain scales of the tokens
     int64_t ts_pitch;      // bytes of a row of them
-    int ts_wide;           // rows of them are whole 16-byte pieces
+    int ts_wide;           // rows of them are whole 16-byte pieces: by TMA
     const int32_t* offs;
     int G;
     int rows;              // packed rows
@@ -100,9 +114,6 @@ __device__ __forceinline__ void grouped_tile(const GroupedArgs& a, const Group* 
     w.n0 = col * kPairM;
 }
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
 __device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
 }
@@ -168,11 +179,12 @@ __device__ __forceinline__ void store_column(void* p, int64_t N, const float (&v
 template <class F, Out OT>
 __global__ void __launch_bounds__(pair_threads<F>(), 1) k_grouped(const __grid_constant__ GroupedArgs a) {
     extern __shared__ __align__(1024) unsigned char s_raw[];
-    __shared__ PairShared sh;
+    __shared__ GroupedShared sh;
     __shared__ __align__(16) float s_ga[F::kGlobal ? 4 : 1][kTokTile];  // the tokens' decode scales
     unsigned char* base = s_raw + ((1024u - (smem_u32(s_raw) & 1023u)) & 1023u);
     const int ns = a.stages;
-    constexpr int kSfSlots = sf_slots<F>();
+    constexpr int kSfSlots = grp_slots<F>();
+    static_assert(kSfSlots % sf_groups<F>() == 0 && kSfSlots <= 8, "a slot belongs to one group");
     unsigned char* sA = base;
     unsigned char* sB = sA + ns * kPairABytes;
     unsigned char* sS = sB + ns * kPairBBytes;  // scale chunks: the weights', then the tokens'
@@ -190,7 +202,7 @@ __global__ void __launch_bounds__(pair_threads<F>(), 1) k_grouped(const __grid_c
             bar_init(&sh.acc_empty[b], 8);
         }
         for (int b = 0; b < kSfSlots; ++b) {
-            bar_init(&sh.sf_full[b], 33);  // the TMA copy's, and each lane's of warp 10
+            bar_init(&sh.sf_full[b], a.ts_wide ? 1 : 33);  // TMA's, and each lane's of warp 10
             bar_init(&sh.sf_empty[b], 4);
         }
         for (int b = 0; b < kSfBufs; ++b) {
@@ -323,22 +335,28 @@ __global__ void __launch_bounds__(pair_threads<F>(), 1) k_grouped(const __grid_c
                 }
                 unsigned char* ps = sS + f.slot * kGrpSfBytes;
                 uint64_t* bar = &sh.sf_full[f.slot];
+                unsigned char* pt = ps + kSfChunkA;
                 if (elected) {
-                    mbar_expect_tx(bar, (uint32_t)kSfChunkA);
+                    const int boxes = w.cols > kTokTile / 2 ? 6 : w.cols >> 5;
+                    mbar_expect_tx(bar, (uint32_t)(kSfChunkA + (a.ts_wide ? 512 * boxes : 0)));
                     sf_load_3d(ps, &a.tsw, k, ra, bar);
-                }
-                __syncwarp();
-                for (int r = lane; r < w.live; r += 32) {
-                    const uint8_t* p = src + r * a.ts_pitch + 4 * k;
-                    const uint32_t d = smem_u32(ps) + kSfChunkA + 16 * r;
                     if (a.ts_wide) {
-                        cp_async16(d, p);
-                    } else {
-                        for (int j = 0; j < min(kSfChunkTiles, a.kb - k); ++j) cp_async4(d + 4 * j, p + 4 * j);
+                        if (boxes == 6) tma_load_2d(pt, &a.tst, 4 * k, w.t0, bar);
+                        else
+                            for (int j = 0; j < boxes; ++j)
+                                tma_load_2d(pt + 512 * j, &a.tst32, 4 * k, w.t0 + 32 * j, bar);
                     }
                 }
-                cp_async_arrive(bar);
                 __syncwarp();
+                if (!a.ts_wide) {
+                    for (int r = lane; r < w.live; r += 32) {
+                        const uint8_t* p = src + r * a.ts_pitch + 4 * k;
+                        for (int j = 0; j < min(kSfChunkTiles, a.kb - k); ++j)
+                            cp_async4(smem_u32(pt) + 16 * r + 4 * j, p + 4 * j);
+                    }
+                    cp_async_arrive(bar);
+                    __syncwarp();
+                }
                 ++chunks;
                 f.next(kSfSlots);
             }

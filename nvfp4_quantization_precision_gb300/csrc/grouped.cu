@@ -41,6 +41,11 @@ cudaError_t go(const GroupedCall& c, cudaStream_t s) {
     a.ts = c.as;
     a.ts_pitch = F::kGlobal ? c.K / 16 : c.K / 32;
     a.ts_wide = a.ts_pitch % 16 == 0;
+    if (a.ts_wide && (!matrix_map(&a.tst, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, c.as, c.rows, a.ts_pitch, 16, kTokTile,
+                                  CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_64B) ||
+                      !matrix_map(&a.tst32, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, c.as, c.rows, a.ts_pitch, 16, 32,
+                                  CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_64B)))
+        return cudaErrorInvalidValue;
     a.offs = c.offs;
     a.G = c.G;
     a.rows = (int)c.rows;
@@ -48,12 +53,12 @@ cudaError_t go(const GroupedCall& c, cudaStream_t s) {
     a.tiles_n = (int)((c.N + kPairM - 1) / kPairM);
     a.band = band_rows(kTokTile * row_bytes);
     // 4 KB for the kernel's own shared memory and 1 KB to align the stages
-    constexpr int kFixed = 4096 + 1024 + sf_slots<F>() * kGrpSfBytes;
+    constexpr int kFixed = 4096 + 1024 + grp_slots<F>() * kGrpSfBytes;
     static_assert((kSmemLimit - kFixed - (int)group_table_bytes(kMaxGroups)) / kPairStageBytes >= kSfBufs, "stages");
     const int table = (int)group_table_bytes(c.G);
     a.stages = (kSmemLimit - kFixed - table) / kPairStageBytes;
     if (a.stages > kPairMaxStages) a.stages = kPairMaxStages;
-    const int smem = a.stages * kPairStageBytes + sf_slots<F>() * kGrpSfBytes + table + 1024;
+    const int smem = a.stages * kPairStageBytes + grp_slots<F>() * kGrpSfBytes + table + 1024;
     return launch_pairs(k_grouped<F, OT>, pair_threads<F>(), group_tiles_max(c.rows, c.G, kTokTile) * a.tiles_n,
                         smem, a, s);
 }
