@@ -24,10 +24,11 @@
 //            MMAs, four a time: any order of k serves as long as x has the same.
 //   x fp32   is split into three bf16 of 8 significant bits each (exactly: by
 //            truncation), which take three columns; two rows at a time.
-// A CTA takes 64 weight rows: rows 32 i + 16 h + 0 .. 15, i = 0 .. 3, of one
-// 128-row tile of scales, so that a lane's 16 bytes of scales serve four of its
-// rows.  Its eight warps split K by steps of 128, and with few CTAs the CTAs of a
-// cluster do too; partial sums are added in one fixed order, warps first.
+// A CTA takes 16 kR weight rows, kR of 1 .. 4 chosen so that the CTAs fill the device
+// evenly.  Its eight warps split K by steps of 128, each with a ring of its own of
+// kRing steps' codes, filled by TMA (zeros past K), and with few CTAs the CTAs of a
+// cluster split K too; partial sums are added in one fixed order, warps first.
+// Measured, GPU time in a graph: TOKENUS
 // With ids, grid row p handles the rows of expert ids[p] at once if p is the first
 // of them (the weights are read once), else nothing.
 #pragma once
@@ -38,9 +39,9 @@
 namespace fos {
 
 struct MatvecArgs {
+    CUtensorMap codes;      // [G * N, K / 2], box 16 kR rows x 64 bytes
     const void* x;          // [M / rep, K]
     const int32_t* ids;     // [M] or null
-    const uint8_t* codes;   // [G, N, K / 2]
     const uint8_t* scales;  // [G] x tiled
     Epilogue ep;            // b_amax [G]
     int64_t scale_bytes;    // of one expert
@@ -52,103 +53,139 @@ struct MatvecArgs {
 
 namespace matvec {
 
-constexpr int kWarpsMv = 8, kRows = 64, kStepK = 128, kMaxRows = 1024;
-constexpr int kLine = 68;  // floats of a column of partial sums: its stores touch every bank once
+constexpr int kWarpsMv = 8, kStepK = 128, kMaxRows = 1024;
+constexpr int kStepBytes = kStepK / 2;  // of a row of codes
+template <int kR> constexpr int ring() { return kR < 4 ? 3 : 2; }  // steps of a warp: two CTAs an SM
+// Floats of a column of partial sums: a multiple of 16, but not of 32, plus 4, so that a
+// warp's stores touch every bank once.
+template <int kR> constexpr int line() { return 16 * kR + (kR % 2 ? 20 : 4); }
+template <int kR> constexpr int ring_bytes() { return kWarpsMv * ring<kR>() * 16 * kR * kStepBytes; }
+// x in fp16: kXBytes of columns and steps, of each one factor, and a step of zeros.
+constexpr int kXStep = kStepK * 2, kXBytes = 128 * kXStep;
+template <int kR> constexpr int smem_bytes() { return ring_bytes<kR>() + kXBytes + 64 + 128 * 4; }
 
 template <In XT> constexpr int tokens() { return XT == In::F32 ? 2 : 8; }
 
+__device__ __forceinline__ uint32_t mul_pair(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+// The eight weights of a word of codes as pairs of neighbours, times the scale pair.
+__device__ __forceinline__ void unpack(uint32_t w, uint32_t s, uint32_t (&v)[4]) {
+    asm("{\n\t.reg .b8 q0, q1, q2, q3;\n\tmov.b32 {q0, q1, q2, q3}, %4;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %0, q0;\n\tcvt.rn.f16x2.e2m1x2 %1, q1;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %2, q2;\n\tcvt.rn.f16x2.e2m1x2 %3, q3;\n\t}"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]) : "r"(w));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = mul_pair(v[i], s);
+}
+// Two scales' E4M3 bytes (low half of `two`) as a pair.
+__device__ __forceinline__ uint32_t scale_pair(uint32_t two) {
+    uint32_t r;
+    asm("{\n\t.reg .b16 c;\n\tcvt.u16.u32 c, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, c;\n\t}" : "=r"(r) : "r"(two));
+    return r;
+}
+__device__ __forceinline__ void mma16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                      uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t f16_pair(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
 __device__ __forceinline__ uint4 ld128(const void* p) {
     uint4 v;
-    asm volatile("ld.global.nc.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];"
+    asm volatile("ld.global.v4.b32 {%0, %1, %2, %3}, [%4];"
                  : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
     return v;
 }
-
-template <In XT>
-__device__ __forceinline__ uint32_t mul_pair(uint32_t a, uint32_t b) {
-    uint32_t r;
-    if constexpr (XT == In::F16) asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-    else asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-    return r;
+__device__ __forceinline__ uint32_t ld_u16(const void* p) {
+    uint32_t v;
+    asm volatile("{\n\t.reg .b16 h;\n\tld.global.nc.b16 h, [%1];\n\tcvt.u32.u16 %0, h;\n\t}" : "=r"(v) : "l"(p));
+    return v;
 }
-// Pairs (element i, element i + 4) of a word of eight codes, times the scale pair.
-template <In XT>
-__device__ __forceinline__ void unpack(uint32_t w, uint32_t s, uint32_t (&v)[4]) {
-    constexpr uint32_t kSign = 0x80008000u, kMag = XT == In::F16 ? 0x0E000E00u : 0x01C001C0u;
-    if constexpr (XT == In::F16) {
-        v[0] = ((w << 9) & kMag) | ((w << 12) & kSign);
-        v[1] = ((w << 5) & kMag) | ((w << 8) & kSign);
-        v[2] = ((w << 1) & kMag) | ((w << 4) & kSign);
-        v[3] = ((w >> 3) & kMag) | (w & kSign);
-    } else {
-        v[0] = ((w << 6) & kMag) | ((w << 12) & kSign);
-        v[1] = ((w << 2) & kMag) | ((w << 8) & kSign);
-        v[2] = ((w >> 2) & kMag) | ((w << 4) & kSign);
-        v[3] = ((w >> 6) & kMag) | (w & kSign);
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = mul_pair<XT>(v[i], s);
+// Ordered before what follows: the ring's slot is filled again behind its last load.
+__device__ __forceinline__ uint4 lds128(uint32_t addr) {
+    uint4 v;
+    asm volatile("ld.volatile.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+    return v;
 }
-// Scale byte (0x00 .. 0x7E) as a pair, 2^119 (fp16 2^7) times its value.
-template <In XT>
-__device__ __forceinline__ uint32_t scale_pair(uint32_t byte) {
-    if constexpr (XT == In::F16) {
-        return mul_pair<XT>((byte & 0x7Fu) * 0x00800080u, 0x78007800u);  // 2^15
-    } else {
-        const uint32_t a = mul_pair<XT>((byte & 0x7Fu) * 0x00100010u, 0x7F007F00u);  // 2^127
-        return mul_pair<XT>(a, 0x77807780u);                                          // 2^112
-    }
-}
-template <In XT>
-__device__ __forceinline__ void mma16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                      uint32_t a3, uint32_t b0, uint32_t b1) {
-    if constexpr (XT == In::F16)
-        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
-            "{%8,%9}, {%0,%1,%2,%3};"
-            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-    else
-        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
-            "{%8,%9}, {%0,%1,%2,%3};"
-            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-// Piece `p` (0 .. 2) of an fp32 as the top half of a word: x = the sum of its pieces,
-// each a truncation to 8 significant bits of what is left.  An infinity is its first
-// piece, the others 0; a NaN keeps a NaN.
-__device__ __forceinline__ uint32_t piece(float x, int p) {
-    const float hi = __uint_as_float(__float_as_uint(x) & 0xFFFF0000u);
-    if (!(fabsf(x) <= kFltMax))
-        return p > 0 ? 0u : (x != x ? 0x7FC00000u : __float_as_uint(x));
-    const float r = x - hi;
-    const float mid = __uint_as_float(__float_as_uint(r) & 0xFFFF0000u);
-    return __float_as_uint(p == 0 ? hi : p == 1 ? mid : r - mid) & 0xFFFF0000u;
+__device__ __forceinline__ void sts128(uint32_t addr, const uint32_t* v) {
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3])
+                 : "memory");
 }
 
-// x's 32 elements of a lane as the MMAs' second operand, in the order of unpack().
+// Where the 16-byte piece q (0 .. 3) of lane t's 32 elements of a column's step lies in
+// its 256 bytes: the four lanes of two neighbouring columns touch every bank once.
+__device__ __forceinline__ uint32_t x_piece(int t, int col, int q) {
+    return (uint32_t)((t >> 1) * 128 + ((((t & 1) * 4 + q) ^ ((t >> 1) + 2 * (col & 1))) << 4));
+}
+
+// Lane t's 32 elements of a row of x in fp16, at `to` (the row's column, or the first of
+// its three) of the step, times a power of two that brings the largest finite one of the
+// row's 128 of the step to 2^14 .. 2^15 (of the quad t = 0 .. 3 together); returns its
+// inverse.  fp16 holds every bf16 down to 2^-32 of the largest exactly, and 2^-40 of it
+// is what it rounds off below that, far beneath the sum's own roundings.  fp32: y = the
+// sum of three pieces, each the rounding of what is left to 11 significant bits; an
+// infinity or a NaN is its first piece, the others 0.
 template <In XT>
-struct Frag {
-    uint32_t b[4][4];  // word of codes, pair
-};
-template <In XT>
-__device__ __forceinline__ void load_x(Frag<XT>& f, const void* x, int64_t at, int col) {
+__device__ __forceinline__ float put_x(const char* x, bool in, uint32_t to, uint32_t col_bytes, int col, int t) {
+    constexpr int kQ = XT == In::F32 ? 8 : 4;
+    uint32_t w[4 * kQ];
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-        if constexpr (XT == In::F32) {
-            const uint4 lo = ld128(static_cast<const float*>(x) + at + 8 * q);
-            const uint4 hi = ld128(static_cast<const float*>(x) + at + 8 * q + 4);
-            const uint32_t l[4] = {lo.x, lo.y, lo.z, lo.w}, h[4] = {hi.x, hi.y, hi.z, hi.w};
+    for (int q = 0; q < kQ; ++q) {
+        const uint4 v = in ? ld128(x + 16 * q) : make_uint4(0, 0, 0, 0);
+        w[4 * q] = v.x; w[4 * q + 1] = v.y; w[4 * q + 2] = v.z; w[4 * q + 3] = v.w;
+    }
+    if constexpr (XT == In::F16) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                f.b[q][i] = (piece(__uint_as_float(l[i]), col % 3) >> 16) |
-                            piece(__uint_as_float(h[i]), col % 3);
-        } else {
-            const uint4 w = ld128(static_cast<const unsigned short*>(x) + at + 8 * q);
-            f.b[q][0] = __byte_perm(w.x, w.z, 0x5410);
-            f.b[q][1] = __byte_perm(w.x, w.z, 0x7632);
-            f.b[q][2] = __byte_perm(w.y, w.w, 0x5410);
-            f.b[q][3] = __byte_perm(w.y, w.w, 0x7632);
+        for (int q = 0; q < 4; ++q) sts128(to + x_piece(t, col, q), w + 4 * q);
+        return 1.0f;
+    } else {
+        auto value = [&](int i) {  // element i
+            if constexpr (XT == In::F32) return __uint_as_float(w[i]);
+            else return __uint_as_float(i & 1 ? w[i >> 1] & 0xFFFF0000u : w[i >> 1] << 16);
+        };
+        float most = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+            const float a = fabsf(value(i));
+            most = a <= kFltMax ? fmaxf(most, a) : most;
         }
+        most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, 1));
+        most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, 2));
+        // exponent of the largest + 127 (0: a subnormal one or zero); 2^(14 - e), at most 2^127
+        const int e = max(14, (int)(__float_as_uint(most) >> 23));
+        const float up = __uint_as_float((uint32_t)(268 - e) << 23);
+        constexpr int kPieces = XT == In::F32 ? 3 : 1;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            float y[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) y[i] = fmul(value(8 * q + i), up);
+#pragma unroll
+            for (int p = 0; p < kPieces; ++p) {
+                uint32_t h[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    h[i] = f16_pair(y[2 * i], y[2 * i + 1]);
+                    if (p + 1 < kPieces) {
+                        float a, b;
+                        upk(f16x2_f32x2(h[i]), a, b);
+                        y[2 * i] = fabsf(y[2 * i]) <= kFltMax ? y[2 * i] - a : 0.0f;
+                        y[2 * i + 1] = fabsf(y[2 * i + 1]) <= kFltMax ? y[2 * i + 1] - b : 0.0f;
+                    }
+                }
+                sts128(to + p * col_bytes + x_piece(t, col + p, q), h);
+            }
+        }
+        return fdiv(1.0f, up);
     }
 }
 
@@ -172,19 +209,29 @@ __device__ __forceinline__ void finish(const Epilogue& ep, float v, int64_t n_at
     lin::store_out<OT>(ep.out, at, a[0]);
 }
 
-template <In XT>
+template <In XT, int kR>
 __global__ void __launch_bounds__(32 * kWarpsMv, 2) k_matvec4(const __grid_constant__ MatvecArgs a) {
-    __shared__ float s_part[kWarpsMv][8 * kLine];
+    constexpr int kRows = 16 * kR, kLine = line<kR>(), kSlot = kRows * kStepBytes, kRing = ring<kR>();
+    constexpr int kTok = tokens<XT>(), kPieces = XT == In::F32 ? 3 : 1;
+    extern __shared__ __align__(128) unsigned char s_ring[];
     __shared__ __align__(16) float s_sum[8 * kLine];
+    __shared__ __align__(8) uint64_t s_full[kWarpsMv][kRing];
     __shared__ int s_ids[kMaxRows];
-    __shared__ int s_count;
-    constexpr int kTok = tokens<XT>();
+    __shared__ int s_count, s_fail;
+    float* s_down = reinterpret_cast<float*>(s_ring + ring_bytes<kR>() + kXBytes + 64);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
     const int S = a.splits, rank = (int)(blockIdx.x % S), block = (int)(blockIdx.x / S);
-    const int row0 = (block >> 1) * 128 + (block & 1) * 16;  // of i = 0
+    const int row0 = block * kRows;
+    if (lane == 0) {
+        for (int b = 0; b < kRing; ++b) mma::bar_init(&s_full[warp][b], 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (tid == 0) s_fail = 0;
+    const uint32_t s_x = smem_u32(s_ring) + ring_bytes<kR>();
+    if (tid < 16) reinterpret_cast<uint32_t*>(s_ring + ring_bytes<kR>() + kXBytes)[tid] = 0u;
+    __syncthreads();
     chain_wait();
     chain_release();
-    if (row0 >= a.N) return;  // the second half of a last tile
     int first = blockIdx.y * kTok, count = min(kTok, a.M - first), e = 0;
     if (a.ids) {
         // the rows of this expert from blockIdx.y on, in order
@@ -213,95 +260,157 @@ __global__ void __launch_bounds__(32 * kWarpsMv, 2) k_matvec4(const __grid_const
     }
     const int nsteps = (a.K + kStepK - 1) / kStepK;
     const int lo = nsteps * rank / S, hi = nsteps * (rank + 1) / S;
-    const uint8_t* codes = a.codes + (int64_t)e * a.N * (a.K / 2);
-    const uint8_t* scales = a.scales + (int64_t)e * a.scale_bytes +
-                            (int64_t)(row0 >> 7) * a.kt * lin::kSfTileBytes +
-                            16 * ((row0 & 31) + g);
-    // with the 2^7 that unpacked weights lack (exact, and in range: g <= FLT_MAX / 1536)
-    const float gb = fmul(fdiv(1.0f, global_scale(a.ep.b_amax[e], a.ep.six_bound)), 128.0f);
-    for (int c0 = 0; c0 < count; c0 += kTok) {
-        const int ntok = min(kTok, count - c0);
-        // this lane's column of the second operand: a row of x, or nothing
-        const int tok = XT == In::F32 ? g / 3 : g;
-        const bool live = tok < ntok;
-        int64_t xrow = 0;
-        if (live) xrow = (a.ids ? s_ids[c0 + tok] : first + c0 + tok) / a.rep;
-        float acc[4][4];
+    // this lane's scales: of rows g and g + 8 of row tile i, two bytes of tile t / 2 of a step
+    const uint8_t* scales[kR];
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < kR; ++i) {
+        const int r = row0 + 16 * i;
+        scales[i] = r < a.N ? a.scales + (int64_t)e * a.scale_bytes +
+                                  ((int64_t)(r >> 7) * a.kt + (t >> 1)) * lin::kSfTileBytes +
+                                  16 * ((r & 31) + g) + 4 * ((r >> 5) & 3) + 2 * (t & 1)
+                            : nullptr;
+    }
+    // the steps in which this lane's 32 elements lie below K
+    const int mine = min(hi, (a.K - 32 * t + kStepK - 1) / kStepK);
+    const uint32_t lane_at = smem_u32(s_ring) + warp * kRing * kSlot + g * kStepBytes + 16 * t;
+    uint32_t slot = 0, parity = 0;  // of the next step
+    bool bad = false;
+    const float gb = fdiv(1.0f, global_scale(a.ep.b_amax[e], a.ep.six_bound));
+    // step's codes into ring slot b
+    auto fetch = [&](int step, uint32_t b) {
+        if (lane == 0 && step < hi) {
+            mbar_expect_tx(&s_full[warp][b], kSlot);
+            tma_load_2d(s_ring + (warp * kRing + b) * kSlot, &a.codes, step * kStepBytes, e * a.N + row0,
+                        &s_full[warp][b]);
+        }
+    };
+    for (int c0 = 0; c0 < count; c0 += kTok) {
+        const int ntok = min(kTok, count - c0), cols = ntok * kPieces;
+        float acc[kR][4];
+#pragma unroll
+        for (int i = 0; i < kR; ++i)
 #pragma unroll
             for (int j = 0; j < 4; ++j) acc[i][j] = 0.0f;
-        for (int step = lo + warp; step < hi; step += kWarpsMv) {
-            const int k = step * kStepK + 32 * t;
-            const bool in = k < a.K;
-            uint4 c[4][2], sc[2];
-            const uint4 zero = make_uint4(0, 0, 0, 0);
+        uint32_t sc[kR][2];
+        auto load_scales = [&](int step) {
 #pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                sc[r] = in ? ld128(scales + (int64_t)(2 * step + (t >> 1)) * lin::kSfTileBytes + 128 * r)
-                           : zero;
+            for (int i = 0; i < kR; ++i)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int row = row0 + 32 * i + 8 * r + g;
-                    c[i][r] = in && row < a.N ? ld128(codes + ((int64_t)row * a.K + k) / 2) : zero;
-                }
-            }
-            Frag<XT> f;
-            if (in && live) {
-                load_x<XT>(f, a.x, xrow * a.K + k, g);
-            } else {
+                for (int r = 0; r < 2; ++r)
+                    sc[i][r] = step < mine && scales[i] ?
+                                   ld_u16(scales[i] + (int64_t)step * (2 * lin::kSfTileBytes) + 128 * r) : 0u;
+        };
+        {
+            uint32_t b = slot;
 #pragma unroll
-                for (int q = 0; q < 4; ++q)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) f.b[q][i] = 0u;
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                uint32_t s[2][2];  // row half, block
-#pragma unroll
-                for (int r = 0; r < 2; ++r) {
-                    const uint32_t word = i == 0 ? sc[r].x : i == 1 ? sc[r].y : i == 2 ? sc[r].z : sc[r].w;
-                    const uint32_t two = word >> (16 * (t & 1));
-                    s[r][0] = scale_pair<XT>(two & 0xFFu);
-                    s[r][1] = scale_pair<XT>((two >> 8) & 0xFFu);
-                }
-                const uint32_t w0[4] = {c[i][0].x, c[i][0].y, c[i][0].z, c[i][0].w};
-                const uint32_t w1[4] = {c[i][1].x, c[i][1].y, c[i][1].z, c[i][1].w};
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    uint32_t u[4], v[4];
-                    unpack<XT>(w0[q], s[0][q >> 1], u);
-                    unpack<XT>(w1[q], s[1][q >> 1], v);
-                    mma16<XT>(acc[i], u[0], v[0], u[1], v[1], f.b[q][0], f.b[q][1]);
-                    mma16<XT>(acc[i], u[2], v[2], u[3], v[3], f.b[q][2], f.b[q][3]);
-                }
+            for (int j = 0; j < kRing; ++j) {
+                fetch(lo + warp + j * kWarpsMv, b);
+                b = b + 1 == kRing ? 0 : b + 1;
             }
         }
-        // partial sums: column-major, 64 rows a column
-        float* mine = s_part[warp];
+        load_scales(lo + warp);
+        // x by as many steps at a time as its place in shared memory holds
+        const int seg = kXBytes / kXStep / cols / kWarpsMv * kWarpsMv;
+        const uint32_t col_bytes = (uint32_t)(seg * kXStep);
+        for (int s0 = lo; s0 < hi; s0 += seg) {
+            const int steps = min(seg, hi - s0);
+            // a quad of lanes a row and step; whole warps go round together
+            for (int u = warp * 8 + g; u < (ntok * steps + 7) / 8 * 8; u += kWarpsMv * 8) {
+                const int tk = min(u / steps, ntok - 1), st = min(u - tk * steps, steps - 1);
+                const int64_t p = a.ids ? s_ids[c0 + tk] : first + c0 + tk;
+                const int k = (s0 + st) * kStepK + 32 * t;
+                constexpr int kElt = XT == In::F32 ? 4 : 2;
+                const float down = put_x<XT>(static_cast<const char*>(a.x) + ((p / a.rep) * a.K + k) * kElt,
+                                             k < a.K, s_x + tk * kPieces * col_bytes + st * kXStep, col_bytes,
+                                             tk * kPieces, t);
+                if (XT != In::F16 && t == 0) s_down[tk * seg + st] = down;
+            }
+            __syncthreads();
+            // a column that is not there reads the step of zeros
+            const bool live = g < cols;
+            const uint32_t xs = live ? s_x + g * col_bytes : s_x + kXBytes;
+            for (int step = s0 + warp; step < s0 + steps; step += kWarpsMv) {
+                uint32_t two[kR][2];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            mine[(2 * t) * kLine + 16 * i + g] = acc[i][0];
-            mine[(2 * t + 1) * kLine + 16 * i + g] = acc[i][1];
-            mine[(2 * t) * kLine + 16 * i + 8 + g] = acc[i][2];
-            mine[(2 * t + 1) * kLine + 16 * i + 8 + g] = acc[i][3];
+                for (int i = 0; i < kR; ++i)
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) two[i][r] = sc[i][r];
+                load_scales(step + kWarpsMv);
+                uint4 f[4];
+                const uint32_t xa = live ? xs + (step - s0) * kXStep : xs;
+#pragma unroll
+                for (int q = 0; q < 4; ++q) f[q] = lds128(xa + (live ? x_piece(t, g, q) : 16 * q));
+                float d0 = 1.0f, d1 = 1.0f;  // of the two columns that this lane has products of
+                if constexpr (XT != In::F16) {
+                    d0 = s_down[min(2 * t / kPieces, ntok - 1) * seg + step - s0];
+                    d1 = s_down[min((2 * t + 1) / kPieces, ntok - 1) * seg + step - s0];
+                }
+                if (!lin::warp_wait(&s_full[warp][slot], parity)) bad = true;  // goes on: every copy is waited for
+                const uint32_t at = lane_at + slot * kSlot;
+#pragma unroll
+                for (int i = 0; i < kR; ++i) {
+                    const uint4 lo4 = lds128(at + 16 * i * kStepBytes), hi4 = lds128(at + (16 * i + 8) * kStepBytes);
+                    const uint32_t w0[4] = {lo4.x, lo4.y, lo4.z, lo4.w}, w1[4] = {hi4.x, hi4.y, hi4.z, hi4.w};
+                    const uint32_t p0 = scale_pair(two[i][0]), p1 = scale_pair(two[i][1]);
+                    float sum[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) sum[j] = XT == In::F16 ? acc[i][j] : 0.0f;
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        uint32_t u[4], v[4];
+                        unpack(w0[q], __byte_perm(p0, 0u, q < 2 ? 0x1010 : 0x3232), u);
+                        unpack(w1[q], __byte_perm(p1, 0u, q < 2 ? 0x1010 : 0x3232), v);
+                        mma16(sum, u[0], v[0], u[1], v[1], f[q].x, f[q].y);
+                        mma16(sum, u[2], v[2], u[3], v[3], f[q].z, f[q].w);
+                    }
+                    if constexpr (XT == In::F16) {
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) acc[i][j] = sum[j];
+                    } else {
+                        acc[i][0] = __fmaf_rn(sum[0], d0, acc[i][0]);
+                        acc[i][1] = __fmaf_rn(sum[1], d1, acc[i][1]);
+                        acc[i][2] = __fmaf_rn(sum[2], d0, acc[i][2]);
+                        acc[i][3] = __fmaf_rn(sum[3], d1, acc[i][3]);
+                    }
+                }
+                __syncwarp();  // every lane has its codes: the slot is free
+                fetch(step + kRing * kWarpsMv, slot);
+                if (++slot == kRing) {
+                    slot = 0;
+                    parity ^= 1u;
+                }
+            }
+            __syncthreads();  // this part of x has been read
+        }
+        if (bad) s_fail = 1;
+        // partial sums, column-major, over this warp's ring, whose copies have all been
+        // waited for
+        static_assert(kRing * kSlot >= 8 * kLine * 4, "partial sums");
+        float* part = reinterpret_cast<float*>(s_ring + warp * kRing * kSlot);
+#pragma unroll
+        for (int i = 0; i < kR; ++i) {
+            part[(2 * t) * kLine + 16 * i + g] = acc[i][0];
+            part[(2 * t + 1) * kLine + 16 * i + g] = acc[i][1];
+            part[(2 * t) * kLine + 16 * i + 8 + g] = acc[i][2];
+            part[(2 * t + 1) * kLine + 16 * i + 8 + g] = acc[i][3];
         }
         __syncthreads();
         for (int idx = tid; idx < ntok * kRows; idx += 32 * kWarpsMv) {
-            const int r = idx & (kRows - 1), tk = idx >> 6;
+            const int r = idx % kRows, tk = idx / kRows;
             float v = 0.0f;
 #pragma unroll
             for (int p = XT == In::F32 ? 2 : 0; p >= 0; --p) {  // the smallest piece first
                 const int at = (XT == In::F32 ? 3 * tk + p : tk) * kLine + r;
 #pragma unroll
-                for (int w = 0; w < kWarpsMv; ++w) v = fadd(v, s_part[w][at]);
+                for (int w = 0; w < kWarpsMv; ++w)
+                    v = fadd(v, reinterpret_cast<const float*>(s_ring + w * kRing * kSlot)[at]);
             }
-            s_sum[tk * kLine + r] = v;
+            s_sum[tk * kLine + r] = s_fail ? __int_as_float(0x7FC00000) : v;
         }
         lin::tile_sync(S);
         for (int idx = rank * 32 * kWarpsMv + tid; idx < ntok * kRows; idx += S * 32 * kWarpsMv) {
-            const int r = idx & (kRows - 1), tk = idx >> 6;
-            const int row = row0 + 32 * (r >> 4) + (r & 15);
+            const int r = idx % kRows, tk = idx / kRows;
+            const int row = row0 + r;
             float v = s_sum[tk * kLine + r];
             if (S > 1) {
                 v = 0.0f;
@@ -317,6 +426,7 @@ __global__ void __launch_bounds__(32 * kWarpsMv, 2) k_matvec4(const __grid_const
                 default: finish<Out::F32>(a.ep, v, n_at, at); break;
             }
         }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the ring is TMA's again
         lin::tile_sync(S);  // the sums have been read
     }
 }

@@ -652,7 +652,6 @@ fos_status fos_matvec4(const void* x, fos_dtype dt, int64_t x_rows, const int32_
     a.ep.six_bound = 6.0f * (float)cfg->e4m3_bound;
     a.x = x;
     a.ids = ids;
-    a.codes = b_codes;
     a.scales = b_scales_tiled;
     a.scale_bytes = tiled_bytes(N, K, 16);
     a.M = (int)M;
@@ -663,7 +662,7 @@ fos_status fos_matvec4(const void* x, fos_dtype dt, int64_t x_rows, const int32_
     a.kt = (int)((K + 63) / 64);
     const In o = in_of(static_cast<fos_dtype>(e->out_dt));
     a.out_dt = static_cast<int>(o == In::BF16 ? Out::BF16 : o == In::F16 ? Out::F16 : Out::F32);
-    return cuda_status(launch_matvec4(in_of(dt), a, stream_of(stream)));
+    return cuda_status(launch_matvec4(in_of(dt), a, b_codes, stream_of(stream)));
 }
 
 }  // extern "C"

@@ -46,7 +46,7 @@ cudaError_t launch_rms_bwd(In, NormBwdArgs, float* dw, float* part, int64_t max_
 cudaError_t launch_linear(const LinearCall&, cudaStream_t);
 cudaError_t launch_quant8(In, Act, const Quant8Args&, cudaStream_t);
 cudaError_t launch_quant8_grouped(In, Act, const GroupedQuant8Args&, float* sums, cudaStream_t);
-cudaError_t launch_matvec4(In, const MatvecArgs&, cudaStream_t);
+cudaError_t launch_matvec4(In, const MatvecArgs&, const uint8_t* codes, cudaStream_t);
 cudaError_t launch_grouped(const GroupedCall&, cudaStream_t);
 
 }  // namespace fos
