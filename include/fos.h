@@ -612,13 +612,13 @@ FOS_API fos_status fos_linear8_grouped_wgrad(const uint8_t* d_codes_t, const uin
  *   out[p] = act(x[p / (M / x_rows)] . b[e]^T + bias[e]) + residual[p],  e = ids[p]
  * x [x_rows, K] of dt; ids (device int32 [M]) or NULL (e = 0, G = 1); x_rows divides M:
  * the experts of one token stand next to one another, or every row has its own x.
- * b_codes [G, N, K/2], b_scales_tiled (scale bytes 0x00 .. 0x7E, as the quantizer writes
- * them) and b_amax [G] as in fos_linear4_grouped; cfg->granularity is not read.  epilogue
- * bias [G, N]; residual and out [M, N] (out may be in the residual's place); pre must be
- * NULL.  A row whose id is outside 0 .. G - 1 is left as it was.  Weights are decoded
- * exactly and products summed in fp32; an expert's weights are read once for up to eight
- * rows (two of fp32 x).  M <= FOS_MATVEC_MAX_ROWS; N % 16 == 0; K % 32 == 0, K > 0.
- * x, codes, scales and the epilogue's tensors 16-byte aligned.
+ * b_codes [G, N, K/2], b_scales_tiled and b_amax [G] as in fos_linear4_grouped;
+ * cfg->granularity is not read.  epilogue bias [G, N]; residual and out [M, N] (out may be
+ * in the residual's place); pre must be NULL.  A row whose id is outside 0 .. G - 1 is
+ * left as it was.  Weights are decoded exactly and products summed in fp32; an expert's
+ * weights are read once for up to eight rows (two of fp32 x).  M <= FOS_MATVEC_MAX_ROWS;
+ * G <= FOS_LINEAR_MAX_GROUPS; N % 16 == 0; K % 32 == 0, K > 0.  x, codes, scales and the
+ * epilogue's tensors 16-byte aligned.
  */
 #define FOS_MATVEC_MAX_ROWS 1024
 FOS_API fos_status fos_matvec4(const void* x, fos_dtype dt, int64_t x_rows, const int32_t* ids,

@@ -137,28 +137,6 @@ __device__ __forceinline__ void grouped_stage(uint32_t acc, uint32_t a0, uint32_
     }
 }
 
-// One value of the output's type as it is stored: a load that the stores of the
-// same thread may not overtake (out may be in the residual's place).
-template <Out OT>
-__device__ __forceinline__ uint32_t ld_raw(const void* p, int64_t i) {
-    uint32_t v;
-    if constexpr (OT == Out::F32)
-        asm volatile("ld.global.b32 %0, [%1];" : "=r"(v) : "l"(static_cast<const float*>(p) + i) : "memory");
-    else
-        asm volatile("{\n\t.reg .b16 h;\n\tld.global.b16 h, [%1];\n\tcvt.u32.u16 %0, h;\n\t}"
-                     : "=r"(v) : "l"(static_cast<const unsigned short*>(p) + i) : "memory");
-    return v;
-}
-template <Out OT>
-__device__ __forceinline__ float raw_value(uint32_t v) {
-    if constexpr (OT == Out::F32) return __uint_as_float(v);
-    else if constexpr (OT == Out::BF16) return __uint_as_float(v << 16);
-    else {
-        float f;
-        asm("{\n\t.reg .b16 h;\n\tcvt.u16.u32 h, %1;\n\tcvt.f32.f16 %0, h;\n\t}" : "=f"(f) : "r"(v));
-        return f;
-    }
-}
 // 32 values of a lane's column n to rows 0 .. of `p` (at row 0, column n) below `rows`.
 template <Out OT>
 __device__ __forceinline__ void store_column(void* p, int64_t N, const float (&v)[32], int rows) {
@@ -451,7 +429,8 @@ __global__ void __launch_bounds__(pair_threads<F>(), 1) k_grouped(const __grid_c
             float bias = 0.0f, gb = 1.0f, ga0 = 1.0f;
             if (a.ep.bias && in) {
                 const int64_t i = (int64_t)w.g * a.N + n;
-                bias = a.ep.bias32 ? static_cast<const float*>(a.ep.bias)[i] : load_out<OT>(a.ep.bias, i);
+                bias = a.ep.bias32 ? ld_f32(static_cast<const float*>(a.ep.bias) + i)
+                                   : raw_value<OT>(ld_raw<OT>(a.ep.bias, i));
             }
             uint32_t rs[32];
             auto fetch = [&](int c0) {  // the residual of tokens c0 .. c0 + 31
@@ -461,12 +440,12 @@ __global__ void __launch_bounds__(pair_threads<F>(), 1) k_grouped(const __grid_c
             };
             if (res) fetch(0);
             if constexpr (F::kGlobal) {
-                gb = fdiv(1.0f, global_scale(a.ep.b_amax[w.g], a.ep.six_bound));
+                gb = fdiv(1.0f, global_scale(ld_f32(a.ep.b_amax + w.g), a.ep.six_bound));
                 if (a.ep.a_row) {
                     for (int c = lane; c < w.live; c += 32)
-                        s_ga[e][c] = fdiv(1.0f, global_scale(a.ep.a_amax[w.t0 + c], a.ep.six_bound));
+                        s_ga[e][c] = fdiv(1.0f, global_scale(ld_f32(a.ep.a_amax + w.t0 + c), a.ep.six_bound));
                 } else {
-                    ga0 = fdiv(1.0f, global_scale(a.ep.a_amax[w.g], a.ep.six_bound));
+                    ga0 = fdiv(1.0f, global_scale(ld_f32(a.ep.a_amax + w.g), a.ep.six_bound));
                 }
             }
             const int ab = j & 1;

@@ -32,6 +32,34 @@ __device__ __forceinline__ int32_t ld_s32(const int32_t* p) {
     return v;
 }
 
+namespace lin {
+
+// One value of type OT as it is stored, by a load that stays where it is written: behind
+// the wait for the kernel before, and before the same thread's stores (out may be in the
+// residual's place).
+template <Out OT>
+__device__ __forceinline__ uint32_t ld_raw(const void* p, int64_t i) {
+    uint32_t v;
+    if constexpr (OT == Out::F32)
+        asm volatile("ld.global.b32 %0, [%1];" : "=r"(v) : "l"(static_cast<const float*>(p) + i) : "memory");
+    else
+        asm volatile("{\n\t.reg .b16 h;\n\tld.global.b16 h, [%1];\n\tcvt.u32.u16 %0, h;\n\t}"
+                     : "=r"(v) : "l"(static_cast<const unsigned short*>(p) + i) : "memory");
+    return v;
+}
+template <Out OT>
+__device__ __forceinline__ float raw_value(uint32_t v) {
+    if constexpr (OT == Out::F32) return __uint_as_float(v);
+    else if constexpr (OT == Out::BF16) return __uint_as_float(v << 16);
+    else {
+        float f;
+        asm("{\n\t.reg .b16 h;\n\tcvt.u16.u32 h, %1;\n\tcvt.f32.f16 %0, h;\n\t}" : "=f"(f) : "r"(v));
+        return f;
+    }
+}
+
+}  // namespace lin
+
 // The table by one converged warp; lane l takes ceil(G / 32) neighbouring groups.
 template <int kUnit>
 __device__ __forceinline__ void group_table(Group* t, const int32_t* offs, int G, int32_t rows,

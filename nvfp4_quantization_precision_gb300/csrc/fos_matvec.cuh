@@ -7,28 +7,30 @@
 // sum.  Bound by the weights' bytes (9/16 byte an element), close behind by the
 // instructions that unpack them.
 //
-// A weight w is exact in bf16 and in fp16 (two significant bits times four, 2^-10
-// to 2688), so the sums are formed by mma.m16n8k16 with weights as the 16 rows,
-// rows of x as the 8 columns and fp32 accumulators: one instruction for 2048
-// products, whose cost in the tensor cores does not show beside the unpacking.
-// tcgen05 would take its operands through shared or tensor memory, two more moves
-// of every unpacked weight, for tiles of 128 rows that eight columns never fill.
-//   unpack   the magnitude bits eem of a code, moved to the exponent's low bits and
-//            the mantissa's top bit, are 2^-126 (bf16) or 2^-14 (fp16) times its
-//            value, subnormal for 0.5; nibbles i and i + 4 of a word make a pair by
-//            one shift each for sign and magnitude.  An E4M3 byte moved likewise is
-//            2^-120 or 2^-8 times its value.  The scale is brought to 2^119 (2^7),
-//            so that code times scale is 2^-7 w, a normal bf16 (an fp16 multiple of
-//            2^-17), exactly.
+// A weight w is exact in fp16 (two significant bits times four, 2^-10 to 2688), so the
+// sums are formed by mma.m16n8k16 with weights as the 16 rows, rows of x as the 8
+// columns and fp32 accumulators.  tcgen05 would take its operands through shared or
+// tensor memory, two more moves of every unpacked weight, for tiles of 128 rows that
+// eight columns never fill.
+//   unpack   two weights by one conversion from E2M1, times the pair's scale: 16.4 cycles
+//            of an SM's quarter for the 256 weights of a warp's word, 10.4 of them the MMA's (by
+//            masks and shifts 28.3, whose ALU takes 2 cycles an instruction: 16.8 us
+//            instead of 11.7 for one row x 14336 x 4096).
 //   order    a lane takes 32 elements of a row (16 bytes) and gives them to eight
 //            MMAs, four a time: any order of k serves as long as x has the same.
-//   x fp32   is split into three bf16 of 8 significant bits each (exactly: by
-//            truncation), which take three columns; two rows at a time.
+//   x        is brought to fp16 in shared memory once a CTA (put_x below): bf16 times a power
+//            of two, fp32 in three pieces of 11 significant bits, which take three
+//            columns, two rows at a time.
 // A CTA takes 16 kR weight rows, kR of 1 .. 4 chosen so that the CTAs fill the device
 // evenly.  Its eight warps split K by steps of 128, each with a ring of its own of
 // kRing steps' codes, filled by TMA (zeros past K), and with few CTAs the CTAs of a
 // cluster split K too; partial sums are added in one fixed order, warps first.
-// Measured, GPU time in a graph: TOKENUS
+// Measured, GPU time in a graph: one row x 14336 x 4096 (33 MB) 11.7 us, 2.8 TB/s, of
+// which about 4 us are the launch, x's way to shared memory and the sums; eight rows of
+// six experts x 4096 x 14336 (198 MB) 49 us, 4.0 TB/s.  Issue slots are half busy: waits
+// for a result's latency with four warps a scheduler.  Measured and not kept: shares of
+// row tiles walked by as many CTAs as fit, the ring running ahead over their ends, 54 us;
+// 256 elements a step 68.
 // With ids, grid row p handles the rows of expert ids[p] at once if p is the first
 // of them (the weights are read once), else nothing.
 #pragma once
@@ -201,11 +203,11 @@ __device__ __forceinline__ float ld_cluster(const float* p, int rank) {
 template <Out OT>
 __device__ __forceinline__ void finish(const Epilogue& ep, float v, int64_t n_at, int64_t at) {
     if (ep.bias)
-        v = fadd(v, ep.bias32 ? static_cast<const float*>(ep.bias)[n_at]
-                              : lin::load_out<OT>(ep.bias, n_at));
+        v = fadd(v, ep.bias32 ? ld_f32(static_cast<const float*>(ep.bias) + n_at)
+                              : lin::raw_value<OT>(lin::ld_raw<OT>(ep.bias, n_at)));
     float a[1] = {v};
     lin::act_apply<OT>(ep.act, a);
-    if (ep.residual) a[0] = fadd(a[0], lin::load_out<OT>(ep.residual, at));
+    if (ep.residual) a[0] = fadd(a[0], lin::raw_value<OT>(lin::ld_raw<OT>(ep.residual, at)));
     lin::store_out<OT>(ep.out, at, a[0]);
 }
 
@@ -275,7 +277,7 @@ __global__ void __launch_bounds__(32 * kWarpsMv, 2) k_matvec4(const __grid_const
     const uint32_t lane_at = smem_u32(s_ring) + warp * kRing * kSlot + g * kStepBytes + 16 * t;
     uint32_t slot = 0, parity = 0;  // of the next step
     bool bad = false;
-    const float gb = fdiv(1.0f, global_scale(a.ep.b_amax[e], a.ep.six_bound));
+    const float gb = fdiv(1.0f, global_scale(ld_f32(a.ep.b_amax + e), a.ep.six_bound));
     // step's codes into ring slot b
     auto fetch = [&](int step, uint32_t b) {
         if (lane == 0 && step < hi) {
@@ -367,10 +369,11 @@ __global__ void __launch_bounds__(32 * kWarpsMv, 2) k_matvec4(const __grid_const
 #pragma unroll
                         for (int j = 0; j < 4; ++j) acc[i][j] = sum[j];
                     } else {
-                        acc[i][0] = __fmaf_rn(sum[0], d0, acc[i][0]);
-                        acc[i][1] = __fmaf_rn(sum[1], d1, acc[i][1]);
-                        acc[i][2] = __fmaf_rn(sum[2], d0, acc[i][2]);
-                        acc[i][3] = __fmaf_rn(sum[3], d1, acc[i][3]);
+                        // the decode scale first: the result's range, not the codes', bounds x
+                        acc[i][0] = __fmaf_rn(fmul(sum[0], gb), d0, acc[i][0]);
+                        acc[i][1] = __fmaf_rn(fmul(sum[1], gb), d1, acc[i][1]);
+                        acc[i][2] = __fmaf_rn(fmul(sum[2], gb), d0, acc[i][2]);
+                        acc[i][3] = __fmaf_rn(fmul(sum[3], gb), d1, acc[i][3]);
                     }
                 }
                 __syncwarp();  // every lane has its codes: the slot is free
@@ -417,7 +420,7 @@ __global__ void __launch_bounds__(32 * kWarpsMv, 2) k_matvec4(const __grid_const
                 for (int k = 0; k < S; ++k) v = fadd(v, ld_cluster(s_sum + tk * kLine + r, k));
             }
             if (row >= a.N) continue;
-            v = fmul(v, gb);
+            if (XT == In::F16) v = fmul(v, gb);
             const int64_t p = a.ids ? s_ids[c0 + tk] : first + c0 + tk;
             const int64_t at = p * a.N + row, n_at = (int64_t)e * a.N + row;
             switch (static_cast<Out>(a.out_dt)) {

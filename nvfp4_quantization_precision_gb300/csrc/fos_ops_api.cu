@@ -627,8 +627,8 @@ fos_status fos_matvec4(const void* x, fos_dtype dt, int64_t x_rows, const int32_
     if (cfg->block != FOS_BLOCK_1X16 || (cfg->e4m3_bound != 448 && cfg->e4m3_bound != 256) ||
         epilogue->pre)
         return FOS_ERR_UNSUPPORTED;
-    if (N % 16 || K % 32 || K == 0 || M > FOS_MATVEC_MAX_ROWS || N >= kMostRows || K >= kMostRows ||
-        G * N > INT64_C(0x7FFFFFFF) || !within(G, N, K))
+    if (N % 16 || K % 32 || K == 0 || M > FOS_MATVEC_MAX_ROWS || G > kMaxGroups || N >= kMostRows || K >= kMostRows ||
+        G * N > INT64_C(0x7FFFFFFF) || M * ((N + 15) / 16) > INT64_C(0x7FFFFFFF) || !within(G, N, K))
         return FOS_ERR_UNSUPPORTED;
     if (M == 0 || N == 0) return FOS_OK;
     if (x_rows < 1 || M % x_rows || !x || !b_codes || !b_scales_tiled || !b_amax || !out)

@@ -34,7 +34,11 @@ cudaError_t go(MatvecArgs a, const uint8_t* codes, int groups, cudaStream_t s) {
 
 // Row tiles of a CTA and CTAs of a cluster: the pair with the least time, in row
 // tiles times steps of a warp, of all CTAs over the device's places (two an SM) and
-// half of a last one; what a CTA does once takes as long as two of them.
+// half of a last one; what a CTA does once takes as long as eight, its cluster's sums
+// as two more.  Measured (us; this pair, the best of 14 others): 4096 x 14336 1 row
+// 11.8 (two tiles, two CTAs), 11.9; 14336 x 4096 8 rows 15.0 (three, one), 15.1;
+// eight experts 2048 x 7168 18.7 (four, one), 18.7; six of eight 4096 x 14336 49.6 (four,
+// one), 48.4 (three, one).
 template <In XT>
 cudaError_t by_shape(MatvecArgs a, const uint8_t* codes, cudaStream_t s) {
     const int groups = a.ids ? a.M : (a.M + tokens<XT>() - 1) / tokens<XT>();
@@ -48,7 +52,7 @@ cudaError_t by_shape(MatvecArgs a, const uint8_t* codes, cudaStream_t s) {
         const int steps = ((nsteps + S - 1) / S + kWarpsMv - 1) / kWarpsMv;
         for (int r = 1; r <= 4; ++r) {
             const int64_t ctas = (a.N + 16 * r - 1) / (16 * r) * S * distinct;
-            const double one = (r + 0.3) * steps + 2.0 + (S > 1 ? 0.5 : 0.0);
+            const double one = (r + 0.3) * steps + 8.0 + (S > 1 ? 1.9 : 0.0);
             const double cost = ctas <= slots ? one : one * ((double)ctas / (double)slots + 0.5);
             if (cost < least) {
                 least = cost;
