@@ -713,3 +713,19 @@ def test_refusals():
     with pytest.raises(fos.FosError) as e:  # ids no multiple of the rows of x
         fos.matvec4(x[:2], m.unsqueeze(0), sm.unsqueeze(0), am, ids=_offs([0, 0, 0]))
     assert e.value.status == fos.FOS_ERR_INVALID_ARG
+
+
+def test_moe_block_example():
+    """The example's training step, served batch and served tokens: results of quantized
+    operands lie within a few hundredths (8 bit), two or three tenths (NVFP4 on both sides),
+    a tenth and a half (NVFP4 weights) of the unquantized block's."""
+    import importlib.util
+    import os
+    p = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "moe_block.py")
+    spec = importlib.util.spec_from_file_location("moe_block", p)
+    m = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(m)
+    for tokens, experts, act in ((77, 4, "silu"), (5, 16, "gelu")):
+        err = m.run(tokens, 256, 384, experts, act=act)
+        for k, v in err.items():
+            assert v < (0.3 if "batch" in k else 0.2 if "tokens" in k else 0.1), (k, v)
