@@ -9,13 +9,6 @@ namespace lin {
 
 namespace {
 
-// Tile rows of a band: their rows of the operand that stays in L2 take at most 30 MB, a
-// quarter of it (pair_go()).
-int band_rows(int64_t tile_bytes) {
-    const int64_t fit = 30000000 / tile_bytes;
-    return (int)(fit < 1 ? 1 : fit > 4096 ? 4096 : fit);
-}
-
 template <class Kernel, class Args>
 cudaError_t launch_pairs(Kernel k, int threads, int64_t tiles, int smem, const Args& a, cudaStream_t s) {
     const cudaError_t e = allow_smem(reinterpret_cast<const void*>(k), (size_t)kSmemLimit - 4096);
@@ -51,7 +44,9 @@ cudaError_t go(const GroupedCall& c, cudaStream_t s) {
     a.rows = (int)c.rows;
     a.N = (int)c.N;
     a.tiles_n = (int)((c.N + kPairM - 1) / kPairM);
-    a.band = band_rows(kTokTile * row_bytes);
+    // Token tiles of a band: their rows take at most 30 MB, a quarter of L2 (pair_go()).
+    const int64_t fit = 30000000 / (kTokTile * row_bytes);
+    a.band = (int)(fit < 1 ? 1 : fit > 4096 ? 4096 : fit);
     // 4 KB for the kernel's own shared memory and 1 KB to align the stages
     constexpr int kFixed = 4096 + 1024 + grp_slots<F>() * kGrpSfBytes;
     static_assert((kSmemLimit - kFixed - (int)group_table_bytes(kMaxGroups)) / kPairStageBytes >= kSfBufs, "stages");
@@ -82,7 +77,10 @@ cudaError_t go_wgrad(const GroupedCall& c, cudaStream_t s) {
     a.N = (int)c.N;
     a.tiles_m = (int)((c.M + kPairM - 1) / kPairM);
     a.tiles_n = (int)((c.N + kPairN - 1) / kPairN);
-    a.band = band_rows(kPairM * (c.K / c.G + 1));  // a group's share of the columns
+    // Four tile rows: a group's columns are few, so both operands stay in L2 in any
+    // order, and out is written in pieces of rows that lie close (8 x 14336 x 4096 fp32 of
+    // 8192 tokens: 438 us; 1 row 449, 8 rows 438 .. 455, all of them 477).
+    a.band = 4;
     constexpr int kOther = 8 * kChunkBytes + sf_slots<F8>() * kSfChunkBytes;
     static_assert((kSmemLimit - 4096 - 1024 - kOther - (int)group_table_bytes(kMaxGroups)) / kPairStageBytes >=
                       kSfBufs, "stages");
