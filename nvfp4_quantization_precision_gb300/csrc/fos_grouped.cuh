@@ -48,7 +48,9 @@ static_assert(kPairABytes == 128 * kRowBytes && kPairBBytes == 96 * kRowBytes, "
 //              as they are
 //   epilogue   a lane has one weight row: its 32 neighbours' results of a token are 64
 //              or 128 contiguous bytes of out, stored (and the residual loaded) as
-//              they are, without a way through shared memory
+//              they are, without a way through shared memory; by eight warps, two a
+//              quadrant, which take every other 16 tokens (1003 tokens x
+//              1040 x 640 with everything, one tile a pair: 13.1 us with four, 12.2 with eight)
 
 constexpr int kTokTile = 192;                    // tokens of a tile
 constexpr int kTokStep = 32;                     // an MMA's columns come in steps of these
@@ -59,6 +61,10 @@ constexpr int kGrpSfBytes = kSfChunkA + kTokSfBytes;
 // the groups of scale warps while they wait for a buffer in tensor memory, and the
 // others have to cover the copies' latency.
 template <class F> constexpr int grp_slots() { return F::kGlobal ? 8 : 3; }
+
+// Four more warps than k_linear_pair: the second half of the epilogue.
+template <class F> constexpr int grouped_threads() { return pair_threads<F>() + 128; }
+constexpr int kEpiTok = 16;                      // tokens of a chunk of the epilogue
 
 struct __align__(8) GroupedShared {
     uint64_t full[kPairMaxStages], empty[kPairMaxStages], acc_full[2], acc_empty[2], done;
@@ -137,16 +143,24 @@ __device__ __forceinline__ void grouped_stage(uint32_t acc, uint32_t a0, uint32_
     }
 }
 
-// 32 values of a lane's column n to rows 0 .. of `p` (at row 0, column n) below `rows`.
+__device__ __forceinline__ void prefetch_line(const void* p) {
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
+}
+__device__ __forceinline__ void prefetch_chunk(const CUtensorMap* map, int32_t x, int32_t y) {
+    asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y) : "memory");
+}
+
+// Values of a lane's column n to rows 0 .. of `p` (at row 0, column n) below `rows`.
 template <Out OT>
-__device__ __forceinline__ void store_column(void* p, int64_t N, const float (&v)[32], int rows) {
+__device__ __forceinline__ void store_column(void* p, int64_t N, const float (&v)[kEpiTok], int rows) {
     if constexpr (OT == Out::F32) {
 #pragma unroll
-        for (int i = 0; i < 32; ++i)
+        for (int i = 0; i < kEpiTok; ++i)
             if (i < rows) st32(static_cast<float*>(p) + i * N, __float_as_uint(v[i]));
     } else {
 #pragma unroll
-        for (int i = 0; i < 32; i += 2) {
+        for (int i = 0; i < kEpiTok; i += 2) {
             const uint32_t w = out_pair<OT>(pk(v[i], v[i + 1]));
             if (i < rows) st16(static_cast<unsigned short*>(p) + i * N, w);
             if (i + 1 < rows) st16(static_cast<unsigned short*>(p) + (i + 1) * N, w >> 16);
@@ -155,10 +169,10 @@ __device__ __forceinline__ void store_column(void* p, int64_t N, const float (&v
 }
 
 template <class F, Out OT>
-__global__ void __launch_bounds__(pair_threads<F>(), 1) k_grouped(const __grid_constant__ GroupedArgs a) {
+__global__ void __launch_bounds__(grouped_threads<F>(), 1) k_grouped(const __grid_constant__ GroupedArgs a) {
     extern __shared__ __align__(1024) unsigned char s_raw[];
     __shared__ GroupedShared sh;
-    __shared__ __align__(16) float s_ga[F::kGlobal ? 4 : 1][kTokTile];  // the tokens' decode scales
+    __shared__ __align__(16) float s_ga[F::kGlobal ? 8 : 1][kTokTile];  // the tokens' decode scales
     unsigned char* base = s_raw + ((1024u - (smem_u32(s_raw) & 1023u)) & 1023u);
     const int ns = a.stages;
     constexpr int kSfSlots = grp_slots<F>();
@@ -177,7 +191,7 @@ __global__ void __launch_bounds__(pair_threads<F>(), 1) k_grouped(const __grid_c
         }
         for (int b = 0; b < 2; ++b) {
             bar_init(&sh.acc_full[b], 1);
-            bar_init(&sh.acc_empty[b], 8);
+            bar_init(&sh.acc_empty[b], 16);
         }
         for (int b = 0; b < kSfSlots; ++b) {
             bar_init(&sh.sf_full[b], a.ts_wide ? 1 : 33);  // TMA's, and each lane's of warp 10
@@ -349,7 +363,7 @@ __global__ void __launch_bounds__(pair_threads<F>(), 1) k_grouped(const __grid_c
             }
             if (!warp_wait(&sh.sf_empty[sl], p)) bad = true;
         }
-    } else if (warp < 6 || warp > 10) {
+    } else if (warp < 6 || (sf_groups<F>() == 2 && warp > 10 && warp < 15)) {
         // scales: lane l of quadrant q writes the weights' (rows l, 32 + l, .. in the words
         // of tile kk) to columns 4 kk ..., the tokens' (token 32 i + l, tiles in the words)
         // to columns 16 + 6 kk ...
@@ -416,7 +430,8 @@ __global__ void __launch_bounds__(pair_threads<F>(), 1) k_grouped(const __grid_c
             }
         }
     } else {
-        const int q = warp & 3, e = warp - 6;
+        // quadrant, and which of the two warps of it
+        const int q = warp & 3, half = warp < 10 ? 0 : 1, e = 4 * half + q;
         const bool pre = a.ep.pre != nullptr, res = a.ep.residual != nullptr;
         int j = 0;
         for (int t = first; t < tiles; t += step, ++j) {
@@ -432,13 +447,20 @@ __global__ void __launch_bounds__(pair_threads<F>(), 1) k_grouped(const __grid_c
                 bias = a.ep.bias32 ? ld_f32(static_cast<const float*>(a.ep.bias) + i)
                                    : raw_value<OT>(ld_raw<OT>(a.ep.bias, i));
             }
-            uint32_t rs[32];
-            auto fetch = [&](int c0) {  // the residual of tokens c0 .. c0 + 31
+            uint32_t rs[kEpiTok];
+            auto fetch = [&](int c0) {  // the residual of a chunk
 #pragma unroll
-                for (int i = 0; i < 32; ++i)
+                for (int i = 0; i < kEpiTok; ++i)
                     if (c0 + i < live) rs[i] = ld_raw<OT>(a.ep.residual, at + (int64_t)(c0 + i) * a.N);
             };
-            if (res) fetch(0);
+            if (res) {
+                // all of it on its way to L2: a chunk's loads are asked for one chunk ahead only
+                for (int c = lane + 32 * half; c < w.live; c += 64)
+                    if (w.n0 + 128 * rank + 32 * q < a.N)
+                        prefetch_line(static_cast<const char*>(a.ep.residual) +
+                                      (at - lane + (int64_t)c * a.N) * (OT == Out::F32 ? 4 : 2));
+                fetch(kEpiTok * half);
+            }
             if constexpr (F::kGlobal) {
                 gb = fdiv(1.0f, global_scale(ld_f32(a.ep.b_amax + w.g), a.ep.six_bound));
                 if (a.ep.a_row) {
@@ -452,21 +474,21 @@ __global__ void __launch_bounds__(pair_threads<F>(), 1) k_grouped(const __grid_c
             if (!bad && !warp_wait<Sync::TENSOR>(&sh.acc_full[ab], (uint32_t)(j >> 1) & 1)) bad = true;
             __syncwarp();
             tc_fence_after();
-            for (int c0 = 0; c0 < w.cols; c0 += 32) {
-                uint32_t u[32];
-                tmem_ld32(tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(ab * kTokTile + c0), u);
-                if (c0 + 32 == w.cols) {  // this warp has read the accumulator
+            for (int c0 = kEpiTok * half; c0 < w.cols; c0 += 2 * kEpiTok) {
+                uint32_t u[kEpiTok];
+                tmem_ld16(tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(ab * kTokTile + c0), u);
+                if (c0 + 2 * kEpiTok >= w.cols) {  // this warp has read the accumulator
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) cluster_arrive(map_rank(smem_u32(&sh.acc_empty[ab]), 0));
                 }
-                float v[32];
+                float v[kEpiTok];
 #pragma unroll
-                for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(u[i]);
+                for (int i = 0; i < kEpiTok; ++i) v[i] = __uint_as_float(u[i]);
                 if constexpr (F::kGlobal) {
                     if (a.ep.a_row) {
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) {
+                        for (int i = 0; i < kEpiTok / 4; ++i) {
                             const float4 ga = *reinterpret_cast<const float4*>(&s_ga[e][c0 + 4 * i]);
                             v[4 * i] = fmul(fmul(v[4 * i], ga.x), gb);
                             v[4 * i + 1] = fmul(fmul(v[4 * i + 1], ga.y), gb);
@@ -475,12 +497,12 @@ __global__ void __launch_bounds__(pair_threads<F>(), 1) k_grouped(const __grid_c
                         }
                     } else {
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) v[i] = fmul(fmul(v[i], ga0), gb);
+                        for (int i = 0; i < kEpiTok; ++i) v[i] = fmul(fmul(v[i], ga0), gb);
                     }
                 }
                 if (a.ep.bias) {
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) v[i] = fadd(v[i], bias);
+                    for (int i = 0; i < kEpiTok; ++i) v[i] = fadd(v[i], bias);
                 }
                 constexpr int kElt = OT == Out::F32 ? 4 : 2;
                 const int64_t to = (at + (int64_t)c0 * a.N) * kElt;
@@ -488,8 +510,8 @@ __global__ void __launch_bounds__(pair_threads<F>(), 1) k_grouped(const __grid_c
                 act_apply<OT>(a.ep.act, v);
                 if (res) {
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) v[i] = fadd(v[i], raw_value<OT>(rs[i]));
-                    fetch(c0 + 32);
+                    for (int i = 0; i < kEpiTok; ++i) v[i] = fadd(v[i], raw_value<OT>(rs[i]));
+                    fetch(c0 + 2 * kEpiTok);
                 }
                 store_column<OT>(static_cast<char*>(a.ep.out) + to, a.N, v, live - c0);
             }
@@ -834,6 +856,15 @@ __global__ void __launch_bounds__(pair_threads<F8>(), 1) k_grouped_wgrad(const _
                 tma_load_2d(bufs + (c & 1) * kChunkBytes, &a.tres, w.n0 + k * kCols, orow, bar);
             };
             if (res && live > 0 && lane == 0) fetch(0);
+            if (res && t + step < tiles && lane < kChunks) {
+                // the next tile's residual on its way to L2: a chunk is asked for one chunk
+                // ahead only
+                WgradTile x = w;
+                wgrad_tile(a, groups, t + step, x);
+                const int32_t row = x.m0 + 128 * rank + 32 * q;
+                if (row < x.m_end && x.n0 + lane * kCols < a.N)
+                    prefetch_chunk(&a.tres, x.n0 + lane * kCols, x.out_row + row);
+            }
             const bool sum = w.nkb > 0;  // there is a product
             const int ab = j & 1;
             if (sum) {

@@ -9,9 +9,10 @@ namespace lin {
 
 namespace {
 
+// `own`: bytes left for the kernel's static shared memory.
 template <class Kernel, class Args>
-cudaError_t launch_pairs(Kernel k, int threads, int64_t tiles, int smem, const Args& a, cudaStream_t s) {
-    const cudaError_t e = allow_smem(reinterpret_cast<const void*>(k), (size_t)kSmemLimit - 4096);
+cudaError_t launch_pairs(Kernel k, int own, int threads, int64_t tiles, int smem, const Args& a, cudaStream_t s) {
+    const cudaError_t e = allow_smem(reinterpret_cast<const void*>(k), (size_t)(kSmemLimit - own));
     if (e != cudaSuccess) return e;
     int64_t clusters = resident_clusters(k, threads, smem, 2);
     if (clusters > tiles) clusters = tiles;
@@ -47,14 +48,14 @@ cudaError_t go(const GroupedCall& c, cudaStream_t s) {
     // Token tiles of a band: their rows take at most 30 MB, a quarter of L2 (pair_go()).
     const int64_t fit = 30000000 / (kTokTile * row_bytes);
     a.band = (int)(fit < 1 ? 1 : fit > 4096 ? 4096 : fit);
-    // 4 KB for the kernel's own shared memory and 1 KB to align the stages
-    constexpr int kFixed = 4096 + 1024 + grp_slots<F>() * kGrpSfBytes;
+    constexpr int kOwn = 8192;
+    constexpr int kFixed = kOwn + 1024 + grp_slots<F>() * kGrpSfBytes;
     static_assert((kSmemLimit - kFixed - (int)group_table_bytes(kMaxGroups)) / kPairStageBytes >= kSfBufs, "stages");
     const int table = (int)group_table_bytes(c.G);
     a.stages = (kSmemLimit - kFixed - table) / kPairStageBytes;
     if (a.stages > kPairMaxStages) a.stages = kPairMaxStages;
     const int smem = a.stages * kPairStageBytes + grp_slots<F>() * kGrpSfBytes + table + 1024;
-    return launch_pairs(k_grouped<F, OT>, pair_threads<F>(), group_tiles_max(c.rows, c.G, kTokTile) * a.tiles_n,
+    return launch_pairs(k_grouped<F, OT>, kOwn, grouped_threads<F>(), group_tiles_max(c.rows, c.G, kTokTile) * a.tiles_n,
                         smem, a, s);
 }
 
@@ -81,14 +82,15 @@ cudaError_t go_wgrad(const GroupedCall& c, cudaStream_t s) {
     // order, and out is written in pieces of rows that lie close (8 x 14336 x 4096 fp32 of
     // 8192 tokens: 438 us; 1 row 449, 8 rows 438 .. 455, all of them 477).
     a.band = 4;
+    constexpr int kOwn = 2048;
     constexpr int kOther = 8 * kChunkBytes + sf_slots<F8>() * kSfChunkBytes;
-    static_assert((kSmemLimit - 4096 - 1024 - kOther - (int)group_table_bytes(kMaxGroups)) / kPairStageBytes >=
+    static_assert((kSmemLimit - kOwn - 1024 - kOther - (int)group_table_bytes(kMaxGroups)) / kPairStageBytes >=
                       kSfBufs, "stages");
     const int table = (int)group_table_bytes(c.G);
-    a.stages = (kSmemLimit - 4096 - 1024 - kOther - table) / kPairStageBytes;
+    a.stages = (kSmemLimit - kOwn - 1024 - kOther - table) / kPairStageBytes;
     if (a.stages > kPairMaxStages) a.stages = kPairMaxStages;
     const int smem = a.stages * kPairStageBytes + kOther + table + 1024;
-    return launch_pairs(k_grouped_wgrad<OT>, pair_threads<F8>(), (int64_t)c.G * a.tiles_m * a.tiles_n, smem, a, s);
+    return launch_pairs(k_grouped_wgrad<OT>, kOwn, pair_threads<F8>(), (int64_t)c.G * a.tiles_m * a.tiles_n, smem, a, s);
 }
 
 template <class F>
