@@ -111,7 +111,6 @@ __device__ __forceinline__ uint32_t ld_u16(const void* p) {
     asm volatile("{\n\t.reg .b16 h;\n\tld.global.nc.b16 h, [%1];\n\tcvt.u32.u16 %0, h;\n\t}" : "=r"(v) : "l"(p));
     return v;
 }
-// Ordered before what follows: the ring's slot is filled again behind its last load.
 __device__ __forceinline__ uint4 lds128(uint32_t addr) {
     uint4 v;
     asm volatile("ld.volatile.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
@@ -376,7 +375,10 @@ __global__ void __launch_bounds__(32 * kWarpsMv, 2) k_matvec4(const __grid_const
                         acc[i][3] = __fmaf_rn(fmul(sum[3], gb), d1, acc[i][3]);
                     }
                 }
-                __syncwarp();  // every lane has its codes: the slot is free
+                // every lane has its codes: the slot is free (without the fence a copy issued
+                // right behind the loads was seen to overtake them)
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                __syncwarp();
                 fetch(step + kRing * kWarpsMv, slot);
                 if (++slot == kRing) {
                     slot = 0;

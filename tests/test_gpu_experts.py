@@ -677,6 +677,16 @@ def test_matvec_repeats_streams_graphs():
         assert torch.equal(out, fos.matvec4(x, *b, ids=_offs(r)))
 
 
+@pytest.mark.parametrize("M,N,K", [(1, 14336, 4096), (2, 4096, 14336), (8, 2048, 7168)])
+def test_matvec_many_calls_one_answer(M, N, K):
+    """The rings of codes are filled again while their warps work: every repeat equals the first."""
+    c, s, a = fos.quantize(_rand(N, K, seed=1).to(BF16), fos.Config(scale_tiled=True))
+    x = _rand(M, K, seed=2).to(BF16)
+    one = fos.matvec4(x, c, s, a, out_dtype=F32)
+    outs = [fos.matvec4(x, c, s, a, out_dtype=F32) for _ in range(60)]
+    assert all(torch.equal(one, o) for o in outs)
+
+
 # ------------------------------------------------------------------ refusals
 def test_refusals():
     w, _ = _weights(8, _rand(2, 64, 128, seed=1))
