@@ -575,7 +575,7 @@ FOS_API fos_status fos_linear4_grouped(const uint8_t* a_codes, const uint8_t* a_
  * p_0 = 0, p_{e+1} = p_e + 128 ceil(n_e / 128), with zeros up to p_{e+1}, so that each
  * expert's part is an operand by itself; codes_t [cols, P], scales_t the tiled scales
  * of a [cols, P] tensor.  What they hold past the last expert's part is left as it
- * was.  dbias [G, cols] fp32: the sum of each expert's rows (0 for an empty one); it
+ * was (but the padding of scales_t's rows to 128, zeros everywhere).  dbias [G, cols] fp32: the sum of each expert's rows (0 for an empty one); it
  * needs fos_act_backward_grouped_workspace_bytes(rows, cols, G) bytes of workspace.
  * fos_grouped_cols returns -1 for negative rows or a G out of range.
  */
