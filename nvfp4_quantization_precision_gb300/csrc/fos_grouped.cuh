@@ -546,9 +546,12 @@ __global__ void __launch_bounds__(grouped_threads<F>(), 1) k_grouped(const __gri
 // With a thousand tokens an expert a tile has eight or nine stages, and 96 KB of fp32 an
 // SM leave for every 250 KB that come.  8 x 14336 x 4096 of 8192 tokens 438 us, 323 of
 // them without the stores and 307 without the chunks either; operands and stores
-// together are 15 TB/s through L2.  Measured and not kept: four chunk buffers and four
-// stages, 516 us; rows stored from registers by whole sectors with seven stages, 520;
+// together are 15 TB/s through L2.  Measured and not kept: more chunk buffers and fewer
+// stages, 490 .. 516 us; rows stored from registers by whole sectors with seven stages, 520;
 // L2 priorities for the stores and the operands, 438.
+// With a residual a warp has four chunks and fetches three ahead, over the ends of tiles
+// (one chunk ahead in two: 8 x 14336 x 4096 950 us, 64 x 2048 x 1408 of 4096 tokens 342;
+// two ahead in three 724, 263; three ahead in four 650, 232, 6.4 TB/s).
 struct WgradArgs {
     CUtensorMap ta;    // a codes, box 128 bytes x 128 rows
     CUtensorMap tb;    // b codes, box 128 bytes x 96 rows
@@ -607,18 +610,23 @@ __device__ __forceinline__ void copy_rows(uint32_t buf, void* dst, int64_t row, 
     }
 }
 
-template <Out OT>
+// Chunks of a warp of the epilogue in shared memory.
+template <bool kRes> constexpr int wgrad_slots() { return kRes ? 4 : 2; }
+
+template <Out OT, bool kRes>
 __global__ void __launch_bounds__(pair_threads<F8>(), 1) k_grouped_wgrad(const __grid_constant__ WgradArgs a) {
     using F = F8;
     extern __shared__ __align__(1024) unsigned char s_raw[];
     __shared__ PairShared sh;
+    constexpr int kSlots = wgrad_slots<kRes>();
+    __shared__ __align__(8) uint64_t s_res[4][kSlots];  // the residual's chunks are here
     unsigned char* base = s_raw + ((1024u - (smem_u32(s_raw) & 1023u)) & 1023u);
     const int ns = a.stages;
     constexpr int kSfSlots = sf_slots<F>();
     unsigned char* sA = base;
     unsigned char* sB = sA + ns * kPairABytes;
     unsigned char* sC = sB + ns * kPairBBytes;          // epilogue chunks
-    unsigned char* sS = sC + 8 * kChunkBytes;  // scale chunks: a, then b's two row tiles
+    unsigned char* sS = sC + 4 * kSlots * kChunkBytes;  // scale chunks: a, then b's two row tiles
     Group* groups = reinterpret_cast<Group*>(sS + kSfSlots * kSfChunkBytes);
     const int warp = (int)uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
     const int rank = (int)uniform(cluster_rank());
@@ -641,7 +649,7 @@ __global__ void __launch_bounds__(pair_threads<F8>(), 1) k_grouped_wgrad(const _
             bar_init(&sh.sf_free[b], 1);
         }
         for (int w = 0; w < 4; ++w)
-            for (int b = 0; b < 2; ++b) bar_init(&sh.res_full[w][b], 1);
+            for (int b = 0; b < kSlots; ++b) bar_init(&s_res[w][b], 1);
         bar_init(&sh.done, 1);
         sh.fail = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -842,23 +850,44 @@ __global__ void __launch_bounds__(pair_threads<F8>(), 1) k_grouped_wgrad(const _
         constexpr int kElt = OT == Out::F32 ? 4 : 2;
         constexpr int kCols = 128 / kElt;               // columns of a chunk
         constexpr int kChunks = kPairN / kCols;         // chunks of a tile
-        const bool res = a.ep.residual != nullptr;
-        unsigned char* bufs = sC + e * 2 * kChunkBytes;  // two slots, for out and the residual
-        int c = 0, j = 0;  // chunks of this warp, accumulators used
+        unsigned char* bufs = sC + e * kSlots * kChunkBytes;  // for out and the residual
+        uint32_t c = 0;  // chunks of this warp
+        int j = 0;       // accumulators used
+        // The residual's chunks come kSlots - 1 ahead of the sums, over the ends of tiles: a walk
+        // of their own.
+        uint32_t fc = 0;
+        int ft = first, fk = 0;
+        WgradTile f = w;
+        auto fetch = [&] {
+            for (; ft < tiles; ft += step) {
+                if (fk == 0) wgrad_tile(a, groups, ft, f);
+                const int32_t row = f.m0 + 128 * rank + 32 * q;
+                if (row >= f.m_end) continue;
+                if (lane == 0) {
+                    const uint32_t s = fc % kSlots;
+                    mbar_expect_tx(&s_res[e][s], kChunkBytes);
+                    tma_load_2d(bufs + s * kChunkBytes, &a.tres, f.n0 + fk * kCols, f.out_row + row, &s_res[e][s]);
+                }
+                ++fc;
+                if (++fk == kChunks) {
+                    fk = 0;
+                    ft += step;
+                }
+                return;
+            }
+        };
+        if constexpr (kRes) {
+            for (int i = 0; i + 1 < kSlots; ++i) fetch();
+        }
         for (int t = first; t < tiles; t += step) {
             wgrad_tile(a, groups, t, w);
             const int32_t mw = w.m0 + 128 * rank + 32 * q;           // first row of this warp
             const int live = max(0, min(32, w.m_end - mw));          // rows of the group
             const int32_t orow = w.out_row + mw;
-            auto fetch = [&](int k) {                                // chunk k's residual (one lane)
-                uint64_t* bar = &sh.res_full[e][c & 1];
-                mbar_expect_tx(bar, kChunkBytes);
-                tma_load_2d(bufs + (c & 1) * kChunkBytes, &a.tres, w.n0 + k * kCols, orow, bar);
-            };
-            if (res && live > 0 && lane == 0) fetch(0);
-            if (res && t + step < tiles && lane < kChunks) {
-                // the next tile's residual on its way to L2: a chunk is asked for one chunk
-                // ahead only
+            if (kRes && OT == Out::F32 && t + step < tiles && lane < kChunks) {
+                // The next tile's residual on its way to L2: three chunks are half a tile of
+                // 32 bits (two ahead 264 us instead of 295), but a whole one of 16 (76.5, 74.7
+                // without, 16 x 2048 x 2048).
                 WgradTile x = w;
                 wgrad_tile(a, groups, t + step, x);
                 const int32_t row = x.m0 + 128 * rank + 32 * q;
@@ -882,8 +911,10 @@ __global__ void __launch_bounds__(pair_threads<F8>(), 1) k_grouped_wgrad(const _
                 continue;
             }
             for (int k = 0; k < kChunks; ++k, ++c) {
-                const uint32_t buf = smem_u32(bufs + (c & 1) * kChunkBytes);
-                if (res && !bad && !warp_wait(&sh.res_full[e][c & 1], (uint32_t)(c >> 1) & 1)) bad = true;
+                const uint32_t s = c % kSlots;
+                const uint32_t buf = smem_u32(bufs + s * kChunkBytes);
+                // (also once a wait gave up: no copy is in flight when the CTA leaves)
+                if (kRes && !warp_wait(&s_res[e][s], (c / kSlots) & 1u)) bad = true;
                 __syncwarp();
 #pragma unroll
                 for (int h = 0; h < kCols / 32; ++h) {
@@ -904,7 +935,7 @@ __global__ void __launch_bounds__(pair_threads<F8>(), 1) k_grouped_wgrad(const _
 #pragma unroll
                     for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(u[i]);
                     constexpr int kPieces = 32 * kElt / 16;
-                    if (res) add_pieces<OT>(buf + lane * 128, lane, kPieces * h, v);
+                    if (kRes) add_pieces<OT>(buf + lane * 128, lane, kPieces * h, v);
                     put_pieces<OT>(buf + lane * 128, lane, kPieces * h, v);
                 }
                 const int32_t n = w.n0 + k * kCols;
@@ -914,18 +945,14 @@ __global__ void __launch_bounds__(pair_threads<F8>(), 1) k_grouped_wgrad(const _
                 }
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 __syncwarp();
+                if (lane == 0 && live == 32) store_chunk(&a.tout, n, orow, buf);
                 if (lane == 0) {
-                    if (live == 32) store_chunk(&a.tout, n, orow, buf);
                     asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-                    // the chunk before this one has left its slot, which the
-                    // next one is fetched into and written to
-                    asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
-                    if (res && k + 1 < kChunks) {
-                        uint64_t* bar = &sh.res_full[e][(c + 1) & 1];
-                        mbar_expect_tx(bar, kChunkBytes);
-                        tma_load_2d(bufs + ((c + 1) & 1) * kChunkBytes, &a.tres, n + kCols, orow, bar);
-                    }
+                    // the chunk before this one has left its slot, which the next one takes
+                    // (or the next one to be fetched)
+                    asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(kRes ? 1 : kSlots - 1) : "memory");
                 }
+                if constexpr (kRes) fetch();
             }
         }
         if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");

@@ -59,7 +59,7 @@ cudaError_t go(const GroupedCall& c, cudaStream_t s) {
                         smem, a, s);
 }
 
-template <Out OT>
+template <Out OT, bool kRes>
 cudaError_t go_wgrad(const GroupedCall& c, cudaStream_t s) {
     WgradArgs a;
     std::memset(&a, 0, sizeof(a));
@@ -68,7 +68,7 @@ cudaError_t go_wgrad(const GroupedCall& c, cudaStream_t s) {
         !scale_map(&a.tsa, c.as, c.M, kb, 1, kSfChunkTiles) ||
         !scale_map(&a.tsb, c.bs, c.N, kb, 2, kSfChunkTiles) ||
         !chunk_map<OT>(&a.tout, c.ep.out, c.G * c.M, c.N) ||
-        (c.ep.residual && !chunk_map<OT>(&a.tres, c.ep.residual, c.G * c.M, c.N)))
+        (kRes && !chunk_map<OT>(&a.tres, c.ep.residual, c.G * c.M, c.N)))
         return cudaErrorInvalidValue;
     a.ep = c.ep;
     a.offs = c.offs;
@@ -83,14 +83,14 @@ cudaError_t go_wgrad(const GroupedCall& c, cudaStream_t s) {
     // 8192 tokens: 438 us; 1 row 449, 8 rows 438 .. 455, all of them 477).
     a.band = 4;
     constexpr int kOwn = 2048;
-    constexpr int kOther = 8 * kChunkBytes + sf_slots<F8>() * kSfChunkBytes;
+    constexpr int kOther = 4 * wgrad_slots<kRes>() * kChunkBytes + sf_slots<F8>() * kSfChunkBytes;
     static_assert((kSmemLimit - kOwn - 1024 - kOther - (int)group_table_bytes(kMaxGroups)) / kPairStageBytes >=
                       kSfBufs, "stages");
     const int table = (int)group_table_bytes(c.G);
     a.stages = (kSmemLimit - kOwn - 1024 - kOther - table) / kPairStageBytes;
     if (a.stages > kPairMaxStages) a.stages = kPairMaxStages;
     const int smem = a.stages * kPairStageBytes + kOther + table + 1024;
-    return launch_pairs(k_grouped_wgrad<OT>, kOwn, pair_threads<F8>(), (int64_t)c.G * a.tiles_m * a.tiles_n, smem, a, s);
+    return launch_pairs(k_grouped_wgrad<OT, kRes>, kOwn, pair_threads<F8>(), (int64_t)c.G * a.tiles_m * a.tiles_n, smem, a, s);
 }
 
 template <class F>
@@ -103,11 +103,12 @@ cudaError_t by_out(const GroupedCall& c, cudaStream_t s) {
     return cudaErrorInvalidValue;
 }
 
+template <bool kRes>
 cudaError_t wgrad_by_out(const GroupedCall& c, cudaStream_t s) {
     switch (c.out) {
-        case In::BF16: return go_wgrad<Out::BF16>(c, s);
-        case In::F16: return go_wgrad<Out::F16>(c, s);
-        case In::F32: return go_wgrad<Out::F32>(c, s);
+        case In::BF16: return go_wgrad<Out::BF16, kRes>(c, s);
+        case In::F16: return go_wgrad<Out::F16, kRes>(c, s);
+        case In::F32: return go_wgrad<Out::F32, kRes>(c, s);
     }
     return cudaErrorInvalidValue;
 }
@@ -116,7 +117,7 @@ cudaError_t wgrad_by_out(const GroupedCall& c, cudaStream_t s) {
 }  // namespace lin
 
 cudaError_t launch_grouped(const GroupedCall& c, cudaStream_t s) {
-    if (c.wgrad) return lin::wgrad_by_out(c, s);
+    if (c.wgrad) return c.ep.residual ? lin::wgrad_by_out<true>(c, s) : lin::wgrad_by_out<false>(c, s);
     return c.fmt4 ? lin::by_out<lin::F4>(c, s) : lin::by_out<lin::F8>(c, s);
 }
 

@@ -402,11 +402,14 @@ def test_columns_past_2_to_the_31():
 
 
 # ------------------------------------------------------------------ weight gradients
-def _wgrad(offs, rows, N, K, dt, res, seed=0, inplace=False):
+def _wgrad(offs, rows, N, K, dt, res, seed=0, inplace=False, cut=False):
     d, z = _rand(rows, N, seed=seed + 1).to(BF16), _rand(rows, K, seed=seed + 2).to(BF16)
     o = _offs(offs)
     dct, dst = fos.quantize8_grouped(d, o, rowwise=False)[2:]
     zct, zst = fos.quantize8_grouped(z, o, rowwise=False)[2:]
+    if cut:  # without the last 16 columns of both (the scales' rows come to whole tiles all the same)
+        N, K = N - 16, K - 16
+        dct, zct = dct[:N], zct[:K]
     G, P = len(offs), dct.shape[1]
     r = _rand(G, N, K, seed=seed + 3).to(dt) if res else None
     out = r.clone() if inplace else torch.full((G, N, K), float("nan"), dtype=dt, device=DEV)
@@ -464,6 +467,33 @@ def test_wgrad_many_calls_one_answer():
     one = fos.linear8_grouped_wgrad(dct, dst, zct, zst, o, rows)
     for _ in range(12):
         assert torch.equal(one, fos.linear8_grouped_wgrad(dct, dst, zct, zst, o, rows))
+
+
+@pytest.mark.parametrize("dt", [BF16, F32])
+@pytest.mark.parametrize("N,K", [(64, 224), (288, 416), (416, 1024)])
+def test_wgrad_residual_over_tile_ends(dt, N, K):
+    """More tiles than pairs of SMs, with rows that fill no, one or some of a tile's row
+    chunks: the residual's chunks are fetched ahead of the tile that adds them."""
+    sizes = [(7 * e * e + 3 * e) % 67 for e in range(200)]
+    offs = _sizes(*sizes)
+    _wgrad(offs, offs[-1], N, K, dt, True, seed=N, inplace=True, cut=True)
+
+
+@pytest.mark.parametrize("dt", [BF16, F16, F32])
+def test_wgrad_rows_that_end_inside_a_chunk(dt):
+    """16 more rows than whole chunks of 32: the next expert's rows stay its own."""
+    _wgrad(_sizes(300, 0, 129, 40), 480, 288, 416, dt, False, cut=True)
+
+
+def test_wgrad_with_residual_many_calls_one_answer():
+    offs, rows, N, K = _sizes(*[(5 * e) % 23 for e in range(64)]), 700, 1056, 672
+    o = _offs(offs)
+    dct, dst = fos.quantize8_grouped(_rand(rows, N, seed=1).to(BF16), o, rowwise=False)[2:]
+    zct, zst = fos.quantize8_grouped(_rand(rows, K, seed=2).to(BF16), o, rowwise=False)[2:]
+    r = _rand(64, N, K, seed=3)
+    one = fos.linear8_grouped_wgrad(dct, dst, zct, zst, o, rows, residual=r)
+    for _ in range(20):
+        assert torch.equal(one, fos.linear8_grouped_wgrad(dct, dst, zct, zst, o, rows, residual=r))
 
 
 def test_gradients_against_differences():
