@@ -23,14 +23,15 @@
 //            columns, two rows at a time.
 // A CTA takes 16 kR weight rows, kR of 1 .. 4 chosen so that the CTAs fill the device
 // evenly.  Its eight warps split K by steps of 128, each with a ring of its own of
-// kRing steps' codes, filled by TMA (zeros past K), and with few CTAs the CTAs of a
+// ring<kR>() steps' codes, filled by TMA (zeros past K), and with few CTAs the CTAs of a
 // cluster split K too; partial sums are added in one fixed order, warps first.
 // Measured, GPU time in a graph: one row x 14336 x 4096 (33 MB) 11.7 us, 2.8 TB/s, of
 // which about 4 us are the launch, x's way to shared memory and the sums; eight rows of
-// six experts x 4096 x 14336 (198 MB) 49 us, 4.0 TB/s.  Issue slots are half busy: waits
-// for a result's latency with four warps a scheduler.  Measured and not kept: shares of
-// row tiles walked by as many CTAs as fit, the ring running ahead over their ends, 54 us;
-// 256 elements a step 68.
+// six experts x 4096 x 14336 (198 MB) 49 us, 4.1 TB/s.  The copies alone take 6.4 and 31
+// us, unpacking and MMAs alone 6.2 and 30: with four warps a scheduler they overlap only
+// in part.  Measured and not kept: shares of row tiles walked by as many CTAs as fit, the
+// ring running ahead over their ends, 54 us; 256 elements a step 68; rings as deep as
+// shared memory allows 13.2 and 49; one ring a CTA 12.2 and 61.
 // With ids, grid row p handles the rows of expert ids[p] at once if p is the first
 // of them (the weights are read once), else nothing.
 #pragma once
