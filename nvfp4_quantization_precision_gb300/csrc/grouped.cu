@@ -2,6 +2,7 @@
 #include <cstring>
 
 #include "fos_grouped.cuh"
+#include "fos_grouped_rows.cuh"
 #include "fos_linear_host.cuh"
 
 namespace fos {
@@ -19,8 +20,99 @@ cudaError_t launch_pairs(Kernel k, int own, int threads, int64_t tiles, int smem
     return launch_clusters(k, (int)clusters, 2, threads, smem, a, s);
 }
 
+// Which of the two products, by models of their times (us) for the routing that the
+// host can know: as many experts with rows as there can be, `mean` rows each.
+//   k_grouped_rows  5.0 + rounds (stages / S (0.32, NVFP4 0.37, + 0.00043 nt) + 0.022 mean,
+//                   0.034 without a split) + 4.0 (1.2 without a split) a further round,
+//                   whose first stages come after the last round's sums
+//   k_grouped       6.0 + turns x stages (0.21 + 0.00025 mean, NVFP4 0.36; 0.0036 mean more
+//                   where the tokens' scales come by cp.async)
+// The former is taken where it should need at most 0.85 of the other's time. Measured
+// (rows, k_grouped; * taken): 8 bit, 2 rows of 2 of 17 experts x 320 x 8192 7.4*, 18.3; 855 rows
+// of 2 x 368 x 15360 26.0*, 36.4; 300 of 8 x 1024 x 4096 16.7, 13.8*; 8 of 6 of 8 x
+// 14336 x 4096 68.1, 59.9*; NVFP4, 256 of 4 x 1024 x 8192 12.1*, 15.5; 16 of 8 of 16 x 2048 x 7168
+// 15.7, 16.4*; 128 of 54 of 64 x 2048 x 7168 79.9, 71.5*.  Of 32 sizes the one taken was
+// slower than the other in seven, by 1 us at most.
+struct GroupedRowsPlan {
+    int nt, stages, smem, splits, clusters;
+    double us;
+};
+
+double mean_rows(const GroupedCall& c, int most) {
+    const double mean = (double)c.rows / (double)(c.rows < c.G ? c.rows : c.G);
+    return mean < most ? mean : most;
+}
+template <class F>
+double grouped_us(const GroupedCall& c) {
+    const int64_t tiles = (c.N + kPairM - 1) / kPairM * group_tiles_max(c.rows, c.G, kTokTile);
+    const int64_t pairs = sm_count() / 2;
+    const double mean = mean_rows(c, kTokTile);
+    const bool wide = (c.K / (F::kGlobal ? 16 : 32)) % 16 == 0;
+    const double stage = (F::kGlobal ? 0.36 : 0.21 + 0.00025 * mean) + (wide ? 0.0 : 0.0036 * mean);
+    return 6.0 + (double)((tiles + pairs - 1) / pairs) * k_stages<F>(c.K) * stage;
+}
+
+constexpr int kRowsOwn = 2048;
+template <class F, Out OT>
+GroupedRowsPlan grouped_rows_plan(const GroupedCall& c) {
+    GroupedRowsPlan p;
+    p.nt = c.rows >= kGrpRowsTok ? kGrpRowsTok : (int)((c.rows + 15) / 16 * 16);
+    const int stage = rows_stage_bytes<F>(p.nt), table = (int)group_table_bytes(c.G);
+    static_assert((kSmemLimit - kRowsOwn - 1024 - (int)group_table_bytes(kMaxGroups)) / rows_stage_bytes<F>(kGrpRowsTok) >=
+                      kSfRing, "stages");
+    p.stages = (kSmemLimit - kRowsOwn - 1024 - table) / stage;
+    if (p.stages > kMaxStages) p.stages = kMaxStages;
+    p.smem = p.stages * stage + table + 1024;
+    const int nkb = k_stages<F>(c.K);
+    // most experts that can have rows, each with a chunk begun
+    const int64_t tiles = (c.N + 127) / 128 * group_tiles_max(c.rows, c.G, kGrpRowsTok);
+    const double mean = mean_rows(c, kGrpRowsTok);
+    p.us = 1e30;
+    for (int S = 1; S <= 8 && (S == 1 || nkb / S >= 2); S *= 2) {
+        const int fit = S == 1 ? sm_count() : resident_clusters(k_grouped_rows<F, OT>, kRowsThreads, p.smem, S);
+        const double stage_us = (F::kGlobal ? 0.37 : 0.32) + 0.00043 * p.nt;
+        const double rounds = (double)((tiles + fit - 1) / fit);
+        const double us = 5.0 + rounds * ((nkb + S - 1) / S * stage_us + (S > 1 ? 0.022 : 0.034) * mean) +
+                          (rounds - 1.0) * (S > 1 ? 4.0 : 1.2);
+        if (us < p.us) {
+            p.us = us;
+            p.splits = S;
+            p.clusters = fit < tiles ? fit : (int)tiles;
+        }
+    }
+    return p;
+}
+
+template <class F, Out OT>
+cudaError_t rows_go(const GroupedCall& c, const GroupedRowsPlan& p, cudaStream_t s) {
+    GroupedRowsArgs a;
+    std::memset(&a, 0, sizeof(a));
+    const cudaError_t e = allow_smem(reinterpret_cast<const void*>(k_grouped_rows<F, OT>), (size_t)(kSmemLimit - kRowsOwn));
+    if (e != cudaSuccess) return e;
+    const int64_t row_bytes = F::kGlobal ? c.K / 2 : c.K;
+    a.nt = p.nt;
+    if (!code_map(&a.tp, c.b, c.G * c.N, row_bytes, 128) || !code_map(&a.tq, c.a, c.rows, row_bytes, a.nt))
+        return cudaErrorInvalidValue;
+    a.sfp = c.bs;
+    a.sfq = c.as;
+    a.sfq_pitch = F::kGlobal ? c.K / 16 : c.K / 32;
+    a.ep = c.ep;
+    a.offs = c.offs;
+    a.G = c.G;
+    a.rows = (int)c.rows;
+    a.N = (int)c.N;
+    a.tiles_p = (int)((c.N + 127) / 128);
+    a.kb = k_tiles<F>(c.K);
+    a.nkb = k_stages<F>(c.K);
+    a.stages = p.stages;
+    a.splits = p.splits;
+    return launch_clusters(k_grouped_rows<F, OT>, p.clusters, p.splits, kRowsThreads, p.smem, a, s);
+}
+
 template <class F, Out OT>
 cudaError_t go(const GroupedCall& c, cudaStream_t s) {
+    const GroupedRowsPlan plan = grouped_rows_plan<F, OT>(c);
+    if (plan.us < 0.85 * grouped_us<F>(c)) return rows_go<F, OT>(c, plan, s);
     GroupedArgs a;
     std::memset(&a, 0, sizeof(a));
     const int64_t row_bytes = F::kGlobal ? c.K / 2 : c.K;

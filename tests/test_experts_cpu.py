@@ -203,7 +203,7 @@ def test_waits_for_the_other_cta_are_at_cluster_scope():
 
 
 def test_kernels_wait_before_their_first_load():
-    for name in ("fos_grouped.cuh", "fos_matvec.cuh", "fos_quant8.cuh"):
+    for name in ("fos_grouped.cuh", "fos_grouped_rows.cuh", "fos_matvec.cuh", "fos_quant8.cuh"):
         text = _text(name)
         assert "__ldg" not in text
         kernels = re.findall(r"__global__[^;{]*\)\s*\{(.*?)\n\}", text, flags=re.S)

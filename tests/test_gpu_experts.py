@@ -172,6 +172,38 @@ def test_grouped_many_tiles(fmt, sizes, N, K):
 
 
 @pytest.mark.parametrize("fmt", [8, 4])
+@pytest.mark.parametrize("sizes", [(1,), (2, 0, 3, 1), (0, 0, 40, 0, 24), (17,), (1,) * 12])
+@pytest.mark.parametrize("N,K", [(16, 8192), (144, 256), (336, 4224), (1104, 1664), (4096, 2048)])
+def test_grouped_few_rows(fmt, sizes, N, K):
+    """Few tiles: K in one part, two, four and eight."""
+    offs = _sizes(*sizes)
+    _case(fmt, offs, offs[-1] + 5, N, K, "gelu", True, True, True, (BF16, F16, F32)[(N // 16 + len(sizes)) % 3],
+          row=N == 336, seed=N + len(sizes))
+
+
+@pytest.mark.parametrize("fmt,sizes,N,K", [(8, (300, 5, 0, 550), 368, 15360), (4, (64, 65, 1, 128, 130), 96, 9280),
+                                           (4, (256, 0, 255), 336, 8192), (8, (191, 63), 48, 4224)])
+def test_grouped_few_tiles_of_many_rows(fmt, sizes, N, K):
+    """Chunks of 64 rows, several of an expert and several of a cluster."""
+    offs = _sizes(*sizes)
+    _case(fmt, offs, offs[-1], N, K, "silu", True, True, False, row=True, seed=K)
+
+
+@pytest.mark.parametrize("fmt", [8, 4])
+@pytest.mark.parametrize("sizes,N,K", [((2, 0, 1), 320, 8192), ((1,) * 9, 1104, 5120), ((40, 24), 1024, 2048),
+                                       ((400, 455), 368, 7680)])
+def test_grouped_few_rows_many_calls_one_answer(fmt, sizes, N, K):
+    offs, rows = _sizes(*sizes), sum(sizes)
+    b, _ = _weights(fmt, _rand(len(sizes), N, K, seed=1))
+    a, _ = _tokens(fmt, _rand(rows, K, seed=2), offs)
+    res = _rand(rows, N, seed=3).to(BF16)
+    want = _call(fmt, a, b, offs, act="silu", residual=res, out=res.clone())
+    for _ in range(25):
+        stream = res.clone()
+        assert torch.equal(_call(fmt, a, b, offs, act="silu", residual=stream, out=stream), want)
+
+
+@pytest.mark.parametrize("fmt", [8, 4])
 @pytest.mark.parametrize("offs", [[5, 3, 9], [-4, 10, -7], [100, 200, 300], [0, 0, 0], [64, 64, 64],
                                   [2147483647, 0, 0]])
 def test_ends_that_are_no_ends(fmt, offs):
