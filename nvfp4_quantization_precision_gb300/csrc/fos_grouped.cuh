@@ -47,10 +47,13 @@ static_assert(kPairABytes == 128 * kRowBytes && kPairBBytes == 96 * kRowBytes, "
 //              token by cp.async, and the lanes that hold tokens l, 32 + l, ... read them
 //              as they are
 //   epilogue   a lane has one weight row: its 32 neighbours' results of a token are 64
-//              or 128 contiguous bytes of out, stored (and the residual loaded) as
-//              they are, without a way through shared memory; by eight warps, two a
-//              quadrant, which take every other 16 tokens (1003 tokens x
-//              1040 x 640 with everything, one tile a pair: 13.1 us with four, 12.2 with eight)
+//              or 128 contiguous bytes of out, stored as they are, without a way through
+//              shared memory; by eight warps, two a quadrant, which take every other 16
+//              tokens (1003 tokens x 1040 x 640 with everything, one tile a pair: 13.1 us
+//              with four, 12.2 with eight).  The residual comes by TMA, kResSlots - 1
+//              chunks ahead.  With K of some hundreds the epilogue is what a tile takes:
+//              two warps a scheduler, some 190 instructions a chunk of 16 tokens (tokens
+//              stored without a predicate where a chunk is full: up to 3 % slower)
 
 constexpr int kTokTile = 192;                    // tokens of a tile
 constexpr int kTokStep = 32;                     // an MMA's columns come in steps of these
@@ -65,6 +68,9 @@ template <class F> constexpr int grp_slots() { return F::kGlobal ? 8 : 3; }
 // Four more warps than k_linear_pair: the second half of the epilogue.
 template <class F> constexpr int grouped_threads() { return pair_threads<F>() + 128; }
 constexpr int kEpiTok = 16;                      // tokens of a chunk of the epilogue
+// The residual's chunks of a warp of the epilogue in shared memory: kEpiTok rows of 32 values.
+template <Out OT> constexpr int grp_res_bytes() { return kEpiTok * 32 * (OT == Out::F32 ? 4 : 2); }
+template <Out OT> constexpr int grp_res_slots() { return OT == Out::F32 ? 3 : 4; }
 
 struct __align__(8) GroupedShared {
     uint64_t full[kPairMaxStages], empty[kPairMaxStages], acc_full[2], acc_empty[2], done;
@@ -80,6 +86,7 @@ struct GroupedArgs {
     CUtensorMap tsw;   // weights' tiled scales, box 1 x 4 x 512
     CUtensorMap tst;   // ts_wide: the tokens' plain scales, box 16 bytes x 192 rows
     CUtensorMap tst32; // the same, 32 rows
+    CUtensorMap tres;  // residual [rows, N]: box 32 x kEpiTok
     Epilogue ep;
     const uint8_t* ts;     // plain scales of the tokens
     int64_t ts_pitch;      // bytes of a row of them
@@ -143,9 +150,6 @@ __device__ __forceinline__ void grouped_stage(uint32_t acc, uint32_t a0, uint32_
     }
 }
 
-__device__ __forceinline__ void prefetch_line(const void* p) {
-    asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
-}
 __device__ __forceinline__ void prefetch_chunk(const CUtensorMap* map, int32_t x, int32_t y) {
     asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(
                      reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y) : "memory");
@@ -173,6 +177,8 @@ __global__ void __launch_bounds__(grouped_threads<F>(), 1) k_grouped(const __gri
     extern __shared__ __align__(1024) unsigned char s_raw[];
     __shared__ GroupedShared sh;
     __shared__ __align__(16) float s_ga[F::kGlobal ? 8 : 1][kTokTile];  // the tokens' decode scales
+    constexpr int kResSlots = grp_res_slots<OT>(), kResBytes = grp_res_bytes<OT>();
+    __shared__ __align__(8) uint64_t s_res[8][kResSlots];  // the residual's chunks are here
     unsigned char* base = s_raw + ((1024u - (smem_u32(s_raw) & 1023u)) & 1023u);
     const int ns = a.stages;
     constexpr int kSfSlots = grp_slots<F>();
@@ -180,11 +186,14 @@ __global__ void __launch_bounds__(grouped_threads<F>(), 1) k_grouped(const __gri
     unsigned char* sA = base;
     unsigned char* sB = sA + ns * kPairABytes;
     unsigned char* sS = sB + ns * kPairBBytes;  // scale chunks: the weights', then the tokens'
-    Group* groups = reinterpret_cast<Group*>(sS + kSfSlots * kGrpSfBytes);
+    unsigned char* sR = sS + kSfSlots * kGrpSfBytes;  // chunks of the residual
+    Group* groups = reinterpret_cast<Group*>(sR + (a.ep.residual ? 8 * kResSlots * kResBytes : 0));
     const int warp = (int)uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
     const int rank = (int)uniform(cluster_rank());
     const int first = (int)(blockIdx.x >> 1), step = (int)(gridDim.x >> 1);
     if (threadIdx.x == 0) {
+        for (int w = 0; w < 8; ++w)
+            for (int b = 0; b < kResSlots; ++b) bar_init(&s_res[w][b], 1);
         for (int s = 0; s < ns; ++s) {
             bar_init(&sh.full[s], chunk_is_stage<F>() ? 9 : 1);
             bar_init(&sh.empty[s], 1);
@@ -432,44 +441,74 @@ __global__ void __launch_bounds__(grouped_threads<F>(), 1) k_grouped(const __gri
     } else {
         // quadrant, and which of the two warps of it
         const int q = warp & 3, half = warp < 10 ? 0 : 1, e = 4 * half + q;
-        const bool pre = a.ep.pre != nullptr, res = a.ep.residual != nullptr;
+        const bool pre = a.ep.pre != nullptr;
         int j = 0;
+        // The residual's chunks come kResSlots - 1 ahead of the sums, over the ends of tiles: a
+        // walk of their own (1590 tokens of 11 experts x 13696 x 1024 NVFP4 57 us, with loads into
+        // registers one chunk ahead 64; 5717 x 7728 x 960 fp32 84, 97).
+        uint32_t rc = 0, fc = 0;  // chunks added, fetched
+        int ft = first, f0 = kEpiTok * half;
+        GroupedTile f = w;
+        unsigned char* bufs = sR + e * kResSlots * kResBytes;
+        auto fetch = [&] {
+            for (; ft < tiles; ft += step) {
+                if (f0 == kEpiTok * half) grouped_tile(a, groups, ft, f);
+                const int n = f.n0 + 128 * rank + 32 * q;
+                if (n >= a.N) continue;
+                if (lane == 0) {
+                    const uint32_t s = fc % kResSlots;
+                    mbar_expect_tx(&s_res[e][s], kResBytes);
+                    tma_load_2d(bufs + s * kResBytes, &a.tres, n, f.t0 + f0, &s_res[e][s]);
+                }
+                ++fc;
+                f0 += 2 * kEpiTok;
+                if (f0 >= f.cols) {
+                    f0 = kEpiTok * half;
+                    ft += step;
+                }
+                return;
+            }
+        };
+        if (a.ep.residual)
+            for (int i = 0; i + 1 < kResSlots; ++i) fetch();
+        // What a tile's sums take besides, asked for while the tile before it is finished
+        // (1590 x 13696 x 1024 as above 55 us instead of 57, without a residual 37.9, 39.2).
+        GroupedTile next = w;
+        float next_bias = 0.0f, b_amax = 0.0f, a_amax = 0.0f;
+        auto ask = [&](int t) {
+            grouped_tile(a, groups, t, next);
+            const int n = next.n0 + 128 * rank + 32 * q + lane;
+            if (a.ep.bias && n < a.N) {
+                const int64_t i = (int64_t)next.g * a.N + n;
+                next_bias = a.ep.bias32 ? ld_f32(static_cast<const float*>(a.ep.bias) + i)
+                                        : raw_value<OT>(ld_raw<OT>(a.ep.bias, i));
+            }
+            if constexpr (F::kGlobal) {
+                b_amax = ld_f32(a.ep.b_amax + next.g);
+                if (!a.ep.a_row) a_amax = ld_f32(a.ep.a_amax + next.g);
+            }
+        };
+        if (first < tiles) ask(first);
         for (int t = first; t < tiles; t += step, ++j) {
-            grouped_tile(a, groups, t, w);
+            w = next;
+            const bool res = a.ep.residual && w.n0 + 128 * rank + 32 * q < a.N;
             const int n = w.n0 + 128 * rank + 32 * q + lane;
             const bool in = n < a.N;
             // column n of the tile's rows; rows of this lane (none past the weights)
             const int64_t at = (int64_t)w.t0 * a.N + n;
             const int live = in ? w.live : 0;
-            float bias = 0.0f, gb = 1.0f, ga0 = 1.0f;
-            if (a.ep.bias && in) {
-                const int64_t i = (int64_t)w.g * a.N + n;
-                bias = a.ep.bias32 ? ld_f32(static_cast<const float*>(a.ep.bias) + i)
-                                   : raw_value<OT>(ld_raw<OT>(a.ep.bias, i));
-            }
-            uint32_t rs[kEpiTok];
-            auto fetch = [&](int c0) {  // the residual of a chunk
-#pragma unroll
-                for (int i = 0; i < kEpiTok; ++i)
-                    if (c0 + i < live) rs[i] = ld_raw<OT>(a.ep.residual, at + (int64_t)(c0 + i) * a.N);
-            };
-            if (res) {
-                // all of it on its way to L2: a chunk's loads are asked for one chunk ahead only
-                for (int c = lane + 32 * half; c < w.live; c += 64)
-                    if (w.n0 + 128 * rank + 32 * q < a.N)
-                        prefetch_line(static_cast<const char*>(a.ep.residual) +
-                                      (at - lane + (int64_t)c * a.N) * (OT == Out::F32 ? 4 : 2));
-                fetch(kEpiTok * half);
-            }
+            const float bias = next_bias;
+            float gb = 1.0f, ga0 = 1.0f;
             if constexpr (F::kGlobal) {
-                gb = fdiv(1.0f, global_scale(ld_f32(a.ep.b_amax + w.g), a.ep.six_bound));
+                gb = fdiv(1.0f, global_scale(b_amax, a.ep.six_bound));
                 if (a.ep.a_row) {
                     for (int c = lane; c < w.live; c += 32)
                         s_ga[e][c] = fdiv(1.0f, global_scale(ld_f32(a.ep.a_amax + w.t0 + c), a.ep.six_bound));
                 } else {
-                    ga0 = fdiv(1.0f, global_scale(ld_f32(a.ep.a_amax + w.g), a.ep.six_bound));
+                    ga0 = fdiv(1.0f, global_scale(a_amax, a.ep.six_bound));
                 }
             }
+            if (t + step < tiles) ask(t + step);
             const int ab = j & 1;
             if (!bad && !warp_wait<Sync::TENSOR>(&sh.acc_full[ab], (uint32_t)(j >> 1) & 1)) bad = true;
             __syncwarp();
@@ -509,9 +548,19 @@ __global__ void __launch_bounds__(grouped_threads<F>(), 1) k_grouped(const __gri
                 if (pre) store_column<OT>(static_cast<char*>(a.ep.pre) + to, a.N, v, live - c0);
                 act_apply<OT>(a.ep.act, v);
                 if (res) {
+                    const uint32_t s = rc % kResSlots;
+                    // (also once a wait gave up: no copy is in flight when the CTA leaves)
+                    if (!warp_wait(&s_res[e][s], (rc / kResSlots) & 1u)) bad = true;
+                    const unsigned char* buf = bufs + s * kResBytes;
 #pragma unroll
-                    for (int i = 0; i < kEpiTok; ++i) v[i] = fadd(v[i], raw_value<OT>(rs[i]));
-                    fetch(c0 + 2 * kEpiTok);
+                    for (int i = 0; i < kEpiTok; ++i)
+                        v[i] = fadd(v[i], raw_value<OT>(OT == Out::F32 ? reinterpret_cast<const uint32_t*>(buf)[32 * i + lane]
+                                                                       : reinterpret_cast<const unsigned short*>(buf)[32 * i + lane]));
+                    ++rc;
+                    // read before the slot is filled again
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    __syncwarp();
+                    fetch();
                 }
                 store_column<OT>(static_cast<char*>(a.ep.out) + to, a.N, v, live - c0);
             }

@@ -142,11 +142,21 @@ cudaError_t go(const GroupedCall& c, cudaStream_t s) {
     a.band = (int)(fit < 1 ? 1 : fit > 4096 ? 4096 : fit);
     constexpr int kOwn = 8192;
     constexpr int kFixed = kOwn + 1024 + grp_slots<F>() * kGrpSfBytes;
-    static_assert((kSmemLimit - kFixed - (int)group_table_bytes(kMaxGroups)) / kPairStageBytes >= kSfBufs, "stages");
-    const int table = (int)group_table_bytes(c.G);
-    a.stages = (kSmemLimit - kFixed - table) / kPairStageBytes;
+    constexpr int kRes = 8 * grp_res_slots<OT>() * grp_res_bytes<OT>();
+    static_assert((kSmemLimit - kFixed - kRes - (int)group_table_bytes(kMaxGroups)) / kPairStageBytes >= kSfBufs, "stages");
+    if (c.ep.residual) {
+        constexpr int kElt = OT == Out::F32 ? 4 : 2;
+        constexpr CUtensorMapDataType kType = OT == Out::F32   ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                              : OT == Out::F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                                               : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+        if (!matrix_map(&a.tres, kType, kElt, c.ep.residual, c.rows, c.N * kElt, 32, kEpiTok, CU_TENSOR_MAP_SWIZZLE_NONE,
+                        CU_TENSOR_MAP_L2_PROMOTION_NONE))
+            return cudaErrorInvalidValue;
+    }
+    const int other = grp_slots<F>() * kGrpSfBytes + (c.ep.residual ? kRes : 0) + (int)group_table_bytes(c.G);
+    a.stages = (kSmemLimit - kOwn - 1024 - other) / kPairStageBytes;
     if (a.stages > kPairMaxStages) a.stages = kPairMaxStages;
-    const int smem = a.stages * kPairStageBytes + grp_slots<F>() * kGrpSfBytes + table + 1024;
+    const int smem = a.stages * kPairStageBytes + other + 1024;
     return launch_pairs(k_grouped<F, OT>, kOwn, grouped_threads<F>(), group_tiles_max(c.rows, c.G, kTokTile) * a.tiles_n,
                         smem, a, s);
 }
