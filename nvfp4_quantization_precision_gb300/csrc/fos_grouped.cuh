@@ -100,6 +100,7 @@ struct GroupedArgs {
     int kb, nkb;           // scale tiles and stages along K
     int row_tiles;         // scale row tiles of a group's weights
     int stages;
+    int res_area;          // bytes of the residual's chunks of all warps (none without one)
 };
 
 // One tile of the walk.
@@ -187,7 +188,7 @@ __global__ void __launch_bounds__(grouped_threads<F>(), 1) k_grouped(const __gri
     unsigned char* sB = sA + ns * kPairABytes;
     unsigned char* sS = sB + ns * kPairBBytes;  // scale chunks: the weights', then the tokens'
     unsigned char* sR = sS + kSfSlots * kGrpSfBytes;  // chunks of the residual
-    Group* groups = reinterpret_cast<Group*>(sR + (a.ep.residual ? 8 * kResSlots * kResBytes : 0));
+    Group* groups = reinterpret_cast<Group*>(sR + a.res_area);
     const int warp = (int)uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
     const int rank = (int)uniform(cluster_rank());
     const int first = (int)(blockIdx.x >> 1), step = (int)(gridDim.x >> 1);

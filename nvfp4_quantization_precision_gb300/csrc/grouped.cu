@@ -153,7 +153,8 @@ cudaError_t go(const GroupedCall& c, cudaStream_t s) {
                         CU_TENSOR_MAP_L2_PROMOTION_NONE))
             return cudaErrorInvalidValue;
     }
-    const int other = grp_slots<F>() * kGrpSfBytes + (c.ep.residual ? kRes : 0) + (int)group_table_bytes(c.G);
+    a.res_area = c.ep.residual ? kRes : 0;
+    const int other = grp_slots<F>() * kGrpSfBytes + a.res_area + (int)group_table_bytes(c.G);
     a.stages = (kSmemLimit - kOwn - 1024 - other) / kPairStageBytes;
     if (a.stages > kPairMaxStages) a.stages = kPairMaxStages;
     const int smem = a.stages * kPairStageBytes + other + 1024;

@@ -272,6 +272,21 @@ def test_grouped_in_place_and_repeats(fmt):
         assert got.data_ptr() == stream.data_ptr() and torch.equal(got, want)
 
 
+@pytest.mark.parametrize("fmt", [8, 4])
+@pytest.mark.parametrize("dt", [BF16, F32])
+def test_grouped_residual_many_calls_one_answer(fmt, dt):
+    """Many tiles with few stages: the residual's chunks run ahead over the ends of tiles, some
+    of them without columns for a warp."""
+    offs, rows, N, K = _sizes(*[(37 * e) % 211 for e in range(16)]), 1700, 2064, 384
+    b, _ = _weights(fmt, _rand(16, N, K, seed=1))
+    a, _ = _tokens(fmt, _rand(rows, K, seed=2), offs)
+    res = _rand(rows, N, seed=3).to(dt)
+    want = _call(fmt, a, b, offs, residual=res, out_dtype=dt, out=res.clone())
+    for _ in range(25):
+        stream = res.clone()
+        assert torch.equal(_call(fmt, a, b, offs, residual=stream, out_dtype=dt, out=stream), want)
+
+
 def test_side_stream_and_a_graph_for_every_routing():
     """One captured graph of quantization, product, gradient and weight gradient serves
     other ends than it was captured with."""
