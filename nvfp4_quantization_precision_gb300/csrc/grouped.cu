@@ -87,8 +87,6 @@ template <class F, Out OT>
 cudaError_t rows_go(const GroupedCall& c, const GroupedRowsPlan& p, cudaStream_t s) {
     GroupedRowsArgs a;
     std::memset(&a, 0, sizeof(a));
-    const cudaError_t e = allow_smem(reinterpret_cast<const void*>(k_grouped_rows<F, OT>), (size_t)(kSmemLimit - kRowsOwn));
-    if (e != cudaSuccess) return e;
     const int64_t row_bytes = F::kGlobal ? c.K / 2 : c.K;
     a.nt = p.nt;
     if (!code_map(&a.tp, c.b, c.G * c.N, row_bytes, 128) || !code_map(&a.tq, c.a, c.rows, row_bytes, a.nt))
@@ -111,6 +109,8 @@ cudaError_t rows_go(const GroupedCall& c, const GroupedRowsPlan& p, cudaStream_t
 
 template <class F, Out OT>
 cudaError_t go(const GroupedCall& c, cudaStream_t s) {
+    const cudaError_t e = allow_smem(reinterpret_cast<const void*>(k_grouped_rows<F, OT>), (size_t)(kSmemLimit - kRowsOwn));
+    if (e != cudaSuccess) return e;
     const GroupedRowsPlan plan = grouped_rows_plan<F, OT>(c);
     if (plan.us < 0.85 * grouped_us<F>(c)) return rows_go<F, OT>(c, plan, s);
     GroupedArgs a;
