@@ -531,9 +531,9 @@ FOS_API fos_status fos_linear4(const uint8_t* a_codes, const uint8_t* a_scales_t
  * expert: offs (device int32 [G]) holds the cumulative ends, read as
  * fos_quantize_grouped reads them: expert e has rows [end_{e-1}, end_e),
  * end_e = clamp(offs[e], end_{e-1}, rows).  Any expert may be empty.  The ends
- * are read on the device, so one captured graph serves every routing.  Rows at
- * or past the last end are not read, and what an output holds for them is left
- * as it was.  1 <= G <= FOS_LINEAR_MAX_GROUPS.  Conventions, formats and errors
+ * are read on the device, so one captured graph serves every routing.  What rows
+ * at or past the last end hold does not matter, and what an output holds for them
+ * is left as it was.  1 <= G <= FOS_LINEAR_MAX_GROUPS.  Conventions, formats and errors
  * are those of the feed-forward operators above; sizes, and products of two of
  * them, as there (rows x N, G x N x K and so on up to 2^40, G x N below 2^31).
  */
