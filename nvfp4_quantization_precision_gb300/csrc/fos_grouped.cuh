@@ -111,8 +111,17 @@ struct GroupedTile {
     int32_t n0;
 };
 
+// Token tiles of a band: their rows take at most 30 MB, a quarter of L2 (pair_go()), and
+// they are no more than a group can have.  The latter keeps a band times the tiles of
+// the weight rows below the number of all tiles, which fits 32 bits for every size that
+// the calls take (rows x N up to 2^40, G x N below 2^31), and so grouped_tile()'s products.
+inline int token_band(int64_t rows, int64_t row_bytes) {
+    const int64_t fit = 30000000 / (kTokTile * row_bytes), all = (rows + kTokTile - 1) / kTokTile;
+    return (int)(fit < 1 ? 1 : fit < all ? fit : all);
+}
+
 // Within a group, bands of a.band token tiles, down the tokens first (pair_tile()).
-__device__ __forceinline__ void grouped_tile(const GroupedArgs& a, const Group* t, int tile,
+__host__ __device__ __forceinline__ void grouped_tile(const GroupedArgs& a, const Group* t, int tile,
                                              GroupedTile& w) {
     const int g = group_of(t, a.G, tile / a.tiles_n, w.g);
     const int all = t[g + 1].tile - t[g].tile;

@@ -100,7 +100,7 @@ __device__ __forceinline__ void group_table(Group* t, const int32_t* offs, int G
 
 // The group of tile `tile` (below t[G].tile): `g`, where the caller's walk stands, or
 // the one after it, else by bisection (runs of empty groups).
-__device__ __forceinline__ int group_of(const Group* t, int G, int tile, int g) {
+__host__ __device__ __forceinline__ int group_of(const Group* t, int G, int tile, int g) {
     if (t[g + 1].tile > tile && t[g].tile <= tile) return g;
     if (g + 2 <= G && t[g + 2].tile > tile && t[g + 1].tile <= tile) return g + 1;
     int lo = 0, hi = G;  // t[lo].tile <= tile < t[hi].tile

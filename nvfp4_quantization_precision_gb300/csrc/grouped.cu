@@ -137,9 +137,7 @@ cudaError_t go(const GroupedCall& c, cudaStream_t s) {
     a.rows = (int)c.rows;
     a.N = (int)c.N;
     a.tiles_n = (int)((c.N + kPairM - 1) / kPairM);
-    // Token tiles of a band: their rows take at most 30 MB, a quarter of L2 (pair_go()).
-    const int64_t fit = 30000000 / (kTokTile * row_bytes);
-    a.band = (int)(fit < 1 ? 1 : fit > 4096 ? 4096 : fit);
+    a.band = token_band(c.rows, row_bytes);
     constexpr int kOwn = 8192;
     constexpr int kFixed = kOwn + 1024 + grp_slots<F>() * kGrpSfBytes;
     constexpr int kRes = 8 * grp_res_slots<OT>() * grp_res_bytes<OT>();
