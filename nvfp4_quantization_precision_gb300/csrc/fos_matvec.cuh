@@ -3,9 +3,9 @@
 //   out[p][n] = act(g[e] sum_k x[p / rep][k] w[e][n][k] + bias[e][n]) + residual[p][n]
 //
 // e = ids[p] (0 without ids), w = e2m1(code) * e4m3(scale of its 16 elements) and
-// g[e] the weight's global decode scale.  x keeps its type: no rounding before the
-// sum.  Bound by the weights' bytes (9/16 byte an element), close behind by the
-// instructions that unpack them.
+// g[e] the weight's global decode scale.  No element of x is rounded before the sum,
+// whatever stands beside it.  Bound by the weights' bytes (9/16 byte an element), close
+// behind by the instructions that unpack them.
 //
 // A weight w is exact in fp16 (two significant bits times four, 2^-10 to 2688), so the
 // sums are formed by mma.m16n8k16 with weights as the 16 rows, rows of x as the 8
@@ -20,7 +20,8 @@
 //            MMAs, four a time: any order of k serves as long as x has the same.
 //   x        is brought to fp16 in shared memory once a CTA (put_x below): bf16 times a power
 //            of two, fp32 in three pieces of 11 significant bits, which take three
-//            columns, two rows at a time.
+//            columns, two rows at a time.  Elements too small beside the largest of their
+//            128 are left and take turns of their own.
 // A CTA takes 16 kR weight rows, kR of 1 .. 4 chosen so that the CTAs fill the device
 // evenly.  Its eight warps split K by steps of 128, each with a ring of its own of
 // ring<kR>() steps' codes, filled by TMA (zeros past K), and with few CTAs the CTAs of a
@@ -43,6 +44,7 @@ namespace fos {
 
 struct MatvecArgs {
     CUtensorMap codes;      // [G * N, K / 2], box 16 kR rows x 64 bytes
+    const uint8_t* b;       // the codes themselves
     const void* x;          // [M / rep, K]
     const int32_t* ids;     // [M] or null
     const uint8_t* scales;  // [G] x tiled
@@ -63,9 +65,9 @@ template <int kR> constexpr int ring() { return kR < 4 ? 3 : 2; }  // steps of a
 // warp's stores touch every bank once.
 template <int kR> constexpr int line() { return 16 * kR + (kR % 2 ? 20 : 4); }
 template <int kR> constexpr int ring_bytes() { return kWarpsMv * ring<kR>() * 16 * kR * kStepBytes; }
-// x in fp16: kXBytes of columns and steps, of each one factor, and a step of zeros.
-constexpr int kXStep = kStepK * 2, kXBytes = 128 * kXStep;
-template <int kR> constexpr int smem_bytes() { return ring_bytes<kR>() + kXBytes + 64 + 128 * 4; }
+// x in fp16: kXBytes of columns and steps, a step of zeros, and each row's factor of a step.
+constexpr int kXStep = kStepK * 2, kXSteps = 128, kXBytes = kXSteps * kXStep;
+template <int kR> constexpr int smem_bytes() { return ring_bytes<kR>() + kXBytes + 64 + kXSteps * 4; }
 
 template <In XT> constexpr int tokens() { return XT == In::F32 ? 2 : 8; }
 
@@ -95,6 +97,21 @@ __device__ __forceinline__ void mma16(float (&c)[4], uint32_t a0, uint32_t a1, u
         "{%8,%9}, {%0,%1,%2,%3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// A lane's products of a step's 16 weight rows (32 codes of rows g and g + 8, their two
+// scales each) with its column of x.
+__device__ __forceinline__ void mma_tile(float (&sum)[4], uint4 lo4, uint4 hi4, uint32_t s0, uint32_t s1,
+                                         const uint4 (&f)[4]) {
+    const uint32_t w0[4] = {lo4.x, lo4.y, lo4.z, lo4.w}, w1[4] = {hi4.x, hi4.y, hi4.z, hi4.w};
+    const uint32_t p0 = scale_pair(s0), p1 = scale_pair(s1);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        uint32_t u[4], v[4];
+        unpack(w0[q], __byte_perm(p0, 0u, q < 2 ? 0x1010 : 0x3232), u);
+        unpack(w1[q], __byte_perm(p1, 0u, q < 2 ? 0x1010 : 0x3232), v);
+        mma16(sum, u[0], v[0], u[1], v[1], f[q].x, f[q].y);
+        mma16(sum, u[2], v[2], u[3], v[3], f[q].z, f[q].w);
+    }
 }
 __device__ __forceinline__ uint32_t f16_pair(float lo, float hi) {
     uint32_t r;
@@ -129,15 +146,38 @@ __device__ __forceinline__ uint32_t x_piece(int t, int col, int q) {
     return (uint32_t)((t >> 1) * 128 + ((((t & 1) * 4 + q) ^ ((t >> 1) + 2 * (col & 1))) << 4));
 }
 
-// Lane t's 32 elements of a row of x in fp16, at `to` (the row's column, or the first of
-// its three) of the step, times a power of two that brings the largest finite one of the
-// row's 128 of the step to 2^14 .. 2^15 (of the quad t = 0 .. 3 together); returns its
-// inverse.  fp16 holds every bf16 down to 2^-32 of the largest exactly, and 2^-40 of it
-// is what it rounds off below that, far beneath the sum's own roundings.  fp32: y = the
-// sum of three pieces, each the rounding of what is left to 11 significant bits; an
-// infinity or a NaN is its first piece, the others 0.
-template <In XT>
-__device__ __forceinline__ float put_x(const char* x, bool in, uint32_t to, uint32_t col_bytes, int col, int t) {
+__device__ __forceinline__ uint32_t max_halves(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
+// How x comes to fp16 without a loss.  A row's 128 elements of a step are multiplied by
+// the power of two that brings the largest finite one to 2^14 .. 2^15.  bf16: fp16, whose
+// last place is 2^-24 at least, then holds every element down to 2^-31 of it (by their
+// exponents) exactly.  fp32: three pieces of 11 significant bits, each the rounding of
+// what is left, the second times 2^11, the third times 2^22 (an infinity or a NaN is the
+// first one, the others 0); with a last place of 2^-46 they hold every element down to
+// 2^-37.  Elements below that are left, zeros in their place, and their products are added
+// in turns of their own (add_left), in each of which the largest of those left sets
+// the power, until none is: nine at most for the whole range of either type.  (The
+// large elements cannot decide how the small ones are held: where they meet zero
+// weights the sum is of the small ones alone.)  Looking for them costs 0.1 .. 0.3 us a
+// call (2048 x 7168 6.4 us without, 6.7 with; 14336 x 4096 11.5 and 11.7; ten fp32 rows x 3520 x
+// 6784 33.8 and 35.2).  With the turns in the loop over steps: 11.9, and 20.4 instead of
+// 20.0 for eight rows x 4096 x 14336; with one vote for the two rare cases of put_x, 60 instead
+// of 56 for six experts.
+template <In XT> constexpr int deep() { return XT == In::F32 ? 37 : 31; }
+struct Fit {
+    int e;     // exponent field of the largest (at least 14); x is multiplied by 2^(141 - e)
+    int left;  // elements with an exponent field below it are left; 0: none are
+};
+
+// A row's 32 elements of lane t, of those with exponent fields below `below` (kAll: of all),
+// to `to`, the row's column (or the first of its three) of the step.
+template <In XT, bool kAll>
+__device__ __forceinline__ Fit put_x(const char* x, bool in, int below, uint32_t to, uint32_t col_bytes, int col,
+                                     int t) {
     constexpr int kQ = XT == In::F32 ? 8 : 4;
     uint32_t w[4 * kQ];
 #pragma unroll
@@ -148,29 +188,77 @@ __device__ __forceinline__ float put_x(const char* x, bool in, uint32_t to, uint
     if constexpr (XT == In::F16) {
 #pragma unroll
         for (int q = 0; q < 4; ++q) sts128(to + x_piece(t, col, q), w + 4 * q);
-        return 1.0f;
+        return Fit{0, 0};
     } else {
-        auto value = [&](int i) {  // element i
-            if constexpr (XT == In::F32) return __uint_as_float(w[i]);
-            else return __uint_as_float(i & 1 ? w[i >> 1] & 0xFFFF0000u : w[i >> 1] << 16);
+        auto bits = [&](int i) {  // element i
+            if constexpr (XT == In::F32) return w[i];
+            else return i & 1 ? w[i >> 1] & 0xFFFF0000u : w[i >> 1] << 16;
         };
-        float most = 0.0f;
+        auto field = [](uint32_t u) { return (int)((u >> 23) & 255u); };
+        // zeros in the place of elements with exponent fields outside lo .. hi - 1
+        auto keep = [&](int lo, int hi) {
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
-            const float a = fabsf(value(i));
-            most = a <= kFltMax ? fmaxf(most, a) : most;
+            for (int i = 0; i < 4 * kQ; ++i) {
+                if constexpr (XT == In::F32) {
+                    w[i] = field(w[i]) >= lo && field(w[i]) < hi ? w[i] : 0u;
+                } else {
+                    const int a = field(w[i] << 16), b = field(w[i]);
+                    w[i] &= (a >= lo && a < hi ? 0xFFFFu : 0u) | (b >= lo && b < hi ? 0xFFFF0000u : 0u);
+                }
+            }
+        };
+        if constexpr (!kAll) keep(0, below);
+        // magnitudes as whole numbers, bf16 by halves of words: the largest, and the smallest
+        // but zero's less 1
+        uint32_t most = 0u, least = 0xFFFFFFFFu;
+#pragma unroll
+        for (int i = 0; i < 4 * kQ; ++i) {
+            if constexpr (XT == In::F32) {
+                const uint32_t u = w[i] & 0x7FFFFFFFu;
+                most = max(most, u);
+                least = min(least, u - 1u);
+            } else {
+                const uint32_t u = w[i] & 0x7FFF7FFFu;
+                most = max_halves(most, u);
+                least = __viaddmin_u16x2(u, 0xFFFFFFFFu, least);
+            }
         }
-        most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, 1));
-        most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, 2));
-        // exponent of the largest + 127 (0: a subnormal one or zero); 2^(14 - e), at most 2^127
-        const int e = max(14, (int)(__float_as_uint(most) >> 23));
+        if constexpr (XT != In::F32) {
+            most = max(most << 16, most & 0xFFFF0000u);
+            least = min(least << 16, least & 0xFFFF0000u);
+        }
+#pragma unroll
+        for (int d = 1; d < 4; d <<= 1) {
+            most = max(most, __shfl_xor_sync(0xFFFFFFFFu, most, d));
+            least = min(least, __shfl_xor_sync(0xFFFFFFFFu, least, d));
+        }
+        const bool odd = __any_sync(0xFFFFFFFFu, most >= 0x7F800000u);
+        if (odd) {  // the largest finite one
+            most = 0u;
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+                const uint32_t u = bits(i) & 0x7FFFFFFFu;
+                most = max(most, u < 0x7F800000u ? u : 0u);
+            }
+            most = max(most, __shfl_xor_sync(0xFFFFFFFFu, most, 1));
+            most = max(most, __shfl_xor_sync(0xFFFFFFFFu, most, 2));
+        }
+        const int e = max(14, (int)(most >> 23));
+        Fit fit{e, 0};
+        // (subnormal elements, whose last place is that of the smallest normal ones, count as
+        // of field 0: within `deep` of e they are held too)
+        const int small = (int)(XT == In::F32 ? (least + 1u) >> 23 : ((least >> 16) + 1u) >> 7);
+        if (small < e - deep<XT>()) {
+            fit.left = e - deep<XT>();
+            keep(fit.left, 256);
+        }
         const float up = __uint_as_float((uint32_t)(268 - e) << 23);
         constexpr int kPieces = XT == In::F32 ? 3 : 1;
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
             float y[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) y[i] = fmul(value(8 * q + i), up);
+            for (int i = 0; i < 8; ++i) y[i] = fmul(__uint_as_float(bits(8 * q + i)), up);
 #pragma unroll
             for (int p = 0; p < kPieces; ++p) {
                 uint32_t h[4];
@@ -180,14 +268,95 @@ __device__ __forceinline__ float put_x(const char* x, bool in, uint32_t to, uint
                     if (p + 1 < kPieces) {
                         float a, b;
                         upk(f16x2_f32x2(h[i]), a, b);
-                        y[2 * i] = fabsf(y[2 * i]) <= kFltMax ? y[2 * i] - a : 0.0f;
-                        y[2 * i + 1] = fabsf(y[2 * i + 1]) <= kFltMax ? y[2 * i + 1] - b : 0.0f;
+                        a = (y[2 * i] - a) * 2048.0f;
+                        b = (y[2 * i + 1] - b) * 2048.0f;
+                        if (odd) {
+                            a = fabsf(y[2 * i]) <= kFltMax ? a : 0.0f;
+                            b = fabsf(y[2 * i + 1]) <= kFltMax ? b : 0.0f;
+                        }
+                        y[2 * i] = a;
+                        y[2 * i + 1] = b;
                     }
                 }
                 sts128(to + p * col_bytes + x_piece(t, col + p, q), h);
             }
         }
-        return fdiv(1.0f, up);
+        return fit;
+    }
+}
+// What undoes an fp32 row's factors of its pieces, column `col` of them, and put_x's factor.
+template <In XT>
+__device__ __forceinline__ float piece_down(int col) {
+    return XT == In::F32 ? __uint_as_float((uint32_t)(127 - 11 * (col % 3)) << 23) : 1.0f;
+}
+__device__ __forceinline__ float put_down(const Fit& fit) {
+    return __uint_as_float(fit.e > 14 ? (uint32_t)(fit.e - 14) << 23 : 0x00400000u);
+}
+
+// This lane's 32 elements from k on of the row of x that row p takes.
+template <In XT>
+__device__ __forceinline__ const char* x_at(const MatvecArgs& a, int64_t p, int k) {
+    return static_cast<const char*>(a.x) + ((p / a.rep) * a.K + k) * (XT == In::F32 ? 4 : 2);
+}
+// A lane's scales of row tile r of expert e in the first step: of row g, two bytes (of row g + 8
+// 128 bytes behind, of the next step two tiles).
+__device__ __forceinline__ const uint8_t* scales_at(const MatvecArgs& a, int e, int r, int g, int t) {
+    return a.scales + (int64_t)e * a.scale_bytes + ((int64_t)(r >> 7) * a.kt + (t >> 1)) * lin::kSfTileBytes +
+           16 * ((r & 31) + g) + 4 * ((r >> 5) & 3) + 2 * (t & 1);
+}
+
+// The products of the elements that put_x left, of a warp's steps, added to its partial
+// sums: turn by turn the largest of those left decide the factor.  A function of its
+// own, so that it costs the rows that leave none no registers; its codes come straight
+// from memory (the ring has gone on).  x is laid out at `xs`, the factors at `down`,
+// places of the warp's own.  One row x 4096 x 14336 with one such element 19.7 us instead
+// of 12.4, with gelu's values of normal arguments of deviation 4 (tails to 1e-30 in most
+// steps) 44, with magnitudes spread over 2^-100 .. 2^100 151.
+template <In XT, int kR>
+__device__ __noinline__ void add_left(const MatvecArgs& a, int e, int row0, int lo, int hi, const int* ids,
+                                      int first, int ntok, float gb, float* part, uint32_t xs, float* down) {
+    constexpr int kPieces = XT == In::F32 ? 3 : 1, kLine = line<kR>();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
+    // a quad a row (those behind the last do the last one's work once more)
+    const int tk = min(g, ntok - 1), col = tk * kPieces;
+    const int64_t p = ids ? ids[tk] : first + tk;
+    for (int step = lo + warp; step < hi; step += kWarpsMv) {
+        const int k = step * kStepK + 32 * t;
+        const char* x = x_at<XT>(a, p, k);
+        Fit fit = put_x<XT, true>(x, k < a.K, 256, xs + col * kXStep, kXStep, col, t);
+        while (__any_sync(0xFFFFFFFFu, fit.left > 0)) {
+            __syncwarp();
+            fit = put_x<XT, false>(x, k < a.K, fit.left, xs + col * kXStep, kXStep, col, t);
+            if (t == 0) down[tk] = put_down(fit);
+            __syncwarp();
+            uint4 f[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                f[q] = g < ntok * kPieces ? lds128(xs + g * kXStep + x_piece(t, g, q)) : make_uint4(0, 0, 0, 0);
+            const float d0 = down[min(2 * t / kPieces, ntok - 1)] * piece_down<XT>(2 * t);
+            const float d1 = down[min((2 * t + 1) / kPieces, ntok - 1)] * piece_down<XT>(2 * t + 1);
+#pragma unroll 1
+            for (int i = 0; i < kR; ++i) {
+                uint4 w[2];
+                uint32_t sc[2];
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    const int row = row0 + 16 * i + 8 * r + g;
+                    const bool in = row < a.N && k < a.K;
+                    w[r] = in ? ld128(a.b + (((int64_t)e * a.N + row) * a.K + k) / 2) : make_uint4(0, 0, 0, 0);
+                    sc[r] = in ? ld_u16(scales_at(a, e, row0 + 16 * i, g, t) +
+                                        (int64_t)step * (2 * lin::kSfTileBytes) + 128 * r) : 0u;
+                }
+                float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                mma_tile(sum, w[0], w[1], sc[0], sc[1], f);
+                float* at = part + (2 * t) * kLine + 16 * i + g;
+                at[0] = __fmaf_rn(fmul(sum[0], gb), d0, at[0]);
+                at[kLine] = __fmaf_rn(fmul(sum[1], gb), d1, at[kLine]);
+                at[8] = __fmaf_rn(fmul(sum[2], gb), d0, at[8]);
+                at[kLine + 8] = __fmaf_rn(fmul(sum[3], gb), d1, at[kLine + 8]);
+            }
+        }
+        __syncwarp();  // the last turn's x and factors have been read
     }
 }
 
@@ -267,10 +436,7 @@ __global__ void __launch_bounds__(32 * kWarpsMv, 2) k_matvec4(const __grid_const
 #pragma unroll
     for (int i = 0; i < kR; ++i) {
         const int r = row0 + 16 * i;
-        scales[i] = r < a.N ? a.scales + (int64_t)e * a.scale_bytes +
-                                  ((int64_t)(r >> 7) * a.kt + (t >> 1)) * lin::kSfTileBytes +
-                                  16 * ((r & 31) + g) + 4 * ((r >> 5) & 3) + 2 * (t & 1)
-                            : nullptr;
+        scales[i] = r < a.N ? scales_at(a, e, r, g, t) : nullptr;
     }
     // the steps in which this lane's 32 elements lie below K
     const int mine = min(hi, (a.K - 32 * t + kStepK - 1) / kStepK);
@@ -311,25 +477,29 @@ __global__ void __launch_bounds__(32 * kWarpsMv, 2) k_matvec4(const __grid_const
             }
         }
         load_scales(lo + warp);
+        bool again = false;  // put_x left elements of this chunk's rows
         // x by as many steps at a time as its place in shared memory holds
         const int seg = kXBytes / kXStep / cols / kWarpsMv * kWarpsMv;
         const uint32_t col_bytes = (uint32_t)(seg * kXStep);
         for (int s0 = lo; s0 < hi; s0 += seg) {
             const int steps = min(seg, hi - s0);
+            bool left = false;
             // a quad of lanes a row and step; whole warps go round together
             for (int u = warp * 8 + g; u < (ntok * steps + 7) / 8 * 8; u += kWarpsMv * 8) {
                 const int tk = min(u / steps, ntok - 1), st = min(u - tk * steps, steps - 1);
                 const int64_t p = a.ids ? s_ids[c0 + tk] : first + c0 + tk;
                 const int k = (s0 + st) * kStepK + 32 * t;
-                constexpr int kElt = XT == In::F32 ? 4 : 2;
-                const float down = put_x<XT>(static_cast<const char*>(a.x) + ((p / a.rep) * a.K + k) * kElt,
-                                             k < a.K, s_x + tk * kPieces * col_bytes + st * kXStep, col_bytes,
-                                             tk * kPieces, t);
-                if (XT != In::F16 && t == 0) s_down[tk * seg + st] = down;
+                const Fit fit = put_x<XT, true>(x_at<XT>(a, p, k), k < a.K, 256,
+                                                s_x + tk * kPieces * col_bytes + st * kXStep, col_bytes,
+                                                tk * kPieces, t);
+                left |= fit.left > 0;
+                if (XT != In::F16 && t == 0) s_down[tk * seg + st] = put_down(fit);
             }
-            __syncthreads();
+            if constexpr (XT == In::F16) __syncthreads();
+            else again |= __syncthreads_or(left) != 0;
             // a column that is not there reads the step of zeros
             const bool live = g < cols;
+            const float pd0 = piece_down<XT>(2 * t), pd1 = piece_down<XT>(2 * t + 1);
             const uint32_t xs = live ? s_x + g * col_bytes : s_x + kXBytes;
             for (int step = s0 + warp; step < s0 + steps; step += kWarpsMv) {
                 uint32_t two[kR][2];
@@ -338,33 +508,24 @@ __global__ void __launch_bounds__(32 * kWarpsMv, 2) k_matvec4(const __grid_const
 #pragma unroll
                     for (int r = 0; r < 2; ++r) two[i][r] = sc[i][r];
                 load_scales(step + kWarpsMv);
-                uint4 f[4];
                 const uint32_t xa = live ? xs + (step - s0) * kXStep : xs;
+                uint4 f[4];
 #pragma unroll
                 for (int q = 0; q < 4; ++q) f[q] = lds128(xa + (live ? x_piece(t, g, q) : 16 * q));
                 float d0 = 1.0f, d1 = 1.0f;  // of the two columns that this lane has products of
                 if constexpr (XT != In::F16) {
-                    d0 = s_down[min(2 * t / kPieces, ntok - 1) * seg + step - s0];
-                    d1 = s_down[min((2 * t + 1) / kPieces, ntok - 1) * seg + step - s0];
+                    d0 = s_down[min(2 * t / kPieces, ntok - 1) * seg + step - s0] * pd0;
+                    d1 = s_down[min((2 * t + 1) / kPieces, ntok - 1) * seg + step - s0] * pd1;
                 }
                 if (!lin::warp_wait(&s_full[warp][slot], parity)) bad = true;  // goes on: every copy is waited for
                 const uint32_t at = lane_at + slot * kSlot;
 #pragma unroll
                 for (int i = 0; i < kR; ++i) {
                     const uint4 lo4 = lds128(at + 16 * i * kStepBytes), hi4 = lds128(at + (16 * i + 8) * kStepBytes);
-                    const uint32_t w0[4] = {lo4.x, lo4.y, lo4.z, lo4.w}, w1[4] = {hi4.x, hi4.y, hi4.z, hi4.w};
-                    const uint32_t p0 = scale_pair(two[i][0]), p1 = scale_pair(two[i][1]);
                     float sum[4];
 #pragma unroll
                     for (int j = 0; j < 4; ++j) sum[j] = XT == In::F16 ? acc[i][j] : 0.0f;
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        uint32_t u[4], v[4];
-                        unpack(w0[q], __byte_perm(p0, 0u, q < 2 ? 0x1010 : 0x3232), u);
-                        unpack(w1[q], __byte_perm(p1, 0u, q < 2 ? 0x1010 : 0x3232), v);
-                        mma16(sum, u[0], v[0], u[1], v[1], f[q].x, f[q].y);
-                        mma16(sum, u[2], v[2], u[3], v[3], f[q].z, f[q].w);
-                    }
+                    mma_tile(sum, lo4, hi4, two[i][0], two[i][1], f);
                     if constexpr (XT == In::F16) {
 #pragma unroll
                         for (int j = 0; j < 4; ++j) acc[i][j] = sum[j];
@@ -399,6 +560,11 @@ __global__ void __launch_bounds__(32 * kWarpsMv, 2) k_matvec4(const __grid_const
             part[(2 * t + 1) * kLine + 16 * i + g] = acc[i][1];
             part[(2 * t) * kLine + 16 * i + 8 + g] = acc[i][2];
             part[(2 * t + 1) * kLine + 16 * i + 8 + g] = acc[i][3];
+        }
+        if constexpr (XT != In::F16) {
+            if (again)
+                add_left<XT, kR>(a, e, row0, lo, hi, a.ids ? s_ids + c0 : nullptr, first + c0, ntok, gb, part,
+                                 s_x + warp * (kXBytes / kWarpsMv), s_down + warp * 8);
         }
         __syncthreads();
         for (int idx = tid; idx < ntok * kRows; idx += 32 * kWarpsMv) {

@@ -10,6 +10,7 @@ using namespace matvec;
 
 template <In XT, int kR>
 cudaError_t go(MatvecArgs a, const uint8_t* codes, int groups, cudaStream_t s) {
+    a.b = codes;
     auto k = k_matvec4<XT, kR>;
     const cudaError_t e = allow_smem(reinterpret_cast<const void*>(k), smem_bytes<kR>());
     if (e != cudaSuccess) return e;
