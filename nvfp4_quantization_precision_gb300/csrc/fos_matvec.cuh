@@ -163,21 +163,37 @@ __device__ __forceinline__ uint32_t max_halves(uint32_t a, uint32_t b) {
 // the power, until none is: nine at most for the whole range of either type.  (The
 // large elements cannot decide how the small ones are held: where they meet zero
 // weights the sum is of the small ones alone.)  Looking for them costs 0.1 .. 0.3 us a
-// call (2048 x 7168 6.4 us without, 6.7 with; 14336 x 4096 11.5 and 11.7; ten fp32 rows x 3520 x
-// 6784 33.8 and 35.2).  With the turns in the loop over steps: 11.9, and 20.4 instead of
+// call (2048 x 7168 6.5 us without, 6.7 with; 14336 x 4096 11.4 and 11.5; ten fp32 rows x 3520 x
+// 6784 33.8 and 34.9).  With the turns in the loop over steps: 11.9, and 20.4 instead of
 // 20.0 for eight rows x 4096 x 14336; with one vote for the two rare cases of put_x, 60 instead
 // of 56 for six experts.
 template <In XT> constexpr int deep() { return XT == In::F32 ? 37 : 31; }
+// The weight's decode scale as m 2^e, 1 <= m < 2.
+struct Decode {
+    float m;
+    int e;
+};
+__device__ __forceinline__ Decode split(float g) {
+    const bool sub = g < 0x1p-126f;
+    const uint32_t u = __float_as_uint(sub ? g * 0x1p64f : g);
+    return Decode{__uint_as_float((u & 0x007FFFFFu) | 0x3F800000u), (int)(u >> 23) - (sub ? 191 : 127)};
+}
+// What brings a step's products to the result's scale is the decode scale times what undoes
+// x's factor, m 2^(e - 141 + its e).  Where that exponent is outside these bounds (the
+// third piece's is 22 below) a step's elements are left as well, for a factor in two parts
+// (two parts for every step: 58 us instead of 56.7 for six experts x 4096 x 14336, 21.0
+// instead of 20.4 for eight rows of one).
+constexpr int kDownLeast = -100, kDownMost = 127;
 struct Fit {
     int e;     // exponent field of the largest (at least 14); x is multiplied by 2^(141 - e)
     int left;  // elements with an exponent field below it are left; 0: none are
 };
 
 // A row's 32 elements of lane t, of those with exponent fields below `below` (kAll: of all),
-// to `to`, the row's column (or the first of its three) of the step.
+// to `to`, the row's column (or the first of its three) of the step.  ge: Decode's e.
 template <In XT, bool kAll>
-__device__ __forceinline__ Fit put_x(const char* x, bool in, int below, uint32_t to, uint32_t col_bytes, int col,
-                                     int t) {
+__device__ __forceinline__ Fit put_x(const char* x, bool in, int below, int ge, uint32_t to, uint32_t col_bytes,
+                                     int col, int t) {
     constexpr int kQ = XT == In::F32 ? 8 : 4;
     uint32_t w[4 * kQ];
 #pragma unroll
@@ -252,6 +268,10 @@ __device__ __forceinline__ Fit put_x(const char* x, bool in, int below, uint32_t
             fit.left = e - deep<XT>();
             keep(fit.left, 256);
         }
+        if (kAll && most && (e - 141 + ge < kDownLeast || e - 141 + ge > kDownMost)) {
+            fit.left = 256;
+            keep(256, 256);
+        }
         const float up = __uint_as_float((uint32_t)(268 - e) << 23);
         constexpr int kPieces = XT == In::F32 ? 3 : 1;
 #pragma unroll
@@ -284,13 +304,22 @@ __device__ __forceinline__ Fit put_x(const char* x, bool in, int below, uint32_t
         return fit;
     }
 }
-// What undoes an fp32 row's factors of its pieces, column `col` of them, and put_x's factor.
+// What undoes the factor of an fp32 row's piece, column `col` of them.
 template <In XT>
 __device__ __forceinline__ float piece_down(int col) {
     return XT == In::F32 ? __uint_as_float((uint32_t)(127 - 11 * (col % 3)) << 23) : 1.0f;
 }
-__device__ __forceinline__ float put_down(const Fit& fit) {
-    return __uint_as_float(fit.e > 14 ? (uint32_t)(fit.e - 14) << 23 : 0x00400000u);
+// The factor of a step's products.
+__device__ __forceinline__ float put_down(const Fit& fit, const Decode& g) {
+    const int t = min(max(fit.e - 141 + g.e, kDownLeast), kDownMost);
+    return g.m * __uint_as_float((uint32_t)(t + 127) << 23);
+}
+// The same of any exponent, in two parts of half of it each.  One after the other they
+// neither overflow nor lose bits where the result does not (a factor at a time did: weights
+// of 1e35 and x near 1, or x of 1e36 and weights of 1e-35).  Below 2^-250 nothing is left.
+__device__ __forceinline__ float2 put_down2(const Fit& fit, const Decode& g) {
+    const int t = max(fit.e - 141 + g.e, -250), h = t >> 1;
+    return make_float2(g.m * __uint_as_float((uint32_t)(h + 127) << 23), __uint_as_float((uint32_t)(t - h + 127) << 23));
 }
 
 // This lane's 32 elements from k on of the row of x that row p takes.
@@ -314,7 +343,7 @@ __device__ __forceinline__ const uint8_t* scales_at(const MatvecArgs& a, int e, 
 // steps) 44, with magnitudes spread over 2^-100 .. 2^100 151.
 template <In XT, int kR>
 __device__ __noinline__ void add_left(const MatvecArgs& a, int e, int row0, int lo, int hi, const int* ids,
-                                      int first, int ntok, float gb, float* part, uint32_t xs, float* down) {
+                                      int first, int ntok, Decode gd, float* part, uint32_t xs, float2* down) {
     constexpr int kPieces = XT == In::F32 ? 3 : 1, kLine = line<kR>();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
     // a quad a row (those behind the last do the last one's work once more)
@@ -323,18 +352,19 @@ __device__ __noinline__ void add_left(const MatvecArgs& a, int e, int row0, int 
     for (int step = lo + warp; step < hi; step += kWarpsMv) {
         const int k = step * kStepK + 32 * t;
         const char* x = x_at<XT>(a, p, k);
-        Fit fit = put_x<XT, true>(x, k < a.K, 256, xs + col * kXStep, kXStep, col, t);
+        Fit fit = put_x<XT, true>(x, k < a.K, 256, gd.e, xs + col * kXStep, kXStep, col, t);
         while (__any_sync(0xFFFFFFFFu, fit.left > 0)) {
             __syncwarp();
-            fit = put_x<XT, false>(x, k < a.K, fit.left, xs + col * kXStep, kXStep, col, t);
-            if (t == 0) down[tk] = put_down(fit);
+            fit = put_x<XT, false>(x, k < a.K, fit.left, gd.e, xs + col * kXStep, kXStep, col, t);
+            if (t == 0) down[tk] = put_down2(fit, gd);
             __syncwarp();
             uint4 f[4];
 #pragma unroll
             for (int q = 0; q < 4; ++q)
                 f[q] = g < ntok * kPieces ? lds128(xs + g * kXStep + x_piece(t, g, q)) : make_uint4(0, 0, 0, 0);
-            const float d0 = down[min(2 * t / kPieces, ntok - 1)] * piece_down<XT>(2 * t);
-            const float d1 = down[min((2 * t + 1) / kPieces, ntok - 1)] * piece_down<XT>(2 * t + 1);
+            float2 d0 = down[min(2 * t / kPieces, ntok - 1)], d1 = down[min((2 * t + 1) / kPieces, ntok - 1)];
+            d0.y *= piece_down<XT>(2 * t);
+            d1.y *= piece_down<XT>(2 * t + 1);
 #pragma unroll 1
             for (int i = 0; i < kR; ++i) {
                 uint4 w[2];
@@ -350,10 +380,10 @@ __device__ __noinline__ void add_left(const MatvecArgs& a, int e, int row0, int 
                 float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
                 mma_tile(sum, w[0], w[1], sc[0], sc[1], f);
                 float* at = part + (2 * t) * kLine + 16 * i + g;
-                at[0] = __fmaf_rn(fmul(sum[0], gb), d0, at[0]);
-                at[kLine] = __fmaf_rn(fmul(sum[1], gb), d1, at[kLine]);
-                at[8] = __fmaf_rn(fmul(sum[2], gb), d0, at[8]);
-                at[kLine + 8] = __fmaf_rn(fmul(sum[3], gb), d1, at[kLine + 8]);
+                at[0] = __fmaf_rn(fmul(sum[0], d0.x), d0.y, at[0]);
+                at[kLine] = __fmaf_rn(fmul(sum[1], d1.x), d1.y, at[kLine]);
+                at[8] = __fmaf_rn(fmul(sum[2], d0.x), d0.y, at[8]);
+                at[kLine + 8] = __fmaf_rn(fmul(sum[3], d1.x), d1.y, at[kLine + 8]);
             }
         }
         __syncwarp();  // the last turn's x and factors have been read
@@ -444,6 +474,7 @@ __global__ void __launch_bounds__(32 * kWarpsMv, 2) k_matvec4(const __grid_const
     uint32_t slot = 0, parity = 0;  // of the next step
     bool bad = false;
     const float gb = fdiv(1.0f, global_scale(ld_f32(a.ep.b_amax + e), a.ep.six_bound));
+    const Decode gd = split(gb);
     // step's codes into ring slot b
     auto fetch = [&](int step, uint32_t b) {
         if (lane == 0 && step < hi) {
@@ -489,11 +520,11 @@ __global__ void __launch_bounds__(32 * kWarpsMv, 2) k_matvec4(const __grid_const
                 const int tk = min(u / steps, ntok - 1), st = min(u - tk * steps, steps - 1);
                 const int64_t p = a.ids ? s_ids[c0 + tk] : first + c0 + tk;
                 const int k = (s0 + st) * kStepK + 32 * t;
-                const Fit fit = put_x<XT, true>(x_at<XT>(a, p, k), k < a.K, 256,
+                const Fit fit = put_x<XT, true>(x_at<XT>(a, p, k), k < a.K, 256, gd.e,
                                                 s_x + tk * kPieces * col_bytes + st * kXStep, col_bytes,
                                                 tk * kPieces, t);
                 left |= fit.left > 0;
-                if (XT != In::F16 && t == 0) s_down[tk * seg + st] = put_down(fit);
+                if (XT != In::F16 && t == 0) s_down[tk * seg + st] = put_down(fit, gd);
             }
             if constexpr (XT == In::F16) __syncthreads();
             else again |= __syncthreads_or(left) != 0;
@@ -530,11 +561,10 @@ __global__ void __launch_bounds__(32 * kWarpsMv, 2) k_matvec4(const __grid_const
 #pragma unroll
                         for (int j = 0; j < 4; ++j) acc[i][j] = sum[j];
                     } else {
-                        // the decode scale first: the result's range, not the codes', bounds x
-                        acc[i][0] = __fmaf_rn(fmul(sum[0], gb), d0, acc[i][0]);
-                        acc[i][1] = __fmaf_rn(fmul(sum[1], gb), d1, acc[i][1]);
-                        acc[i][2] = __fmaf_rn(fmul(sum[2], gb), d0, acc[i][2]);
-                        acc[i][3] = __fmaf_rn(fmul(sum[3], gb), d1, acc[i][3]);
+                        acc[i][0] = __fmaf_rn(sum[0], d0, acc[i][0]);
+                        acc[i][1] = __fmaf_rn(sum[1], d1, acc[i][1]);
+                        acc[i][2] = __fmaf_rn(sum[2], d0, acc[i][2]);
+                        acc[i][3] = __fmaf_rn(sum[3], d1, acc[i][3]);
                     }
                 }
                 // every lane has its codes: the slot is free (without the fence a copy issued
@@ -563,8 +593,8 @@ __global__ void __launch_bounds__(32 * kWarpsMv, 2) k_matvec4(const __grid_const
         }
         if constexpr (XT != In::F16) {
             if (again)
-                add_left<XT, kR>(a, e, row0, lo, hi, a.ids ? s_ids + c0 : nullptr, first + c0, ntok, gb, part,
-                                 s_x + warp * (kXBytes / kWarpsMv), s_down + warp * 8);
+                add_left<XT, kR>(a, e, row0, lo, hi, a.ids ? s_ids + c0 : nullptr, first + c0, ntok, gd, part,
+                                 s_x + warp * (kXBytes / kWarpsMv), reinterpret_cast<float2*>(s_down) + warp * 8);
         }
         __syncthreads();
         for (int idx = tid; idx < ntok * kRows; idx += 32 * kWarpsMv) {

@@ -1,6 +1,6 @@
-"""matvec4 takes every element of x as it is, whatever stands beside it: rows whose
-large elements meet zero weights, so that a result is of the small ones alone,
-against 64 bits.
+"""matvec4 takes every element of x as it is, whatever stands beside it and whatever
+the weights' decode scale: rows whose large elements meet zero weights, so that a
+result is of the small ones alone, and weights and rows far from 1, against 64 bits.
 
 Bounds, e = 2^-24, K terms: 2 (K + 16) e sum |x w| as in test_gpu_experts.py, of the terms
 that a result has.  For results of one term: the weight and its decode scale are
@@ -198,3 +198,27 @@ def test_repeats_with_rows_of_many_magnitudes():
     one = fos.matvec4(x, *b, out_dtype=F32)
     outs = [fos.matvec4(x, *b, out_dtype=F32) for _ in range(40)]
     assert all(torch.equal(one, o) for o in outs)
+
+
+def _scaled_weights(N, K, size, seed):
+    """Weights of magnitudes around `size`, as whole parts of it, and their exact values."""
+    w = (_rand(N, K, seed=seed).to(BF16).to(D) * size).to(F32)
+    c, s, a = fos.quantize(w, CFG)
+    S = torch.clamp(torch.tensor(2688.0) / a.cpu(), max=torch.finfo(F32).max)
+    return (c, s, a), ex.values4(c, ex.untile(s, N, K // 16)) * (1 / S).to(D).to(DEV)
+
+
+# the decode scale and x far from 1 in either direction, their product in range
+@pytest.mark.parametrize("dt", [BF16, F16, F32])
+@pytest.mark.parametrize("weights,size", [(1e35, 1.0), (1e35, 1e-4), (2e36, 0.5), (1e30, 100.0), (1e-35, 1.0), (1e-30, 1e-3),
+                                          (1e-38, 1e4), (1e-35, 1e36), (1e-38, 1e37), (1e35, 1e-36), (1e35, 1e-38),
+                                          (1e10, 1e-40), (1e-20, 1e-15)])
+def test_scales_of_the_weights(dt, weights, size):
+    if dt == F16 and not 1e-4 <= size <= 1e4:
+        size = 1.0
+    K, N = 544, 48
+    b, wv = _scaled_weights(N, K, weights, 1)
+    _check((_rand(3, K, seed=2) * size).to(dt), b, wv)
+    if dt != F16:
+        x = _magnitudes(_rand(3, K, seed=3), -40, 0, 4) * size
+        _check(x.to(dt), b, wv)
