@@ -126,7 +126,7 @@ __device__ __forceinline__ uint4 ld128(const void* p) {
 }
 __device__ __forceinline__ uint32_t ld_u16(const void* p) {
     uint32_t v;
-    asm volatile("{\n\t.reg .b16 h;\n\tld.global.nc.b16 h, [%1];\n\tcvt.u32.u16 %0, h;\n\t}" : "=r"(v) : "l"(p));
+    asm volatile("{\n\t.reg .b16 h;\n\tld.global.b16 h, [%1];\n\tcvt.u32.u16 %0, h;\n\t}" : "=r"(v) : "l"(p));
     return v;
 }
 __device__ __forceinline__ uint4 lds128(uint32_t addr) {
@@ -538,7 +538,10 @@ __global__ void __launch_bounds__(32 * kWarpsMv, 2) k_matvec4(const __grid_const
                 for (int i = 0; i < kR; ++i)
 #pragma unroll
                     for (int r = 0; r < 2; ++r) two[i][r] = sc[i][r];
-                load_scales(step + kWarpsMv);
+                // Where they are asked for: with four row tiles here (six experts x 4096 x 14336 56.7
+                // us; behind the wait 62, registers spill), else behind the wait for the codes
+                // (14336 x 4096 11.3, here 11.8: the fence below waits for loads under way).
+                if constexpr (kR == 4) load_scales(step + kWarpsMv);
                 const uint32_t xa = live ? xs + (step - s0) * kXStep : xs;
                 uint4 f[4];
 #pragma unroll
@@ -549,6 +552,7 @@ __global__ void __launch_bounds__(32 * kWarpsMv, 2) k_matvec4(const __grid_const
                     d1 = s_down[min((2 * t + 1) / kPieces, ntok - 1) * seg + step - s0] * pd1;
                 }
                 if (!lin::warp_wait(&s_full[warp][slot], parity)) bad = true;  // goes on: every copy is waited for
+                if constexpr (kR < 4) load_scales(step + kWarpsMv);
                 const uint32_t at = lane_at + slot * kSlot;
 #pragma unroll
                 for (int i = 0; i < kR; ++i) {
