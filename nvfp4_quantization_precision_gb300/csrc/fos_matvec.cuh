@@ -26,9 +26,9 @@
 // evenly.  Its eight warps split K by steps of 128, each with a ring of its own of
 // ring<kR>() steps' codes, filled by TMA (zeros past K), and with few CTAs the CTAs of a
 // cluster split K too; partial sums are added in one fixed order, warps first.
-// Measured, GPU time in a graph: one row x 14336 x 4096 (33 MB) 11.7 us, 2.8 TB/s, of
-// which about 4 us are the launch, x's way to shared memory and the sums; eight rows of
-// six experts x 4096 x 14336 (198 MB) 49 us, 4.1 TB/s.  The copies alone take 6.4 and 31
+// Measured, GPU time in a graph: one row x 14336 x 4096 (33 MB), bias and silu 11.9 us, 2.8
+// TB/s, of which about 4 us are the launch, x's way to shared memory and the sums; eight
+// rows of six experts x 4096 x 14336 (198 MB) 48.6 us, 4.1 TB/s.  The copies alone take 6.4 and 31
 // us, unpacking and MMAs alone 6.2 and 30: with four warps a scheduler they overlap only
 // in part.  Measured and not kept: shares of row tiles walked by as many CTAs as fit, the
 // ring running ahead over their ends, 54 us; 256 elements a step 68; rings as deep as
@@ -156,17 +156,17 @@ __device__ __forceinline__ uint32_t max_halves(uint32_t a, uint32_t b) {
 // the power of two that brings the largest finite one to 2^14 .. 2^15.  bf16: fp16, whose
 // last place is 2^-24 at least, then holds every element down to 2^-31 of it (by their
 // exponents) exactly.  fp32: three pieces of 11 significant bits, each the rounding of
-// what is left, the second times 2^11, the third times 2^22 (an infinity or a NaN is the
-// first one, the others 0); with a last place of 2^-46 they hold every element down to
-// 2^-37.  Elements below that are left, zeros in their place, and their products are added
+// what is left, the second times 2^11, the third times 2^22; with a last place of 2^-46
+// they hold every element down to 2^-37.  Elements below that are left, zeros in their place, and their products are added
 // in turns of their own (add_left), in each of which the largest of those left sets
 // the power, until none is: nine at most for the whole range of either type.  (The
 // large elements cannot decide how the small ones are held: where they meet zero
-// weights the sum is of the small ones alone.)  Looking for them costs 0.1 .. 0.3 us a
-// call (2048 x 7168 6.5 us without, 6.7 with; 14336 x 4096 11.4 and 11.5; ten fp32 rows x 3520 x
-// 6784 33.8 and 34.9).  With the turns in the loop over steps: 11.9, and 20.4 instead of
-// 20.0 for eight rows x 4096 x 14336; with one vote for the two rare cases of put_x, 60 instead
-// of 56 for six experts.
+// weights the sum is of the small ones alone.)  Looking for them costs up to 0.4 us
+// a call (1024 x 1024 3.4 us without, 3.8 with; 2048 x 7168 6.2 .. 6.5 and 6.5 .. 6.8; 14336 x 4096
+// 11.5 and 11.3, which has a product less a sum now; ten fp32 rows x 3520 x 6784 33.8 and
+// 35.3).  With the turns in the loop over steps 14336 x 4096 took 11.9; with infinities
+// and NaN looked for in every block 1408 x 2048 of 16 experts 14.1 instead of 13.6, with one
+// branch for all that is rare 14.7 (six experts x 4096 x 14336 61 instead of 56).
 template <In XT> constexpr int deep() { return XT == In::F32 ? 37 : 31; }
 // The weight's decode scale as m 2^e, 1 <= m < 2.
 struct Decode {
@@ -180,7 +180,8 @@ __device__ __forceinline__ Decode split(float g) {
 }
 // What brings a step's products to the result's scale is the decode scale times what undoes
 // x's factor, m 2^(e - 141 + its e).  Where that exponent is outside these bounds (the
-// third piece's is 22 below) a step's elements are left as well, for a factor in two parts
+// third piece's is 22 below) and where an element is infinite or NaN, all of a row's
+// elements of the step are left, for a factor in two parts
 // (two parts for every step: 58 us instead of 56.7 for six experts x 4096 x 14336, 21.0
 // instead of 20.4 for eight rows of one).
 constexpr int kDownLeast = -100, kDownMost = 127;
@@ -248,16 +249,19 @@ __device__ __forceinline__ Fit put_x(const char* x, bool in, int below, int ge, 
             most = max(most, __shfl_xor_sync(0xFFFFFFFFu, most, d));
             least = min(least, __shfl_xor_sync(0xFFFFFFFFu, least, d));
         }
-        const bool odd = __any_sync(0xFFFFFFFFu, most >= 0x7F800000u);
-        if (odd) {  // the largest finite one
-            most = 0u;
+        bool odd = false;  // infinities or NaN
+        if constexpr (!kAll) {
+            odd = __any_sync(0xFFFFFFFFu, most >= 0x7F800000u);
+            if (odd) {  // the largest finite one
+                most = 0u;
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
-                const uint32_t u = bits(i) & 0x7FFFFFFFu;
-                most = max(most, u < 0x7F800000u ? u : 0u);
+                for (int i = 0; i < 32; ++i) {
+                    const uint32_t u = bits(i) & 0x7FFFFFFFu;
+                    most = max(most, u < 0x7F800000u ? u : 0u);
+                }
+                most = max(most, __shfl_xor_sync(0xFFFFFFFFu, most, 1));
+                most = max(most, __shfl_xor_sync(0xFFFFFFFFu, most, 2));
             }
-            most = max(most, __shfl_xor_sync(0xFFFFFFFFu, most, 1));
-            most = max(most, __shfl_xor_sync(0xFFFFFFFFu, most, 2));
         }
         const int e = max(14, (int)(most >> 23));
         Fit fit{e, 0};
@@ -268,7 +272,7 @@ __device__ __forceinline__ Fit put_x(const char* x, bool in, int below, int ge, 
             fit.left = e - deep<XT>();
             keep(fit.left, 256);
         }
-        if (kAll && most && (e - 141 + ge < kDownLeast || e - 141 + ge > kDownMost)) {
+        if (kAll && most && (e == 255 || e - 141 + ge < kDownLeast || e - 141 + ge > kDownMost)) {
             fit.left = 256;
             keep(256, 256);
         }
@@ -338,9 +342,9 @@ __device__ __forceinline__ const uint8_t* scales_at(const MatvecArgs& a, int e, 
 // sums: turn by turn the largest of those left decide the factor.  A function of its
 // own, so that it costs the rows that leave none no registers; its codes come straight
 // from memory (the ring has gone on).  x is laid out at `xs`, the factors at `down`,
-// places of the warp's own.  One row x 4096 x 14336 with one such element 19.7 us instead
+// places of the warp's own.  One row x 4096 x 14336 with one such element 19.5 us instead
 // of 12.4, with gelu's values of normal arguments of deviation 4 (tails to 1e-30 in most
-// steps) 44, with magnitudes spread over 2^-100 .. 2^100 151.
+// steps) 43, with magnitudes spread over 2^-100 .. 2^100 147.
 template <In XT, int kR>
 __device__ __noinline__ void add_left(const MatvecArgs& a, int e, int row0, int lo, int hi, const int* ids,
                                       int first, int ntok, Decode gd, float* part, uint32_t xs, float2* down) {
@@ -418,7 +422,7 @@ __global__ void __launch_bounds__(32 * kWarpsMv, 2) k_matvec4(const __grid_const
     __shared__ __align__(16) float s_sum[8 * kLine];
     __shared__ __align__(8) uint64_t s_full[kWarpsMv][kRing];
     __shared__ int s_ids[kMaxRows];
-    __shared__ int s_count, s_fail;
+    __shared__ int s_count, s_fail, s_again;
     float* s_down = reinterpret_cast<float*>(s_ring + ring_bytes<kR>() + kXBytes + 64);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
     const int S = a.splits, rank = (int)(blockIdx.x % S), block = (int)(blockIdx.x / S);
@@ -427,7 +431,7 @@ __global__ void __launch_bounds__(32 * kWarpsMv, 2) k_matvec4(const __grid_const
         for (int b = 0; b < kRing; ++b) mma::bar_init(&s_full[warp][b], 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (tid == 0) s_fail = 0;
+    if (tid == 0) s_fail = s_again = 0;
     const uint32_t s_x = smem_u32(s_ring) + ring_bytes<kR>();
     if (tid < 16) reinterpret_cast<uint32_t*>(s_ring + ring_bytes<kR>() + kXBytes)[tid] = 0u;
     __syncthreads();
@@ -527,7 +531,7 @@ __global__ void __launch_bounds__(32 * kWarpsMv, 2) k_matvec4(const __grid_const
                 if (XT != In::F16 && t == 0) s_down[tk * seg + st] = put_down(fit, gd);
             }
             if constexpr (XT == In::F16) __syncthreads();
-            else again |= __syncthreads_or(left) != 0;
+            else { if (left) s_again = 1; __syncthreads(); }
             // a column that is not there reads the step of zeros
             const bool live = g < cols;
             const float pd0 = piece_down<XT>(2 * t), pd1 = piece_down<XT>(2 * t + 1);
@@ -596,7 +600,7 @@ __global__ void __launch_bounds__(32 * kWarpsMv, 2) k_matvec4(const __grid_const
             part[(2 * t + 1) * kLine + 16 * i + 8 + g] = acc[i][3];
         }
         if constexpr (XT != In::F16) {
-            if (again)
+            if (s_again)
                 add_left<XT, kR>(a, e, row0, lo, hi, a.ids ? s_ids + c0 : nullptr, first + c0, ntok, gd, part,
                                  s_x + warp * (kXBytes / kWarpsMv), reinterpret_cast<float2*>(s_down) + warp * 8);
         }
@@ -633,6 +637,7 @@ __global__ void __launch_bounds__(32 * kWarpsMv, 2) k_matvec4(const __grid_const
             }
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the ring is TMA's again
+        if (tid == 0) s_again = 0;
         lin::tile_sync(S);  // the sums have been read
     }
 }

@@ -36,10 +36,10 @@ cudaError_t go(MatvecArgs a, const uint8_t* codes, int groups, cudaStream_t s) {
 // Row tiles of a CTA and CTAs of a cluster: the pair with the least time, in row
 // tiles times steps of a warp, of all CTAs over the device's places (two an SM) and
 // half of a last one; what a CTA does once takes as long as eight, its cluster's sums
-// as two more.  Measured (us; this pair, the best of 14 others): 4096 x 14336 1 row
-// 11.8 (two tiles, two CTAs), 11.9; 14336 x 4096 8 rows 15.0 (three, one), 15.1;
-// eight experts 2048 x 7168 18.7 (four, one), 18.7; six of eight 4096 x 14336 49.6 (four,
-// one), 48.4 (three, one).
+// as two more.  Measured (us; this pair, the best of the others): 4096 x 14336 1 row
+// 12.2 (two tiles, two CTAs), 13.0; 14336 x 4096 8 rows 15.4 (three, one), 17.3;
+// eight experts 2048 x 7168 19.9 (four, one), 25.4; six of eight 4096 x 14336 48.6, 57.5 with
+// the experts' further rows last (four, one), 49.2 (three, one).
 template <In XT>
 cudaError_t by_shape(MatvecArgs a, const uint8_t* codes, cudaStream_t s) {
     const int groups = a.ids ? a.M : (a.M + tokens<XT>() - 1) / tokens<XT>();
