@@ -616,8 +616,9 @@ FOS_API fos_status fos_linear8_grouped_wgrad(const uint8_t* d_codes_t, const uin
  * cfg->granularity is not read.  epilogue bias [G, N]; residual and out [M, N] (out may be
  * in the residual's place); pre must be NULL.  A row whose id is outside 0 .. G - 1 is
  * left as it was.  Weights are decoded exactly, x is taken as it is (no element is rounded,
- * whatever stands beside it) and products are summed in fp32; an expert's weights are read
- * once for up to eight rows (two of fp32 x).  Rows with elements below 2^-31 (fp32: 2^-37)
+ * whatever stands beside it) and products are summed in fp32.  An expert's weights are
+ * read again for every eight rows (two of fp32 x): for a few rows; from 16 on (4 of fp32)
+ * fos_linear4 of quantized rows takes less.  Rows with elements below 2^-31 (fp32: 2^-37)
  * of the largest of their 128 neighbours take longer.  M <= FOS_MATVEC_MAX_ROWS;
  * G <= FOS_LINEAR_MAX_GROUPS; N % 16 == 0; K % 32 == 0, K > 0.  x, codes, scales and the
  * epilogue's tensors 16-byte aligned.

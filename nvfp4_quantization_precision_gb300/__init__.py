@@ -1026,7 +1026,8 @@ def linear8_grouped_wgrad(d_codes_t, d_scales_t, z_codes_t, z_scales_t, offs, ro
 def matvec4(x, b_codes, b_scales, b_amax, ids=None, act="none", bias=None, residual=None,
             out_dtype=None, cfg=Config(), out=None):
     """fos_matvec4: act(x . b[e]^T + bias[e]) + residual for few rows x [X, K] that
-    stay in bf16, fp16 or fp32, with NVFP4 weights.  Without ids b is one matrix
+    stay in bf16, fp16 or fp32 (no element is rounded), with NVFP4 weights; for 16
+    rows and more (4 of fp32) linear4 of quantized rows takes less.  Without ids b is one matrix
     (codes [N, K/2], tiled scales, amax [1], bias [N]); with ids (int32 [M], M a
     multiple of X) row p takes x[p // (M / X)] and expert ids[p] of codes [G, N,
     K/2], their tiled scales, amax [G], bias [G, N]; a row with an id outside 0 ..
