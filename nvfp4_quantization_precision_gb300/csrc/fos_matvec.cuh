@@ -157,16 +157,16 @@ __device__ __forceinline__ uint32_t max_halves(uint32_t a, uint32_t b) {
 // last place is 2^-24 at least, then holds every element down to 2^-31 of it (by their
 // exponents) exactly.  fp32: three pieces of 11 significant bits, each the rounding of
 // what is left, the second times 2^11, the third times 2^22; with a last place of 2^-46
-// they hold every element down to 2^-37.  Elements below that are left, zeros in their place, and their products are added
-// in turns of their own (add_left), in each of which the largest of those left sets
-// the power, until none is: nine at most for the whole range of either type.  (The
-// large elements cannot decide how the small ones are held: where they meet zero
-// weights the sum is of the small ones alone.)  Looking for them costs up to 0.4 us
-// a call (1024 x 1024 3.4 us without, 3.8 with; 2048 x 7168 6.2 .. 6.5 and 6.5 .. 6.8; 14336 x 4096
-// 11.5 and 11.3, which has a product less a sum now; ten fp32 rows x 3520 x 6784 33.8 and
-// 35.3).  With the turns in the loop over steps 14336 x 4096 took 11.9; with infinities
-// and NaN looked for in every block 1408 x 2048 of 16 experts 14.1 instead of 13.6, with one
-// branch for all that is rare 14.7 (six experts x 4096 x 14336 61 instead of 56).
+// they hold every element down to 2^-37.  Elements below that are left, zeros in their
+// place, and their products are added in turns of their own (add_left), in each of which
+// the largest of those left sets the power, until none is: nine at most for the whole
+// range of either type.  (The large elements cannot decide how the small ones are held:
+// where they meet zero weights the sum is of the small ones alone.)  Looking for them
+// costs up to 0.4 us a call (1024 x 1024 3.4 us without, 3.8 with; 2048 x 7168 6.2 .. 6.5 and
+// 6.5 .. 6.8; ten fp32 rows x 3520 x 6784 33.8 and 35.3; 14336 x 4096 11.5 and 11.3, a product
+// less a sum).  With the turns in the loop over steps 14336 x 4096 took 11.9; with
+// infinities and NaN looked for in every block 1408 x 2048 of 16 experts 14.1 instead of 13.6,
+// with one branch for all that is rare 14.7 (six experts x 4096 x 14336 61 instead of 56).
 template <In XT> constexpr int deep() { return XT == In::F32 ? 37 : 31; }
 // The weight's decode scale as m 2^e, 1 <= m < 2.
 struct Decode {
@@ -180,10 +180,9 @@ __device__ __forceinline__ Decode split(float g) {
 }
 // What brings a step's products to the result's scale is the decode scale times what undoes
 // x's factor, m 2^(e - 141 + its e).  Where that exponent is outside these bounds (the
-// third piece's is 22 below) and where an element is infinite or NaN, all of a row's
-// elements of the step are left, for a factor in two parts
-// (two parts for every step: 58 us instead of 56.7 for six experts x 4096 x 14336, 21.0
-// instead of 20.4 for eight rows of one).
+// third piece's is 22 below), and where an element is infinite or NaN, all of a row's
+// elements of the step are left, for a factor in two parts (two parts for every step: 58
+// us instead of 56.7 for six experts x 4096 x 14336, 21.0 instead of 20.4 for eight rows of one).
 constexpr int kDownLeast = -100, kDownMost = 127;
 struct Fit {
     int e;     // exponent field of the largest (at least 14); x is multiplied by 2^(141 - e)
@@ -512,7 +511,6 @@ __global__ void __launch_bounds__(32 * kWarpsMv, 2) k_matvec4(const __grid_const
             }
         }
         load_scales(lo + warp);
-        bool again = false;  // put_x left elements of this chunk's rows
         // x by as many steps at a time as its place in shared memory holds
         const int seg = kXBytes / kXStep / cols / kWarpsMv * kWarpsMv;
         const uint32_t col_bytes = (uint32_t)(seg * kXStep);
@@ -530,8 +528,8 @@ __global__ void __launch_bounds__(32 * kWarpsMv, 2) k_matvec4(const __grid_const
                 left |= fit.left > 0;
                 if (XT != In::F16 && t == 0) s_down[tk * seg + st] = put_down(fit, gd);
             }
-            if constexpr (XT == In::F16) __syncthreads();
-            else { if (left) s_again = 1; __syncthreads(); }
+            if (left) s_again = 1;
+            __syncthreads();
             // a column that is not there reads the step of zeros
             const bool live = g < cols;
             const float pd0 = piece_down<XT>(2 * t), pd1 = piece_down<XT>(2 * t + 1);
@@ -600,7 +598,7 @@ __global__ void __launch_bounds__(32 * kWarpsMv, 2) k_matvec4(const __grid_const
             part[(2 * t + 1) * kLine + 16 * i + 8 + g] = acc[i][3];
         }
         if constexpr (XT != In::F16) {
-            if (s_again)
+            if (s_again)  // put_x left elements of this chunk's rows
                 add_left<XT, kR>(a, e, row0, lo, hi, a.ids ? s_ids + c0 : nullptr, first + c0, ntok, gd, part,
                                  s_x + warp * (kXBytes / kWarpsMv), reinterpret_cast<float2*>(s_down) + warp * 8);
         }
